@@ -29,7 +29,7 @@ HSA_DEVERR_BAD_LEN = 16
 HSA_DEVERR_TIMEOUT = 32
 
 # every symbol include/hsa.h declares
-EXPORTS = ("hsa_kv_append", "hsa_decode_workspace_bytes", "hsa_decode_attn",
+EXPORTS = ("hsa_kv_append", "hsa_rope", "hsa_rope_kv_append", "hsa_decode_workspace_bytes", "hsa_decode_attn",
            "hsa_decode_attn_append", "hsa_decode_attn_ex", "hsa_decode_attn_noalloc",
            "hsa_prefill_attn",
            "hsa_swa_prefetch",
@@ -68,6 +68,18 @@ class HsaPools(ctypes.Structure):
     ]
 
 
+class HsaRopeParams(ctypes.Structure):
+    """Mirror of the C struct hsa_rope_params."""
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+        ("axis_of_pair", ctypes.POINTER(ctypes.c_uint8)),
+    ]
+
+
 _lib = None
 
 
@@ -82,6 +94,13 @@ def lib():
         pp = ctypes.POINTER(HsaPools)
         L.hsa_kv_append.restype = ctypes.c_int
         L.hsa_kv_append.argtypes = [pp, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp]
+        i64 = ctypes.c_int64
+        rp = ctypes.POINTER(HsaRopeParams)
+        L.hsa_rope.restype = ctypes.c_int
+        L.hsa_rope.argtypes = [rp, vp, i64, vp, i64, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.hsa_rope_kv_append.restype = ctypes.c_int
+        L.hsa_rope_kv_append.argtypes = [pp, i32, rp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                         i32, i32, vp, vp, vp, vp]
         L.hsa_decode_workspace_bytes.restype = sz
         L.hsa_decode_workspace_bytes.argtypes = [pp, i32, i32]
         L.hsa_decode_attn.restype = ctypes.c_int
@@ -327,6 +346,167 @@ def hsa_kv_append(pool, layer, k_new, v_new, cu_tokens, seq_idx, start_pos, dev_
                             _ptr(seq_idx), _ptr(start_pos), R, k_new.shape[0], _ptr(dev_err),
                             _stream(stream))
     _check("hsa_kv_append", s)
+
+
+class Rope:
+    """Rotary positions: the C struct hsa_rope_params and the arrays it points at.
+
+    rot_dim        the leading values of a head that are turned (a multiple of 16)
+    base           inv_freq[i] = base ** (-2 i / rot_dim), unless inv_freq is given
+                   (rot_dim / 2 numbers, or a tensor: any scaled frequencies)
+    sections       pairs on each axis in order, e.g. (16, 24, 24) for time, height and
+                   width; or axis_of_pair, the axis of each pair (any interleaving)
+    interleaved    pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2)
+    scale          of the turned values
+    """
+
+    def __init__(self, rot_dim=128, base=10000.0, sections=None, interleaved=False, scale=1.0,
+                 inv_freq=None, axis_of_pair=None):
+        half = int(rot_dim) // 2
+        if inv_freq is None:
+            inv_freq = [float(base) ** (-2.0 * i / rot_dim) for i in range(half)]
+        elif isinstance(inv_freq, torch.Tensor):
+            inv_freq = inv_freq.detach().double().cpu().tolist()
+        inv_freq = [float(f) for f in inv_freq]
+        if len(inv_freq) != half:
+            raise ValueError("inv_freq must hold rot_dim / 2 = %d numbers, got %d"
+                             % (half, len(inv_freq)))
+        if sections is not None:
+            if axis_of_pair is not None:
+                raise ValueError("give sections or axis_of_pair, not both")
+            if any(int(s) < 0 for s in sections) or sum(int(s) for s in sections) != half:
+                raise ValueError("sections must add up to rot_dim / 2 = %d" % half)
+            axis_of_pair = [a for a, s in enumerate(sections) for _ in range(int(s))]
+            n_axes = len(sections)
+        elif axis_of_pair is not None:
+            if isinstance(axis_of_pair, torch.Tensor):
+                axis_of_pair = axis_of_pair.cpu().tolist()
+            axis_of_pair = [int(a) for a in axis_of_pair]
+            n_axes = max(axis_of_pair, default=0) + 1
+        else:
+            axis_of_pair, n_axes = [0] * half, 1
+        if len(axis_of_pair) != half or any(not 0 <= a < 4 for a in axis_of_pair) or n_axes > 4:
+            raise ValueError("axis_of_pair must hold rot_dim / 2 = %d axes, each 0 .. 3" % half)
+        self.rot_dim, self.n_axes = int(rot_dim), n_axes
+        self._inv = (ctypes.c_double * max(half, 1))(*inv_freq)
+        self._axis = (ctypes.c_uint8 * max(half, 1))(*axis_of_pair)
+        self.c = HsaRopeParams(rot_dim=self.rot_dim, n_axes=n_axes, interleaved=int(bool(interleaved)),
+                               scale=float(scale),
+                               inv_freq=ctypes.cast(self._inv, ctypes.POINTER(ctypes.c_double)),
+                               axis_of_pair=ctypes.cast(self._axis, ctypes.POINTER(ctypes.c_uint8)))
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _head_rows(t, name, heads, d, n=None):
+    """The token stride (elements) of a [n, heads, d] bf16 tensor whose tokens' heads are
+    contiguous: dense, or a slice of wider rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d or \
+            (n is not None and t.shape[0] != n):
+        raise ValueError("%s must have shape %s, got %s" % (
+            name, ("n" if n is None else n, "heads" if heads is None else heads, d),
+            tuple(t.shape)))
+    s0, s1, s2 = t.stride()
+    width = t.shape[1] * d
+    if t.shape[0] <= 1:
+        s0 = width
+    if s2 != 1 or (s1 != d and t.shape[1] > 1) or s0 < width or s0 % 8:
+        raise ValueError("%s: a token's heads must be contiguous and its stride a multiple of 8, "
+                         "got strides %s" % (name, tuple(t.stride())))
+    return s0
+
+
+def _positions(rope, positions, n):
+    _need(positions, "positions", torch.int32)
+    if tuple(positions.shape) != (rope.n_axes, n) and not (
+            rope.n_axes == 1 and tuple(positions.shape) == (n,)):
+        raise ValueError("positions must have shape %s, got %s" % ((rope.n_axes, n),
+                                                                   tuple(positions.shape)))
+
+
+def _current_device(t):
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError("tensors on %s, but the current device is cuda:%d"
+                         % (t.device, torch.cuda.current_device()))
+
+
+def hsa_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
+    """Turn the query heads q [n, Hq, d] and key heads k [n, Hkv, d] (bf16; dense, or slices
+    of a QKV projection's rows) by positions [n_axes, n] int32 -> (q_out, k_out), dense.
+    Either side may be None.  q_out may be a dense q itself (in place), and k_out k."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("give q, k or both")
+    n, d = some.shape[0], some.shape[-1]
+    Hq = Hkv = qs = ks = 0
+    if q is not None:
+        qs, Hq = _head_rows(q, "q", None, d, n), q.shape[1]
+        q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _need(q_out, "q_out", torch.bfloat16)
+        _shape(q_out, "q_out", (n, Hq, d))
+    if k is not None:
+        ks, Hkv = _head_rows(k, "k", None, d, n), k.shape[1]
+        k_out = torch.empty((n, Hkv, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
+        _need(k_out, "k_out", torch.bfloat16)
+        _shape(k_out, "k_out", (n, Hkv, d))
+    _positions(rope, positions, n)
+    _same_device(positions, q, k, q_out if q is not None else None,
+                 k_out if k is not None else None)
+    _current_device(positions)
+    s = lib().hsa_rope(rope.ref(), _ptr(q), qs, _ptr(k), ks, _ptr(positions), n, Hq, Hkv, d,
+                       _ptr(q_out) if q is not None else None,
+                       _ptr(k_out) if k is not None else None, _stream(stream))
+    _check("hsa_rope", s)
+    return q_out, k_out
+
+
+def hsa_rope_kv_append(pool, layer, rope, q, k_new, v_new, cu_tokens, seq_idx, start_pos,
+                       positions=None, q_out=None, k_out=None, dev_err=None, stream=None):
+    """hsa_kv_append with the rotation on the way -> (q_out, k_out).  q [ntok, Hq, d] (or
+    None: keys alone), k_new and v_new [ntok, Hkv, d] as in hsa_rope; positions [n_axes,
+    ntok] int32, or None: each token's cache position on every axis.  k_out=False leaves
+    the turned keys out (they go to the pool alone)."""
+    n = k_new.shape[0] if isinstance(k_new, torch.Tensor) else 0
+    ks = _head_rows(k_new, "k_new", pool.Hkv, pool.d)
+    vs = _head_rows(v_new, "v_new", pool.Hkv, pool.d, n)
+    qs = 0
+    if q is not None:
+        qs = _head_rows(q, "q", pool.Hq, pool.d, n)
+        if q_out is None:
+            q_out = torch.empty((n, pool.Hq, pool.d), dtype=q.dtype, device=q.device)
+        _need(q_out, "q_out", torch.bfloat16)
+        _shape(q_out, "q_out", (n, pool.Hq, pool.d))
+    else:
+        q_out = None
+    if k_out is False:
+        k_out = None
+    else:
+        if k_out is None:
+            k_out = torch.empty((n, pool.Hkv, pool.d), dtype=k_new.dtype, device=k_new.device)
+        _need(k_out, "k_out", torch.bfloat16)
+        _shape(k_out, "k_out", (n, pool.Hkv, pool.d))
+    for nm, t in (("cu_tokens", cu_tokens), ("seq_idx", seq_idx), ("start_pos", start_pos)):
+        _need(t, nm, torch.int32, ndim=1)
+    R = seq_idx.shape[0]
+    if cu_tokens.shape[0] != R + 1 or start_pos.shape[0] != R:
+        raise ValueError("cu_tokens must be [R+1] and start_pos [R]")
+    if positions is not None:
+        _positions(rope, positions, n)
+    _need_err(dev_err)
+    _same_device(k_new, q, v_new, cu_tokens, seq_idx, start_pos, positions, q_out, k_out, dev_err,
+                 pool.block_tables)
+    _current_device(k_new)
+    s = lib().hsa_rope_kv_append(pool.ref(), int(layer), rope.ref(), _ptr(q), qs, _ptr(k_new), ks,
+                                 _ptr(v_new), vs, _ptr(positions), _ptr(cu_tokens), _ptr(seq_idx),
+                                 _ptr(start_pos), R, n, _ptr(q_out), _ptr(k_out), _ptr(dev_err),
+                                 _stream(stream))
+    _check("hsa_rope_kv_append", s)
+    return q_out, k_out
 
 
 def hsa_decode_workspace_bytes(pool, B, T):

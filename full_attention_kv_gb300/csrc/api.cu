@@ -4,6 +4,7 @@
 // pool tensors, sizes grids and queues kernels on the caller's stream.  It never
 // allocates device memory and never synchronises.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "hsa_internal.h"
@@ -133,6 +134,80 @@ hsa_status check_pools(const hsa_pools *p, int32_t layer)
     return HSA_OK;
 }
 
+// inv_freq / (2 pi) as a 64-bit binary fraction of a turn (whole turns dropped, a
+// negative frequency as the two's complement): the quotient as an unevaluated sum r + e
+// of two doubles, so that the fraction is good to about 2^-63 and pos * fraction to
+// 2^-32 of a turn at |pos| = 2^31.
+uint64_t turn_fraction(double f)
+{
+    const double hi = 0.15915494309189535;     // 1 / (2 pi), rounded
+    const double lo = -9.839338337591243e-18;  // what the rounding left
+    const double a = std::fabs(f);
+    double r = a * hi;
+    const double e = std::fma(a, hi, -r) + a * lo;
+    r -= std::floor(r);  // exact
+    // the top and the low 32 bits of r, each exact in a double; then e, in units of 2^-63
+    const double top = std::floor(r * 4294967296.0);
+    const double low = (r * 4294967296.0 - top) * 4294967296.0;
+    const double rest = std::nearbyint((e - std::nearbyint(e)) * 9223372036854775808.0);
+    const uint64_t t = ((uint64_t)top << 32) + (uint64_t)low + 2u * (uint64_t)(int64_t)rest;
+    return f < 0 ? 0u - t : t;
+}
+
+// Checks a rope description and fills the kernel's form of it.
+hsa_status fill_rope(const hsa_rope_params *r, int32_t d, hsa::RopeParams *p)
+{
+    if (!r || !r->inv_freq)
+        return HSA_INVALID_ARG;
+    if (d != 128 || r->rot_dim < 16 || r->rot_dim > d || r->rot_dim % 16 != 0)
+        return HSA_UNSUPPORTED_SHAPE;
+    if (r->n_axes < 1 || r->n_axes > 4 || (r->interleaved & ~1) || !std::isfinite(r->scale))
+        return HSA_INVALID_ARG;
+    for (int i = 0; i < r->rot_dim / 2; ++i) {
+        // beyond 2^40 radians a position the product has no fraction left to give
+        if (!std::isfinite(r->inv_freq[i]) || std::fabs(r->inv_freq[i]) > 1099511627776.0)
+            return HSA_INVALID_ARG;
+        const int ax = r->axis_of_pair ? r->axis_of_pair[i] : 0;
+        if (ax >= r->n_axes)
+            return HSA_INVALID_ARG;
+        p->axis2[i >> 4] |= (uint32_t)ax << (2 * (i & 15));
+        p->turn[i] = turn_fraction(r->inv_freq[i]);
+    }
+    p->rot16 = r->rot_dim / 16;
+    p->interleaved = r->interleaved;
+    p->scale = r->scale;
+    return HSA_OK;
+}
+
+// n rows of `heads` heads of 128 bf16, `stride` elements apart (0 = dense, resolved here)
+struct Rows {
+    const uint8_t *lo = nullptr, *hi = nullptr;  // bytes spanned
+    int64_t stride = 0;
+    bool dense = true;
+};
+
+bool rows_ok(const void *ptr, int64_t stride, int32_t n, int32_t heads, Rows *r)
+{
+    const int64_t row = (int64_t)heads * 128;
+    if (!ptr || !aligned16(ptr) || stride < 0 || stride % 8 != 0)
+        return false;
+    r->stride = stride ? stride : row;
+    if (n > 1 && r->stride < row)
+        return false;
+    r->dense = n <= 1 || r->stride == row;
+    r->lo = static_cast<const uint8_t *>(ptr);
+    r->hi = r->lo + ((n - 1) * r->stride + row) * 2;
+    return true;
+}
+
+bool overlap(const Rows &a, const Rows &b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// An output's rows against an input's: disjoint, or the same dense rows (in place).
+bool out_ok(const Rows &out, const Rows &in, bool own)
+{
+    return !overlap(out, in) || (own && out.lo == in.lo && in.dense);
+}
+
 }  // namespace
 
 extern "C" {
@@ -195,6 +270,115 @@ hsa_status hsa_kv_append(const hsa_pools *pools, int32_t layer, const void *k_ne
     a.fp8 = layer_fp8(pools, layer) == HSA_KV_E5M2 ? 2 : layer_fp8(pools, layer) ? 1 : 0;
     return hsa::launch_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HSA_OK
                                                                                   : HSA_CUDA_ERROR;
+}
+
+hsa_status hsa_rope(const hsa_rope_params *rope, const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const int32_t *positions, int32_t n, int32_t Hq, int32_t Hkv,
+                    int32_t d, void *q_out, void *k_out, void *stream)
+{
+    hsa::RopeParams p{};
+    const hsa_status st = fill_rope(rope, d, &p);
+    if (st != HSA_OK)
+        return st;
+    if (n < 0 || Hq < 0 || Hkv < 0)
+        return HSA_INVALID_ARG;
+    if (n == 0 || (Hq == 0 && Hkv == 0))
+        return HSA_OK;
+    Rows rq, rk, oq, ok;
+    if (!positions)
+        return HSA_INVALID_ARG;
+    if (Hq > 0 && (!rows_ok(q, q_stride, n, Hq, &rq) || !rows_ok(q_out, 0, n, Hq, &oq)))
+        return HSA_INVALID_ARG;
+    if (Hkv > 0 && (!rows_ok(k, k_stride, n, Hkv, &rk) || !rows_ok(k_out, 0, n, Hkv, &ok)))
+        return HSA_INVALID_ARG;
+    if (!out_ok(oq, rq, true) || !out_ok(oq, rk, false) || !out_ok(ok, rk, true) ||
+        !out_ok(ok, rq, false) || overlap(oq, ok))
+        return HSA_INVALID_ARG;
+    p.q = static_cast<const uint4 *>(q);
+    p.k = static_cast<const uint4 *>(k);
+    p.q_out = static_cast<uint4 *>(q_out);
+    p.k_out = static_cast<uint4 *>(k_out);
+    p.q_stride = rq.stride / 8;
+    p.k_stride = rk.stride / 8;
+    p.pos = positions;
+    p.n = n;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return HSA_CUDA_ERROR;
+    return hsa::launch_rope(p, false, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
+}
+
+hsa_status hsa_rope_kv_append(const hsa_pools *pools, int32_t layer, const hsa_rope_params *rope,
+                              const void *q, int64_t q_stride, const void *k_new,
+                              int64_t k_stride, const void *v_new, int64_t v_stride,
+                              const int32_t *positions, const int32_t *cu_tokens,
+                              const int32_t *seq_idx, const int32_t *start_pos, int32_t R,
+                              int32_t ntok, void *q_out, void *k_out, int32_t *dev_err,
+                              void *stream)
+{
+    hsa_status st = check_pools(pools, layer);
+    if (st != HSA_OK)
+        return st;
+    hsa::RopeParams p{};
+    st = fill_rope(rope, pools->d, &p);
+    if (st != HSA_OK)
+        return st;
+    if (R < 0 || ntok < 0)
+        return HSA_INVALID_ARG;
+    if (ntok == 0 || R == 0)
+        return HSA_OK;
+    if (!cu_tokens || !seq_idx || !start_pos || (q == nullptr) != (q_out == nullptr))
+        return HSA_INVALID_ARG;
+    const int32_t Hq = q ? pools->Hq : 0, Hkv = pools->Hkv;
+    Rows rq, rk, rv, oq, ok;
+    if (!rows_ok(k_new, k_stride, ntok, Hkv, &rk) || !rows_ok(v_new, v_stride, ntok, Hkv, &rv))
+        return HSA_INVALID_ARG;
+    if (q && (!rows_ok(q, q_stride, ntok, Hq, &rq) || !rows_ok(q_out, 0, ntok, Hq, &oq)))
+        return HSA_INVALID_ARG;
+    if (k_out && !rows_ok(k_out, 0, ntok, Hkv, &ok))
+        return HSA_INVALID_ARG;
+    if (!out_ok(oq, rq, true) || !out_ok(oq, rk, false) || !out_ok(oq, rv, false) ||
+        !out_ok(ok, rk, true) || !out_ok(ok, rq, false) || !out_ok(ok, rv, false) ||
+        overlap(oq, ok))
+        return HSA_INVALID_ARG;
+    p.q = static_cast<const uint4 *>(q);
+    p.k = static_cast<const uint4 *>(k_new);
+    p.v = static_cast<const uint4 *>(v_new);
+    p.q_out = static_cast<uint4 *>(q_out);
+    p.k_out = static_cast<uint4 *>(k_out);
+    p.q_stride = rq.stride / 8;
+    p.k_stride = rk.stride / 8;
+    p.v_stride = rv.stride / 8;
+    p.pos = positions;
+    p.n = ntok;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.cu_tokens = cu_tokens;
+    p.seq_idx = seq_idx;
+    p.start_pos = start_pos;
+    p.k_dst = static_cast<uint4 *>(pools->k[layer]);
+    p.v_dst = static_cast<uint4 *>(pools->v[layer]);
+    p.block_tables = pools->block_tables;
+    p.ring_row = pools->ring_row;
+    p.dev_err = dev_err;
+    p.R = R;
+    p.batch = pools->batch;
+    p.max_blocks = pools->max_blocks;
+    p.num_blocks = pools->num_blocks;
+    p.n_ring_rows = pools->n_ring_rows;
+    p.W = pools->W;
+    p.ring_mode = pools->layer_is_full[layer] ? 0 : 1;
+    p.fp8 = layer_fp8(pools, layer) == HSA_KV_E5M2 ? 2 : layer_fp8(pools, layer) ? 1 : 0;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return HSA_CUDA_ERROR;
+    return hsa::launch_rope(p, true, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
 }
 
 size_t hsa_decode_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T)

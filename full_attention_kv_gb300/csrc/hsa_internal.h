@@ -77,6 +77,34 @@ struct AppendParams {
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 
+// Rotary positions (rope.cu).  Rows are counted in 16-byte chunks: a head is 16 of them.
+struct RopeParams {
+    const uint4 *q, *k, *v;      // n rows of heads; row strides below
+    uint4 *q_out, *k_out;        // [n, Hq, d], [n, Hkv, d] dense (k_out may be null)
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *pos;          // [n_axes, n]; null: the cache position on every axis
+    int32_t n, Hq, Hkv;
+    int32_t rot16;               // rot_dim / 16
+    int32_t interleaved;
+    int32_t quads;               // head quads an item takes (set by launch_rope)
+    float scale;
+    uint32_t axis2[4];           // axis of pair i: two bits at 2 (i % 16) of word i / 16
+    uint64_t turn[64];           // inv_freq / 2 pi as a 64-bit fraction of a turn
+    // append only
+    const int32_t *cu_tokens;    // [R+1]
+    const int32_t *seq_idx;      // [R]
+    const int32_t *start_pos;    // [R]
+    uint4 *k_dst, *v_dst;        // the layer's pool / ring
+    const int32_t *block_tables;
+    const int32_t *ring_row;
+    int32_t *dev_err;
+    int32_t R, batch, max_blocks, num_blocks, n_ring_rows, W;
+    int32_t ring_mode;
+    int32_t fp8;                 // 0 bf16, 1 E4M3, 2 E5M2
+};
+
+cudaError_t launch_rope(RopeParams &p, bool append, int sms, cudaStream_t stream);
+
 // Prefill keeps its larger by-value struct: promoted into registers (<= 128
 // bytes) it raised the prefill kernel's spills from 76 to 252 bytes.
 struct PrefillParams {

@@ -1,0 +1,344 @@
+// rope.cu -- rotary positions on several axes, alone and on the way into the dual KV
+// pool (sm_103a).
+//
+// What it computes: for token n, a query or key head x[0 .. d-1] and pair i of its first
+// rot_dim values, (a, b) = (i, i + rot_dim / 2) or (2 i, 2 i + 1),
+//   y_a = s (x_a cos t - x_b sin t),  y_b = s (x_b cos t + x_a sin t),
+//   t = pos[axis(i)][n] * inv_freq[i],
+// values past rot_dim unchanged.  Several axes (time, height, width) give an image's or
+// a video's tokens a position on each [youleyou.com "小米MiMo首次公开模型推理系统全链路优化
+// 降价99%", s2 "Decode加速与多模态优化": the stack serves images and video].  The append
+// form also writes the turned keys and the values where hsa_kv_append would: a page row of
+// a full layer (bf16, or FP8 codes and a scale), or a ring slot.
+//
+// The angle: an fp32 product pos * inv_freq is off by 2^-24 of itself, 0.06 rad at a
+// million tokens.  Only its fraction of a turn matters, so the host gives inv_freq / 2 pi
+// as a 64-bit binary fraction F of a turn and the kernel takes the low 64 bits of
+// pos * F: the whole turns fall off the top, exactly, and the top 32 bits are the angle
+// to 2^-32 of a turn for every 32-bit position, negative ones too.  One integer
+// multiply; cos and sin then see an argument in [-1, 1] half turns.
+//
+// Layout: eight lanes take a head, lane c its 16-byte chunks c and c + rot_dim / 16, which
+// hold both sides of each of its eight pairs (or, interleaved, eight whole pairs), so a
+// pair never crosses lanes; chunks past rot_dim go to the remaining lanes.  A warp takes
+// four heads at a time and reads 128 contiguous bytes of each.  Each lane computes two of
+// a token's 64 angles and the warp exchanges them by shuffles, once for all heads.
+#include "fp8_kv.cuh"
+#include "hsa_device.cuh"
+#include "hsa_internal.h"
+
+namespace hsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;  // head quads whose loads are in flight together
+
+enum Kind { kRope = 0, kAppend = 1, kAppendFp8 = 2 };
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8])
+{
+    x[0] = bf16_lo(w.x);
+    x[1] = bf16_hi(w.x);
+    x[2] = bf16_lo(w.y);
+    x[3] = bf16_hi(w.y);
+    x[4] = bf16_lo(w.z);
+    x[5] = bf16_hi(w.z);
+    x[6] = bf16_lo(w.w);
+    x[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+{
+    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                      pack_bf16(x[6], x[7]));
+}
+
+// The eight pairs of a lane's two chunks turned by (cs, sn) j = 0 .. 7.
+template <bool INTER>
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&cs)[8],
+                                     const float (&sn)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float &x = INTER ? (j < 4 ? a[2 * j] : b[2 * (j - 4)]) : a[j];
+        float &y = INTER ? (j < 4 ? a[2 * j + 1] : b[2 * (j - 4) + 1]) : b[j];
+        const float x0 = x, y0 = y;
+        x = x0 * cs[j] - y0 * sn[j];
+        y = y0 * cs[j] + x0 * sn[j];
+    }
+}
+
+// Request that owns token tok: the r with cu[r] <= tok < cu[r + 1], by a 32-way search (one
+// coalesced read a level, not log2 R dependent ones).  Called by a whole warp.
+__device__ __forceinline__ int find_request(const int32_t *cu, int R, int tok, int lane)
+{
+    int lo = 0, hi = R;  // cu[lo] <= tok (or lo = 0), tok < cu[hi] (or hi = R)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int at = lo + (lane + 1) * step;  // candidates lo + step, lo + 2 step, ...
+        const bool le = at < hi && __ldg(cu + at) <= tok;
+        const int k = __popc(__ballot_sync(0xffffffffu, le));
+        const int nlo = lo + k * step;
+        hi = min(hi, nlo + step);
+        lo = nlo;
+    }
+    return lo;
+}
+
+// Destination row of cache position pos of sequence seq (units of one head's rows), or
+// -1 with *err set.
+__device__ __forceinline__ int64_t pool_row(const RopeParams &p, int seq, int64_t pos, int *err)
+{
+    if (seq < 0 || seq >= p.batch) {
+        *err = HSA_DEVERR_BAD_SEQ;
+        return -1;
+    }
+    if (p.ring_mode) {
+        const int rr = __ldg(p.ring_row + seq);
+        if (rr < 0 || rr >= p.n_ring_rows) {
+            *err = HSA_DEVERR_BAD_RING;
+            return -1;
+        }
+        return (int64_t)rr * p.Hkv * p.W + pos % p.W;
+    }
+    const int64_t page = pos / 64;
+    if (page >= p.max_blocks) {
+        *err = HSA_DEVERR_BAD_PAGE;
+        return -1;
+    }
+    const int blk = __ldg(p.block_tables + (int64_t)seq * p.max_blocks + page);
+    if (blk < 0 || blk >= p.num_blocks) {
+        *err = HSA_DEVERR_BAD_BLOCK;
+        return -1;
+    }
+    return (int64_t)blk * p.Hkv * 64 + pos % 64;
+}
+
+// One FP8 row a lane octet: a, b the lane's chunks ca, cb of the head in fp32 (quantised
+// straight from them: one rounding).  K rows go through `stage` (128 bytes of shared memory
+// an octet) into 16-byte stores; V rows are stored transposed, a byte a dimension.
+__device__ __forceinline__ void store_fp8(const float (&a)[8], const float (&b)[8], int ca, int cb,
+                                          bool on, bool is_v, int64_t row, int h,
+                                          const RopeParams &p, uint8_t *stage, int c)
+{
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        amax = fmaxf(amax, fmaxf(fabsf(a[j]), fabsf(b[j])));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const bool e5 = p.fp8 == 2;
+    const float scale = __fdiv_rn(amax, e5 ? 57344.0f : 448.0f);
+    uint32_t code[8];  // two codes each: a's four pairs of neighbours, then b's
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = j < 4 ? a[2 * j] : b[2 * j - 8], y = j < 4 ? a[2 * j + 1] : b[2 * j - 7];
+        code[j] = 0;
+        if (amax > 0.f) {
+            const float u = __fdiv_rn(x, scale), w = __fdiv_rn(y, scale);
+            code[j] = e5 ? f32x2_to_e5m2x2(u, w) : f32x2_to_e4m3x2(u, w);
+        }
+    }
+    // row = blk * Hkv * 64 + off: head h's page is blk * Hkv + h
+    const int off = (int)(row & 63);
+    const int64_t page = (row >> 6) + h;
+    uint8_t *const base = reinterpret_cast<uint8_t *>(is_v ? p.v_dst : p.k_dst);
+    float *const scales = reinterpret_cast<float *>(base + fp8_codes_bytes(p.num_blocks, p.Hkv));
+    if (on && c == 0)
+        scales[page * 64 + off] = amax > 0.f ? scale : 0.f;
+    if (!is_v) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int ch = j < 4 ? ca : cb;  // dims 8 ch + 2 (j % 4), +1
+            *reinterpret_cast<uint16_t *>(stage + 16 * (ch >> 1) + 2 * (ch & 1) + 4 * (j & 3)) =
+                (uint16_t)code[j];
+        }
+        __syncwarp();
+        if (on)
+            *reinterpret_cast<uint4 *>(base + (page * 64 + off) * 128 + 16 * c) =
+                *reinterpret_cast<const uint4 *>(stage + 16 * c);
+    } else if (on) {
+        const int kb = 16 * (off >> 4) + perm16(off & 15);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int dim = 8 * (j < 4 ? ca : cb) + 2 * (j & 3);
+            base[(page * 128 + dim) * 64 + kb] = (uint8_t)code[j];
+            base[(page * 128 + dim + 1) * 64 + kb] = (uint8_t)(code[j] >> 8);
+        }
+    }
+}
+
+// One warp an item: a token and a slice of its head quads (q heads, k heads, then, when
+// appending, v heads).
+template <int KIND, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p)
+{
+    __shared__ uint4 stage_all[KIND == kAppendFp8 ? kWarps * 32 : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = lane & 7, hl = lane >> 3;
+    const bool rot = c < p.rot16;
+    const int ca = rot ? c : 2 * c, cb = rot ? c + p.rot16 : 2 * c + 1;
+    // this lane computes angles j = 2 hl, 2 hl + 1 of the eight of its chunk pair
+    uint64_t F[2] = {0, 0};
+    int ax[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int j = 2 * hl + e;
+        const int i = INTER ? (j < 4 ? 4 * c + j : 4 * (c + p.rot16) + j - 4) : 8 * c + j;
+        if (rot) {
+            F[e] = p.turn[i];
+            ax[e] = (p.axis2[i >> 4] >> (2 * (i & 15))) & 3;
+        }
+    }
+    const int qq = (p.Hq + 3) >> 2, kq = (p.Hkv + 3) >> 2;
+    const int nq = qq + kq + (KIND == kRope ? 0 : kq);
+    const int slices = (nq + p.quads - 1) / p.quads;
+    const int64_t items = (int64_t)p.n * slices;
+    uint8_t *const stage =
+        reinterpret_cast<uint8_t *>(stage_all) + (KIND == kAppendFp8 ? (warp * 4 + hl) * 128 : 0);
+    grid_dependency_wait();
+    for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
+         it += (int64_t)gridDim.x * kWarps) {
+        const int tok = (int)(it / slices);
+        const int q0 = (int)(it % slices) * p.quads, q1 = min(nq, q0 + p.quads);
+        // ---- the token's request and pool row -------------------------------------
+        int64_t row = -1, first_pos = 0;
+        bool skip = false;
+        if constexpr (KIND != kRope) {
+            const int r = find_request(p.cu_tokens, p.R, tok, lane);
+            const int first = __ldg(p.cu_tokens + r), last = __ldg(p.cu_tokens + r + 1);
+            const int seq = __ldg(p.seq_idx + r);
+            first_pos = (int64_t)__ldg(p.start_pos + r) + (tok - first);
+            int err = 0;
+            if (tok < first || tok >= last || first_pos < 0) {
+                err = HSA_DEVERR_BAD_LEN;
+                skip = true;
+            } else if (!p.ring_mode || tok - first >= (last - first) - p.W) {
+                // (an earlier ring token is overwritten later in this same request)
+                row = pool_row(p, seq, first_pos, &err);
+            }
+            if (err && lane == 0 && q0 == 0)
+                set_err(p.dev_err, err);
+        }
+        if (skip)
+            continue;
+        // ---- cos and sin of the token's angles ---------------------------------------
+        float cs[8], sn[8];
+        {
+            float c2[2], s2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t ps = p.pos ? (int64_t)__ldg(p.pos + (int64_t)ax[e] * p.n + tok)
+                                         : first_pos;
+                const int32_t t = (int32_t)(((uint64_t)ps * F[e]) >> 32);  // 2^-32 of a turn
+                sincospif((float)t * 0x1p-31f, &s2[e], &c2[e]);
+                c2[e] *= p.scale;
+                s2[e] *= p.scale;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                cs[j] = __shfl_sync(0xffffffffu, c2[j & 1], (j >> 1) * 8 + c);
+                sn[j] = __shfl_sync(0xffffffffu, s2[j & 1], (j >> 1) * 8 + c);
+            }
+        }
+        // ---- the head quads -----------------------------------------------------------
+        for (int qb = q0; qb < q1; qb += kBatch) {
+            uint4 wa[kBatch], wb[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int qd = qb + u;
+                const int part = qd < qq ? 0 : (qd < qq + kq ? 1 : 2);
+                const int h = 4 * (qd - (part == 0 ? 0 : (part == 1 ? qq : qq + kq))) + hl;
+                const uint4 *src = part == 0   ? p.q + (int64_t)tok * p.q_stride
+                                   : part == 1 ? p.k + (int64_t)tok * p.k_stride
+                                               : p.v + (int64_t)tok * p.v_stride;
+                wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
+                if (qd < q1 && h < (part == 0 ? p.Hq : p.Hkv) && (part < 2 || row >= 0)) {
+                    wa[u] = __ldcs(src + h * 16 + ca);
+                    wb[u] = __ldcs(src + h * 16 + cb);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int qd = qb + u;
+                if (qd >= q1)
+                    break;
+                const int part = qd < qq ? 0 : (qd < qq + kq ? 1 : 2);
+                const int h = 4 * (qd - (part == 0 ? 0 : (part == 1 ? qq : qq + kq))) + hl;
+                const bool on = h < (part == 0 ? p.Hq : p.Hkv);
+                float a[8], b[8];
+                if (part < 2) {
+                    unpack8(wa[u], a);
+                    unpack8(wb[u], b);
+                    if (rot) {
+                        turn<INTER>(a, b, cs, sn);
+                        wa[u] = pack8(a);
+                        wb[u] = pack8(b);
+                    }
+                    uint4 *const dst =
+                        part == 0 ? p.q_out + ((int64_t)tok * p.Hq + h) * 16
+                                  : (p.k_out ? p.k_out + ((int64_t)tok * p.Hkv + h) * 16 : nullptr);
+                    if (on && dst) {
+                        __stcs(dst + ca, wa[u]);
+                        __stcs(dst + cb, wb[u]);
+                    }
+                }
+                if constexpr (KIND == kAppend) {
+                    if (part > 0 && on && row >= 0) {
+                        uint4 *const dst = (part == 1 ? p.k_dst : p.v_dst) +
+                                           (row + (int64_t)h * (p.ring_mode ? p.W : 64)) * 16;
+                        dst[ca] = wa[u];
+                        dst[cb] = wb[u];
+                    }
+                }
+                if constexpr (KIND == kAppendFp8) {
+                    if (part > 0 && row >= 0) {  // uniform across the warp
+                        if (part == 2) {
+                            unpack8(wa[u], a);
+                            unpack8(wb[u], b);
+                        }
+                        store_fp8(a, b, ca, cb, on, part == 2, row, on ? h : 0, p, stage, c);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int KIND>
+cudaError_t launch(const RopeParams &p, unsigned blocks, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return p.interleaved ? cudaLaunchKernelEx(&cfg, rope_kernel<KIND, true>, p)
+                         : cudaLaunchKernelEx(&cfg, rope_kernel<KIND, false>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeParams &p, bool append, int sms, cudaStream_t stream)
+{
+    const int nq = (p.Hq + 3) / 4 + (p.Hkv + 3) / 4 * (append ? 2 : 1);
+    if (p.n == 0 || nq == 0)
+        return cudaSuccess;
+    p.quads = nq;
+    const int64_t slices = (nq + p.quads - 1) / p.quads;
+    int64_t blocks = ((int64_t)p.n * slices + kWarps - 1) / kWarps;
+    blocks = blocks < (int64_t)sms * 8 ? blocks : (int64_t)sms * 8;
+    if (!append)
+        return launch<kRope>(p, (unsigned)blocks, stream);
+    return p.fp8 ? launch<kAppendFp8>(p, (unsigned)blocks, stream)
+                 : launch<kAppend>(p, (unsigned)blocks, stream);
+}
+
+}  // namespace hsa

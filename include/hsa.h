@@ -144,6 +144,75 @@ hsa_status hsa_kv_append(const hsa_pools *pools, int32_t layer, const void *k_ne
                          int32_t *dev_err, void *stream);
 
 /*
+ * Rotary positions.  Token n's position on axis a is positions[a * n_tokens + n]; pair i of a
+ * head's first rot_dim values, (x[i], x[i + rot_dim / 2]) or, interleaved, (x[2i],
+ * x[2i + 1]), is turned by the angle t = position on axis axis_of_pair[i] * inv_freq[i]:
+ *   (x, y) -> scale * (x cos t - y sin t, y cos t + x sin t)
+ * Values past rot_dim pass unchanged (not scaled).  Text has one axis; an image's or a
+ * video's tokens have several (time, height, width), each with a section of the pairs.
+ * Angles are exact to 2^-31 of a turn at every int32 position (not an fp32 product);
+ * the turn itself is fp32, rounded once to bf16.  Positions may be negative: negated
+ * positions undo a rotation (scale 1).
+ *  rot_dim       a multiple of 16 in [16, d] (else HSA_UNSUPPORTED_SHAPE)
+ *  n_axes        1 .. 4
+ *  interleaved   0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)
+ *  scale         of the turned values (1, or a context extension's attention factor)
+ *  inv_freq      host double [rot_dim / 2]; finite
+ *  axis_of_pair  host uint8 [rot_dim / 2], each < n_axes, or NULL: every pair on axis 0
+ * The host arrays are read during the call only.
+ */
+typedef struct hsa_rope_params {
+    int32_t rot_dim;
+    int32_t n_axes;
+    int32_t interleaved;
+    float scale;
+    const double *inv_freq;
+    const uint8_t *axis_of_pair;
+} hsa_rope_params;
+
+/*
+ * Turns the query and key heads of n tokens.  Before attention with several new tokens on
+ * a sliding layer (MTP verify, prefill chunks), where the append has to come after it;
+ * otherwise hsa_rope_kv_append does both in one launch.
+ *  q  [n, Hq, d] bf16, k [n, Hkv, d] bf16: the heads of a token are contiguous, tokens are
+ *     q_stride / k_stride elements apart (0 = dense; else a multiple of 8, at least one
+ *     token's heads), so slices of a QKV projection's rows serve.
+ *  q_out, k_out  dense; q_out may be q itself and k_out k itself when those are dense, and
+ *     must not overlap an input or each other otherwise (HSA_INVALID_ARG).
+ *  positions     device int32 [n_axes, n]
+ * Hq = 0 or Hkv = 0 leaves that side out (its pointers may be NULL).  d = 128.
+ */
+hsa_status hsa_rope(const hsa_rope_params *rope, const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const int32_t *positions, int32_t n, int32_t Hq, int32_t Hkv,
+                    int32_t d, void *q_out, void *k_out, void *stream);
+
+/*
+ * hsa_kv_append with the rotation on the way: the keys are turned, then keys and values
+ * are written where hsa_kv_append would write them (same requests, same pool rows, same
+ * dev_err bits), and the query heads are turned beside them.  Any layer: full (bf16 or
+ * FP8) or sliding.
+ *  q, k_new, v_new  as hsa_rope's q and k, with strides of their own.  q and q_out may
+ *     both be NULL (keys alone).
+ *  q_out            [ntok, Hq, d]: the turned queries
+ *  k_out            [ntok, Hkv, d] or NULL: the turned keys, for the attention calls
+ *  positions        device int32 [n_axes, ntok], or NULL: a token's cache position
+ *                   (start_pos[r] + i) on every axis
+ * An FP8 layer quantises the turned fp32 values (one rounding); hsa_rope followed by
+ * hsa_kv_append would round them to bf16 first.  bf16 pools get the same bits either way.
+ * A token of no request, or at a negative cache position, is skipped whole and flagged
+ * (HSA_DEVERR_BAD_LEN): its rows of q_out and k_out stay as they were.  A token whose
+ * pool row cannot be reached is flagged and not appended, but its q_out and k_out rows are
+ * written.  On a sliding layer with several new tokens append only after attention.
+ */
+hsa_status hsa_rope_kv_append(const hsa_pools *pools, int32_t layer, const hsa_rope_params *rope,
+                              const void *q, int64_t q_stride, const void *k_new,
+                              int64_t k_stride, const void *v_new, int64_t v_stride,
+                              const int32_t *positions, const int32_t *cu_tokens,
+                              const int32_t *seq_idx, const int32_t *start_pos, int32_t R,
+                              int32_t ntok, void *q_out, void *k_out, int32_t *dev_err,
+                              void *stream);
+
+/*
  * Decode / MTP-verify attention [youleyou s1: decode latency tracks the KV bytes
  * read; s2 "Decode加速与多模态优化": 3-layer MTP, several candidate tokens verified
  * per step].  Sequence b (row b of block_tables / ring_row) has cached_len[b]
