@@ -31,6 +31,7 @@ HSA_DEVERR_TIMEOUT = 32
 # every symbol include/hsa.h declares
 EXPORTS = ("hsa_kv_append", "hsa_rope", "hsa_rope_kv_append", "hsa_decode_workspace_bytes", "hsa_decode_attn",
            "hsa_decode_attn_append", "hsa_decode_attn_ex", "hsa_decode_attn_noalloc",
+           "hsa_decode_shared_workspace_bytes", "hsa_decode_attn_shared",
            "hsa_prefill_attn",
            "hsa_swa_prefetch",
            "hsa_window_safe_len", "hsa_window_safe_len_bitmap", "hsa_status_string")
@@ -115,6 +116,11 @@ def lib():
         L.hsa_decode_attn_noalloc.restype = ctypes.c_int
         L.hsa_decode_attn_noalloc.argtypes = [pp, i32, vp, vp, vp, vp, i32, i32, f32, vp, i32,
                                               vp, vp]
+        L.hsa_decode_shared_workspace_bytes.restype = sz
+        L.hsa_decode_shared_workspace_bytes.argtypes = [pp, i32, i32, i32]
+        L.hsa_decode_attn_shared.restype = ctypes.c_int
+        L.hsa_decode_attn_shared.argtypes = [pp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32,
+                                             vp, vp, sz, i32, i32, vp, vp]
         L.hsa_prefill_attn.restype = ctypes.c_int
         L.hsa_prefill_attn.argtypes = [pp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32, vp,
                                        vp, vp]
@@ -592,6 +598,53 @@ def hsa_decode_attn_noalloc(pool, layer, q, k_new, v_new, cached_len, scale, out
                                       _ptr(cached_len), B, T, float(scale), _ptr(out),
                                       int(max_ctas), _ptr(dev_err), _stream(stream))
     _check("hsa_decode_attn_noalloc", s)
+    return out
+
+
+def hsa_decode_shared_workspace_bytes(pool, B, T, n_groups):
+    return int(lib().hsa_decode_shared_workspace_bytes(pool.ref(), int(B), int(T), int(n_groups)))
+
+
+def decode_shared_workspace(pool, B, T, n_groups, device="cuda"):
+    """Workspace for hsa_decode_attn_shared (allocate once, reuse; zero-filled)."""
+    n = hsa_decode_shared_workspace_bytes(pool, B, T, n_groups)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def hsa_decode_attn_shared(pool, layer, q, k_new, v_new, cached_len, cu_group, shared_len, scale,
+                           out=None, workspace=None, max_ctas=0, dev_err=None, stream=None,
+                           append=False, early_pool_read=False):
+    """Decode attention of a batch whose group g, sequences cu_group[g] .. cu_group[g + 1] - 1,
+    shares the pages of its first shared_len[g] tokens (cu_group [n_groups + 1] and shared_len
+    [n_groups], device int32): hsa_decode_attn's results, with a full layer's shared pages
+    read once a group."""
+    _need(q, "q", torch.bfloat16, ndim=4)
+    _need(k_new, "k_new", torch.bfloat16, ndim=4)
+    _need(v_new, "v_new", torch.bfloat16, ndim=4)
+    for nm, t in (("cached_len", cached_len), ("cu_group", cu_group), ("shared_len", shared_len)):
+        _need(t, nm, torch.int32, ndim=1)
+    B, T = q.shape[0], q.shape[1]
+    _decode_shapes(pool, q, k_new, v_new, cached_len)
+    n_groups = shared_len.shape[0]
+    _shape(cu_group, "cu_group", (n_groups + 1,))
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, ndim=4)
+    _shape(out, "out", q.shape)
+    if workspace is None:
+        workspace = decode_shared_workspace(pool, B, T, n_groups, device=q.device)
+    _need(workspace, "workspace", torch.uint8)
+    _need_err(dev_err)
+    _same_device(q, out, workspace, dev_err, cu_group, shared_len, pool.block_tables)
+    _current_device(q)
+    opts = (HSA_DECODE_APPEND if append else 0) | \
+        (HSA_DECODE_EARLY_POOL_READ if early_pool_read else 0)
+    s = lib().hsa_decode_attn_shared(pool.ref(), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new),
+                                     _ptr(cached_len), _ptr(cu_group), _ptr(shared_len), n_groups,
+                                     B, T, float(scale), _ptr(out), _ptr(workspace),
+                                     workspace.numel(), int(max_ctas), opts, _ptr(dev_err),
+                                     _stream(stream))
+    _check("hsa_decode_attn_shared", s)
     return out
 
 

@@ -426,6 +426,20 @@ hsa_status decode_host_check(const hsa_pools *pools, int32_t layer, const void *
 
 namespace {
 
+// The workspace of a shared-prefix decode: the decode workspace, the plan, the states.
+struct SharedLayout {
+    size_t plan, slots, total;
+};
+
+SharedLayout shared_layout(int ctas, int B, int T, int G, int Hkv, int n_groups)
+{
+    SharedLayout l;
+    l.plan = (hsa::decode_workspace_bytes(ctas, B, Hkv) + 255) & ~size_t(255);
+    l.slots = l.plan + hsa::shared_plan_bytes(n_groups);
+    l.total = l.slots + hsa::shared_slot_bytes(ctas, B, T, G, Hkv, n_groups);
+    return l;
+}
+
 hsa_status decode_common(const hsa_pools *pools, int32_t layer, const void *q, const void *k_new,
                          const void *v_new, const int32_t *cached_len, int32_t B, int32_t T,
                          float scale, void *out, void *workspace, size_t ws_bytes,
@@ -534,6 +548,85 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
 {
     return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out, workspace,
                          ws_bytes, max_ctas, dev_err, stream, options);
+}
+
+size_t hsa_decode_shared_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
+                                         int32_t n_groups)
+{
+    const size_t plain = hsa_decode_workspace_bytes(pools, B, T);
+    if (plain == 0 || T < 1 || n_groups < 0 || pools->Hq <= 0)
+        return 0;
+    const int sms = std::max(device_sms(), 1);
+    return std::max(plain, shared_layout(sms, B, T, pools->Hq / pools->Hkv, pools->Hkv, n_groups).total);
+}
+
+hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const void *q,
+                                  const void *k_new, const void *v_new,
+                                  const int32_t *cached_len, const int32_t *cu_group,
+                                  const int32_t *shared_len, int32_t n_groups, int32_t B,
+                                  int32_t T, float scale, void *out, void *workspace,
+                                  size_t ws_bytes, int32_t max_ctas, int32_t options,
+                                  int32_t *dev_err, void *stream)
+{
+    if (options & ~(HSA_DECODE_APPEND | HSA_DECODE_EARLY_POOL_READ))
+        return HSA_INVALID_ARG;
+    bool done = false;
+    const hsa_status st = hsa::decode_host_check(pools, layer, q, k_new, v_new, cached_len, B, T,
+                                                 out, max_ctas, &done);
+    if (st != HSA_OK)
+        return st;
+    if (n_groups < 0 || !(scale > 0.f) || !std::isfinite(scale))
+        return HSA_INVALID_ARG;
+    if (done)
+        return HSA_OK;
+    if (n_groups > 0 && (!cu_group || !shared_len))
+        return HSA_INVALID_ARG;
+    if (n_groups == 0 || !pools->layer_is_full[layer] || layer_fp8(pools, layer))
+        return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                             workspace, ws_bytes, max_ctas, dev_err, stream, options);
+    int ctas = device_sms();
+    if (ctas <= 0)
+        return HSA_CUDA_ERROR;
+    if (max_ctas > 0 && ctas > max_ctas)
+        ctas = max_ctas;
+    const int Hkv = pools->Hkv, G = pools->Hq / Hkv;
+    const SharedLayout lay = shared_layout(ctas, B, T, G, Hkv, n_groups);
+    if (!workspace || ws_bytes < lay.total || !aligned16(workspace))
+        return HSA_INVALID_ARG;
+    CUtensorMap tmK, tmV, tmQ;
+    const uint64_t rows = (uint64_t)pools->num_blocks * Hkv * pools->page_size;
+    if (!encode_2d(&tmK, pools->k[layer], 128, rows, 128, 64, 64) ||
+        !encode_2d(&tmV, pools->v[layer], 128, rows, 128, 64, 64) ||
+        !encode_3d(&tmQ, q, 128, pools->Hq, (uint64_t)B * T, 64, 128 / G, G))
+        return HSA_CUDA_ERROR;
+    hsa::SharedParams p{};
+    p.d.q = static_cast<const __nv_bfloat16 *>(q);
+    p.d.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    p.d.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    p.d.cached_len = cached_len;
+    p.d.block_tables = pools->block_tables;
+    p.d.out = static_cast<__nv_bfloat16 *>(out);
+    p.d.ws = static_cast<uint8_t *>(workspace);
+    p.d.dev_err = dev_err;
+    p.d.k_dst = static_cast<uint4 *>(pools->k[layer]);
+    p.d.v_dst = static_cast<uint4 *>(pools->v[layer]);
+    p.d.max_blocks = pools->max_blocks;
+    p.d.num_blocks = pools->num_blocks;
+    p.d.B = B;
+    p.d.Hkv = Hkv;
+    p.d.T = (int16_t)T;
+    p.d.G = (int16_t)G;
+    p.d.flags = (options & HSA_DECODE_APPEND) ? hsa::kDecodeAppend : 0;
+    p.d.scale_log2 = scale * 1.4426950408889634f;
+    p.cu_group = cu_group;
+    p.shared_len = shared_len;
+    p.plan_off = (int64_t)lay.plan;
+    p.slot_off = (int64_t)lay.slots;
+    p.n_groups = n_groups;
+    return hsa::launch_shared(tmK, tmV, tmQ, p, ctas, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
 }
 
 hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q,

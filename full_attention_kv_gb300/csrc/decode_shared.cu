@@ -1,0 +1,1222 @@
+// decode_shared.cu -- decode / MTP-verify attention for groups of sequences that share
+// their first pages (sm_103a).
+//
+// What it computes: what decode.cu computes on a full layer, o = softmax(scale q . K^T) V
+// over a sequence's cached keys and its T new ones.  The prefix tree lets sequences share
+// pages (a system prompt, a document, samples of one prompt); decode.cu reads those pages
+// once for every sequence.  Here a group's shared pages are read once for all of its rows:
+// softmax over a union of key sets splits into per-set states (m, l, o) that merge exactly,
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m) / l,
+// so the shared pages and each sequence's own pages are separate passes.
+//
+// Pass 1, shared_kernel (tcgen05): the query rows of a group for one KV head -- members x T
+// tokens x G heads -- are packed into 128-row tiles, a pair of tiles (256 rows) a unit, and
+// meet the shared keys in 128-key tiles as a dense product: K and V are read once a unit
+// instead of once a sequence.  The key tiles of all units are laid end to end and cut into
+// equal ranges, one per CTA; each (CTA, unit) segment leaves an unnormalised fp32 state.
+// Pass 2, own_kernel: decode.cu's stream-K walk over the pages past the shared ones, plus
+// the new tokens; three fold warps merge the segments' states of each finished unit while
+// the consumer warps run its pages, and join as one more key slice.
+//
+// The passes overlap by programmatic dependent launch: pass 2's CTAs start as pass 1's
+// leave their SMs, and only the fold warps wait for pass 1 to complete.
+#include "decode_tile.cuh"
+#include "hsa_device.cuh"
+#include "hsa_internal.h"
+
+namespace hsa {
+namespace {
+
+// ------------------------------------------------------------------ groups, both passes
+
+// A group's shared whole pages, or 0 (nothing is shared).
+__device__ __forceinline__ int group_pages(const SharedParams &p, int g)
+{
+    const int len = __ldg(p.shared_len + g);
+    return len > 0 ? min(len / kTileKeys, p.d.max_blocks) : 0;
+}
+
+// Whether cu_group is 0 = cu[0] <= cu[1] <= ... <= cu[n] = B.  Called by a whole warp.
+// Offsets out of order share nothing: every sequence then reads all of its pages itself.
+__device__ __forceinline__ bool groups_ok(const SharedParams &p, int lane)
+{
+    bool ok = true;
+    for (int g = lane; g < p.n_groups; g += 32) {
+        const int a = __ldg(p.cu_group + g), b = __ldg(p.cu_group + g + 1);
+        ok = ok && a <= b && (g > 0 || a == 0) && (g + 1 < p.n_groups || b == p.d.B);
+    }
+    return __all_sync(0xffffffffu, ok) && p.n_groups > 0;
+}
+
+// The group of sequence b (offsets in order).
+__device__ __forceinline__ int group_of(const SharedParams &p, int b)
+{
+    int lo = 0, hi = p.n_groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.cu_group + mid) <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
+
+// ------------------------------------------------------------------ pass 1: shared pages
+
+constexpr int kBM = 128;
+constexpr int kBN = 128;
+constexpr int kHalfBytes = 128 * 128;       // 128 rows x 64 bf16 (one swizzle column block)
+constexpr int kOpBytes = 2 * kHalfBytes;    // 32 KB
+constexpr int kSharedThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;             // S_A, S_B at 0 / 128; O_A, O_B at 256 / 384
+// A segment's state: m[256], l[256], then o as [tile][dim / 4][row][4] (a warp's 32 rows
+// store 512 contiguous bytes; a sequence's rows of one dim / 4 are contiguous)
+constexpr int kSlotFloats = 2 * 2 * kBM + 2 * kBM * kD;
+
+struct SharedSmem {
+    alignas(1024) uint8_t q[2][kOpBytes];
+    alignas(1024) uint8_t k[2][kOpBytes];
+    alignas(1024) uint8_t v[2][kOpBytes];
+    alignas(8) uint64_t q_full, q_empty;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint32_t tmem_base;
+    int32_t g0, unit0;
+    int64_t item0, N;
+};
+
+// A CTA's walk over the segments of its item range: every role runs its own copy.
+struct SegWalk {
+    int64_t it, i1, item0;  // next item, end, first item of group g
+    int g, unit0;           // group, units before it
+    int pairs, kt;          // the group's 256-row units a head, 128-key tiles a unit
+    int seq0, ntok, pages;
+    // the current segment
+    int h, pair, n0, n1, unit, rows;
+};
+
+__device__ __forceinline__ void load_group(const SharedParams &p, SegWalk &w)
+{
+    w.seq0 = __ldg(p.cu_group + w.g);
+    w.ntok = (__ldg(p.cu_group + w.g + 1) - w.seq0) * p.d.T;
+    w.pages = group_pages(p, w.g);
+    w.kt = (w.pages + 1) >> 1;
+    w.pairs = w.kt > 0 ? (w.ntok * p.d.G + 2 * kBM - 1) / (2 * kBM) : 0;
+}
+
+__device__ __forceinline__ bool next_seg(const SharedParams &p, SegWalk &w)
+{
+    if (w.it >= w.i1)
+        return false;
+    int64_t n = (int64_t)w.pairs * p.d.Hkv * w.kt;
+    while (w.it >= w.item0 + n) {
+        w.item0 += n;
+        w.unit0 += w.pairs * p.d.Hkv;
+        ++w.g;
+        load_group(p, w);
+        n = (int64_t)w.pairs * p.d.Hkv * w.kt;
+    }
+    const int64_t off = w.it - w.item0;
+    const int u = (int)(off / w.kt);
+    w.n0 = (int)(off % w.kt);
+    w.n1 = (int)min((int64_t)w.kt, w.n0 + (w.i1 - w.it));
+    w.h = u / w.pairs;
+    w.pair = u % w.pairs;
+    w.unit = w.unit0 + u;
+    w.rows = w.ntok * p.d.G - w.pair * 2 * kBM;
+    w.it += w.n1 - w.n0;
+    return true;
+}
+
+__device__ __forceinline__ bool page_ok(const SharedParams &p, int seq, int page, int *blk)
+{
+    const int b = __ldg(p.d.block_tables + (int64_t)seq * p.d.max_blocks + page);
+    if (b < 0 || b >= p.d.num_blocks)
+        return false;
+    *blk = b;
+    return true;
+}
+
+__global__ void __launch_bounds__(kSharedThreads, 1)
+    shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ SharedParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    SharedSmem &sh = *reinterpret_cast<SharedSmem *>(align_smem_1024(smem_raw));
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 32) {
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.k_full[s], 1);
+            mbar_init(&sh.k_empty[s], 1);
+            mbar_init(&sh.v_full[s], 1);
+            mbar_init(&sh.v_empty[s], 1);
+            mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.p_full[s], 4 * 32);
+            mbar_init(&sh.o_full[s], 1);
+            mbar_init(&sh.o_empty[s], 4 * 32);
+        }
+        fence_barrier_init();
+    }
+    if (tid == 64) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- the item space: warp 0 sums the groups and finds this CTA's first item ------
+    if (warp == 0) {
+        const bool ok = groups_ok(p, lane);
+        SharedPlan *const plan = reinterpret_cast<SharedPlan *>(p.d.ws + p.plan_off);
+        int64_t total = 0;
+        int units = 0;
+        for (int base = 0; ok && base < p.n_groups; base += 32) {
+            SegWalk w{};
+            w.g = base + lane;
+            if (w.g < p.n_groups)
+                load_group(p, w);
+            int64_t n = (int64_t)w.pairs * p.d.Hkv * w.kt, incl = n;
+            int un = w.pairs * p.d.Hkv, uincl = un;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+                const int b = __shfl_up_sync(0xffffffffu, uincl, o);
+                if (lane >= o) {
+                    incl += a;
+                    uincl += b;
+                }
+            }
+            if (blockIdx.x == 0 && w.g < p.n_groups) {
+                SharedGroup &gp = plan->group[w.g];
+                gp.item0 = total + incl - n;
+                gp.unit0 = units + uincl - un;
+                gp.pairs = w.pairs;
+                gp.kt = w.kt;
+                const int len = __ldg(p.shared_len + w.g);
+                if (len < 0)
+                    set_err(p.d.dev_err, HSA_DEVERR_BAD_LEN);
+                if (len / kTileKeys > p.d.max_blocks)
+                    set_err(p.d.dev_err, HSA_DEVERR_BAD_PAGE);
+            }
+            total += __shfl_sync(0xffffffffu, incl, 31);
+            units += __shfl_sync(0xffffffffu, uincl, 31);
+        }
+        if (lane == 0)
+            sh.N = total;
+        const int64_t C = min(total, (int64_t)gridDim.x);
+        if (blockIdx.x == 0 && lane == 0) {
+            plan->N = total;
+            plan->C = C;
+            if (!ok)
+                set_err(p.d.dev_err, HSA_DEVERR_BAD_LEN);
+        }
+        // second walk: the group that holds item i0
+        const int64_t i0 = blockIdx.x < C ? (int64_t)blockIdx.x * total / C : total;
+        total = 0;
+        units = 0;
+        for (int base = 0; ok && base < p.n_groups; base += 32) {
+            SegWalk w{};
+            w.g = base + lane;
+            if (w.g < p.n_groups)
+                load_group(p, w);
+            int64_t n = (int64_t)w.pairs * p.d.Hkv * w.kt, incl = n;
+            int un = w.pairs * p.d.Hkv, uincl = un;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+                const int b = __shfl_up_sync(0xffffffffu, uincl, o);
+                if (lane >= o) {
+                    incl += a;
+                    uincl += b;
+                }
+            }
+            if (total + incl - n <= i0 && i0 < total + incl) {
+                sh.g0 = w.g;
+                sh.unit0 = units + uincl - un;
+                sh.item0 = total + incl - n;
+            }
+            total += __shfl_sync(0xffffffffu, incl, 31);
+            units += __shfl_sync(0xffffffffu, uincl, 31);
+        }
+    }
+    __syncthreads();
+    const int64_t N = sh.N;
+    const int64_t C = min(N, (int64_t)gridDim.x);
+    if ((int64_t)blockIdx.x >= C)
+        return;
+    SegWalk w{};
+    w.it = (int64_t)blockIdx.x * N / C;
+    w.i1 = ((int64_t)blockIdx.x + 1) * N / C;
+    w.item0 = sh.item0;
+    w.g = sh.g0;
+    w.unit0 = sh.unit0;
+    load_group(p, w);
+
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+
+    if (warp == 0) {
+        // ================================================================ producer
+        if (lane == 0) {
+            const uint64_t pol_first = policy_evict_first(), pol_keep = policy_evict_last();
+            bool ok = true;
+            int kc = 0, sc = 0;
+            while (ok && next_seg(p, w)) {
+                const int nq = w.rows > kBM ? 2 : 1;
+                if (!mbar_wait_sleep(&sh.q_empty, (sc & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&sh.q_full, nq * kOpBytes);
+                const int tok0 = w.seq0 * p.d.T + w.pair * (2 * kBM / p.d.G);
+                for (int t = 0; t < nq; ++t)
+                    for (int hf = 0; hf < 2; ++hf)
+                        tma_load_3d(sh.q[t] + hf * kHalfBytes, &tmQ, &sh.q_full, hf * 64,
+                                    w.h * p.d.G, tok0 + t * (kBM / p.d.G), pol_keep);
+                ++sc;
+                // pages that more than one unit reads stay in L2
+                const uint64_t pol = w.pairs > 1 ? pol_keep : pol_first;
+                const int32_t *const table =
+                    p.d.block_tables + (int64_t)w.seq0 * p.d.max_blocks;
+                auto entry = [&](int page) { return page < w.pages ? __ldg(table + page) : 0; };
+                int b0 = entry(2 * w.n0), b1 = entry(2 * w.n0 + 1);
+                for (int n = w.n0; n < w.n1 && ok; ++n, ++kc) {
+                    const int s = kc & 1;
+                    const uint32_t ph = (kc >> 1) & 1;
+                    // the next tile's block-table reads, ahead of the waits
+                    int c0 = 0, c1 = 0;
+                    if (n + 1 < w.n1) {
+                        c0 = entry(2 * n + 2);
+                        c1 = entry(2 * n + 3);
+                    }
+                    // an entry out of range: page 0 as a stand-in, masked below
+                    if (b0 < 0 || b0 >= p.d.num_blocks || b1 < 0 || b1 >= p.d.num_blocks) {
+                        set_err(p.d.dev_err, HSA_DEVERR_BAD_BLOCK);
+                        b0 = b0 < 0 || b0 >= p.d.num_blocks ? 0 : b0;
+                        b1 = b1 < 0 || b1 >= p.d.num_blocks ? 0 : b1;
+                    }
+                    if (2 * n + 1 >= w.pages)
+                        b1 = b0;  // past the shared pages: loaded again, masked
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!mbar_wait_sleep(kv ? &sh.v_empty[s] : &sh.k_empty[s], ph ^ 1)) {
+                            ok = false;
+                            break;
+                        }
+                        uint64_t *full = kv ? &sh.v_full[s] : &sh.k_full[s];
+                        uint8_t *dst = kv ? sh.v[s] : sh.k[s];
+                        const CUtensorMap *map = kv ? &tmV : &tmK;
+                        mbar_arrive_expect_tx(full, kOpBytes);
+                        for (int pg = 0; pg < 2; ++pg) {
+                            const int32_t y = ((pg ? b1 : b0) * p.d.Hkv + w.h) * kTileKeys;
+                            tma_load_2d(dst + pg * 8192, map, full, 0, y, pol);
+                            tma_load_2d(dst + kHalfBytes + pg * 8192, map, full, 64, y, pol);
+                        }
+                    }
+                    b0 = c0;
+                    b1 = c1;
+                }
+            }
+            if (!ok)
+                set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+            // drain: no TMA write may still be in flight when the CTA exits
+            for (int s = 0; s < 2 && kc > s; ++s) {
+                const int last = s + ((kc - 1 - s) / 2) * 2;
+                mbar_wait_sleep(&sh.k_full[s], (last >> 1) & 1);
+                mbar_wait_sleep(&sh.v_full[s], (last >> 1) & 1);
+            }
+            if (sc > 0)
+                mbar_wait_sleep(&sh.q_full, (sc - 1) & 1);
+        }
+    } else if (warp == 1) {
+        // ================================================================ MMA issuer
+        if (lane == 0) {
+            const uint32_t id_s = idesc_bf16_f32(kBM, kBN, 0, 0);
+            const uint32_t id_pv = idesc_bf16_f32(kBM, kD, 0, 1);
+            const uint32_t dhi = smem_desc_sw128_hi(1024);
+            const uint32_t q_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.q[0]), 16),
+                                      smem_desc_sw128_lo(smem_u32(sh.q[1]), 16)};
+            const uint32_t k_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.k[0]), 16),
+                                      smem_desc_sw128_lo(smem_u32(sh.k[1]), 16)};
+            const uint32_t v_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.v[0]), kHalfBytes),
+                                      smem_desc_sw128_lo(smem_u32(sh.v[1]), kHalfBytes)};
+            // S_t = Q_t K^T of stage s; O_t (+)= P_t V of stage s, P_t in TMEM over S_t
+            auto issue_s = [&](int t, int s) {
+                const uint32_t qa = t ? q_lo[1] : q_lo[0], kb = s ? k_lo[1] : k_lo[0];
+                const uint32_t d = tmem + t * 128;
+                tc_mma_ss_k<0>(d, desc_join(qa, dhi), desc_join(kb, dhi), id_s);
+#pragma unroll
+                for (int ks = 1; ks < kD / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
+                    tc_mma_ss_k<1>(d, desc_join(qa + off, dhi), desc_join(kb + off, dhi), id_s);
+                }
+                tc_commit(&sh.s_full[t]);
+            };
+            auto issue_pv = [&](int t, int s, bool first) {
+                const uint32_t vb = s ? v_lo[1] : v_lo[0];
+                const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
+                if (first)
+                    tc_mma_ts_k<0>(d, a, desc_join(vb, dhi), id_pv);
+                else
+                    tc_mma_ts_k<1>(d, a, desc_join(vb, dhi), id_pv);
+#pragma unroll
+                for (int ks = 1; ks < kBN / 16; ++ks)
+                    tc_mma_ts_k<1>(d, a + ks * 8, desc_join(vb + ks * (2048 >> 4), dhi), id_pv);
+            };
+            bool ok = true;
+            int kc = 0, sc = 0;              // key tiles, segments so far
+            int np[2] = {0, 0}, ns[2] = {0, 0};  // the same, of each query tile
+            while (ok && next_seg(p, w)) {
+                const int nt = w.rows > kBM ? 2 : 1;
+                if (!mbar_wait_sleep(&sh.q_full, sc & 1) ||
+                    !mbar_wait_sleep(&sh.k_full[kc & 1], (kc >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                ++sc;
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (t < nt)
+                        issue_s(t, kc & 1);
+                tc_commit(&sh.k_empty[kc & 1]);
+                if (w.n1 - w.n0 == 1)
+                    tc_commit(&sh.q_empty);
+                for (int n = w.n0; n < w.n1 && ok; ++n, ++kc) {
+                    const int s = kc & 1;
+                    const bool more = n + 1 < w.n1;
+                    if (more && !mbar_wait_sleep(&sh.k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= nt || !ok)
+                            continue;
+                        if (!mbar_wait_sleep(&sh.p_full[t], np[t] & 1) ||
+                            (t == 0 && !mbar_wait_sleep(&sh.v_full[s], (kc >> 1) & 1)) ||
+                            (n == w.n0 && !mbar_wait_sleep(&sh.o_empty[t], (ns[t] & 1) ^ 1))) {
+                            ok = false;
+                            continue;
+                        }
+                        ++np[t];
+                        tc_fence_after();
+                        issue_pv(t, s, n == w.n0);
+                        if (more)
+                            issue_s(t, (kc + 1) & 1);
+                        else
+                            tc_commit(&sh.o_full[t]);
+                    }
+                    if (!ok)
+                        break;
+                    if (more)
+                        tc_commit(&sh.k_empty[(kc + 1) & 1]);
+                    if (n + 2 == w.n1)
+                        tc_commit(&sh.q_empty);  // the segment's last S products are issued
+                    tc_commit(&sh.v_empty[s]);
+                }
+                ++ns[0];
+                ns[1] += nt - 1;
+            }
+            if (ok) {
+                // every MMA done before TMEM is released
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (ok && ns[t] > 0)
+                        ok = mbar_wait_sleep(&sh.o_full[t], (ns[t] - 1) & 1);
+            }
+            if (!ok)
+                set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+        }
+    } else {
+        // ================================================================ softmax
+        const int t = (warp - 2) >> 2;  // query tile: 0 = A (warps 2-5), 1 = B (warps 6-9)
+        const int wq = warp & 3;
+        const int row = wq * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t col_s = t * 128, col_o = kColO + t * 128;
+        int np = 0, ns = 0;  // key tiles and segments of this query tile so far
+        bool ok = true;
+        while (ok && next_seg(p, w)) {
+            if (t == 1 && w.rows <= kBM)
+                continue;
+            const int r = w.pair * 2 * kBM + t * kBM + row;  // row of the group and head
+            const bool row_ok = r < w.ntok * p.d.G;
+            // a member may hold less than the shared pages
+            int hi_row = 0;
+            if (row_ok)
+                hi_row = min(w.pages * kTileKeys,
+                             clamp_len(__ldg(p.d.cached_len + w.seq0 + r / p.d.G / p.d.T)));
+            float m_used = -INFINITY, l = 0.f;
+            auto page_bits = [&](int n) -> int {
+                int blk, bits = 0;
+                if (2 * n < w.pages && page_ok(p, w.seq0, 2 * n, &blk))
+                    bits |= 1;
+                if (2 * n + 1 < w.pages && page_ok(p, w.seq0, 2 * n + 1, &blk))
+                    bits |= 2;
+                return bits;
+            };
+            int bits = page_bits(w.n0);
+            for (int n = w.n0; n < w.n1; ++n, ++np) {
+                const int next_bits = n + 1 < w.n1 ? page_bits(n + 1) : 0;
+                if (!mbar_wait_sleep(&sh.s_full[t], np & 1)) {
+                    set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int hi = min(kBN, hi_row - n * kBN);
+                const bool whole_tile = hi == kBN && bits == 3;
+                // ---- the row's 128 scores: one TMEM read, kept in registers --------
+                uint32_t r32[4][32];
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4)
+                    tmem_ld32(lane_addr + col_s + c4 * 32, r32[c4]);
+                tmem_wait_ld();
+                if (!whole_tile) {
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (c4 * 32 + c >= hi || !(bits & (c4 < 2 ? 1 : 2)))
+                                r32[c4][c] = __float_as_uint(-INFINITY);
+                }
+                // ---- row max (three-input max, four chains) -----------------------
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4)
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        m4[0] = fmax3(m4[0], __uint_as_float(r32[c4][c + 0]), __uint_as_float(r32[c4][c + 1]));
+                        m4[1] = fmax3(m4[1], __uint_as_float(r32[c4][c + 2]), __uint_as_float(r32[c4][c + 3]));
+                        m4[2] = fmax3(m4[2], __uint_as_float(r32[c4][c + 4]), __uint_as_float(r32[c4][c + 5]));
+                        m4[3] = fmax3(m4[3], __uint_as_float(r32[c4][c + 6]), __uint_as_float(r32[c4][c + 7]));
+                    }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.d.scale_log2;
+                // ---- running max, raised only when it grows by more than 2^8 -------
+                float m_new = m_used;
+                if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleSlack))
+                    m_new = mx;
+                const bool resc = m_used != -INFINITY && m_new != m_used;
+                const float alpha = resc ? fast_exp2(m_used - m_new) : 1.0f;
+                m_used = m_new;
+                const float base = m_used == -INFINITY ? 0.f : m_used;
+                // ---- P = 2^(s scale log2e - m) as bf16 pairs over S -----------------
+                // whole tiles: the row sum takes the unrounded P (128 keys: bf16's
+                // rounding averages out); partial ones the rounded P that PV multiplies
+                const uint64_t sc2 = f2_make(p.d.scale_log2, p.d.scale_log2);
+                const uint64_t nb2 = f2_make(-base, -base);
+                uint64_t acc2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+                float accr = 0.f;
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const uint64_t x2 = f2_fma(f2_make(__uint_as_float(r32[c4][2 * c]),
+                                                           __uint_as_float(r32[c4][2 * c + 1])),
+                                                   sc2, nb2);
+                        float x0, x1;
+                        f2_split(x2, x0, x1);
+                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                        pk[c] = pack_bf16(p0, p1);
+                        if (whole_tile)
+                            acc2[c & 1] = f2_add(acc2[c & 1], f2_make(p0, p1));
+                        else
+                            accr += bf16_lo(pk[c]) + bf16_hi(pk[c]);
+                    }
+                    tmem_st16(lane_addr + col_s + c4 * 16, pk);
+                }
+                // O (read by PV of this tile, which waits for this warp) is rescaled once
+                // the score registers are free; the segment's first PV overwrites it
+                if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        uint32_t o32[32];
+                        tmem_ld32(lane_addr + col_o + c4 * 32, o32);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o32[c] = __float_as_uint(__uint_as_float(o32[c]) * alpha);
+                        tmem_st32(lane_addr + col_o + c4 * 32, o32);
+                    }
+                }
+                {
+                    float a0, a1;
+                    f2_split(f2_add(acc2[0], acc2[1]), a0, a1);
+                    l = l * alpha + ((a0 + a1) + accr);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[t]);
+                bits = next_bits;
+            }
+            if (!ok)
+                break;
+            // ---- the segment's state -----------------------------------------------
+            if (!mbar_wait_sleep(&sh.o_full[t], ns & 1)) {
+                set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+                ok = false;
+                break;
+            }
+            ++ns;
+            tc_fence_after();
+            float *const slot = reinterpret_cast<float *>(p.d.ws + p.slot_off) +
+                                ((int64_t)blockIdx.x + w.unit) * kSlotFloats;
+            float4 *const dst = reinterpret_cast<float4 *>(slot + 4 * kBM) + t * (kD / 4) * kBM + row;
+            if (row_ok) {
+                slot[t * kBM + row] = m_used;
+                slot[2 * kBM + t * kBM + row] = l;
+            }
+#pragma unroll 1
+            for (int c4 = 0; c4 < 4; ++c4) {
+                uint32_t o32[32];
+                tmem_ld32(lane_addr + col_o + c4 * 32, o32);
+                tmem_wait_ld();
+                if (row_ok) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4)
+                        dst[(c4 * 8 + c / 4) * kBM] =
+                            make_float4(__uint_as_float(o32[c]), __uint_as_float(o32[c + 1]),
+                                        __uint_as_float(o32[c + 2]), __uint_as_float(o32[c + 3]));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&sh.o_empty[t]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------- pass 2: own pages, new tokens, merge
+
+constexpr int kStages = 4;
+constexpr int kTileBytes = kTileKeys * kD * 2;  // 16 KB: one K or V tile
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kConsumerWarps = 4;
+constexpr int kFoldWarps = 3;
+constexpr int kProducerWarp = kConsumerWarps + kFoldWarps;
+constexpr int kOwnThreads = (kProducerWarp + 1) * 32;      // 256: up to 255 registers a thread
+constexpr int kMergeThreads = kProducerWarp * 32;          // consumers and fold warps
+constexpr int kCombFloats = 16 + 16 + 16 * kD;             // per consumer warp: m, l, o[16][128]
+constexpr int kFoldFloats = 2 * kMaxRows + kMaxRows * kD;  // m[32], l[32], o[32][128]
+constexpr int kPartFloats = kMaxRows * (kD + 2);           // decode.cu's split-unit slot
+
+struct OwnSmem {
+    alignas(1024) uint8_t stage[kStages * kStageBytes];  // [K lo|K hi|V lo|V hi] per stage
+    alignas(16) uint8_t new_k[kNewRows * kD * 2];
+    alignas(16) uint8_t new_v[kNewRows * kD * 2];
+    alignas(16) float comb[kConsumerWarps][kCombFloats];
+    alignas(16) float fold[kFoldFloats];
+    float mscale[kMaxRows][kConsumerWarps + 1];
+    float mrow[kMaxRows][2];
+    alignas(8) uint64_t full[kStages];
+    alignas(8) uint64_t empty[kStages];
+    int32_t tile_ok[kStages];
+    int32_t scan[kOwnThreads];
+    int32_t first_b, first_items_before, total_items, is_last, share;
+};
+
+// Position in the item space: sequence b, head h, own tile j of n; c cached tokens past
+// the first page `fp` that is the sequence's own.
+struct OwnWalk {
+    int b, h, j, n, c, fp;
+};
+
+__device__ __forceinline__ void own_load(const SharedParams &p, bool share, OwnWalk &w)
+{
+    w.fp = share ? group_pages(p, group_of(p, w.b)) : 0;
+    w.c = max(0, clamp_len(__ldg(p.d.cached_len + w.b)) - w.fp * kTileKeys);
+    w.n = max(1, (w.c + kTileKeys - 1) / kTileKeys);
+}
+
+__device__ __forceinline__ void own_next(const SharedParams &p, bool share, OwnWalk &w)
+{
+    if (++w.j == w.n) {
+        w.j = 0;
+        if (++w.h == p.d.Hkv) {
+            w.h = 0;
+            ++w.b;
+            if (w.b < p.d.B)
+                own_load(p, share, w);
+        }
+    }
+}
+
+// TMA row of tile (b, h, j), or -1: no cached keys, or out of range (flagged).
+__device__ __forceinline__ int64_t own_row(const SharedParams &p, const OwnWalk &w)
+{
+    if (w.c == 0)
+        return -1;
+    const int page = w.fp + w.j;
+    if (page >= p.d.max_blocks) {
+        set_err(p.d.dev_err, HSA_DEVERR_BAD_PAGE);
+        return -1;
+    }
+    int blk = 0;
+    if (!page_ok(p, w.b, page, &blk)) {
+        set_err(p.d.dev_err, HSA_DEVERR_BAD_BLOCK);
+        return -1;
+    }
+    return ((int64_t)blk * p.d.Hkv + w.h) * kTileKeys;
+}
+
+// The shared segments' states of unit (b, h) merged into sh.fold.  Called by the fold
+// warps; ft = 0 .. kFoldWarps * 32 - 1.
+__device__ __forceinline__ void fold_unit(const SharedParams &p, OwnSmem &sh, const OwnWalk &u,
+                                          int64_t N, int64_t C, int ft)
+{
+    const int rows = p.d.G * p.d.T;
+    const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(p.d.ws + p.plan_off);
+    int kt = 0, pairs = 0, unit0 = 0, r0 = 0;
+    int64_t item0 = 0;
+    if (u.fp > 0 && N > 0) {
+        const int g = group_of(p, u.b);
+        const SharedGroup &gp = plan->group[g];
+        item0 = __ldcg(&gp.item0);
+        unit0 = __ldcg(&gp.unit0);
+        pairs = __ldcg(&gp.pairs);
+        kt = __ldcg(&gp.kt);
+        r0 = (u.b - __ldg(p.cu_group + g)) * rows;
+    }
+    const float *const slots = reinterpret_cast<const float *>(p.d.ws + p.slot_off);
+    for (int e = ft; e < rows * (kD / 4); e += kFoldWarps * 32) {
+        const int rr = e % rows, d4 = e / rows;
+        float M = -INFINITY, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kt > 0) {
+            const int r = r0 + rr;
+            const int un = u.h * pairs + r / (2 * kBM);
+            const int64_t s0 = item0 + (int64_t)un * kt;
+            const int64_t c_lo = ((s0 + 1) * C - 1) / N, c_hi = ((s0 + kt) * C - 1) / N;
+            const int t = (r / kBM) & 1, row = r % kBM;
+            const float *sl = slots + (c_lo + unit0 + un) * kSlotFloats;
+            const int n = (int)(c_hi - c_lo) + 1;
+            constexpr int U = 8;
+            for (int c0 = 0; c0 < n; c0 += U) {
+                float m[U], l[U];
+                float4 x[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    m[i] = -INFINITY;
+                    l[i] = 0.f;
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c0 + i < n) {
+                        const float *s = sl + (int64_t)(c0 + i) * kSlotFloats;
+                        m[i] = __ldcg(s + t * kBM + row);
+                        l[i] = __ldcg(s + 2 * kBM + t * kBM + row);
+                        x[i] = __ldcg(reinterpret_cast<const float4 *>(s + 4 * kBM) +
+                                      (t * (kD / 4) + d4) * kBM + row);
+                    }
+                }
+                float M1 = M;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    M1 = fmaxf(M1, m[i]);
+                const float base = M1 == -INFINITY ? 0.f : M1;
+                const float a = fast_exp2(M - base);
+                M = M1;
+                L *= a;
+                o.x *= a;
+                o.y *= a;
+                o.z *= a;
+                o.w *= a;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const float b = fast_exp2(m[i] - base);
+                    L += l[i] * b;
+                    o.x += x[i].x * b;
+                    o.y += x[i].y * b;
+                    o.z += x[i].z * b;
+                    o.w += x[i].w * b;
+                }
+            }
+        }
+        if (d4 == 0) {
+            sh.fold[rr] = M;
+            sh.fold[kMaxRows + rr] = L;
+        }
+        *reinterpret_cast<float4 *>(&sh.fold[2 * kMaxRows + rr * kD + 4 * d4]) = o;
+    }
+}
+
+// MT: 16-row m-tiles of a sequence's G T query rows (1 or 2).
+template <int MT>
+__global__ void __launch_bounds__(kOwnThreads, 1)
+    own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ SharedParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    OwnSmem &sh = *reinterpret_cast<OwnSmem *>(align_smem_1024(smem_raw));
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5, lane = tid & 31;
+    const DecodeParams &d = p.d;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], MT);  // the warps of the stage's group
+        }
+        fence_barrier_init();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    // Pass 1's CTAs signal only after their own wait, so everything queued before pass 1
+    // has completed here: q, the new rows, lengths, tables and pool are final.  Only the
+    // fold warps read what pass 1 writes, and wait for it.
+    grid_launch_dependents();
+    if (warp == 0) {
+        const bool ok = groups_ok(p, lane);
+        if (lane == 0)
+            sh.share = ok;
+    }
+    __syncthreads();
+    const bool share = sh.share != 0;
+
+    // ---- locate this CTA's contiguous range of items ------------------------
+    const int per = (d.B + kOwnThreads - 1) / kOwnThreads;
+    const int b_lo = min(d.B, tid * per), b_hi = min(d.B, b_lo + per);
+    {
+        int local = 0;
+        for (int b = b_lo; b < b_hi; ++b) {
+            OwnWalk w;
+            w.b = b;
+            own_load(p, share, w);
+            local += w.n;
+        }
+        sh.scan[tid] = local;
+        __syncthreads();
+        if (warp == 0) {
+            constexpr int kPer = kOwnThreads / 32;
+            int v[kPer];
+            int sum = 0;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                v[j] = sh.scan[lane * kPer + j];
+                sum += v[j];
+            }
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += u;
+            }
+            int acc = incl - sum;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                sh.scan[lane * kPer + j] = acc;
+                acc += v[j];
+            }
+            if (lane == 31)
+                sh.total_items = incl;
+        }
+        __syncthreads();
+    }
+    const int64_t N = (int64_t)sh.total_items * d.Hkv;
+    const int64_t C = min(N, (int64_t)gridDim.x);
+    if ((int64_t)blockIdx.x >= C) {
+        grid_dependency_wait();  // every CTA's exit stays ordered after pass 1
+        return;
+    }
+    const int64_t i0 = (int64_t)blockIdx.x * N / C;
+    const int64_t i1 = ((int64_t)blockIdx.x + 1) * N / C;
+    {
+        int before = sh.scan[tid];
+        for (int b = b_lo; b < b_hi; ++b) {
+            OwnWalk w;
+            w.b = b;
+            own_load(p, share, w);
+            if ((int64_t)(before + w.n) * d.Hkv > i0 && (int64_t)before * d.Hkv <= i0) {
+                sh.first_b = b;
+                sh.first_items_before = before;
+            }
+            before += w.n;
+        }
+        __syncthreads();
+    }
+    OwnWalk w;
+    w.b = sh.first_b;
+    own_load(p, share, w);
+    {
+        const int64_t off = i0 - (int64_t)sh.first_items_before * d.Hkv;
+        w.h = (int)(off / w.n);
+        w.j = (int)(off % w.n);
+    }
+
+    if (warp == kProducerWarp) {
+        // ---------------------------------------------------------------- producer
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_first();
+            int64_t k = 0;
+            int64_t row = own_row(p, w);
+            for (int64_t i = i0; i < i1; ++i, ++k) {
+                const int st = (int)(k % kStages);
+                const int64_t r = row;
+                own_next(p, share, w);
+                row = i + 1 < i1 ? own_row(p, w) : -1;  // read ahead of the wait
+                if (!mbar_wait(&sh.empty[st], (uint32_t)((k / kStages) & 1) ^ 1)) {
+                    set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+                    break;
+                }
+                sh.tile_ok[st] = r >= 0 ? 1 : 0;
+                if (r >= 0) {
+                    mbar_arrive_expect_tx(&sh.full[st], kStageBytes);
+                    uint8_t *dst = sh.stage + st * kStageBytes;
+                    tma_load_2d(dst, &tmK, &sh.full[st], 0, (int32_t)r, pol);
+                    tma_load_2d(dst + kTileBytes / 2, &tmK, &sh.full[st], 64, (int32_t)r, pol);
+                    tma_load_2d(dst + kTileBytes, &tmV, &sh.full[st], 0, (int32_t)r, pol);
+                    tma_load_2d(dst + kTileBytes + kTileBytes / 2, &tmV, &sh.full[st], 64,
+                                (int32_t)r, pol);
+                } else {
+                    mbar_arrive(&sh.full[st]);
+                }
+            }
+            // drain: no TMA write may still be in flight when the CTA exits
+            for (int64_t s = 0; s < kStages && s < k; ++s) {
+                const int64_t last = s + ((k - 1 - s) / kStages) * kStages;
+                mbar_wait(&sh.full[s], (uint32_t)((last / kStages) & 1));
+            }
+        }
+        return;
+    }
+
+    // ------------------------------------------------- consumers (0-3), fold warps (4-6)
+    // Tile-parallel groups as in decode.cu: the MT warps of group `slice` (one per 16-row
+    // m-tile) run every (4 / MT)-th tile of the CTA's range with all 64 keys.
+    constexpr int kSlices = kConsumerWarps / MT;
+    static_assert(kStages % kSlices == 0, "each stage belongs to one group");
+    const bool folder = warp >= kConsumerWarps;
+    const int mt = warp % MT, slice = warp / MT;
+    const int g = lane >> 2, tq = lane & 3;
+    const int q_r0 = mt * 16 + g, q_r1 = q_r0 + 8;
+    const int t0 = q_r0 / d.G, t1 = q_r1 / d.G;
+    const int rows_valid = d.G * d.T;
+    const int Hq = d.G * d.Hkv;
+    int32_t *const ws_cnt = reinterpret_cast<int32_t *>(d.ws);
+    float *const ws_part = reinterpret_cast<float *>(d.ws + decode_counter_bytes(d.B, d.Hkv));
+    int64_t sN = 0, sC = 0;
+    if (folder) {
+        grid_dependency_wait();
+        const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
+        sN = __ldcg(&plan->N);
+        sC = __ldcg(&plan->C);
+    }
+
+    RowState st;
+    uint32_t qa[kD / 16][4];
+    bool timed_out = false;
+    int64_t i = i0, k = 0, unit_start = i0 - w.j;
+    while (i < i1) {
+        // ---- this CTA's share of unit (w.b, w.h): items i .. i_end ----------------
+        const int64_t unit_end = unit_start + w.n;
+        const int64_t i_end = min(i1, unit_end);
+        const bool whole = unit_start >= i0 && unit_end <= i1;
+        const bool has_new = unit_end <= i1;  // owns the unit's last tile
+        const OwnWalk cur = w;
+        if (folder) {
+            // the owner of the unit's last tile takes the shared keys
+            if (has_new) {
+                fold_unit(p, sh, cur, sN, sC, tid - kConsumerWarps * 32);
+            } else if (tid - kConsumerWarps * 32 < kMaxRows) {
+                const int rr = tid - kConsumerWarps * 32;
+                sh.fold[rr] = -INFINITY;
+                sh.fold[kMaxRows + rr] = 0.f;
+            }
+        } else {
+            st.m[0] = st.m[1] = -INFINITY;
+            st.l[0] = st.l[1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < kD / 8; ++n)
+                st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
+            const bool v0 = t0 < d.T, v1 = t1 < d.T;
+            const __nv_bfloat16 *q0 =
+                d.q + ((int64_t)(cur.b * d.T + t0) * Hq + cur.h * d.G + q_r0 % d.G) * kD;
+            const __nv_bfloat16 *q1 =
+                d.q + ((int64_t)(cur.b * d.T + t1) * Hq + cur.h * d.G + q_r1 % d.G) * kD;
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                const int c0 = ks * 16 + 2 * tq;
+                qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
+                qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
+                qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
+                qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
+            }
+            if (has_new) {
+                for (int e = tid; e < kNewRows * kD / 8; e += kConsumerWarps * 32) {
+                    const int rr = e / (kD / 8), col = (e % (kD / 8)) * 8;
+                    uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
+                    if (rr < d.T) {
+                        const int64_t src = ((int64_t)(cur.b * d.T + rr) * d.Hkv + cur.h) * kD + col;
+                        kv = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
+                        vv = __ldg(reinterpret_cast<const uint4 *>(d.v_new + src));
+                    }
+                    *reinterpret_cast<uint4 *>(sh.new_k + swz128_offset(rr, col, kNewRows)) = kv;
+                    *reinterpret_cast<uint4 *>(sh.new_v + swz128_offset(rr, col, kNewRows)) = vv;
+                }
+            }
+            for (; i < i_end; ++i, ++k) {
+                const int j = (int)(i - unit_start);
+                if ((int)(k % kSlices) != slice)
+                    continue;
+                const int stg = (int)(k % kStages);
+                if (!timed_out && !mbar_wait(&sh.full[stg], (uint32_t)((k / kStages) & 1))) {
+                    set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+                    timed_out = true;
+                }
+                const int valid = cur.c - j * kTileKeys;
+                if (!timed_out && sh.tile_ok[stg] != 0 && valid > 0) {
+                    uint8_t *const base = sh.stage + stg * kStageBytes;
+                    const uint32_t sK = smem_u32(base), sV = sK + kTileBytes;
+                    const int T = d.T;
+                    if (valid < kTileKeys) {
+                        // rows past the sequence's end may hold anything, and 0 x NaN is NaN:
+                        // their values become 0 (their scores are masked)
+                        for (int e = lane; e < (kTileKeys - valid) * (kD / 8); e += 32)
+                            *reinterpret_cast<uint4 *>(
+                                base + kTileBytes +
+                                swz128_offset(valid + e / (kD / 8), (e % (kD / 8)) * 8, kTileKeys)) =
+                                make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();  // before the stage's next TMA write
+                        __syncwarp();
+                    }
+                    auto vis = [&](int rr, int key) -> bool {
+                        return (rr == g ? t0 : t1) < T && key < valid;
+                    };
+                    run_tile<kTileKeys / 8>(st, qa, sK, sV, kTileKeys, 0, d.scale_log2,
+                                            valid >= kTileKeys, t0 < T, t1 < T, vis);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.empty[stg]);
+            }
+            if (has_new) {
+                named_bar_sync(2, kConsumerWarps * 32);  // new rows staged by every warp
+                if (slice == 0) {
+                    const int T = d.T;
+                    auto vis_new = [&](int rr, int key) -> bool {
+                        const int t = rr == g ? t0 : t1;
+                        return t < T && key <= t;
+                    };
+                    run_tile<2>(st, qa, smem_u32(sh.new_k), smem_u32(sh.new_v), kNewRows, 0,
+                                d.scale_log2, false, t0 < T, t1 < T, vis_new);
+                }
+            }
+            float l0 = st.l[0], l1 = st.l[1];
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+            float *cb = sh.comb[warp];
+            if (tq == 0) {
+                cb[g] = st.m[0];
+                cb[g + 8] = st.m[1];
+                cb[16 + g] = l0;
+                cb[16 + g + 8] = l1;
+            }
+            float *co = cb + 32;
+#pragma unroll
+            for (int n = 0; n < kD / 8; ++n) {
+                *reinterpret_cast<float2 *>(co + g * kD + n * 8 + 2 * tq) =
+                    make_float2(st.o[n][0], st.o[n][1]);
+                *reinterpret_cast<float2 *>(co + (g + 8) * kD + n * 8 + 2 * tq) =
+                    make_float2(st.o[n][2], st.o[n][3]);
+            }
+        }
+        i = i_end;
+        named_bar_sync(1, kMergeThreads);
+
+        // ---- merge: the key slices and the shared keys' state -----------------------
+        const int slot = 2 * (int)blockIdx.x + (i0 < unit_start ? 1 : 0);
+        float *const part = ws_part + (int64_t)slot * kPartFloats;
+        for (int rr = tid; rr < rows_valid; rr += kMergeThreads) {
+            const int m_t = rr / 16, rl = rr % 16;
+            float M = sh.fold[rr];
+#pragma unroll
+            for (int s = 0; s < kSlices; ++s)
+                M = fmaxf(M, sh.comb[m_t + MT * s][rl]);
+            const float base = M == -INFINITY ? 0.f : M;
+            float a[kSlices + 1], L = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSlices; ++s) {
+                a[s] = fast_exp2(sh.comb[m_t + MT * s][rl] - base);
+                L += sh.comb[m_t + MT * s][16 + rl] * a[s];
+            }
+            a[kSlices] = fast_exp2(sh.fold[rr] - base);
+            L += sh.fold[kMaxRows + rr] * a[kSlices];
+            const float norm = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+#pragma unroll
+            for (int s = 0; s <= kSlices; ++s)
+                sh.mscale[rr][s] = a[s] * norm;
+            sh.mrow[rr][0] = M;
+            sh.mrow[rr][1] = L;
+        }
+        named_bar_sync(1, kMergeThreads);
+        for (int e = tid; e < rows_valid * (kD / 8); e += kMergeThreads) {
+            const int rr = e / (kD / 8), d0 = (e % (kD / 8)) * 8;
+            const int m_t = rr / 16, rl = rr % 16;
+            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s <= kSlices; ++s) {
+                if (s == kSlices && !has_new)
+                    break;  // no shared state: sh.fold's o is not this unit's
+                const float wgt = sh.mscale[rr][s];
+                const float4 *src = reinterpret_cast<const float4 *>(
+                    s < kSlices ? &sh.comb[m_t + MT * s][32 + rl * kD + d0]
+                                : &sh.fold[2 * kMaxRows + rr * kD + d0]);
+                const float4 x = src[0], y = src[1];
+                o[0] += x.x * wgt;
+                o[1] += x.y * wgt;
+                o[2] += x.z * wgt;
+                o[3] += x.w * wgt;
+                o[4] += y.x * wgt;
+                o[5] += y.y * wgt;
+                o[6] += y.z * wgt;
+                o[7] += y.w * wgt;
+            }
+            if (whole) {
+                const int t = rr / d.G, hh = rr % d.G;
+                *reinterpret_cast<uint4 *>(
+                    d.out + ((int64_t)(cur.b * d.T + t) * Hq + cur.h * d.G + hh) * kD + d0) =
+                    make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                               pack_bf16(o[6], o[7]));
+            } else {
+                if (d0 == 0) {
+                    __stcg(part + rr, sh.mrow[rr][0]);
+                    __stcg(part + kMaxRows + rr, sh.mrow[rr][1]);
+                }
+                float4 *dst = reinterpret_cast<float4 *>(part + 2 * kMaxRows + rr * kD + d0);
+                __stcg(dst, make_float4(o[0], o[1], o[2], o[3]));
+                __stcg(dst + 1, make_float4(o[4], o[5], o[6], o[7]));
+            }
+        }
+        bool append = whole;
+        if (!whole) {
+            // count this CTA's part in; the last to arrive (no waiting) merges them all
+            const int unit = cur.b * d.Hkv + cur.h;
+            const int64_t c_lo = ((unit_start + 1) * C - 1) / N;
+            const int64_t c_hi = (unit_end * C - 1) / N;
+            named_bar_sync(1, kMergeThreads);
+            if (tid == 0) {
+                __threadfence();
+                const int prev = atomicAdd(ws_cnt + unit, 1);
+                sh.is_last = (prev == (int)(c_hi - c_lo));
+            }
+            named_bar_sync(1, kMergeThreads);
+            append = sh.is_last != 0;
+            if (append) {
+                __threadfence();
+                for (int e = tid; e < rows_valid * kD; e += kMergeThreads) {
+                    const int rr = e / kD, dim = e % kD;
+                    float M = -INFINITY;
+                    for (int64_t cc = c_lo; cc <= c_hi; ++cc) {
+                        const int sl = 2 * (int)cc + (cc * N / C < unit_start ? 1 : 0);
+                        M = fmaxf(M, __ldcg(ws_part + (int64_t)sl * kPartFloats + rr));
+                    }
+                    const float base = M == -INFINITY ? 0.f : M;
+                    float L = 0.f, O = 0.f;
+                    for (int64_t cc = c_lo; cc <= c_hi; ++cc) {
+                        const int sl = 2 * (int)cc + (cc * N / C < unit_start ? 1 : 0);
+                        const float *pp = ws_part + (int64_t)sl * kPartFloats;
+                        const float a = fast_exp2(__ldcg(pp + rr) - base);
+                        L += __ldcg(pp + kMaxRows + rr) * a;
+                        O += __ldcg(pp + 2 * kMaxRows + rr * kD + dim) * a;
+                    }
+                    const int t = rr / d.G, hh = rr % d.G;
+                    d.out[((int64_t)(cur.b * d.T + t) * Hq + cur.h * d.G + hh) * kD + dim] =
+                        __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+                }
+                if (tid == 0)
+                    ws_cnt[unit] = 0;
+            }
+        }
+        if (append && (d.flags & kDecodeAppend))
+            // the unit's new rows, at their absolute positions (every read of it is done)
+            append_unit(d, cur.b, cur.h, clamp_len(__ldg(d.cached_len + cur.b)), tid,
+                        kMergeThreads);
+        named_bar_sync(1, kMergeThreads);  // merge buffers and new rows free again
+        unit_start = unit_end;
+        // the next unit
+        w.j = w.n - 1;
+        own_next(p, share, w);
+    }
+}
+
+}  // namespace
+
+size_t shared_plan_bytes(int n_groups)
+{
+    return (sizeof(SharedPlan) + (size_t)n_groups * sizeof(SharedGroup) + 255) & ~size_t(255);
+}
+
+// Slots: a CTA starts at most one segment that is not the first of its unit, so segment
+// (CTA, unit) has slot CTA + unit; units: 256 rows of a group and a KV head.
+size_t shared_slot_bytes(int ctas, int B, int T, int G, int Hkv, int n_groups)
+{
+    const size_t units = ((size_t)B * T * G / (2 * kBM) + (n_groups < B ? n_groups : B)) * Hkv;
+    return (ctas + units) * kSlotFloats * sizeof(float);
+}
+
+cudaError_t launch_shared(const CUtensorMap &tmK128, const CUtensorMap &tmV128,
+                          const CUtensorMap &tmQ, const SharedParams &p, int ctas,
+                          cudaStream_t stream)
+{
+    const size_t smem1 = sizeof(SharedSmem) + 1024, smem2 = sizeof(OwnSmem) + 1024;
+    const int MT = (p.d.G * p.d.T + 15) / 16;
+    auto own = MT == 1 ? own_kernel<1> : own_kernel<2>;
+    static bool attr_set[3] = {false, false, false};
+    if (!attr_set[0]) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
+        if (e != cudaSuccess)
+            return e;
+        attr_set[0] = true;
+    }
+    if (!attr_set[MT]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem2);
+        if (e != cudaSuccess)
+            return e;
+        attr_set[MT] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kSharedThreads);
+    cfg.dynamicSmemBytes = smem1;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_kernel, tmK128, tmV128, tmQ, p);
+    if (e != cudaSuccess)
+        return e;
+    cfg.blockDim = dim3(kOwnThreads);
+    cfg.dynamicSmemBytes = smem2;
+    return cudaLaunchKernelEx(&cfg, own, tmK128, tmV128, p);
+}
+
+}  // namespace hsa

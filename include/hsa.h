@@ -284,6 +284,38 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
                               int32_t *dev_err, void *stream);
 
 /*
+ * Decode / MTP-verify attention of a batch whose groups of sequences share their first
+ * pages (a system prompt, a document, several samples of one prompt: what the prefix tree
+ * hands out).  Same results as hsa_decode_attn_ex, beyond rounding; on a bf16 full layer
+ * the shared pages are read once for a group instead of once for each sequence.
+ *  cu_group    device int32 [n_groups + 1], 0 = cu_group[0] <= ... <= cu_group[n_groups]
+ *              = B: group g is sequences cu_group[g] .. cu_group[g + 1] - 1
+ *  shared_len  device int32 [n_groups]: tokens whose pages the group shares (>= 0).  Their
+ *              whole pages, shared_len[g] / 64, have to be the same block-table entries in
+ *              every row of the group (they are read through its first row) as far as a
+ *              member's cached tokens go; a part of a page is each sequence's own.
+ *  n_groups    0 is hsa_decode_attn_ex.  Groups may be empty or of one sequence.
+ *  options     as in hsa_decode_attn_ex.  The appended rows go to each sequence's own pages.
+ *  workspace   at least hsa_decode_shared_workspace_bytes() bytes, with the rules of
+ *              hsa_decode_attn's; a workspace of one serves hsa_decode_attn_ex too.
+ *  scale       > 0
+ * Offsets out of order are flagged (HSA_DEVERR_BAD_LEN) and nothing is shared then: every
+ * sequence reads its own pages, with the same results.  A negative shared_len is flagged and
+ * taken as 0, one past the block table (HSA_DEVERR_BAD_PAGE) as its width.  Sliding layers
+ * (a ring is its sequence's own) and FP8 layers run hsa_decode_attn_ex.
+ */
+size_t hsa_decode_shared_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
+                                         int32_t n_groups);
+
+hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const void *q,
+                                  const void *k_new, const void *v_new,
+                                  const int32_t *cached_len, const int32_t *cu_group,
+                                  const int32_t *shared_len, int32_t n_groups, int32_t B,
+                                  int32_t T, float scale, void *out, void *workspace,
+                                  size_t ws_bytes, int32_t max_ctas, int32_t options,
+                                  int32_t *dev_err, void *stream);
+
+/*
  * hsa_decode_attn without a caller workspace.  The pages have no counterpart: this
  * is a convenience of this library for callers that cannot allocate device memory
  * where they run decode (while a stream is being captured, inside a host runtime
