@@ -426,20 +426,6 @@ hsa_status decode_host_check(const hsa_pools *pools, int32_t layer, const void *
 
 namespace {
 
-// The workspace of a shared-prefix decode: the decode workspace, the plan, the states.
-struct SharedLayout {
-    size_t plan, slots, total;
-};
-
-SharedLayout shared_layout(int ctas, int B, int T, int G, int Hkv, int n_groups)
-{
-    SharedLayout l;
-    l.plan = (hsa::decode_workspace_bytes(ctas, B, Hkv) + 255) & ~size_t(255);
-    l.slots = l.plan + hsa::shared_plan_bytes(n_groups);
-    l.total = l.slots + hsa::shared_slot_bytes(ctas, B, T, G, Hkv, n_groups);
-    return l;
-}
-
 hsa_status decode_common(const hsa_pools *pools, int32_t layer, const void *q, const void *k_new,
                          const void *v_new, const int32_t *cached_len, int32_t B, int32_t T,
                          float scale, void *out, void *workspace, size_t ws_bytes,
@@ -557,7 +543,10 @@ size_t hsa_decode_shared_workspace_bytes(const hsa_pools *pools, int32_t B, int3
     if (plain == 0 || T < 1 || n_groups < 0 || pools->Hq <= 0)
         return 0;
     const int sms = std::max(device_sms(), 1);
-    return std::max(plain, shared_layout(sms, B, T, pools->Hq / pools->Hkv, pools->Hkv, n_groups).total);
+    // behind the plain call's counters, which have to stay zero
+    return std::max(plain, hsa::shared_layout(hsa::decode_counter_bytes(B, pools->Hkv), sms, B, T,
+                                              pools->Hq / pools->Hkv, pools->Hkv, n_groups)
+                               .total);
 }
 
 hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const void *q,
@@ -590,7 +579,8 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     if (max_ctas > 0 && ctas > max_ctas)
         ctas = max_ctas;
     const int Hkv = pools->Hkv, G = pools->Hq / Hkv;
-    const SharedLayout lay = shared_layout(ctas, B, T, G, Hkv, n_groups);
+    const hsa::SharedLayout lay = hsa::shared_layout(hsa::decode_counter_bytes(B, Hkv), ctas, B, T,
+                                                     G, Hkv, n_groups);
     if (!workspace || ws_bytes < lay.total || !aligned16(workspace))
         return HSA_INVALID_ARG;
     CUtensorMap tmK, tmV, tmQ;
@@ -621,7 +611,9 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     p.cu_group = cu_group;
     p.shared_len = shared_len;
     p.plan_off = (int64_t)lay.plan;
+    p.own_plan_off = (int64_t)lay.own_plan;
     p.slot_off = (int64_t)lay.slots;
+    p.own_off = (int64_t)lay.own;
     p.n_groups = n_groups;
     return hsa::launch_shared(tmK, tmV, tmQ, p, ctas, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

@@ -13,13 +13,14 @@
 // tokens x G heads -- are packed into 128-row tiles, a pair of tiles (256 rows) a unit, and
 // meet the shared keys in 128-key tiles as a dense product: K and V are read once a unit
 // instead of once a sequence.  The key tiles of all units are laid end to end and cut into
-// equal ranges, one per CTA; each (CTA, unit) segment leaves an unnormalised fp32 state.
+// equal ranges, one per CTA; each (CTA, unit) segment leaves unnormalised fp32 states.
 // Pass 2, own_kernel: decode.cu's stream-K walk over the pages past the shared ones, plus
-// the new tokens; three fold warps merge the segments' states of each finished unit while
-// the consumer warps run its pages, and join as one more key slice.
+// the new tokens; each (CTA, sequence, head) segment leaves its state.
+// Pass 3, merge_kernel: a thread for four output dimensions of a row merges the row's
+// states and writes bf16; it also appends the new rows.
 //
-// The passes overlap by programmatic dependent launch: pass 2's CTAs start as pass 1's
-// leave their SMs, and only the fold warps wait for pass 1 to complete.
+// The passes overlap by programmatic dependent launch: pass 2 reads nothing of pass 1, and
+// its CTAs start as pass 1's leave their SMs; pass 3 is resident before pass 2 ends.
 #include "decode_tile.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
@@ -43,6 +44,7 @@ __device__ __forceinline__ bool groups_ok(const SharedParams &p, int lane)
     bool ok = true;
     for (int g = lane; g < p.n_groups; g += 32) {
         const int a = __ldg(p.cu_group + g), b = __ldg(p.cu_group + g + 1);
+        __ldg(p.shared_len + g);  // wanted next: one latency for all three
         ok = ok && a <= b && (g > 0 || a == 0) && (g + 1 < p.n_groups || b == p.d.B);
     }
     return __all_sync(0xffffffffu, ok) && p.n_groups > 0;
@@ -73,9 +75,11 @@ constexpr int kOpBytes = 2 * kHalfBytes;    // 32 KB
 constexpr int kSharedThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;             // S_A, S_B at 0 / 128; O_A, O_B at 256 / 384
-// A segment's state: m[256], l[256], then o as [tile][dim / 4][row][4] (a warp's 32 rows
-// store 512 contiguous bytes; a sequence's rows of one dim / 4 are contiguous)
-constexpr int kSlotFloats = 2 * 2 * kBM + 2 * kBM * kD;
+// A segment's states, by octets of rows: m[8], l[8], then o as [dim / 4][8 rows][4], so
+// that the warps that write (a row a lane) and those that merge (eight rows x four
+// 16-byte pieces) both move whole 128-byte lines.
+constexpr int kOctFloats = 16 + 8 * kD;
+constexpr int kSlotFloats = 2 * kBM / 8 * kOctFloats;
 
 struct SharedSmem {
     alignas(1024) uint8_t q[2][kOpBytes];
@@ -90,6 +94,9 @@ struct SharedSmem {
 };
 
 // A CTA's walk over the segments of its item range: every role runs its own copy.
+// A unit of at most 128 rows has one query tile; the two softmax warpgroups, S and O
+// regions then take its key tiles in turn (split()), so that one tile's products still
+// run under the other's softmax, and the segment leaves two states a row.
 struct SegWalk {
     int64_t it, i1, item0;  // next item, end, first item of group g
     int g, unit0;           // group, units before it
@@ -97,6 +104,7 @@ struct SegWalk {
     int seq0, ntok, pages;
     // the current segment
     int h, pair, n0, n1, unit, rows;
+    __device__ __forceinline__ bool split() const { return rows <= kBM; }
 };
 
 __device__ __forceinline__ void load_group(const SharedParams &p, SegWalk &w)
@@ -169,6 +177,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem_base, kTmemCols);
+        tmem_relinquish();
     }
     grid_dependency_wait();
     grid_launch_dependents();
@@ -248,11 +260,16 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             units += __shfl_sync(0xffffffffu, uincl, 31);
         }
     }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     const int64_t N = sh.N;
     const int64_t C = min(N, (int64_t)gridDim.x);
-    if ((int64_t)blockIdx.x >= C)
+    if ((int64_t)blockIdx.x >= C) {
+        if (warp == 1)
+            tmem_dealloc(sh.tmem_base, kTmemCols);
         return;
+    }
     SegWalk w{};
     w.it = (int64_t)blockIdx.x * N / C;
     w.i1 = ((int64_t)blockIdx.x + 1) * N / C;
@@ -260,14 +277,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     w.g = sh.g0;
     w.unit0 = sh.unit0;
     load_group(p, w);
-
-    if (warp == 1) {
-        tmem_alloc(&sh.tmem_base, kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
 
     if (warp == 0) {
@@ -277,7 +286,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             bool ok = true;
             int kc = 0, sc = 0;
             while (ok && next_seg(p, w)) {
-                const int nq = w.rows > kBM ? 2 : 1;
+                const int nq = w.split() ? 1 : 2;
                 if (!mbar_wait_sleep(&sh.q_empty, (sc & 1) ^ 1)) {
                     ok = false;
                     break;
@@ -354,9 +363,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                                       smem_desc_sw128_lo(smem_u32(sh.k[1]), 16)};
             const uint32_t v_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.v[0]), kHalfBytes),
                                       smem_desc_sw128_lo(smem_u32(sh.v[1]), kHalfBytes)};
-            // S_t = Q_t K^T of stage s; O_t (+)= P_t V of stage s, P_t in TMEM over S_t
-            auto issue_s = [&](int t, int s) {
-                const uint32_t qa = t ? q_lo[1] : q_lo[0], kb = s ? k_lo[1] : k_lo[0];
+            // S_t = Q_q K^T of stage s; O_t (+)= P_t V of stage s, P_t in TMEM over S_t
+            auto issue_s = [&](int t, int q, int s) {
+                const uint32_t qa = q ? q_lo[1] : q_lo[0], kb = s ? k_lo[1] : k_lo[0];
                 const uint32_t d = tmem + t * 128;
                 tc_mma_ss_k<0>(d, desc_join(qa, dhi), desc_join(kb, dhi), id_s);
 #pragma unroll
@@ -381,7 +390,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             int kc = 0, sc = 0;              // key tiles, segments so far
             int np[2] = {0, 0}, ns[2] = {0, 0};  // the same, of each query tile
             while (ok && next_seg(p, w)) {
-                const int nt = w.rows > kBM ? 2 : 1;
                 if (!mbar_wait_sleep(&sh.q_full, sc & 1) ||
                     !mbar_wait_sleep(&sh.k_full[kc & 1], (kc >> 1) & 1)) {
                     ok = false;
@@ -389,10 +397,60 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 }
                 ++sc;
                 tc_fence_after();
+                if (w.split()) {
+                    // key tile j of the segment in region j % 2: S(j + 2) behind PV(j)
+                    const int nn = w.n1 - w.n0;
+                    issue_s(0, 0, kc & 1);
+                    tc_commit(&sh.k_empty[kc & 1]);
+                    if (nn > 1) {
+                        if (!mbar_wait_sleep(&sh.k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        issue_s(1, 0, (kc + 1) & 1);
+                        tc_commit(&sh.k_empty[(kc + 1) & 1]);
+                    }
+                    if (nn <= 2)
+                        tc_commit(&sh.q_empty);
+                    for (int j = 0; j < nn && ok; j += 2) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (t < nt)
-                        issue_s(t, kc & 1);
+                        for (int t = 0; t < 2; ++t) {
+                            if (j + t >= nn || !ok)
+                                continue;
+                            const int s = kc & 1;
+                            if (!mbar_wait_sleep(&sh.p_full[t], np[t] & 1) ||
+                                !mbar_wait_sleep(&sh.v_full[s], (kc >> 1) & 1) ||
+                                (j == 0 && !mbar_wait_sleep(&sh.o_empty[t], (ns[t] & 1) ^ 1))) {
+                                ok = false;
+                                continue;
+                            }
+                            ++np[t];
+                            tc_fence_after();
+                            issue_pv(t, s, j == 0);
+                            tc_commit(&sh.v_empty[s]);
+                            if (j + t + 2 < nn) {
+                                if (!mbar_wait_sleep(&sh.k_full[s], ((kc + 2) >> 1) & 1)) {
+                                    ok = false;
+                                    continue;
+                                }
+                                tc_fence_after();
+                                issue_s(t, 0, s);
+                                tc_commit(&sh.k_empty[s]);
+                                if (j + t + 3 == nn)
+                                    tc_commit(&sh.q_empty);  // the segment's last S product
+                            } else {
+                                tc_commit(&sh.o_full[t]);
+                            }
+                            ++kc;
+                        }
+                    }
+                    ++ns[0];
+                    ns[1] += nn > 1;
+                    continue;
+                }
+                issue_s(0, 0, kc & 1);
+                issue_s(1, 1, kc & 1);
                 tc_commit(&sh.k_empty[kc & 1]);
                 if (w.n1 - w.n0 == 1)
                     tc_commit(&sh.q_empty);
@@ -405,7 +463,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                     }
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        if (t >= nt || !ok)
+                        if (!ok)
                             continue;
                         if (!mbar_wait_sleep(&sh.p_full[t], np[t] & 1) ||
                             (t == 0 && !mbar_wait_sleep(&sh.v_full[s], (kc >> 1) & 1)) ||
@@ -417,7 +475,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                         tc_fence_after();
                         issue_pv(t, s, n == w.n0);
                         if (more)
-                            issue_s(t, (kc + 1) & 1);
+                            issue_s(t, t, (kc + 1) & 1);
                         else
                             tc_commit(&sh.o_full[t]);
                     }
@@ -430,7 +488,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                     tc_commit(&sh.v_empty[s]);
                 }
                 ++ns[0];
-                ns[1] += nt - 1;
+                ++ns[1];
             }
             if (ok) {
                 // every MMA done before TMEM is released
@@ -452,10 +510,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         int np = 0, ns = 0;  // key tiles and segments of this query tile so far
         bool ok = true;
         while (ok && next_seg(p, w)) {
-            if (t == 1 && w.rows <= kBM)
-                continue;
-            const int r = w.pair * 2 * kBM + t * kBM + row;  // row of the group and head
+            const int step = w.split() ? 2 : 1;       // key tiles n0 + first, + step, ...
+            const int first = w.split() ? t : 0;
+            const int r = w.pair * 2 * kBM + (w.split() ? 0 : t * kBM) + row;  // of the group and head
             const bool row_ok = r < w.ntok * p.d.G;
+            float *const oct = reinterpret_cast<float *>(p.d.ws + p.slot_off) +
+                               ((int64_t)blockIdx.x + w.unit) * kSlotFloats +
+                               (t * kBM + row) / 8 * kOctFloats;
+            if (w.n0 + first >= w.n1) {  // one key tile, not this warpgroup's
+                if (row_ok) {
+                    oct[row & 7] = -INFINITY;
+                    oct[8 + (row & 7)] = 0.f;
+                }
+                continue;
+            }
             // a member may hold less than the shared pages
             int hi_row = 0;
             if (row_ok)
@@ -470,9 +538,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                     bits |= 2;
                 return bits;
             };
-            int bits = page_bits(w.n0);
-            for (int n = w.n0; n < w.n1; ++n, ++np) {
-                const int next_bits = n + 1 < w.n1 ? page_bits(n + 1) : 0;
+            int bits = page_bits(w.n0 + first);
+            for (int n = w.n0 + first; n < w.n1; n += step, ++np) {
+                const int next_bits = n + step < w.n1 ? page_bits(n + step) : 0;
                 if (!mbar_wait_sleep(&sh.s_full[t], np & 1)) {
                     set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
                     ok = false;
@@ -575,12 +643,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             }
             ++ns;
             tc_fence_after();
-            float *const slot = reinterpret_cast<float *>(p.d.ws + p.slot_off) +
-                                ((int64_t)blockIdx.x + w.unit) * kSlotFloats;
-            float4 *const dst = reinterpret_cast<float4 *>(slot + 4 * kBM) + t * (kD / 4) * kBM + row;
+            float4 *const dst = reinterpret_cast<float4 *>(oct + 16) + (row & 7);
             if (row_ok) {
-                slot[t * kBM + row] = m_used;
-                slot[2 * kBM + t * kBM + row] = l;
+                oct[row & 7] = m_used;
+                oct[8 + (row & 7)] = l;
             }
 #pragma unroll 1
             for (int c4 = 0; c4 < 4; ++c4) {
@@ -590,7 +656,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 4)
-                        dst[(c4 * 8 + c / 4) * kBM] =
+                        dst[(c4 * 8 + c / 4) * 8] =
                             make_float4(__uint_as_float(o32[c]), __uint_as_float(o32[c + 1]),
                                         __uint_as_float(o32[c + 2]), __uint_as_float(o32[c + 3]));
                 }
@@ -608,33 +674,26 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     }
 }
 
-// ------------------------------------------------- pass 2: own pages, new tokens, merge
+// ------------------------------------------------------ pass 2: own pages and new tokens
 
 constexpr int kStages = 4;
 constexpr int kTileBytes = kTileKeys * kD * 2;  // 16 KB: one K or V tile
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kConsumerWarps = 4;
-constexpr int kFoldWarps = 3;
-constexpr int kProducerWarp = kConsumerWarps + kFoldWarps;
-constexpr int kOwnThreads = (kProducerWarp + 1) * 32;      // 256: up to 255 registers a thread
-constexpr int kMergeThreads = kProducerWarp * 32;          // consumers and fold warps
-constexpr int kCombFloats = 16 + 16 + 16 * kD;             // per consumer warp: m, l, o[16][128]
-constexpr int kFoldFloats = 2 * kMaxRows + kMaxRows * kD;  // m[32], l[32], o[32][128]
-constexpr int kPartFloats = kMaxRows * (kD + 2);           // decode.cu's split-unit slot
+constexpr int kOwnThreads = (kConsumerWarps + 1) * 32;
+constexpr int kCombFloats = 16 + 16 + 16 * kD;  // per consumer warp: m, l, o[16][128]
 
 struct OwnSmem {
     alignas(1024) uint8_t stage[kStages * kStageBytes];  // [K lo|K hi|V lo|V hi] per stage
     alignas(16) uint8_t new_k[kNewRows * kD * 2];
     alignas(16) uint8_t new_v[kNewRows * kD * 2];
     alignas(16) float comb[kConsumerWarps][kCombFloats];
-    alignas(16) float fold[kFoldFloats];
-    float mscale[kMaxRows][kConsumerWarps + 1];
-    float mrow[kMaxRows][2];
+    float mscale[kMaxRows][kConsumerWarps];
     alignas(8) uint64_t full[kStages];
     alignas(8) uint64_t empty[kStages];
     int32_t tile_ok[kStages];
     int32_t scan[kOwnThreads];
-    int32_t first_b, first_items_before, total_items, is_last, share;
+    int32_t first_b, first_items_before, total_items, share;
 };
 
 // Position in the item space: sequence b, head h, own tile j of n; c cached tokens past
@@ -681,84 +740,10 @@ __device__ __forceinline__ int64_t own_row(const SharedParams &p, const OwnWalk 
     return ((int64_t)blk * p.d.Hkv + w.h) * kTileKeys;
 }
 
-// The shared segments' states of unit (b, h) merged into sh.fold.  Called by the fold
-// warps; ft = 0 .. kFoldWarps * 32 - 1.
-__device__ __forceinline__ void fold_unit(const SharedParams &p, OwnSmem &sh, const OwnWalk &u,
-                                          int64_t N, int64_t C, int ft)
-{
-    const int rows = p.d.G * p.d.T;
-    const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(p.d.ws + p.plan_off);
-    int kt = 0, pairs = 0, unit0 = 0, r0 = 0;
-    int64_t item0 = 0;
-    if (u.fp > 0 && N > 0) {
-        const int g = group_of(p, u.b);
-        const SharedGroup &gp = plan->group[g];
-        item0 = __ldcg(&gp.item0);
-        unit0 = __ldcg(&gp.unit0);
-        pairs = __ldcg(&gp.pairs);
-        kt = __ldcg(&gp.kt);
-        r0 = (u.b - __ldg(p.cu_group + g)) * rows;
-    }
-    const float *const slots = reinterpret_cast<const float *>(p.d.ws + p.slot_off);
-    for (int e = ft; e < rows * (kD / 4); e += kFoldWarps * 32) {
-        const int rr = e % rows, d4 = e / rows;
-        float M = -INFINITY, L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (kt > 0) {
-            const int r = r0 + rr;
-            const int un = u.h * pairs + r / (2 * kBM);
-            const int64_t s0 = item0 + (int64_t)un * kt;
-            const int64_t c_lo = ((s0 + 1) * C - 1) / N, c_hi = ((s0 + kt) * C - 1) / N;
-            const int t = (r / kBM) & 1, row = r % kBM;
-            const float *sl = slots + (c_lo + unit0 + un) * kSlotFloats;
-            const int n = (int)(c_hi - c_lo) + 1;
-            constexpr int U = 8;
-            for (int c0 = 0; c0 < n; c0 += U) {
-                float m[U], l[U];
-                float4 x[U];
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    m[i] = -INFINITY;
-                    l[i] = 0.f;
-                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c0 + i < n) {
-                        const float *s = sl + (int64_t)(c0 + i) * kSlotFloats;
-                        m[i] = __ldcg(s + t * kBM + row);
-                        l[i] = __ldcg(s + 2 * kBM + t * kBM + row);
-                        x[i] = __ldcg(reinterpret_cast<const float4 *>(s + 4 * kBM) +
-                                      (t * (kD / 4) + d4) * kBM + row);
-                    }
-                }
-                float M1 = M;
-#pragma unroll
-                for (int i = 0; i < U; ++i)
-                    M1 = fmaxf(M1, m[i]);
-                const float base = M1 == -INFINITY ? 0.f : M1;
-                const float a = fast_exp2(M - base);
-                M = M1;
-                L *= a;
-                o.x *= a;
-                o.y *= a;
-                o.z *= a;
-                o.w *= a;
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const float b = fast_exp2(m[i] - base);
-                    L += l[i] * b;
-                    o.x += x[i].x * b;
-                    o.y += x[i].y * b;
-                    o.z += x[i].z * b;
-                    o.w += x[i].w * b;
-                }
-            }
-        }
-        if (d4 == 0) {
-            sh.fold[rr] = M;
-            sh.fold[kMaxRows + rr] = L;
-        }
-        *reinterpret_cast<float4 *>(&sh.fold[2 * kMaxRows + rr * kD + 4 * d4]) = o;
-    }
-}
+// Floats of an own segment's state: m[R], l[R], o[R][128] for R = G T rows, m and l padded
+// to 16 bytes.
+__host__ __device__ inline int own_pad(int rows) { return (rows + 3) & ~3; }
+__host__ __device__ inline int own_slot_floats(int rows) { return 2 * own_pad(rows) + rows * kD; }
 
 // MT: 16-row m-tiles of a sequence's G T query rows (1 or 2).
 template <int MT>
@@ -779,13 +764,13 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         }
         fence_barrier_init();
     }
-    if (warp == kProducerWarp && lane == 0) {
+    if (warp == kConsumerWarps && lane == 0) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
     // Pass 1's CTAs signal only after their own wait, so everything queued before pass 1
-    // has completed here: q, the new rows, lengths, tables and pool are final.  Only the
-    // fold warps read what pass 1 writes, and wait for it.
+    // has completed here: q, the new rows, lengths, tables and pool are final.  Nothing
+    // here reads what pass 1 writes; the wait before the exit keeps pass 3 behind it.
     grid_launch_dependents();
     if (warp == 0) {
         const bool ok = groups_ok(p, lane);
@@ -837,13 +822,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
     }
     const int64_t N = (int64_t)sh.total_items * d.Hkv;
     const int64_t C = min(N, (int64_t)gridDim.x);
-    if ((int64_t)blockIdx.x >= C) {
-        grid_dependency_wait();  // every CTA's exit stays ordered after pass 1
-        return;
-    }
-    const int64_t i0 = (int64_t)blockIdx.x * N / C;
-    const int64_t i1 = ((int64_t)blockIdx.x + 1) * N / C;
+    const int64_t i0 = min(N, (int64_t)blockIdx.x * N / C);
+    const int64_t i1 = min(N, ((int64_t)blockIdx.x + 1) * N / C);
     {
+        OwnPlan *const plan = reinterpret_cast<OwnPlan *>(d.ws + p.own_plan_off);
         int before = sh.scan[tid];
         for (int b = b_lo; b < b_hi; ++b) {
             OwnWalk w;
@@ -853,9 +835,19 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
                 sh.first_b = b;
                 sh.first_items_before = before;
             }
+            if (blockIdx.x == 0)  // for pass 3
+                plan->before[b] = before;
             before += w.n;
         }
+        if (blockIdx.x == 0 && tid == 0) {
+            plan->N = N;
+            plan->C = C;
+        }
         __syncthreads();
+    }
+    if ((int64_t)blockIdx.x >= C) {
+        grid_dependency_wait();  // every CTA's exit stays ordered after pass 1
+        return;
     }
     OwnWalk w;
     w.b = sh.first_b;
@@ -866,7 +858,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         w.j = (int)(off % w.n);
     }
 
-    if (warp == kProducerWarp) {
+    if (warp == kConsumerWarps) {
         // ---------------------------------------------------------------- producer
         if (lane == 0) {
             const uint64_t pol = policy_evict_first();
@@ -899,31 +891,23 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
                 const int64_t last = s + ((k - 1 - s) / kStages) * kStages;
                 mbar_wait(&sh.full[s], (uint32_t)((last / kStages) & 1));
             }
+            grid_dependency_wait();
         }
         return;
     }
 
-    // ------------------------------------------------- consumers (0-3), fold warps (4-6)
+    // ------------------------------------------------------------------ consumers
     // Tile-parallel groups as in decode.cu: the MT warps of group `slice` (one per 16-row
     // m-tile) run every (4 / MT)-th tile of the CTA's range with all 64 keys.
     constexpr int kSlices = kConsumerWarps / MT;
+    constexpr int kThr = kConsumerWarps * 32;
     static_assert(kStages % kSlices == 0, "each stage belongs to one group");
-    const bool folder = warp >= kConsumerWarps;
     const int mt = warp % MT, slice = warp / MT;
     const int g = lane >> 2, tq = lane & 3;
     const int q_r0 = mt * 16 + g, q_r1 = q_r0 + 8;
     const int t0 = q_r0 / d.G, t1 = q_r1 / d.G;
     const int rows_valid = d.G * d.T;
     const int Hq = d.G * d.Hkv;
-    int32_t *const ws_cnt = reinterpret_cast<int32_t *>(d.ws);
-    float *const ws_part = reinterpret_cast<float *>(d.ws + decode_counter_bytes(d.B, d.Hkv));
-    int64_t sN = 0, sC = 0;
-    if (folder) {
-        grid_dependency_wait();
-        const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
-        sN = __ldcg(&plan->N);
-        sC = __ldcg(&plan->C);
-    }
 
     RowState st;
     uint32_t qa[kD / 16][4];
@@ -933,259 +917,334 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         // ---- this CTA's share of unit (w.b, w.h): items i .. i_end ----------------
         const int64_t unit_end = unit_start + w.n;
         const int64_t i_end = min(i1, unit_end);
-        const bool whole = unit_start >= i0 && unit_end <= i1;
         const bool has_new = unit_end <= i1;  // owns the unit's last tile
         const OwnWalk cur = w;
-        if (folder) {
-            // the owner of the unit's last tile takes the shared keys
-            if (has_new) {
-                fold_unit(p, sh, cur, sN, sC, tid - kConsumerWarps * 32);
-            } else if (tid - kConsumerWarps * 32 < kMaxRows) {
-                const int rr = tid - kConsumerWarps * 32;
-                sh.fold[rr] = -INFINITY;
-                sh.fold[kMaxRows + rr] = 0.f;
-            }
-        } else {
-            st.m[0] = st.m[1] = -INFINITY;
-            st.l[0] = st.l[1] = 0.f;
+        st.m[0] = st.m[1] = -INFINITY;
+        st.l[0] = st.l[1] = 0.f;
 #pragma unroll
-            for (int n = 0; n < kD / 8; ++n)
-                st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
-            const bool v0 = t0 < d.T, v1 = t1 < d.T;
-            const __nv_bfloat16 *q0 =
-                d.q + ((int64_t)(cur.b * d.T + t0) * Hq + cur.h * d.G + q_r0 % d.G) * kD;
-            const __nv_bfloat16 *q1 =
-                d.q + ((int64_t)(cur.b * d.T + t1) * Hq + cur.h * d.G + q_r1 % d.G) * kD;
+        for (int n = 0; n < kD / 8; ++n)
+            st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
+        const bool v0 = t0 < d.T, v1 = t1 < d.T;
+        const __nv_bfloat16 *q0 =
+            d.q + ((int64_t)(cur.b * d.T + t0) * Hq + cur.h * d.G + q_r0 % d.G) * kD;
+        const __nv_bfloat16 *q1 =
+            d.q + ((int64_t)(cur.b * d.T + t1) * Hq + cur.h * d.G + q_r1 % d.G) * kD;
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-                const int c0 = ks * 16 + 2 * tq;
-                qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
-                qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
-                qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
-                qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
-            }
-            if (has_new) {
-                for (int e = tid; e < kNewRows * kD / 8; e += kConsumerWarps * 32) {
-                    const int rr = e / (kD / 8), col = (e % (kD / 8)) * 8;
-                    uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
-                    if (rr < d.T) {
-                        const int64_t src = ((int64_t)(cur.b * d.T + rr) * d.Hkv + cur.h) * kD + col;
-                        kv = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
-                        vv = __ldg(reinterpret_cast<const uint4 *>(d.v_new + src));
-                    }
-                    *reinterpret_cast<uint4 *>(sh.new_k + swz128_offset(rr, col, kNewRows)) = kv;
-                    *reinterpret_cast<uint4 *>(sh.new_v + swz128_offset(rr, col, kNewRows)) = vv;
+        for (int ks = 0; ks < kD / 16; ++ks) {
+            const int c0 = ks * 16 + 2 * tq;
+            qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
+            qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
+            qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
+            qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
+        }
+        if (has_new) {
+            for (int e = tid; e < kNewRows * kD / 8; e += kThr) {
+                const int rr = e / (kD / 8), col = (e % (kD / 8)) * 8;
+                uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
+                if (rr < d.T) {
+                    const int64_t src = ((int64_t)(cur.b * d.T + rr) * d.Hkv + cur.h) * kD + col;
+                    kv = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
+                    vv = __ldg(reinterpret_cast<const uint4 *>(d.v_new + src));
                 }
-            }
-            for (; i < i_end; ++i, ++k) {
-                const int j = (int)(i - unit_start);
-                if ((int)(k % kSlices) != slice)
-                    continue;
-                const int stg = (int)(k % kStages);
-                if (!timed_out && !mbar_wait(&sh.full[stg], (uint32_t)((k / kStages) & 1))) {
-                    set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
-                    timed_out = true;
-                }
-                const int valid = cur.c - j * kTileKeys;
-                if (!timed_out && sh.tile_ok[stg] != 0 && valid > 0) {
-                    uint8_t *const base = sh.stage + stg * kStageBytes;
-                    const uint32_t sK = smem_u32(base), sV = sK + kTileBytes;
-                    const int T = d.T;
-                    if (valid < kTileKeys) {
-                        // rows past the sequence's end may hold anything, and 0 x NaN is NaN:
-                        // their values become 0 (their scores are masked)
-                        for (int e = lane; e < (kTileKeys - valid) * (kD / 8); e += 32)
-                            *reinterpret_cast<uint4 *>(
-                                base + kTileBytes +
-                                swz128_offset(valid + e / (kD / 8), (e % (kD / 8)) * 8, kTileKeys)) =
-                                make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();  // before the stage's next TMA write
-                        __syncwarp();
-                    }
-                    auto vis = [&](int rr, int key) -> bool {
-                        return (rr == g ? t0 : t1) < T && key < valid;
-                    };
-                    run_tile<kTileKeys / 8>(st, qa, sK, sV, kTileKeys, 0, d.scale_log2,
-                                            valid >= kTileKeys, t0 < T, t1 < T, vis);
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.empty[stg]);
-            }
-            if (has_new) {
-                named_bar_sync(2, kConsumerWarps * 32);  // new rows staged by every warp
-                if (slice == 0) {
-                    const int T = d.T;
-                    auto vis_new = [&](int rr, int key) -> bool {
-                        const int t = rr == g ? t0 : t1;
-                        return t < T && key <= t;
-                    };
-                    run_tile<2>(st, qa, smem_u32(sh.new_k), smem_u32(sh.new_v), kNewRows, 0,
-                                d.scale_log2, false, t0 < T, t1 < T, vis_new);
-                }
-            }
-            float l0 = st.l[0], l1 = st.l[1];
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            float *cb = sh.comb[warp];
-            if (tq == 0) {
-                cb[g] = st.m[0];
-                cb[g + 8] = st.m[1];
-                cb[16 + g] = l0;
-                cb[16 + g + 8] = l1;
-            }
-            float *co = cb + 32;
-#pragma unroll
-            for (int n = 0; n < kD / 8; ++n) {
-                *reinterpret_cast<float2 *>(co + g * kD + n * 8 + 2 * tq) =
-                    make_float2(st.o[n][0], st.o[n][1]);
-                *reinterpret_cast<float2 *>(co + (g + 8) * kD + n * 8 + 2 * tq) =
-                    make_float2(st.o[n][2], st.o[n][3]);
+                *reinterpret_cast<uint4 *>(sh.new_k + swz128_offset(rr, col, kNewRows)) = kv;
+                *reinterpret_cast<uint4 *>(sh.new_v + swz128_offset(rr, col, kNewRows)) = vv;
             }
         }
-        i = i_end;
-        named_bar_sync(1, kMergeThreads);
+        for (; i < i_end; ++i, ++k) {
+            const int j = (int)(i - unit_start);
+            if ((int)(k % kSlices) != slice)
+                continue;
+            const int stg = (int)(k % kStages);
+            if (!timed_out && !mbar_wait(&sh.full[stg], (uint32_t)((k / kStages) & 1))) {
+                set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+                timed_out = true;
+            }
+            const int valid = cur.c - j * kTileKeys;
+            if (!timed_out && sh.tile_ok[stg] != 0 && valid > 0) {
+                uint8_t *const base = sh.stage + stg * kStageBytes;
+                const uint32_t sK = smem_u32(base), sV = sK + kTileBytes;
+                const int T = d.T;
+                if (valid < kTileKeys) {
+                    // rows past the sequence's end may hold anything, and 0 x NaN is NaN:
+                    // their values become 0 (their scores are masked)
+                    for (int e = lane; e < (kTileKeys - valid) * (kD / 8); e += 32)
+                        *reinterpret_cast<uint4 *>(
+                            base + kTileBytes +
+                            swz128_offset(valid + e / (kD / 8), (e % (kD / 8)) * 8, kTileKeys)) =
+                            make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();  // before the stage's next TMA write
+                    __syncwarp();
+                }
+                auto vis = [&](int rr, int key) -> bool {
+                    return (rr == g ? t0 : t1) < T && key < valid;
+                };
+                run_tile<kTileKeys / 8>(st, qa, sK, sV, kTileKeys, 0, d.scale_log2,
+                                        valid >= kTileKeys, t0 < T, t1 < T, vis);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[stg]);
+        }
+        if (has_new) {
+            named_bar_sync(1, kThr);  // new rows staged by every warp
+            if (slice == 0) {
+                const int T = d.T;
+                auto vis_new = [&](int rr, int key) -> bool {
+                    const int t = rr == g ? t0 : t1;
+                    return t < T && key <= t;
+                };
+                run_tile<2>(st, qa, smem_u32(sh.new_k), smem_u32(sh.new_v), kNewRows, 0,
+                            d.scale_log2, false, t0 < T, t1 < T, vis_new);
+            }
+        }
+        float l0 = st.l[0], l1 = st.l[1];
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        float *cb = sh.comb[warp];
+        if (tq == 0) {
+            cb[g] = st.m[0];
+            cb[g + 8] = st.m[1];
+            cb[16 + g] = l0;
+            cb[16 + g + 8] = l1;
+        }
+        float *co = cb + 32;
+#pragma unroll
+        for (int n = 0; n < kD / 8; ++n) {
+            *reinterpret_cast<float2 *>(co + g * kD + n * 8 + 2 * tq) =
+                make_float2(st.o[n][0], st.o[n][1]);
+            *reinterpret_cast<float2 *>(co + (g + 8) * kD + n * 8 + 2 * tq) =
+                make_float2(st.o[n][2], st.o[n][3]);
+        }
+        named_bar_sync(1, kThr);
 
-        // ---- merge: the key slices and the shared keys' state -----------------------
-        const int slot = 2 * (int)blockIdx.x + (i0 < unit_start ? 1 : 0);
-        float *const part = ws_part + (int64_t)slot * kPartFloats;
-        for (int rr = tid; rr < rows_valid; rr += kMergeThreads) {
+        // ---- the warps' states merged into the segment's -----------------------------
+        const int unit = cur.b * d.Hkv + cur.h;
+        float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
+                            ((int64_t)blockIdx.x + unit) * own_slot_floats(rows_valid);
+        const int pad = own_pad(rows_valid);
+        for (int rr = tid; rr < rows_valid; rr += kThr) {
             const int m_t = rr / 16, rl = rr % 16;
-            float M = sh.fold[rr];
+            float M = -INFINITY;
 #pragma unroll
             for (int s = 0; s < kSlices; ++s)
                 M = fmaxf(M, sh.comb[m_t + MT * s][rl]);
             const float base = M == -INFINITY ? 0.f : M;
-            float a[kSlices + 1], L = 0.f;
+            float L = 0.f;
 #pragma unroll
             for (int s = 0; s < kSlices; ++s) {
-                a[s] = fast_exp2(sh.comb[m_t + MT * s][rl] - base);
-                L += sh.comb[m_t + MT * s][16 + rl] * a[s];
+                const float a = fast_exp2(sh.comb[m_t + MT * s][rl] - base);
+                sh.mscale[rr][s] = a;
+                L += sh.comb[m_t + MT * s][16 + rl] * a;
             }
-            a[kSlices] = fast_exp2(sh.fold[rr] - base);
-            L += sh.fold[kMaxRows + rr] * a[kSlices];
-            const float norm = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-#pragma unroll
-            for (int s = 0; s <= kSlices; ++s)
-                sh.mscale[rr][s] = a[s] * norm;
-            sh.mrow[rr][0] = M;
-            sh.mrow[rr][1] = L;
+            part[rr] = M;
+            part[pad + rr] = L;
         }
-        named_bar_sync(1, kMergeThreads);
-        for (int e = tid; e < rows_valid * (kD / 8); e += kMergeThreads) {
-            const int rr = e / (kD / 8), d0 = (e % (kD / 8)) * 8;
+        named_bar_sync(1, kThr);
+        for (int e = tid; e < rows_valid * (kD / 4); e += kThr) {
+            const int rr = e / (kD / 4), d0 = (e % (kD / 4)) * 4;
             const int m_t = rr / 16, rl = rr % 16;
-            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int s = 0; s <= kSlices; ++s) {
-                if (s == kSlices && !has_new)
-                    break;  // no shared state: sh.fold's o is not this unit's
+            for (int s = 0; s < kSlices; ++s) {
                 const float wgt = sh.mscale[rr][s];
-                const float4 *src = reinterpret_cast<const float4 *>(
-                    s < kSlices ? &sh.comb[m_t + MT * s][32 + rl * kD + d0]
-                                : &sh.fold[2 * kMaxRows + rr * kD + d0]);
-                const float4 x = src[0], y = src[1];
-                o[0] += x.x * wgt;
-                o[1] += x.y * wgt;
-                o[2] += x.z * wgt;
-                o[3] += x.w * wgt;
-                o[4] += y.x * wgt;
-                o[5] += y.y * wgt;
-                o[6] += y.z * wgt;
-                o[7] += y.w * wgt;
+                const float4 x =
+                    *reinterpret_cast<const float4 *>(&sh.comb[m_t + MT * s][32 + rl * kD + d0]);
+                o.x += x.x * wgt;
+                o.y += x.y * wgt;
+                o.z += x.z * wgt;
+                o.w += x.w * wgt;
             }
-            if (whole) {
-                const int t = rr / d.G, hh = rr % d.G;
-                *reinterpret_cast<uint4 *>(
-                    d.out + ((int64_t)(cur.b * d.T + t) * Hq + cur.h * d.G + hh) * kD + d0) =
-                    make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                               pack_bf16(o[6], o[7]));
-            } else {
-                if (d0 == 0) {
-                    __stcg(part + rr, sh.mrow[rr][0]);
-                    __stcg(part + kMaxRows + rr, sh.mrow[rr][1]);
-                }
-                float4 *dst = reinterpret_cast<float4 *>(part + 2 * kMaxRows + rr * kD + d0);
-                __stcg(dst, make_float4(o[0], o[1], o[2], o[3]));
-                __stcg(dst + 1, make_float4(o[4], o[5], o[6], o[7]));
-            }
+            *reinterpret_cast<float4 *>(part + 2 * pad + rr * kD + d0) = o;
         }
-        bool append = whole;
-        if (!whole) {
-            // count this CTA's part in; the last to arrive (no waiting) merges them all
-            const int unit = cur.b * d.Hkv + cur.h;
-            const int64_t c_lo = ((unit_start + 1) * C - 1) / N;
-            const int64_t c_hi = (unit_end * C - 1) / N;
-            named_bar_sync(1, kMergeThreads);
-            if (tid == 0) {
-                __threadfence();
-                const int prev = atomicAdd(ws_cnt + unit, 1);
-                sh.is_last = (prev == (int)(c_hi - c_lo));
-            }
-            named_bar_sync(1, kMergeThreads);
-            append = sh.is_last != 0;
-            if (append) {
-                __threadfence();
-                for (int e = tid; e < rows_valid * kD; e += kMergeThreads) {
-                    const int rr = e / kD, dim = e % kD;
-                    float M = -INFINITY;
-                    for (int64_t cc = c_lo; cc <= c_hi; ++cc) {
-                        const int sl = 2 * (int)cc + (cc * N / C < unit_start ? 1 : 0);
-                        M = fmaxf(M, __ldcg(ws_part + (int64_t)sl * kPartFloats + rr));
-                    }
-                    const float base = M == -INFINITY ? 0.f : M;
-                    float L = 0.f, O = 0.f;
-                    for (int64_t cc = c_lo; cc <= c_hi; ++cc) {
-                        const int sl = 2 * (int)cc + (cc * N / C < unit_start ? 1 : 0);
-                        const float *pp = ws_part + (int64_t)sl * kPartFloats;
-                        const float a = fast_exp2(__ldcg(pp + rr) - base);
-                        L += __ldcg(pp + kMaxRows + rr) * a;
-                        O += __ldcg(pp + 2 * kMaxRows + rr * kD + dim) * a;
-                    }
-                    const int t = rr / d.G, hh = rr % d.G;
-                    d.out[((int64_t)(cur.b * d.T + t) * Hq + cur.h * d.G + hh) * kD + dim] =
-                        __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
-                }
-                if (tid == 0)
-                    ws_cnt[unit] = 0;
-            }
-        }
-        if (append && (d.flags & kDecodeAppend))
-            // the unit's new rows, at their absolute positions (every read of it is done)
-            append_unit(d, cur.b, cur.h, clamp_len(__ldg(d.cached_len + cur.b)), tid,
-                        kMergeThreads);
-        named_bar_sync(1, kMergeThreads);  // merge buffers and new rows free again
+        named_bar_sync(1, kThr);  // merge buffers and new rows free again
         unit_start = unit_end;
-        // the next unit
-        w.j = w.n - 1;
+        w.j = w.n - 1;  // the next unit
         own_next(p, share, w);
+    }
+    grid_dependency_wait();
+}
+
+// ---------------------------------------------------------------- pass 3: merge, append
+
+constexpr int kMergeThreads = 256;  // eight rows x 32 pieces of four dimensions
+constexpr int kMergeBatch = 8;      // states whose loads are in flight together
+
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ SharedParams p)
+{
+    const DecodeParams &d = p.d;
+    const int tid = threadIdx.x;
+    const int RT = d.G * d.T, Hq = d.G * d.Hkv;
+    const int64_t rows = (int64_t)d.B * RT;
+    const int h = blockIdx.x % d.Hkv;
+    const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + (tid & 7);
+    const int d4 = tid >> 3;
+    const bool on = r < rows;
+    grid_launch_dependents();
+    // inputs, final since before pass 1
+    const int b = on ? (int)(r / RT) : 0, rr = (int)(r % RT);
+    const int g = group_of(p, b);
+    const int seq0 = __ldg(p.cu_group + g), seq1 = __ldg(p.cu_group + g + 1);
+    grid_dependency_wait();
+
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // n states at m (l at m + l_at, o at m + o_at), `step` floats apart
+    auto take = [&](const float *m0, int l_at, int o_at, int64_t step, int n) {
+        for (int c0 = 0; c0 < n; c0 += kMergeBatch) {
+            float m[kMergeBatch], l[kMergeBatch];
+            float4 x[kMergeBatch];
+#pragma unroll
+            for (int i = 0; i < kMergeBatch; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + i < n) {
+                    const float *s = m0 + (c0 + i) * step;
+                    m[i] = __ldcg(s);
+                    l[i] = __ldcg(s + l_at);
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(s + o_at));
+                }
+            }
+            float M1 = M;
+#pragma unroll
+            for (int i = 0; i < kMergeBatch; ++i)
+                M1 = fmaxf(M1, m[i]);
+            if (M1 == -INFINITY)
+                continue;
+            const float a = fast_exp2(M - M1);
+            M = M1;
+            L *= a;
+            o.x *= a;
+            o.y *= a;
+            o.z *= a;
+            o.w *= a;
+#pragma unroll
+            for (int i = 0; i < kMergeBatch; ++i) {
+                if (m[i] == -INFINITY)
+                    continue;  // a state of no keys: its o was not written
+                const float f = fast_exp2(m[i] - M1);
+                L += l[i] * f;
+                o.x += x[i].x * f;
+                o.y += x[i].y * f;
+                o.z += x[i].z * f;
+                o.w += x[i].w * f;
+            }
+        }
+    };
+    if (on) {
+        const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
+        const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
+        const SharedGroup *const gp = &plan->group[g];
+        const int64_t oN = __ldcg(&own->N), oC = __ldcg(&own->C);
+        const int before = __ldcg(&own->before[b]);
+        const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : (int)(oN / d.Hkv);
+        const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
+        const int64_t item0 = __ldcg(&gp->item0);
+        const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), kt = __ldcg(&gp->kt);
+        // the sequence's own states: CTAs c_lo .. c_hi of pass 2
+        {
+            const int n = next - before;
+            const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
+            const int64_t c_lo = ((s0 + 1) * oC - 1) / oN, c_hi = ((s0 + n) * oC - 1) / oN;
+            const int step = own_slot_floats(RT), pad = own_pad(RT);
+            const float *s = reinterpret_cast<const float *>(d.ws + p.own_off) +
+                             (c_lo + b * d.Hkv + h) * step;
+            take(s + rr, pad, 2 * pad - rr + rr * kD + 4 * d4, step, (int)(c_hi - c_lo) + 1);
+        }
+        // the shared segments' states
+        if (N > 0 && kt > 0) {
+            const int64_t rg = r - (int64_t)seq0 * RT;  // row of the group
+            const int pair = (int)(rg / (2 * kBM)), row = (int)(rg % (2 * kBM));
+            const int un = h * pairs + pair;
+            const int64_t s0 = item0 + (int64_t)un * kt;
+            const int64_t c_lo = ((s0 + 1) * C - 1) / N, c_hi = ((s0 + kt) * C - 1) / N;
+            const float *s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
+                             (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + (row & 7);
+            const int n = (int)(c_hi - c_lo) + 1;
+            const int o_at = 16 - (row & 7) + (d4 * 8 + (row & 7)) * 4;
+            // a unit of one query tile left two states a row, 128 rows apart
+            const bool split = (int64_t)(seq1 - seq0) * RT - (int64_t)pair * 2 * kBM <= kBM;
+            if (split)
+                take(s, 8, o_at, kSlotFloats / 2, 2 * n);
+            else
+                take(s, 8, o_at, kSlotFloats, n);
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int t = rr / d.G, hh = rr % d.G;
+        *reinterpret_cast<uint2 *>(d.out + ((int64_t)(b * d.T + t) * Hq + h * d.G + hh) * kD + 4 * d4) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    }
+    if (d.flags & kDecodeAppend) {
+        // every read of the pool is done: the new rows, one 16-byte chunk of K and V a thread
+        const int64_t chunks = (int64_t)d.B * d.T * d.Hkv * (kD / 8);
+        for (int64_t e = (int64_t)blockIdx.x * kMergeThreads + tid; e < chunks;
+             e += (int64_t)gridDim.x * kMergeThreads) {
+            const int ch = (int)(e % (kD / 8));
+            const int64_t th = e / (kD / 8);
+            const int hk = (int)(th % d.Hkv);
+            const int64_t bt = th / d.Hkv;
+            const int sb = (int)(bt / d.T);
+            const int64_t pos = (int64_t)clamp_len(__ldg(d.cached_len + sb)) + bt % d.T;
+            if (pos / kTileKeys >= d.max_blocks) {
+                set_err(d.dev_err, HSA_DEVERR_BAD_PAGE);
+                continue;
+            }
+            int blk = 0;
+            if (!page_ok(p, sb, (int)(pos / kTileKeys), &blk)) {
+                set_err(d.dev_err, HSA_DEVERR_BAD_BLOCK);
+                continue;
+            }
+            const int64_t to = (((int64_t)blk * d.Hkv + hk) * kTileKeys + pos % kTileKeys) * (kD / 8) + ch;
+            d.k_dst[to] = __ldg(reinterpret_cast<const uint4 *>(d.k_new) + e);
+            d.v_dst[to] = __ldg(reinterpret_cast<const uint4 *>(d.v_new) + e);
+        }
     }
 }
 
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), unsigned grid, unsigned threads, size_t smem,
+                             cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
+
 }  // namespace
 
-size_t shared_plan_bytes(int n_groups)
+SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv, int n_groups)
 {
-    return (sizeof(SharedPlan) + (size_t)n_groups * sizeof(SharedGroup) + 255) & ~size_t(255);
-}
-
-// Slots: a CTA starts at most one segment that is not the first of its unit, so segment
-// (CTA, unit) has slot CTA + unit; units: 256 rows of a group and a KV head.
-size_t shared_slot_bytes(int ctas, int B, int T, int G, int Hkv, int n_groups)
-{
+    SharedLayout l;
+    l.plan = pad256(start);
+    l.own_plan = l.plan + pad256(sizeof(SharedPlan) + (size_t)n_groups * sizeof(SharedGroup));
+    l.slots = l.own_plan + pad256(sizeof(OwnPlan) + (size_t)B * sizeof(int32_t));
+    // segments in order move on by a CTA, a unit or both, so (CTA, unit)'s slot is
+    // CTA + unit; units of pass 1: 256 rows of a group and a KV head
     const size_t units = ((size_t)B * T * G / (2 * kBM) + (n_groups < B ? n_groups : B)) * Hkv;
-    return (ctas + units) * kSlotFloats * sizeof(float);
+    l.own = l.slots + pad256((ctas + units) * kSlotFloats * sizeof(float));
+    l.total = l.own + ((size_t)ctas + (size_t)B * Hkv) * own_slot_floats(G * T) * sizeof(float);
+    return l;
 }
 
-cudaError_t launch_shared(const CUtensorMap &tmK128, const CUtensorMap &tmV128,
-                          const CUtensorMap &tmQ, const SharedParams &p, int ctas,
-                          cudaStream_t stream)
+cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
+                          const SharedParams &p, int ctas, cudaStream_t stream)
 {
     const size_t smem1 = sizeof(SharedSmem) + 1024, smem2 = sizeof(OwnSmem) + 1024;
     const int MT = (p.d.G * p.d.T + 15) / 16;
     auto own = MT == 1 ? own_kernel<1> : own_kernel<2>;
+    // the opt-in shared-memory sizes are set once per process
     static bool attr_set[3] = {false, false, false};
     if (!attr_set[0]) {
         const cudaError_t e = cudaFuncSetAttribute(
@@ -1201,22 +1260,15 @@ cudaError_t launch_shared(const CUtensorMap &tmK128, const CUtensorMap &tmV128,
             return e;
         attr_set[MT] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kSharedThreads);
-    cfg.dynamicSmemBytes = smem1;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_kernel, tmK128, tmV128, tmQ, p);
-    if (e != cudaSuccess)
-        return e;
-    cfg.blockDim = dim3(kOwnThreads);
-    cfg.dynamicSmemBytes = smem2;
-    return cudaLaunchKernelEx(&cfg, own, tmK128, tmV128, p);
+    cudaError_t e = launch_dependent(shared_kernel, (unsigned)ctas, kSharedThreads, smem1, stream,
+                                     tmK, tmV, tmQ, p);
+    if (e == cudaSuccess)
+        e = launch_dependent(own, (unsigned)ctas, kOwnThreads, smem2, stream, tmK, tmV, p);
+    if (e == cudaSuccess) {
+        const int64_t octs = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8;
+        e = launch_dependent(merge_kernel, (unsigned)(octs * p.d.Hkv), kMergeThreads, 0, stream, p);
+    }
+    return e;
 }
 
 }  // namespace hsa

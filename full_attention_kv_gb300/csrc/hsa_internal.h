@@ -57,27 +57,33 @@ hsa_status decode_host_check(const hsa_pools *pools, int32_t layer, const void *
 cudaError_t launch_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const DecodeParams &p,
                           int ctas, cudaStream_t stream);
 
-// Decode over shared prefixes (decode_shared.cu).  The workspace holds the decode
-// workspace, the plan pass 1 writes for pass 2, and pass 1's segment states.
+// Decode over shared prefixes (decode_shared.cu): what its three passes leave one another
+// in the workspace.
 struct SharedGroup {
     int64_t item0;               // first key tile of the group in pass 1's item space
     int32_t unit0;               // units of the groups before it
     int32_t pairs, kt;           // 256-row units a KV head; 128-key tiles a unit
 };
 struct SharedPlan {
-    int64_t N, C;                // items, and the CTAs they were cut over
+    int64_t N, C;                // pass 1's items, and the CTAs they were cut over
     SharedGroup group[1];        // [n_groups]
+};
+struct OwnPlan {
+    int64_t N, C;                // pass 2's
+    int32_t before[1];           // [B]: own tiles (of one head) of the sequences before
+};
+struct SharedLayout {            // byte offsets in the workspace
+    size_t plan, own_plan, slots, own, total;
 };
 struct SharedParams {
     DecodeParams d;
     const int32_t *cu_group;     // [n_groups + 1]
     const int32_t *shared_len;   // [n_groups]
-    int64_t plan_off, slot_off;  // byte offsets in the workspace
+    int64_t plan_off, own_plan_off, slot_off, own_off;
     int32_t n_groups;
 };
 
-size_t shared_plan_bytes(int n_groups);
-size_t shared_slot_bytes(int ctas, int B, int T, int G, int Hkv, int n_groups);
+SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv, int n_groups);
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
                           const SharedParams &p, int ctas, cudaStream_t stream);
 
