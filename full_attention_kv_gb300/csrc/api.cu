@@ -583,10 +583,12 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
                                                      G, Hkv, n_groups);
     if (!workspace || ws_bytes < lay.total || !aligned16(workspace))
         return HSA_INVALID_ARG;
-    CUtensorMap tmK, tmV, tmQ;
+    CUtensorMap tmK, tmV, tmK32, tmV32, tmQ;
     const uint64_t rows = (uint64_t)pools->num_blocks * Hkv * pools->page_size;
     if (!encode_2d(&tmK, pools->k[layer], 128, rows, 128, 64, 64) ||
         !encode_2d(&tmV, pools->v[layer], 128, rows, 128, 64, 64) ||
+        !encode_2d(&tmK32, pools->k[layer], 128, rows, 128, 64, 32) ||
+        !encode_2d(&tmV32, pools->v[layer], 128, rows, 128, 64, 32) ||
         !encode_3d(&tmQ, q, 128, pools->Hq, (uint64_t)B * T, 64, 128 / G, G))
         return HSA_CUDA_ERROR;
     hsa::SharedParams p{};
@@ -615,8 +617,8 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     p.slot_off = (int64_t)lay.slots;
     p.own_off = (int64_t)lay.own;
     p.n_groups = n_groups;
-    return hsa::launch_shared(tmK, tmV, tmQ, p, ctas, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
+    return hsa::launch_shared(tmK, tmV, tmQ, tmK32, tmV32, p, ctas,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HSA_OK
                : HSA_CUDA_ERROR;
 }

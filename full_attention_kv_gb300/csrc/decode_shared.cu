@@ -14,8 +14,8 @@
 // meet the shared keys in 128-key tiles as a dense product: K and V are read once a unit
 // instead of once a sequence.  The key tiles of all units are laid end to end and cut into
 // equal ranges, one per CTA; each (CTA, unit) segment leaves unnormalised fp32 states.
-// Pass 2, own_kernel: decode.cu's stream-K walk over the pages past the shared ones, plus
-// the new tokens; each (CTA, sequence, head) segment leaves its state.
+// Pass 2, own_kernel (mma.sync, 8 to 32 rows a sequence and head): a stream-K walk over the
+// pages past the shared ones and the new tokens; each segment leaves its state.
 // Pass 3, merge_kernel: a thread for four output dimensions of a row merges the row's
 // states and writes bf16; it also appends the new rows.
 //
@@ -675,41 +675,61 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 }
 
 // ------------------------------------------------------ pass 2: own pages and new tokens
+//
+// What a sequence holds past the shared pages is often short (a question on a document), so
+// the work is cut over many small streams instead of CTAs: four groups of MT warps a CTA,
+// each with a range of 32-key items, a ring of stages and softmax states of its own, which
+// loads its own tiles (lane 0, one item's stage refilled as it is done with) and writes its
+// own state at the end of a (sequence, head) unit.  No barrier joins the groups, so one
+// group's start and end of a unit hides under the others' tiles.  The T new tokens are the
+// unit's last keys: their rows are written into the staged tile that they fall in.
 
-constexpr int kStages = 4;
-constexpr int kTileBytes = kTileKeys * kD * 2;  // 16 KB: one K or V tile
-constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kConsumerWarps = 4;
-constexpr int kOwnThreads = (kConsumerWarps + 1) * 32;
-constexpr int kCombFloats = 16 + 16 + 16 * kD;  // per consumer warp: m, l, o[16][128]
+constexpr int kKT = 32;                         // keys an item: half a page
+constexpr int kGroups = 4;
+constexpr int kDepth = 3;                       // stages a group
+constexpr int kHalfTile = kKT * kD * 2;         // 8 KB: K or V of an item
+constexpr int kItemBytes = 2 * kHalfTile;
+constexpr int kInfoCap = 1024;                  // sequences whose lengths are kept in shared memory
+constexpr int kOwnMaxThreads = kGroups * 2 * 32;
 
 struct OwnSmem {
-    alignas(1024) uint8_t stage[kStages * kStageBytes];  // [K lo|K hi|V lo|V hi] per stage
-    alignas(16) uint8_t new_k[kNewRows * kD * 2];
-    alignas(16) uint8_t new_v[kNewRows * kD * 2];
-    alignas(16) float comb[kConsumerWarps][kCombFloats];
-    float mscale[kMaxRows][kConsumerWarps];
-    alignas(8) uint64_t full[kStages];
-    alignas(8) uint64_t empty[kStages];
-    int32_t tile_ok[kStages];
-    int32_t scan[kOwnThreads];
-    int32_t first_b, first_items_before, total_items, share;
+    alignas(1024) uint8_t stage[kGroups][kDepth][kItemBytes];  // [K lo|K hi|V lo|V hi]
+    alignas(8) uint64_t full[kGroups][kDepth];
+    alignas(8) uint64_t empty[kGroups][kDepth];  // MT = 2: the second warp is done with it
+    int32_t ok[kGroups][kDepth];                 // the item's cached keys were loaded
+    int2 info[kInfoCap];                         // (c, fp) of a sequence
+    int32_t scan[kOwnMaxThreads];
+    int32_t first_b[kGroups], first_before[kGroups];
+    int32_t total_items, share;
 };
 
-// Position in the item space: sequence b, head h, own tile j of n; c cached tokens past
-// the first page `fp` that is the sequence's own.
+// Position in a stream: sequence b, head h, item j of n; c cached tokens past the first
+// page `fp` that is the sequence's own.
 struct OwnWalk {
     int b, h, j, n, c, fp;
 };
 
-__device__ __forceinline__ void own_load(const SharedParams &p, bool share, OwnWalk &w)
+// c and fp of sequence b, from the inputs.
+__device__ __forceinline__ int2 own_info(const SharedParams &p, bool share, int b)
 {
-    w.fp = share ? group_pages(p, group_of(p, w.b)) : 0;
-    w.c = max(0, clamp_len(__ldg(p.d.cached_len + w.b)) - w.fp * kTileKeys);
-    w.n = max(1, (w.c + kTileKeys - 1) / kTileKeys);
+    const int fp = share ? group_pages(p, group_of(p, b)) : 0;
+    return make_int2(max(0, clamp_len(__ldg(p.d.cached_len + b)) - fp * kTileKeys), fp);
 }
 
-__device__ __forceinline__ void own_next(const SharedParams &p, bool share, OwnWalk &w)
+__device__ __forceinline__ int own_items(const SharedParams &p, int c)
+{
+    return (c + p.d.T + kKT - 1) / kKT;
+}
+
+__device__ __forceinline__ void own_load(const SharedParams &p, const OwnSmem &sh, OwnWalk &w)
+{
+    const int2 v = w.b < kInfoCap ? sh.info[w.b] : own_info(p, sh.share != 0, w.b);
+    w.c = v.x;
+    w.fp = v.y;
+    w.n = own_items(p, w.c);
+}
+
+__device__ __forceinline__ void own_next(const SharedParams &p, const OwnSmem &sh, OwnWalk &w)
 {
     if (++w.j == w.n) {
         w.j = 0;
@@ -717,27 +737,18 @@ __device__ __forceinline__ void own_next(const SharedParams &p, bool share, OwnW
             w.h = 0;
             ++w.b;
             if (w.b < p.d.B)
-                own_load(p, share, w);
+                own_load(p, sh, w);
         }
     }
 }
 
-// TMA row of tile (b, h, j), or -1: no cached keys, or out of range (flagged).
-__device__ __forceinline__ int64_t own_row(const SharedParams &p, const OwnWalk &w)
+// Block-table entry of item w (-1: past the table); only read where it has cached keys.
+__device__ __forceinline__ int own_entry(const SharedParams &p, const OwnWalk &w)
 {
-    if (w.c == 0)
+    const int page = w.fp + w.j / (kTileKeys / kKT);
+    if (w.j * kKT >= w.c || page >= p.d.max_blocks)
         return -1;
-    const int page = w.fp + w.j;
-    if (page >= p.d.max_blocks) {
-        set_err(p.d.dev_err, HSA_DEVERR_BAD_PAGE);
-        return -1;
-    }
-    int blk = 0;
-    if (!page_ok(p, w.b, page, &blk)) {
-        set_err(p.d.dev_err, HSA_DEVERR_BAD_BLOCK);
-        return -1;
-    }
-    return ((int64_t)blk * p.d.Hkv + w.h) * kTileKeys;
+    return __ldg(p.d.block_tables + (int64_t)w.b * p.d.max_blocks + page);
 }
 
 // Floats of an own segment's state: m[R], l[R], o[R][128] for R = G T rows, m and l padded
@@ -745,26 +756,27 @@ __device__ __forceinline__ int64_t own_row(const SharedParams &p, const OwnWalk 
 __host__ __device__ inline int own_pad(int rows) { return (rows + 3) & ~3; }
 __host__ __device__ inline int own_slot_floats(int rows) { return 2 * own_pad(rows) + rows * kD; }
 
-// MT: 16-row m-tiles of a sequence's G T query rows (1 or 2).
+// MT: 16-row m-tiles of a sequence's G T query rows (1 or 2), a warp each.
 template <int MT>
-__global__ void __launch_bounds__(kOwnThreads, 1)
+__global__ void __launch_bounds__(kGroups *MT * 32, 1)
     own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ SharedParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     OwnSmem &sh = *reinterpret_cast<OwnSmem *>(align_smem_1024(smem_raw));
+    constexpr int kThr = kGroups * MT * 32;
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
+    const int grp = warp / MT, mt = warp % MT;
     const DecodeParams &d = p.d;
 
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], MT);  // the warps of the stage's group
-        }
+        for (int i = 0; i < kGroups; ++i)
+            for (int s = 0; s < kDepth; ++s) {
+                mbar_init(&sh.full[i][s], 1);
+                mbar_init(&sh.empty[i][s], 1);
+            }
         fence_barrier_init();
-    }
-    if (warp == kConsumerWarps && lane == 0) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
@@ -780,21 +792,21 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
     __syncthreads();
     const bool share = sh.share != 0;
 
-    // ---- locate this CTA's contiguous range of items ------------------------
-    const int per = (d.B + kOwnThreads - 1) / kOwnThreads;
+    // ---- items before each sequence; a stream an equal contiguous range ----------
+    const int per = (d.B + kThr - 1) / kThr;
     const int b_lo = min(d.B, tid * per), b_hi = min(d.B, b_lo + per);
     {
         int local = 0;
         for (int b = b_lo; b < b_hi; ++b) {
-            OwnWalk w;
-            w.b = b;
-            own_load(p, share, w);
-            local += w.n;
+            const int2 v = own_info(p, share, b);
+            if (b < kInfoCap)
+                sh.info[b] = v;
+            local += own_items(p, v.x);
         }
         sh.scan[tid] = local;
         __syncthreads();
         if (warp == 0) {
-            constexpr int kPer = kOwnThreads / 32;
+            constexpr int kPer = kThr / 32;
             int v[kPer];
             int sum = 0;
 #pragma unroll
@@ -821,23 +833,26 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         __syncthreads();
     }
     const int64_t N = (int64_t)sh.total_items * d.Hkv;
-    const int64_t C = min(N, (int64_t)gridDim.x);
-    const int64_t i0 = min(N, (int64_t)blockIdx.x * N / C);
-    const int64_t i1 = min(N, ((int64_t)blockIdx.x + 1) * N / C);
+    const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
+    // streams 0 .. gridDim - 1 on different CTAs: few items still use every SM
+    const int64_t stream = (int64_t)grp * gridDim.x + blockIdx.x;
+    const int64_t i0 = min(N, stream * N / C), i1 = min(N, (stream + 1) * N / C);
     {
         OwnPlan *const plan = reinterpret_cast<OwnPlan *>(d.ws + p.own_plan_off);
         int before = sh.scan[tid];
         for (int b = b_lo; b < b_hi; ++b) {
-            OwnWalk w;
-            w.b = b;
-            own_load(p, share, w);
-            if ((int64_t)(before + w.n) * d.Hkv > i0 && (int64_t)before * d.Hkv <= i0) {
-                sh.first_b = b;
-                sh.first_items_before = before;
+            const int n = own_items(p, b < kInfoCap ? sh.info[b].x : own_info(p, share, b).x);
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int64_t at = min(N, ((int64_t)i * gridDim.x + blockIdx.x) * N / C);
+                if ((int64_t)(before + n) * d.Hkv > at && (int64_t)before * d.Hkv <= at) {
+                    sh.first_b[i] = b;
+                    sh.first_before[i] = before;
+                }
             }
             if (blockIdx.x == 0)  // for pass 3
                 plan->before[b] = before;
-            before += w.n;
+            before += n;
         }
         if (blockIdx.x == 0 && tid == 0) {
             plan->N = N;
@@ -845,223 +860,179 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         }
         __syncthreads();
     }
-    if ((int64_t)blockIdx.x >= C) {
+    if (i0 >= i1) {
         grid_dependency_wait();  // every CTA's exit stays ordered after pass 1
         return;
     }
     OwnWalk w;
-    w.b = sh.first_b;
-    own_load(p, share, w);
+    w.b = sh.first_b[grp];
+    own_load(p, sh, w);
     {
-        const int64_t off = i0 - (int64_t)sh.first_items_before * d.Hkv;
+        const int64_t off = i0 - (int64_t)sh.first_before[grp] * d.Hkv;
         w.h = (int)(off / w.n);
         w.j = (int)(off % w.n);
     }
 
-    if (warp == kConsumerWarps) {
-        // ---------------------------------------------------------------- producer
-        if (lane == 0) {
-            const uint64_t pol = policy_evict_first();
-            int64_t k = 0;
-            int64_t row = own_row(p, w);
-            for (int64_t i = i0; i < i1; ++i, ++k) {
-                const int st = (int)(k % kStages);
-                const int64_t r = row;
-                own_next(p, share, w);
-                row = i + 1 < i1 ? own_row(p, w) : -1;  // read ahead of the wait
-                if (!mbar_wait(&sh.empty[st], (uint32_t)((k / kStages) & 1) ^ 1)) {
-                    set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
-                    break;
-                }
-                sh.tile_ok[st] = r >= 0 ? 1 : 0;
-                if (r >= 0) {
-                    mbar_arrive_expect_tx(&sh.full[st], kStageBytes);
-                    uint8_t *dst = sh.stage + st * kStageBytes;
-                    tma_load_2d(dst, &tmK, &sh.full[st], 0, (int32_t)r, pol);
-                    tma_load_2d(dst + kTileBytes / 2, &tmK, &sh.full[st], 64, (int32_t)r, pol);
-                    tma_load_2d(dst + kTileBytes, &tmV, &sh.full[st], 0, (int32_t)r, pol);
-                    tma_load_2d(dst + kTileBytes + kTileBytes / 2, &tmV, &sh.full[st], 64,
-                                (int32_t)r, pol);
-                } else {
-                    mbar_arrive(&sh.full[st]);
-                }
-            }
-            // drain: no TMA write may still be in flight when the CTA exits
-            for (int64_t s = 0; s < kStages && s < k; ++s) {
-                const int64_t last = s + ((k - 1 - s) / kStages) * kStages;
-                mbar_wait(&sh.full[s], (uint32_t)((last / kStages) & 1));
-            }
-            grid_dependency_wait();
+    // ---- loads: item li of the stream, kDepth items ahead of the products ------------
+    const uint64_t pol = policy_evict_first();
+    OwnWalk lw = w;
+    int64_t li = i0;
+    int lst = 0;
+    uint32_t lph = 0;  // parity of the stage's next empty phase (MT = 2)
+    int entry = own_entry(p, lw);
+    bool timed_out = false;
+    auto load = [&](bool refill) {  // the group's first warp
+        if (li >= i1)
+            return;
+        if (MT == 2 && refill && !timed_out && !mbar_wait(&sh.empty[grp][lst], lph)) {
+            set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+            timed_out = true;
         }
-        return;
-    }
+        if (lane == 0) {
+            bool ok = lw.j * kKT < lw.c && !timed_out;
+            if (ok && (entry < 0 || entry >= d.num_blocks)) {
+                set_err(d.dev_err, lw.fp + lw.j / (kTileKeys / kKT) >= d.max_blocks
+                                       ? HSA_DEVERR_BAD_PAGE
+                                       : HSA_DEVERR_BAD_BLOCK);
+                ok = false;
+            }
+            uint64_t *const full = &sh.full[grp][lst];
+            sh.ok[grp][lst] = ok;
+            if (ok) {
+                uint8_t *const dst = sh.stage[grp][lst];
+                const int32_t r = (entry * d.Hkv + lw.h) * kTileKeys + lw.j * kKT % kTileKeys;
+                mbar_arrive_expect_tx(full, kItemBytes);
+                tma_load_2d(dst, &tmK, full, 0, r, pol);
+                tma_load_2d(dst + kHalfTile / 2, &tmK, full, 64, r, pol);
+                tma_load_2d(dst + kHalfTile, &tmV, full, 0, r, pol);
+                tma_load_2d(dst + kHalfTile + kHalfTile / 2, &tmV, full, 64, r, pol);
+            } else {
+                mbar_arrive(full);
+            }
+        }
+        __syncwarp();
+        ++li;
+        if (li < i1) {
+            own_next(p, sh, lw);
+            entry = own_entry(p, lw);  // used at the next load
+        }
+        if (++lst == kDepth) {
+            lst = 0;
+            lph ^= refill ? 1 : 0;
+        }
+    };
+    if (mt == 0)
+        for (int i = 0; i < kDepth; ++i)
+            load(false);
 
-    // ------------------------------------------------------------------ consumers
-    // Tile-parallel groups as in decode.cu: the MT warps of group `slice` (one per 16-row
-    // m-tile) run every (4 / MT)-th tile of the CTA's range with all 64 keys.
-    constexpr int kSlices = kConsumerWarps / MT;
-    constexpr int kThr = kConsumerWarps * 32;
-    static_assert(kStages % kSlices == 0, "each stage belongs to one group");
-    const int mt = warp % MT, slice = warp / MT;
+    // ---- products ---------------------------------------------------------------------
     const int g = lane >> 2, tq = lane & 3;
     const int q_r0 = mt * 16 + g, q_r1 = q_r0 + 8;
     const int t0 = q_r0 / d.G, t1 = q_r1 / d.G;
-    const int rows_valid = d.G * d.T;
-    const int Hq = d.G * d.Hkv;
-
+    const bool v0 = t0 < d.T, v1 = t1 < d.T;
+    const int Hq = d.G * d.Hkv, rows = d.G * d.T;
     RowState st;
     uint32_t qa[kD / 16][4];
-    bool timed_out = false;
-    int64_t i = i0, k = 0, unit_start = i0 - w.j;
-    while (i < i1) {
-        // ---- this CTA's share of unit (w.b, w.h): items i .. i_end ----------------
-        const int64_t unit_end = unit_start + w.n;
-        const int64_t i_end = min(i1, unit_end);
-        const bool has_new = unit_end <= i1;  // owns the unit's last tile
-        const OwnWalk cur = w;
-        st.m[0] = st.m[1] = -INFINITY;
-        st.l[0] = st.l[1] = 0.f;
+    int stg = 0;
+    uint32_t ph = 0;
+    bool fresh = true;
+    for (int64_t i = i0; i < i1; ++i) {
+        if (fresh) {
+            fresh = false;
+            st.m[0] = st.m[1] = -INFINITY;
+            st.l[0] = st.l[1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < kD / 8; ++n)
-            st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
-        const bool v0 = t0 < d.T, v1 = t1 < d.T;
-        const __nv_bfloat16 *q0 =
-            d.q + ((int64_t)(cur.b * d.T + t0) * Hq + cur.h * d.G + q_r0 % d.G) * kD;
-        const __nv_bfloat16 *q1 =
-            d.q + ((int64_t)(cur.b * d.T + t1) * Hq + cur.h * d.G + q_r1 % d.G) * kD;
+            for (int n = 0; n < kD / 8; ++n)
+                st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
+            const __nv_bfloat16 *q0 =
+                d.q + ((int64_t)(w.b * d.T + t0) * Hq + w.h * d.G + q_r0 % d.G) * kD;
+            const __nv_bfloat16 *q1 =
+                d.q + ((int64_t)(w.b * d.T + t1) * Hq + w.h * d.G + q_r1 % d.G) * kD;
 #pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks) {
-            const int c0 = ks * 16 + 2 * tq;
-            qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
-            qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
-            qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
-            qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                const int c0 = ks * 16 + 2 * tq;
+                qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
+                qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
+                qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
+                qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
+            }
         }
-        if (has_new) {
-            for (int e = tid; e < kNewRows * kD / 8; e += kThr) {
-                const int rr = e / (kD / 8), col = (e % (kD / 8)) * 8;
-                uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
-                if (rr < d.T) {
-                    const int64_t src = ((int64_t)(cur.b * d.T + rr) * d.Hkv + cur.h) * kD + col;
-                    kv = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
+        if (!timed_out && !mbar_wait(&sh.full[grp][stg], ph)) {
+            set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+            timed_out = true;
+        }
+        uint8_t *const base = sh.stage[grp][stg];
+        // keys 0 .. cached - 1 of the item are cached ones, key news + t is new token t
+        const int news = w.c - w.j * kKT;
+        const int cached = !timed_out && sh.ok[grp][stg] ? min(kKT, news) : 0;
+        if (cached < kKT) {
+            // the new tokens' rows; V rows of no key may hold anything, and 0 x NaN is NaN:
+            // they become 0 (their scores are masked).  Both warps of a pair write the same.
+            for (int e = lane; e < (kKT - cached) * (kD / 8); e += 32) {
+                const int key = cached + e / (kD / 8), col = (e % (kD / 8)) * 8, t = key - news;
+                uint4 vv = make_uint4(0, 0, 0, 0);
+                uint8_t *const at = base + swz128_offset(key, col, kKT);
+                if (t >= 0 && t < d.T) {
+                    const int64_t src = ((int64_t)(w.b * d.T + t) * d.Hkv + w.h) * kD + col;
                     vv = __ldg(reinterpret_cast<const uint4 *>(d.v_new + src));
+                    *reinterpret_cast<uint4 *>(at) = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
                 }
-                *reinterpret_cast<uint4 *>(sh.new_k + swz128_offset(rr, col, kNewRows)) = kv;
-                *reinterpret_cast<uint4 *>(sh.new_v + swz128_offset(rr, col, kNewRows)) = vv;
+                *reinterpret_cast<uint4 *>(at + kHalfTile) = vv;
             }
-        }
-        for (; i < i_end; ++i, ++k) {
-            const int j = (int)(i - unit_start);
-            if ((int)(k % kSlices) != slice)
-                continue;
-            const int stg = (int)(k % kStages);
-            if (!timed_out && !mbar_wait(&sh.full[stg], (uint32_t)((k / kStages) & 1))) {
-                set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
-                timed_out = true;
-            }
-            const int valid = cur.c - j * kTileKeys;
-            if (!timed_out && sh.tile_ok[stg] != 0 && valid > 0) {
-                uint8_t *const base = sh.stage + stg * kStageBytes;
-                const uint32_t sK = smem_u32(base), sV = sK + kTileBytes;
-                const int T = d.T;
-                if (valid < kTileKeys) {
-                    // rows past the sequence's end may hold anything, and 0 x NaN is NaN:
-                    // their values become 0 (their scores are masked)
-                    for (int e = lane; e < (kTileKeys - valid) * (kD / 8); e += 32)
-                        *reinterpret_cast<uint4 *>(
-                            base + kTileBytes +
-                            swz128_offset(valid + e / (kD / 8), (e % (kD / 8)) * 8, kTileKeys)) =
-                            make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();  // before the stage's next TMA write
-                    __syncwarp();
-                }
-                auto vis = [&](int rr, int key) -> bool {
-                    return (rr == g ? t0 : t1) < T && key < valid;
-                };
-                run_tile<kTileKeys / 8>(st, qa, sK, sV, kTileKeys, 0, d.scale_log2,
-                                        valid >= kTileKeys, t0 < T, t1 < T, vis);
-            }
+            fence_proxy_async_smem();  // before the stage's next TMA write
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.empty[stg]);
         }
-        if (has_new) {
-            named_bar_sync(1, kThr);  // new rows staged by every warp
-            if (slice == 0) {
-                const int T = d.T;
-                auto vis_new = [&](int rr, int key) -> bool {
-                    const int t = rr == g ? t0 : t1;
-                    return t < T && key <= t;
-                };
-                run_tile<2>(st, qa, smem_u32(sh.new_k), smem_u32(sh.new_v), kNewRows, 0,
-                            d.scale_log2, false, t0 < T, t1 < T, vis_new);
+        {
+            const int T = d.T;
+            auto vis = [&](int rr, int key) -> bool {
+                const int t = rr == g ? t0 : t1;
+                return t < T && (key < cached || (key >= news && key - news <= t));
+            };
+            const uint32_t sK = smem_u32(base);
+            run_tile<kKT / 8>(st, qa, sK, sK + kHalfTile, kKT, 0, d.scale_log2, cached == kKT, v0, v1, vis);
+        }
+        __syncwarp();
+        if (MT == 2 && mt == 1 && lane == 0)
+            mbar_arrive(&sh.empty[grp][stg]);
+        if (mt == 0)
+            load(true);
+        if (++stg == kDepth) {
+            stg = 0;
+            ph ^= 1;
+        }
+        const bool last = w.j == w.n - 1 || i == i1 - 1;
+        if (last) {
+            // ---- the segment's state, from the registers ------------------------------
+            fresh = true;
+            float l0 = st.l[0], l1 = st.l[1];
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+            const int pad = own_pad(rows);
+            float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
+                                (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
+            if (tq == 0) {
+                if (v0) {
+                    part[q_r0] = st.m[0];
+                    part[pad + q_r0] = l0;
+                }
+                if (v1) {
+                    part[q_r1] = st.m[1];
+                    part[pad + q_r1] = l1;
+                }
+            }
+            float *const o0 = part + 2 * pad + q_r0 * kD + 2 * tq;
+#pragma unroll
+            for (int n = 0; n < kD / 8; ++n) {
+                if (v0)
+                    *reinterpret_cast<float2 *>(o0 + n * 8) = make_float2(st.o[n][0], st.o[n][1]);
+                if (v1)
+                    *reinterpret_cast<float2 *>(o0 + 8 * kD + n * 8) =
+                        make_float2(st.o[n][2], st.o[n][3]);
             }
         }
-        float l0 = st.l[0], l1 = st.l[1];
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        float *cb = sh.comb[warp];
-        if (tq == 0) {
-            cb[g] = st.m[0];
-            cb[g + 8] = st.m[1];
-            cb[16 + g] = l0;
-            cb[16 + g + 8] = l1;
-        }
-        float *co = cb + 32;
-#pragma unroll
-        for (int n = 0; n < kD / 8; ++n) {
-            *reinterpret_cast<float2 *>(co + g * kD + n * 8 + 2 * tq) =
-                make_float2(st.o[n][0], st.o[n][1]);
-            *reinterpret_cast<float2 *>(co + (g + 8) * kD + n * 8 + 2 * tq) =
-                make_float2(st.o[n][2], st.o[n][3]);
-        }
-        named_bar_sync(1, kThr);
-
-        // ---- the warps' states merged into the segment's -----------------------------
-        const int unit = cur.b * d.Hkv + cur.h;
-        float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
-                            ((int64_t)blockIdx.x + unit) * own_slot_floats(rows_valid);
-        const int pad = own_pad(rows_valid);
-        for (int rr = tid; rr < rows_valid; rr += kThr) {
-            const int m_t = rr / 16, rl = rr % 16;
-            float M = -INFINITY;
-#pragma unroll
-            for (int s = 0; s < kSlices; ++s)
-                M = fmaxf(M, sh.comb[m_t + MT * s][rl]);
-            const float base = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-#pragma unroll
-            for (int s = 0; s < kSlices; ++s) {
-                const float a = fast_exp2(sh.comb[m_t + MT * s][rl] - base);
-                sh.mscale[rr][s] = a;
-                L += sh.comb[m_t + MT * s][16 + rl] * a;
-            }
-            part[rr] = M;
-            part[pad + rr] = L;
-        }
-        named_bar_sync(1, kThr);
-        for (int e = tid; e < rows_valid * (kD / 4); e += kThr) {
-            const int rr = e / (kD / 4), d0 = (e % (kD / 4)) * 4;
-            const int m_t = rr / 16, rl = rr % 16;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int s = 0; s < kSlices; ++s) {
-                const float wgt = sh.mscale[rr][s];
-                const float4 x =
-                    *reinterpret_cast<const float4 *>(&sh.comb[m_t + MT * s][32 + rl * kD + d0]);
-                o.x += x.x * wgt;
-                o.y += x.y * wgt;
-                o.z += x.z * wgt;
-                o.w += x.w * wgt;
-            }
-            *reinterpret_cast<float4 *>(part + 2 * pad + rr * kD + d0) = o;
-        }
-        named_bar_sync(1, kThr);  // merge buffers and new rows free again
-        unit_start = unit_end;
-        w.j = w.n - 1;  // the next unit
-        own_next(p, share, w);
+        own_next(p, sh, w);
     }
     grid_dependency_wait();
 }
@@ -1143,7 +1114,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
         const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
         const int64_t item0 = __ldcg(&gp->item0);
         const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), kt = __ldcg(&gp->kt);
-        // the sequence's own states: CTAs c_lo .. c_hi of pass 2
+        // the sequence's own states: streams c_lo .. c_hi of pass 2
         {
             const int n = next - before;
             const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
@@ -1234,11 +1205,12 @@ SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv,
     // CTA + unit; units of pass 1: 256 rows of a group and a KV head
     const size_t units = ((size_t)B * T * G / (2 * kBM) + (n_groups < B ? n_groups : B)) * Hkv;
     l.own = l.slots + pad256((ctas + units) * kSlotFloats * sizeof(float));
-    l.total = l.own + ((size_t)ctas + (size_t)B * Hkv) * own_slot_floats(G * T) * sizeof(float);
+    l.total = l.own + ((size_t)ctas * kGroups + (size_t)B * Hkv) * own_slot_floats(G * T) * sizeof(float);
     return l;
 }
 
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
+                          const CUtensorMap &tmK32, const CUtensorMap &tmV32,
                           const SharedParams &p, int ctas, cudaStream_t stream)
 {
     const size_t smem1 = sizeof(SharedSmem) + 1024, smem2 = sizeof(OwnSmem) + 1024;
@@ -1263,7 +1235,7 @@ cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
     cudaError_t e = launch_dependent(shared_kernel, (unsigned)ctas, kSharedThreads, smem1, stream,
                                      tmK, tmV, tmQ, p);
     if (e == cudaSuccess)
-        e = launch_dependent(own, (unsigned)ctas, kOwnThreads, smem2, stream, tmK, tmV, p);
+        e = launch_dependent(own, (unsigned)ctas, kGroups * MT * 32, smem2, stream, tmK32, tmV32, p);
     if (e == cudaSuccess) {
         const int64_t octs = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8;
         e = launch_dependent(merge_kernel, (unsigned)(octs * p.d.Hkv), kMergeThreads, 0, stream, p);

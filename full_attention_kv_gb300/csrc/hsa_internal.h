@@ -69,8 +69,8 @@ struct SharedPlan {
     SharedGroup group[1];        // [n_groups]
 };
 struct OwnPlan {
-    int64_t N, C;                // pass 2's
-    int32_t before[1];           // [B]: own tiles (of one head) of the sequences before
+    int64_t N, C;                // pass 2's, and its streams
+    int32_t before[1];           // [B]: own items (of one head) of the sequences before
 };
 struct SharedLayout {            // byte offsets in the workspace
     size_t plan, own_plan, slots, own, total;
@@ -84,7 +84,9 @@ struct SharedParams {
 };
 
 SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv, int n_groups);
+// tmK, tmV: boxes of a page; tmK32, tmV32: of half a page
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
+                          const CUtensorMap &tmK32, const CUtensorMap &tmV32,
                           const SharedParams &p, int ctas, cudaStream_t stream);
 
 struct AppendParams {
