@@ -11,8 +11,8 @@
 //
 // Pass 1, shared_kernel (tcgen05): the query rows of a group for one KV head -- members x T
 // tokens x G heads -- are packed into 128-row tiles, a pair of tiles (256 rows) a unit, and
-// meet the shared keys in 128-key tiles as a dense product: K and V are read once a unit
-// instead of once a sequence.  The key tiles of all units are laid end to end and cut into
+// meet the shared keys page by page as a dense product: K and V are read once a unit
+// instead of once a sequence.  The pages of all units are laid end to end and cut into
 // equal ranges, one per CTA; each (CTA, unit) segment leaves unnormalised fp32 states.
 // Pass 2, own_kernel (mma.sync, 8 to 32 rows a sequence and head): a stream-K walk over the
 // pages past the shared ones and the new tokens; each segment leaves its state.
@@ -67,14 +67,26 @@ __device__ __forceinline__ int group_of(const SharedParams &p, int b)
 __device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
 
 // ------------------------------------------------------------------ pass 1: shared pages
+//
+// A step is one 64-key page.  Each query tile has two 64-column S regions in TMEM, so that
+// the next page's scores are there when the softmax warps finish a page.
+//   pair mode (129 .. 256 rows): query tiles A and B, one warpgroup each, every page
+//   split mode (up to 128 rows): one query tile; the warpgroups, with S and O regions of
+//     their own, take the pages in turn and leave two states a row
+// Each warpgroup has an issuing warp of its own: an issuer spends about half of a step in
+// the latency of its waits and commits, and two of them keep the tensor cores fed.
+// K and V pages pass through a ring of two-page stages in the order of their use: with L = 2
+// (pair) or 4 (split) pages of scores ahead, [K0 K1] .. [K(L-2) K(L-1)], then [V(n) K(n+L)].
 
 constexpr int kBM = 128;
-constexpr int kBN = 128;
-constexpr int kHalfBytes = 128 * 128;       // 128 rows x 64 bf16 (one swizzle column block)
-constexpr int kOpBytes = 2 * kHalfBytes;    // 32 KB
-constexpr int kSharedThreads = 320;
+constexpr int kQBytes = kBM * kD * 2;       // 32 KB: two blocks of 128 rows x 64 columns
+constexpr int kQHalf = kQBytes / 2;
+constexpr int kPageBytes = kTileKeys * kD * 2;  // 16 KB: two blocks of 64 rows x 64 columns
+constexpr int kPageHalf = kPageBytes / 2;
+constexpr int kRing = 5;
+constexpr int kSharedThreads = 352;         // producer, issuers 1 and 10, softmax warps 2 .. 9
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;             // S_A, S_B at 0 / 128; O_A, O_B at 256 / 384
+constexpr uint32_t kColO = 256;             // S: tile t, region h at 128 t + 64 h; O_t at 256 + 128 t
 // A segment's states, by octets of rows: m[8], l[8], then o as [dim / 4][8 rows][4], so
 // that the warps that write (a row a lane) and those that merge (eight rows x four
 // 16-byte pieces) both move whole 128-byte lines.
@@ -82,27 +94,37 @@ constexpr int kOctFloats = 16 + 8 * kD;
 constexpr int kSlotFloats = 2 * kBM / 8 * kOctFloats;
 
 struct SharedSmem {
-    alignas(1024) uint8_t q[2][kOpBytes];
-    alignas(1024) uint8_t k[2][kOpBytes];
-    alignas(1024) uint8_t v[2][kOpBytes];
+    alignas(1024) uint8_t q[2][kQBytes];
+    alignas(1024) uint8_t ring[kRing][2][kPageBytes];
     alignas(8) uint64_t q_full, q_empty;
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t full[kRing], empty[kRing];
+    uint64_t s_full[2][2], p_full[2][2];    // [query tile][region]
+    uint64_t pv_done[2], o_empty[2], done[2];
     uint32_t tmem_base;
     int32_t g0, unit0;
     int64_t item0, N;
 };
 
+// a / b of non-negative numbers that mostly fit 32 bits
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
+{
+    return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// First item of part c of N items cut into C equal parts: floor(c N / C)
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t N, int64_t C)
+{
+    const int64_t q = div_pos(N, C);
+    return c * q + div_pos(c * (N - q * C), C);
+}
+
 // A CTA's walk over the segments of its item range: every role runs its own copy.
-// A unit of at most 128 rows has one query tile; the two softmax warpgroups, S and O
-// regions then take its key tiles in turn (split()), so that one tile's products still
-// run under the other's softmax, and the segment leaves two states a row.
 struct SegWalk {
     int64_t it, i1, item0;  // next item, end, first item of group g
     int g, unit0;           // group, units before it
-    int pairs, kt;          // the group's 256-row units a head, 128-key tiles a unit
-    int seq0, ntok, pages;
-    // the current segment
+    int pairs, pages;       // the group's 256-row units a head, pages (items) a unit
+    int seq0, ntok;
+    // the current segment: pages n0 .. n1 - 1
     int h, pair, n0, n1, unit, rows;
     __device__ __forceinline__ bool split() const { return rows <= kBM; }
 };
@@ -112,28 +134,27 @@ __device__ __forceinline__ void load_group(const SharedParams &p, SegWalk &w)
     w.seq0 = __ldg(p.cu_group + w.g);
     w.ntok = (__ldg(p.cu_group + w.g + 1) - w.seq0) * p.d.T;
     w.pages = group_pages(p, w.g);
-    w.kt = (w.pages + 1) >> 1;
-    w.pairs = w.kt > 0 ? (w.ntok * p.d.G + 2 * kBM - 1) / (2 * kBM) : 0;
+    w.pairs = w.pages > 0 ? (w.ntok * p.d.G + 2 * kBM - 1) / (2 * kBM) : 0;
 }
 
 __device__ __forceinline__ bool next_seg(const SharedParams &p, SegWalk &w)
 {
     if (w.it >= w.i1)
         return false;
-    int64_t n = (int64_t)w.pairs * p.d.Hkv * w.kt;
+    int64_t n = (int64_t)w.pairs * p.d.Hkv * w.pages;
     while (w.it >= w.item0 + n) {
         w.item0 += n;
         w.unit0 += w.pairs * p.d.Hkv;
         ++w.g;
         load_group(p, w);
-        n = (int64_t)w.pairs * p.d.Hkv * w.kt;
+        n = (int64_t)w.pairs * p.d.Hkv * w.pages;
     }
     const int64_t off = w.it - w.item0;
-    const int u = (int)(off / w.kt);
-    w.n0 = (int)(off % w.kt);
-    w.n1 = (int)min((int64_t)w.kt, w.n0 + (w.i1 - w.it));
+    const int u = (int)div_pos(off, w.pages);
+    w.n0 = (int)(off - (int64_t)u * w.pages);
+    w.n1 = (int)min((int64_t)w.pages, w.n0 + (w.i1 - w.it));
     w.h = u / w.pairs;
-    w.pair = u % w.pairs;
+    w.pair = u - w.h * w.pairs;
     w.unit = w.unit0 + u;
     w.rows = w.ntok * p.d.G - w.pair * 2 * kBM;
     w.it += w.n1 - w.n0;
@@ -149,6 +170,28 @@ __device__ __forceinline__ bool page_ok(const SharedParams &p, int seq, int page
     return true;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
+// Position in the ring: buffer and the parity of its current phase.
+struct RingPos {
+    int b;
+    uint32_t ph;
+    __device__ __forceinline__ void next()
+    {
+        if (++b == kRing) {
+            b = 0;
+            ph ^= 1;
+        }
+    }
+};
+
 __global__ void __launch_bounds__(kSharedThreads, 1)
     shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ SharedParams p)
@@ -160,16 +203,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 
     if (tid == 32) {
         mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&sh.k_full[s], 1);
-            mbar_init(&sh.k_empty[s], 1);
-            mbar_init(&sh.v_full[s], 1);
-            mbar_init(&sh.v_empty[s], 1);
-            mbar_init(&sh.s_full[s], 1);
-            mbar_init(&sh.p_full[s], 4 * 32);
-            mbar_init(&sh.o_full[s], 1);
-            mbar_init(&sh.o_empty[s], 4 * 32);
+        mbar_init(&sh.q_empty, 2);  // here and for a stage: the two issuers
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 2);
+        }
+        for (int t = 0; t < 2; ++t) {
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sh.s_full[t][h], 1);
+                mbar_init(&sh.p_full[t][h], 4 * 32);
+            }
+            mbar_init(&sh.pv_done[t], 1);
+            mbar_init(&sh.o_empty[t], 4 * 32);
+            mbar_init(&sh.done[t], 1);
         }
         fence_barrier_init();
     }
@@ -179,6 +225,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         tma_prefetch_desc(&tmV);
     }
     if (warp == 1) {
+        __syncwarp();
         tmem_alloc(&sh.tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -189,75 +236,61 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     if (warp == 0) {
         const bool ok = groups_ok(p, lane);
         SharedPlan *const plan = reinterpret_cast<SharedPlan *>(p.d.ws + p.plan_off);
-        int64_t total = 0;
-        int units = 0;
-        for (int base = 0; ok && base < p.n_groups; base += 32) {
-            SegWalk w{};
-            w.g = base + lane;
-            if (w.g < p.n_groups)
-                load_group(p, w);
-            int64_t n = (int64_t)w.pairs * p.d.Hkv * w.kt, incl = n;
-            int un = w.pairs * p.d.Hkv, uincl = un;
+        int64_t N = 0, C = 0, i0 = 0;
+        for (int walk = 0; walk < 2; ++walk) {  // 0: the sums, 1: the group that holds i0
+            int64_t total = 0;
+            int units = 0;
+            for (int base = 0; ok && base < p.n_groups; base += 32) {
+                SegWalk w{};
+                w.g = base + lane;
+                if (w.g < p.n_groups)
+                    load_group(p, w);
+                const int64_t n = (int64_t)w.pairs * p.d.Hkv * w.pages;
+                const int un = w.pairs * p.d.Hkv;
+                int64_t incl = n;
+                int uincl = un;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
-                const int b = __shfl_up_sync(0xffffffffu, uincl, o);
-                if (lane >= o) {
-                    incl += a;
-                    uincl += b;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+                    const int b = __shfl_up_sync(0xffffffffu, uincl, o);
+                    if (lane >= o) {
+                        incl += a;
+                        uincl += b;
+                    }
+                }
+                if (walk == 0 && blockIdx.x == 0 && w.g < p.n_groups) {
+                    SharedGroup &gp = plan->group[w.g];
+                    gp.item0 = total + incl - n;
+                    gp.unit0 = units + uincl - un;
+                    gp.pairs = w.pairs;
+                    gp.pages = w.pages;
+                    const int len = __ldg(p.shared_len + w.g);
+                    if (len < 0)
+                        set_err(p.d.dev_err, HSA_DEVERR_BAD_LEN);
+                    if (len / kTileKeys > p.d.max_blocks)
+                        set_err(p.d.dev_err, HSA_DEVERR_BAD_PAGE);
+                }
+                if (walk == 1 && total + incl - n <= i0 && i0 < total + incl) {
+                    sh.g0 = w.g;
+                    sh.unit0 = units + uincl - un;
+                    sh.item0 = total + incl - n;
+                }
+                total += __shfl_sync(0xffffffffu, incl, 31);
+                units += __shfl_sync(0xffffffffu, uincl, 31);
+            }
+            if (walk == 0) {
+                N = total;
+                C = min(N, (int64_t)gridDim.x);
+                i0 = blockIdx.x < C ? cut(blockIdx.x, N, C) : N;
+                if (lane == 0)
+                    sh.N = N;
+                if (blockIdx.x == 0 && lane == 0) {
+                    plan->N = N;
+                    plan->C = C;
+                    if (!ok)
+                        set_err(p.d.dev_err, HSA_DEVERR_BAD_LEN);
                 }
             }
-            if (blockIdx.x == 0 && w.g < p.n_groups) {
-                SharedGroup &gp = plan->group[w.g];
-                gp.item0 = total + incl - n;
-                gp.unit0 = units + uincl - un;
-                gp.pairs = w.pairs;
-                gp.kt = w.kt;
-                const int len = __ldg(p.shared_len + w.g);
-                if (len < 0)
-                    set_err(p.d.dev_err, HSA_DEVERR_BAD_LEN);
-                if (len / kTileKeys > p.d.max_blocks)
-                    set_err(p.d.dev_err, HSA_DEVERR_BAD_PAGE);
-            }
-            total += __shfl_sync(0xffffffffu, incl, 31);
-            units += __shfl_sync(0xffffffffu, uincl, 31);
-        }
-        if (lane == 0)
-            sh.N = total;
-        const int64_t C = min(total, (int64_t)gridDim.x);
-        if (blockIdx.x == 0 && lane == 0) {
-            plan->N = total;
-            plan->C = C;
-            if (!ok)
-                set_err(p.d.dev_err, HSA_DEVERR_BAD_LEN);
-        }
-        // second walk: the group that holds item i0
-        const int64_t i0 = blockIdx.x < C ? (int64_t)blockIdx.x * total / C : total;
-        total = 0;
-        units = 0;
-        for (int base = 0; ok && base < p.n_groups; base += 32) {
-            SegWalk w{};
-            w.g = base + lane;
-            if (w.g < p.n_groups)
-                load_group(p, w);
-            int64_t n = (int64_t)w.pairs * p.d.Hkv * w.kt, incl = n;
-            int un = w.pairs * p.d.Hkv, uincl = un;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
-                const int b = __shfl_up_sync(0xffffffffu, uincl, o);
-                if (lane >= o) {
-                    incl += a;
-                    uincl += b;
-                }
-            }
-            if (total + incl - n <= i0 && i0 < total + incl) {
-                sh.g0 = w.g;
-                sh.unit0 = units + uincl - un;
-                sh.item0 = total + incl - n;
-            }
-            total += __shfl_sync(0xffffffffu, incl, 31);
-            units += __shfl_sync(0xffffffffu, uincl, 31);
         }
     }
     tc_fence_before();
@@ -271,8 +304,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         return;
     }
     SegWalk w{};
-    w.it = (int64_t)blockIdx.x * N / C;
-    w.i1 = ((int64_t)blockIdx.x + 1) * N / C;
+    w.it = cut(blockIdx.x, N, C);
+    w.i1 = cut((int64_t)blockIdx.x + 1, N, C);
     w.item0 = sh.item0;
     w.g = sh.g0;
     w.unit0 = sh.unit0;
@@ -284,240 +317,201 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         if (lane == 0) {
             const uint64_t pol_first = policy_evict_first(), pol_keep = policy_evict_last();
             bool ok = true;
-            int kc = 0, sc = 0;
+            RingPos rp{0, 0};
+            int64_t fills = 0;
+            int sc = 0;
             while (ok && next_seg(p, w)) {
                 const int nq = w.split() ? 1 : 2;
                 if (!mbar_wait_sleep(&sh.q_empty, (sc & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(&sh.q_full, nq * kOpBytes);
+                mbar_arrive_expect_tx(&sh.q_full, nq * kQBytes);
                 const int tok0 = w.seq0 * p.d.T + w.pair * (2 * kBM / p.d.G);
                 for (int t = 0; t < nq; ++t)
                     for (int hf = 0; hf < 2; ++hf)
-                        tma_load_3d(sh.q[t] + hf * kHalfBytes, &tmQ, &sh.q_full, hf * 64,
-                                    w.h * p.d.G, tok0 + t * (kBM / p.d.G), pol_keep);
+                        tma_load_3d(sh.q[t] + hf * kQHalf, &tmQ, &sh.q_full, hf * 64, w.h * p.d.G,
+                                    tok0 + t * (kBM / p.d.G), pol_keep);
                 ++sc;
                 // pages that more than one unit reads stay in L2
                 const uint64_t pol = w.pairs > 1 ? pol_keep : pol_first;
-                const int32_t *const table =
-                    p.d.block_tables + (int64_t)w.seq0 * p.d.max_blocks;
-                auto entry = [&](int page) { return page < w.pages ? __ldg(table + page) : 0; };
-                int b0 = entry(2 * w.n0), b1 = entry(2 * w.n0 + 1);
-                for (int n = w.n0; n < w.n1 && ok; ++n, ++kc) {
-                    const int s = kc & 1;
-                    const uint32_t ph = (kc >> 1) & 1;
-                    // the next tile's block-table reads, ahead of the waits
-                    int c0 = 0, c1 = 0;
-                    if (n + 1 < w.n1) {
-                        c0 = entry(2 * n + 2);
-                        c1 = entry(2 * n + 3);
+                const int32_t *const table = p.d.block_tables + (int64_t)w.seq0 * p.d.max_blocks;
+                const int ahead = w.split() ? 4 : 2, nn = w.n1 - w.n0;
+                // stages: score pages ahead, two at a time, then one a page
+                const int pre = (min(ahead, nn) + 1) >> 1;
+                for (int j = -pre; j < nn; ++j) {
+                    const int x = j < 0 ? 2 * (j + pre) : j;             // K or V page of half 0
+                    const int y = j < 0 ? 2 * (j + pre) + 1 : j + ahead;  // K page of half 1
+                    const bool has_y = y < nn;
+                    int blk[2] = {__ldg(table + w.n0 + x), has_y ? __ldg(table + w.n0 + y) : 0};
+                    if (!mbar_wait_sleep(&sh.empty[rp.b], rp.ph ^ 1)) {
+                        ok = false;
+                        break;
                     }
-                    // an entry out of range: page 0 as a stand-in, masked below
-                    if (b0 < 0 || b0 >= p.d.num_blocks || b1 < 0 || b1 >= p.d.num_blocks) {
-                        set_err(p.d.dev_err, HSA_DEVERR_BAD_BLOCK);
-                        b0 = b0 < 0 || b0 >= p.d.num_blocks ? 0 : b0;
-                        b1 = b1 < 0 || b1 >= p.d.num_blocks ? 0 : b1;
-                    }
-                    if (2 * n + 1 >= w.pages)
-                        b1 = b0;  // past the shared pages: loaded again, masked
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (!mbar_wait_sleep(kv ? &sh.v_empty[s] : &sh.k_empty[s], ph ^ 1)) {
-                            ok = false;
+                    uint64_t *const full = &sh.full[rp.b];
+                    mbar_arrive_expect_tx(full, has_y ? 2 * kPageBytes : kPageBytes);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (e == 1 && !has_y)
                             break;
+                        if (blk[e] < 0 || blk[e] >= p.d.num_blocks) {
+                            // page 0 as a stand-in, masked by the softmax warps
+                            set_err(p.d.dev_err, HSA_DEVERR_BAD_BLOCK);
+                            blk[e] = 0;
                         }
-                        uint64_t *full = kv ? &sh.v_full[s] : &sh.k_full[s];
-                        uint8_t *dst = kv ? sh.v[s] : sh.k[s];
-                        const CUtensorMap *map = kv ? &tmV : &tmK;
-                        mbar_arrive_expect_tx(full, kOpBytes);
-                        for (int pg = 0; pg < 2; ++pg) {
-                            const int32_t y = ((pg ? b1 : b0) * p.d.Hkv + w.h) * kTileKeys;
-                            tma_load_2d(dst + pg * 8192, map, full, 0, y, pol);
-                            tma_load_2d(dst + kHalfBytes + pg * 8192, map, full, 64, y, pol);
-                        }
+                        const CUtensorMap *const map = e == 0 && j >= 0 ? &tmV : &tmK;
+                        const int32_t row = (blk[e] * p.d.Hkv + w.h) * kTileKeys;
+                        tma_load_2d(sh.ring[rp.b][e], map, full, 0, row, pol);
+                        tma_load_2d(sh.ring[rp.b][e] + kPageHalf, map, full, 64, row, pol);
                     }
-                    b0 = c0;
-                    b1 = c1;
+                    rp.next();
+                    ++fills;
                 }
             }
             if (!ok)
                 set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
             // drain: no TMA write may still be in flight when the CTA exits
-            for (int s = 0; s < 2 && kc > s; ++s) {
-                const int last = s + ((kc - 1 - s) / 2) * 2;
-                mbar_wait_sleep(&sh.k_full[s], (last >> 1) & 1);
-                mbar_wait_sleep(&sh.v_full[s], (last >> 1) & 1);
+            for (int64_t s = 0; s < kRing && s < fills; ++s) {
+                const int64_t last = s + ((fills - 1 - s) / kRing) * kRing;
+                mbar_wait_sleep(&sh.full[s], (uint32_t)((last / kRing) & 1));
             }
             if (sc > 0)
                 mbar_wait_sleep(&sh.q_full, (sc - 1) & 1);
         }
-    } else if (warp == 1) {
-        // ================================================================ MMA issuer
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16_f32(kBM, kBN, 0, 0);
-            const uint32_t id_pv = idesc_bf16_f32(kBM, kD, 0, 1);
-            const uint32_t dhi = smem_desc_sw128_hi(1024);
-            const uint32_t q_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.q[0]), 16),
-                                      smem_desc_sw128_lo(smem_u32(sh.q[1]), 16)};
-            const uint32_t k_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.k[0]), 16),
-                                      smem_desc_sw128_lo(smem_u32(sh.k[1]), 16)};
-            const uint32_t v_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.v[0]), kHalfBytes),
-                                      smem_desc_sw128_lo(smem_u32(sh.v[1]), kHalfBytes)};
-            // S_t = Q_q K^T of stage s; O_t (+)= P_t V of stage s, P_t in TMEM over S_t
-            auto issue_s = [&](int t, int q, int s) {
-                const uint32_t qa = q ? q_lo[1] : q_lo[0], kb = s ? k_lo[1] : k_lo[0];
-                const uint32_t d = tmem + t * 128;
-                tc_mma_ss_k<0>(d, desc_join(qa, dhi), desc_join(kb, dhi), id_s);
+    } else if (warp == 1 || warp == 10) {
+        // ================================================================ MMA issuers
+        // The whole warp runs the loop and one elected lane issues, so that control flow
+        // and descriptors stay uniform across the warp (an issuing branch of lane 0 alone
+        // took 1.3 times as long a step).
+        const int t = warp == 10;
+        const uint32_t id_s = idesc_bf16_f32(kBM, kTileKeys, 0, 0);
+        const uint32_t id_pv = idesc_bf16_f32(kBM, kD, 0, 1);
+        const uint32_t dhi = smem_desc_sw128_hi(1024);
+        const uint32_t q_lo[2] = {smem_desc_sw128_lo(smem_u32(sh.q[0]), 16),
+                                  smem_desc_sw128_lo(smem_u32(sh.q[1]), 16)};
+        const uint32_t k_lo = smem_desc_sw128_lo(smem_u32(sh.ring[0][0]), 16);
+        const uint32_t v_lo = smem_desc_sw128_lo(smem_u32(sh.ring[0][0]), kPageHalf);
+        auto commit = [&](uint64_t *bar) {
+            if (elect_one())
+                tc_commit(bar);
+        };
+        // S region h = Q K^T, K in half e of stage b (k-step: 16 columns, 32 bytes of a
+        // 128-byte swizzle row; 64 columns a block)
+        auto issue_s = [&](uint32_t qa, int h, int b, int e) {
+            const uint32_t kb = k_lo + (2 * b + e) * (kPageBytes >> 4);
+            const uint32_t col = tmem + t * 128 + h * 64;
 #pragma unroll
-                for (int ks = 1; ks < kD / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
-                    tc_mma_ss_k<1>(d, desc_join(qa + off, dhi), desc_join(kb + off, dhi), id_s);
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                const uint64_t qd = desc_join(qa + (ks >> 2) * (kQHalf >> 4) + (ks & 3) * 2, dhi);
+                const uint64_t kd = desc_join(kb + (ks >> 2) * (kPageHalf >> 4) + (ks & 3) * 2, dhi);
+                if (elect_one()) {
+                    if (ks == 0)
+                        tc_mma_ss_k<0>(col, qd, kd, id_s);
+                    else
+                        tc_mma_ss_k<1>(col, qd, kd, id_s);
                 }
-                tc_commit(&sh.s_full[t]);
-            };
-            auto issue_pv = [&](int t, int s, bool first) {
-                const uint32_t vb = s ? v_lo[1] : v_lo[0];
-                const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
-                if (first)
-                    tc_mma_ts_k<0>(d, a, desc_join(vb, dhi), id_pv);
-                else
-                    tc_mma_ts_k<1>(d, a, desc_join(vb, dhi), id_pv);
+            }
+            commit(&sh.s_full[t][h]);
+        };
+        // O (+)= P V: P in TMEM over S region h, V (MN-major) in half 0 of stage b (k-step:
+        // 16 keys, 8 columns of bf16 pairs, 16 rows of V)
+        auto issue_pv = [&](int h, int b, bool first) {
+            const uint32_t vb = v_lo + 2 * b * (kPageBytes >> 4);
+            const uint32_t o = tmem + kColO + t * 128, a = tmem + t * 128 + h * 64;
 #pragma unroll
-                for (int ks = 1; ks < kBN / 16; ++ks)
-                    tc_mma_ts_k<1>(d, a + ks * 8, desc_join(vb + ks * (2048 >> 4), dhi), id_pv);
-            };
-            bool ok = true;
-            int kc = 0, sc = 0;              // key tiles, segments so far
-            int np[2] = {0, 0}, ns[2] = {0, 0};  // the same, of each query tile
-            while (ok && next_seg(p, w)) {
-                if (!mbar_wait_sleep(&sh.q_full, sc & 1) ||
-                    !mbar_wait_sleep(&sh.k_full[kc & 1], (kc >> 1) & 1)) {
+            for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+                const uint64_t vd = desc_join(vb + ks * (2048 >> 4), dhi);
+                if (elect_one()) {
+                    if (ks == 0)
+                        tc_mma_ts(o, a, vd, id_pv, first ? 0u : 1u);
+                    else
+                        tc_mma_ts_k<1>(o, a + ks * 8, vd, id_pv);
+                }
+            }
+            commit(&sh.pv_done[t]);
+        };
+        bool ok = true;
+        RingPos rp{0, 0};
+        int sc = 0;  // segments
+        int c = 0;   // pages of this issuer so far: regions alternate
+        int ns = 0;  // segments with a page of this issuer
+        while (ok && next_seg(p, w)) {
+            const bool split = w.split();
+            const int nn = w.n1 - w.n0, ahead = split ? 4 : 2;
+            const uint32_t qa = split || t == 0 ? q_lo[0] : q_lo[1];
+            ok = mbar_wait_sleep(&sh.q_full, sc & 1);
+            ++sc;
+            const int pre = (min(ahead, nn) + 1) >> 1;
+            for (int j = 0; j < pre && ok; ++j) {
+                ok = mbar_wait_sleep(&sh.full[rp.b], rp.ph);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (!split || t == 0)
+                    issue_s(qa, split ? (c + j) & 1 : (c + 2 * j) & 1, rp.b, 0);
+                if (2 * j + 1 < nn && (!split || t == 1))
+                    issue_s(qa, split ? (c + j) & 1 : (c + 2 * j + 1) & 1, rp.b, 1);
+                commit(&sh.empty[rp.b]);  // arrives at once where nothing was issued
+                rp.next();
+            }
+            if (nn <= ahead + (split ? t : 0))
+                commit(&sh.q_empty);  // none of this issuer's scores are left
+            bool first = true;
+            for (int j = 0; j < nn && ok; ++j) {
+                const int b = rp.b;
+                ok = mbar_wait_sleep(&sh.full[b], rp.ph);
+                rp.next();
+                if (!ok)
+                    break;
+                if (split && (j & 1) != t) {  // the other issuer's page
+                    if (lane == 0)
+                        mbar_arrive(&sh.empty[b]);
+                    __syncwarp();
+                    continue;
+                }
+                const int h = c & 1;
+                if (!mbar_wait_sleep(&sh.p_full[t][h], (c >> 1) & 1) ||
+                    (first && !mbar_wait_sleep(&sh.o_empty[t], (ns & 1) ^ 1))) {
                     ok = false;
                     break;
                 }
-                ++sc;
+                ++c;
                 tc_fence_after();
-                if (w.split()) {
-                    // key tile j of the segment in region j % 2: S(j + 2) behind PV(j)
-                    const int nn = w.n1 - w.n0;
-                    issue_s(0, 0, kc & 1);
-                    tc_commit(&sh.k_empty[kc & 1]);
-                    if (nn > 1) {
-                        if (!mbar_wait_sleep(&sh.k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        issue_s(1, 0, (kc + 1) & 1);
-                        tc_commit(&sh.k_empty[(kc + 1) & 1]);
-                    }
-                    if (nn <= 2)
-                        tc_commit(&sh.q_empty);
-                    for (int j = 0; j < nn && ok; j += 2) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (j + t >= nn || !ok)
-                                continue;
-                            const int s = kc & 1;
-                            if (!mbar_wait_sleep(&sh.p_full[t], np[t] & 1) ||
-                                !mbar_wait_sleep(&sh.v_full[s], (kc >> 1) & 1) ||
-                                (j == 0 && !mbar_wait_sleep(&sh.o_empty[t], (ns[t] & 1) ^ 1))) {
-                                ok = false;
-                                continue;
-                            }
-                            ++np[t];
-                            tc_fence_after();
-                            issue_pv(t, s, j == 0);
-                            tc_commit(&sh.v_empty[s]);
-                            if (j + t + 2 < nn) {
-                                if (!mbar_wait_sleep(&sh.k_full[s], ((kc + 2) >> 1) & 1)) {
-                                    ok = false;
-                                    continue;
-                                }
-                                tc_fence_after();
-                                issue_s(t, 0, s);
-                                tc_commit(&sh.k_empty[s]);
-                                if (j + t + 3 == nn)
-                                    tc_commit(&sh.q_empty);  // the segment's last S product
-                            } else {
-                                tc_commit(&sh.o_full[t]);
-                            }
-                            ++kc;
-                        }
-                    }
-                    ++ns[0];
-                    ns[1] += nn > 1;
-                    continue;
-                }
-                issue_s(0, 0, kc & 1);
-                issue_s(1, 1, kc & 1);
-                tc_commit(&sh.k_empty[kc & 1]);
-                if (w.n1 - w.n0 == 1)
-                    tc_commit(&sh.q_empty);
-                for (int n = w.n0; n < w.n1 && ok; ++n, ++kc) {
-                    const int s = kc & 1;
-                    const bool more = n + 1 < w.n1;
-                    if (more && !mbar_wait_sleep(&sh.k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!ok)
-                            continue;
-                        if (!mbar_wait_sleep(&sh.p_full[t], np[t] & 1) ||
-                            (t == 0 && !mbar_wait_sleep(&sh.v_full[s], (kc >> 1) & 1)) ||
-                            (n == w.n0 && !mbar_wait_sleep(&sh.o_empty[t], (ns[t] & 1) ^ 1))) {
-                            ok = false;
-                            continue;
-                        }
-                        ++np[t];
-                        tc_fence_after();
-                        issue_pv(t, s, n == w.n0);
-                        if (more)
-                            issue_s(t, t, (kc + 1) & 1);
-                        else
-                            tc_commit(&sh.o_full[t]);
-                    }
-                    if (!ok)
-                        break;
-                    if (more)
-                        tc_commit(&sh.k_empty[(kc + 1) & 1]);
-                    if (n + 2 == w.n1)
-                        tc_commit(&sh.q_empty);  // the segment's last S products are issued
-                    tc_commit(&sh.v_empty[s]);
-                }
-                ++ns[0];
-                ++ns[1];
+                issue_pv(h, b, first);
+                first = false;
+                if (j + ahead < nn)
+                    issue_s(qa, h, b, 1);
+                commit(&sh.empty[b]);
+                // this issuer's last scores of the segment
+                if (j + ahead < nn && j + ahead + (split ? 2 : 1) >= nn)
+                    commit(&sh.q_empty);
             }
-            if (ok) {
-                // every MMA done before TMEM is released
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (ok && ns[t] > 0)
-                        ok = mbar_wait_sleep(&sh.o_full[t], (ns[t] - 1) & 1);
-            }
-            if (!ok)
-                set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+            ns += first ? 0 : 1;
         }
+        // every product and every arrival done before the CTA lets go of its memory
+        commit(&sh.done[t]);
+        if (ok)
+            ok = mbar_wait_sleep(&sh.done[t], 0);
+        if (!ok && lane == 0)
+            set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
     } else {
         // ================================================================ softmax
-        const int t = (warp - 2) >> 2;  // query tile: 0 = A (warps 2-5), 1 = B (warps 6-9)
+        const int t = (warp - 2) >> 2;  // warpgroup: warps 2-5, warps 6-9
         const int wq = warp & 3;
         const int row = wq * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
-        const uint32_t col_s = t * 128, col_o = kColO + t * 128;
-        int np = 0, ns = 0;  // key tiles and segments of this query tile so far
+        const uint32_t col_o = kColO + t * 128;
+        int c = 0;  // pages of this warpgroup so far
         bool ok = true;
         while (ok && next_seg(p, w)) {
-            const int step = w.split() ? 2 : 1;       // key tiles n0 + first, + step, ...
-            const int first = w.split() ? t : 0;
+            const int step = w.split() ? 2 : 1;
+            const int first = w.n0 + (w.split() ? t : 0);
             const int r = w.pair * 2 * kBM + (w.split() ? 0 : t * kBM) + row;  // of the group and head
             const bool row_ok = r < w.ntok * p.d.G;
             float *const oct = reinterpret_cast<float *>(p.d.ws + p.slot_off) +
                                ((int64_t)blockIdx.x + w.unit) * kSlotFloats +
                                (t * kBM + row) / 8 * kOctFloats;
-            if (w.n0 + first >= w.n1) {  // one key tile, not this warpgroup's
+            if (first >= w.n1) {  // one page, not this warpgroup's
                 if (row_ok) {
                     oct[row & 7] = -INFINITY;
                     oct[8 + (row & 7)] = 0.f;
@@ -527,55 +521,47 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             // a member may hold less than the shared pages
             int hi_row = 0;
             if (row_ok)
-                hi_row = min(w.pages * kTileKeys,
-                             clamp_len(__ldg(p.d.cached_len + w.seq0 + r / p.d.G / p.d.T)));
+                hi_row = clamp_len(__ldg(p.d.cached_len + w.seq0 + r / p.d.G / p.d.T));
             float m_used = -INFINITY, l = 0.f;
-            auto page_bits = [&](int n) -> int {
-                int blk, bits = 0;
-                if (2 * n < w.pages && page_ok(p, w.seq0, 2 * n, &blk))
-                    bits |= 1;
-                if (2 * n + 1 < w.pages && page_ok(p, w.seq0, 2 * n + 1, &blk))
-                    bits |= 2;
-                return bits;
-            };
-            int bits = page_bits(w.n0 + first);
-            for (int n = w.n0 + first; n < w.n1; n += step, ++np) {
-                const int next_bits = n + step < w.n1 ? page_bits(n + step) : 0;
-                if (!mbar_wait_sleep(&sh.s_full[t], np & 1)) {
-                    set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+            const int32_t *const table = p.d.block_tables + (int64_t)w.seq0 * p.d.max_blocks;
+            int entry = __ldg(table + first);
+            for (int n = first; n < w.n1; n += step, ++c) {
+                const int next_entry = n + step < w.n1 ? __ldg(table + n + step) : 0;
+                const int h = c & 1;
+                const uint32_t col_s = t * 128 + h * 64;
+                if (!mbar_wait_sleep(&sh.s_full[t][h], (c >> 1) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int hi = min(kBN, hi_row - n * kBN);
-                const bool whole_tile = hi == kBN && bits == 3;
-                // ---- the row's 128 scores: one TMEM read, kept in registers --------
-                uint32_t r32[4][32];
-#pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4)
-                    tmem_ld32(lane_addr + col_s + c4 * 32, r32[c4]);
+                const int hi = entry >= 0 && entry < p.d.num_blocks ? hi_row - n * kTileKeys : 0;
+                const bool whole = hi >= kTileKeys;
+                // ---- the row's 64 scores: one TMEM read, kept in registers ----------
+                uint32_t r32[2][32];
+                tmem_ld32(lane_addr + col_s, r32[0]);
+                tmem_ld32(lane_addr + col_s + 32, r32[1]);
                 tmem_wait_ld();
-                if (!whole_tile) {
+                if (!whole) {
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4)
+                    for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c4 * 32 + c >= hi || !(bits & (c4 < 2 ? 1 : 2)))
-                                r32[c4][c] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < 32; ++i)
+                            if (c2 * 32 + i >= hi)
+                                r32[c2][i] = __float_as_uint(-INFINITY);
                 }
-                // ---- row max (three-input max, four chains) -----------------------
+                // ---- row max (three-input max, four chains) ---------------------------
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4)
+                for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        m4[0] = fmax3(m4[0], __uint_as_float(r32[c4][c + 0]), __uint_as_float(r32[c4][c + 1]));
-                        m4[1] = fmax3(m4[1], __uint_as_float(r32[c4][c + 2]), __uint_as_float(r32[c4][c + 3]));
-                        m4[2] = fmax3(m4[2], __uint_as_float(r32[c4][c + 4]), __uint_as_float(r32[c4][c + 5]));
-                        m4[3] = fmax3(m4[3], __uint_as_float(r32[c4][c + 6]), __uint_as_float(r32[c4][c + 7]));
+                    for (int i = 0; i < 32; i += 8) {
+                        m4[0] = fmax3(m4[0], __uint_as_float(r32[c2][i + 0]), __uint_as_float(r32[c2][i + 1]));
+                        m4[1] = fmax3(m4[1], __uint_as_float(r32[c2][i + 2]), __uint_as_float(r32[c2][i + 3]));
+                        m4[2] = fmax3(m4[2], __uint_as_float(r32[c2][i + 4]), __uint_as_float(r32[c2][i + 5]));
+                        m4[3] = fmax3(m4[3], __uint_as_float(r32[c2][i + 6]), __uint_as_float(r32[c2][i + 7]));
                     }
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.d.scale_log2;
-                // ---- running max, raised only when it grows by more than 2^8 -------
+                // ---- running max, raised only when it grows by more than 2^8 -----------
                 float m_new = m_used;
                 if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleSlack))
                     m_new = mx;
@@ -583,43 +569,49 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 const float alpha = resc ? fast_exp2(m_used - m_new) : 1.0f;
                 m_used = m_new;
                 const float base = m_used == -INFINITY ? 0.f : m_used;
-                // ---- P = 2^(s scale log2e - m) as bf16 pairs over S -----------------
-                // whole tiles: the row sum takes the unrounded P (128 keys: bf16's
+                // ---- P = 2^(s scale log2e - m) as bf16 pairs over S ---------------------
+                // whole pages: the row sum takes the unrounded P (64 keys: bf16's
                 // rounding averages out); partial ones the rounded P that PV multiplies
                 const uint64_t sc2 = f2_make(p.d.scale_log2, p.d.scale_log2);
                 const uint64_t nb2 = f2_make(-base, -base);
                 uint64_t acc2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
                 float accr = 0.f;
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
+                for (int c2 = 0; c2 < 2; ++c2) {
                     uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const uint64_t x2 = f2_fma(f2_make(__uint_as_float(r32[c4][2 * c]),
-                                                           __uint_as_float(r32[c4][2 * c + 1])),
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t x2 = f2_fma(f2_make(__uint_as_float(r32[c2][2 * i]),
+                                                           __uint_as_float(r32[c2][2 * i + 1])),
                                                    sc2, nb2);
                         float x0, x1;
                         f2_split(x2, x0, x1);
                         const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        pk[c] = pack_bf16(p0, p1);
-                        if (whole_tile)
-                            acc2[c & 1] = f2_add(acc2[c & 1], f2_make(p0, p1));
+                        pk[i] = pack_bf16(p0, p1);
+                        if (whole)
+                            acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
                         else
-                            accr += bf16_lo(pk[c]) + bf16_hi(pk[c]);
+                            accr += bf16_lo(pk[i]) + bf16_hi(pk[i]);
                     }
-                    tmem_st16(lane_addr + col_s + c4 * 16, pk);
+                    tmem_st16(lane_addr + col_s + c2 * 16, pk);
                 }
-                // O (read by PV of this tile, which waits for this warp) is rescaled once
-                // the score registers are free; the segment's first PV overwrites it
+                // The previous page's PV is done before O is rescaled (and is waited for at
+                // every page: a parity wait must see every phase).  The segment's first PV
+                // overwrites O, so its first page rescales nothing.
+                if (c > 0 && !mbar_wait_sleep(&sh.pv_done[t], (c - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
                 if (__any_sync(0xffffffffu, resc)) {
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c4 = 0; c4 < 4; ++c4) {
                         uint32_t o32[32];
                         tmem_ld32(lane_addr + col_o + c4 * 32, o32);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            o32[c] = __float_as_uint(__uint_as_float(o32[c]) * alpha);
+                        for (int i = 0; i < 32; ++i)
+                            o32[i] = __float_as_uint(__uint_as_float(o32[i]) * alpha);
                         tmem_st32(lane_addr + col_o + c4 * 32, o32);
                     }
                 }
@@ -630,18 +622,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sh.p_full[t]);
-                bits = next_bits;
+                mbar_arrive(&sh.p_full[t][h]);
+                entry = next_entry;
             }
-            if (!ok)
-                break;
             // ---- the segment's state -----------------------------------------------
-            if (!mbar_wait_sleep(&sh.o_full[t], ns & 1)) {
-                set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
+            if (!ok || !mbar_wait_sleep(&sh.pv_done[t], (c - 1) & 1)) {
                 ok = false;
                 break;
             }
-            ++ns;
             tc_fence_after();
             float4 *const dst = reinterpret_cast<float4 *>(oct + 16) + (row & 7);
             if (row_ok) {
@@ -655,15 +643,17 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 tmem_wait_ld();
                 if (row_ok) {
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4)
-                        dst[(c4 * 8 + c / 4) * 8] =
-                            make_float4(__uint_as_float(o32[c]), __uint_as_float(o32[c + 1]),
-                                        __uint_as_float(o32[c + 2]), __uint_as_float(o32[c + 3]));
+                    for (int i = 0; i < 32; i += 4)
+                        dst[(c4 * 8 + i / 4) * 8] =
+                            make_float4(__uint_as_float(o32[i]), __uint_as_float(o32[i + 1]),
+                                        __uint_as_float(o32[i + 2]), __uint_as_float(o32[i + 3]));
                 }
             }
             tc_fence_before();
             mbar_arrive(&sh.o_empty[t]);
         }
+        if (!ok)
+            set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
     }
 
     tc_fence_before();
@@ -836,7 +826,7 @@ __global__ void __launch_bounds__(kGroups *MT * 32, 1)
     const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
     // streams 0 .. gridDim - 1 on different CTAs: few items still use every SM
     const int64_t stream = (int64_t)grp * gridDim.x + blockIdx.x;
-    const int64_t i0 = min(N, stream * N / C), i1 = min(N, (stream + 1) * N / C);
+    const int64_t i0 = min(N, cut(stream, N, C)), i1 = min(N, cut(stream + 1, N, C));
     {
         OwnPlan *const plan = reinterpret_cast<OwnPlan *>(d.ws + p.own_plan_off);
         int before = sh.scan[tid];
@@ -844,7 +834,7 @@ __global__ void __launch_bounds__(kGroups *MT * 32, 1)
             const int n = own_items(p, b < kInfoCap ? sh.info[b].x : own_info(p, share, b).x);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
-                const int64_t at = min(N, ((int64_t)i * gridDim.x + blockIdx.x) * N / C);
+                const int64_t at = min(N, cut((int64_t)i * gridDim.x + blockIdx.x, N, C));
                 if ((int64_t)(before + n) * d.Hkv > at && (int64_t)before * d.Hkv <= at) {
                     sh.first_b[i] = b;
                     sh.first_before[i] = before;
@@ -869,8 +859,8 @@ __global__ void __launch_bounds__(kGroups *MT * 32, 1)
     own_load(p, sh, w);
     {
         const int64_t off = i0 - (int64_t)sh.first_before[grp] * d.Hkv;
-        w.h = (int)(off / w.n);
-        w.j = (int)(off % w.n);
+        w.h = (int)div_pos(off, w.n);
+        w.j = (int)(off - (int64_t)w.h * w.n);
     }
 
     // ---- loads: item li of the stream, kDepth items ahead of the products ------------
@@ -1113,24 +1103,24 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
         const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : (int)(oN / d.Hkv);
         const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
         const int64_t item0 = __ldcg(&gp->item0);
-        const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), kt = __ldcg(&gp->kt);
+        const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
         // the sequence's own states: streams c_lo .. c_hi of pass 2
         {
             const int n = next - before;
             const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
-            const int64_t c_lo = ((s0 + 1) * oC - 1) / oN, c_hi = ((s0 + n) * oC - 1) / oN;
+            const int64_t c_lo = div_pos((s0 + 1) * oC - 1, oN), c_hi = div_pos((s0 + n) * oC - 1, oN);
             const int step = own_slot_floats(RT), pad = own_pad(RT);
             const float *s = reinterpret_cast<const float *>(d.ws + p.own_off) +
                              (c_lo + b * d.Hkv + h) * step;
             take(s + rr, pad, 2 * pad - rr + rr * kD + 4 * d4, step, (int)(c_hi - c_lo) + 1);
         }
         // the shared segments' states
-        if (N > 0 && kt > 0) {
+        if (N > 0 && pages > 0) {
             const int64_t rg = r - (int64_t)seq0 * RT;  // row of the group
             const int pair = (int)(rg / (2 * kBM)), row = (int)(rg % (2 * kBM));
             const int un = h * pairs + pair;
-            const int64_t s0 = item0 + (int64_t)un * kt;
-            const int64_t c_lo = ((s0 + 1) * C - 1) / N, c_hi = ((s0 + kt) * C - 1) / N;
+            const int64_t s0 = item0 + (int64_t)un * pages;
+            const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s0 + pages) * C - 1, N);
             const float *s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
                              (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + (row & 7);
             const int n = (int)(c_hi - c_lo) + 1;

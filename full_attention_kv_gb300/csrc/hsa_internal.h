@@ -60,9 +60,9 @@ cudaError_t launch_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
 // Decode over shared prefixes (decode_shared.cu): what its three passes leave one another
 // in the workspace.
 struct SharedGroup {
-    int64_t item0;               // first key tile of the group in pass 1's item space
+    int64_t item0;               // first item (page) of the group in pass 1's item space
     int32_t unit0;               // units of the groups before it
-    int32_t pairs, kt;           // 256-row units a KV head; 128-key tiles a unit
+    int32_t pairs, pages;        // 256-row units a KV head; shared pages (items a unit)
 };
 struct SharedPlan {
     int64_t N, C;                // pass 1's items, and the CTAs they were cut over

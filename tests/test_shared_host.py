@@ -70,7 +70,7 @@ def test_shared_binding_checks(fake):
 
 @pytest.mark.parametrize("seed", range(40))
 def test_segments_cover_the_items_and_slots_are_their_own(seed):
-    """Pass 1's split: every (unit, key tile) in exactly one segment; a segment's slot, CTA +
+    """Pass 1's split: every (unit, page) in exactly one segment; a segment's slot, CTA +
     unit, is its own and inside the workspace's count; and the range of CTAs that pass 2
     computes for a unit is the one that wrote it."""
     rng = random.Random(seed)
@@ -81,7 +81,7 @@ def test_segments_cover_the_items_and_slots_are_their_own(seed):
     B = sum(members)
     groups, item0, unit0 = [], 0, 0
     for m, pg in zip(members, pages):
-        kt = (pg + 1) // 2
+        kt = pg
         pairs = (m * T * G + 255) // 256 if kt else 0
         groups.append((item0, unit0, pairs, kt))
         item0 += pairs * Hkv * kt
