@@ -9,18 +9,17 @@
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m) / l,
 // so the shared pages and each sequence's own pages are separate passes.
 //
-// Pass 1, shared_kernel (tcgen05): the query rows of a group for one KV head -- members x T
+// attend_kernel, part 1 (tcgen05): the query rows of a group for one KV head -- members x T
 // tokens x G heads -- are packed into 128-row tiles, a pair of tiles (256 rows) a unit, and
 // meet the shared keys page by page as a dense product: K and V are read once a unit
 // instead of once a sequence.  The pages of all units are laid end to end and cut into
 // equal ranges, one per CTA; each (CTA, unit) segment leaves unnormalised fp32 states.
-// Pass 2, own_kernel (mma.sync, 8 to 32 rows a sequence and head): a stream-K walk over the
-// pages past the shared ones and the new tokens; each segment leaves its state.
-// Pass 3, merge_kernel: a thread for four output dimensions of a row merges the row's
-// states and writes bf16; it also appends the new rows.
-//
-// The passes overlap by programmatic dependent launch: pass 2 reads nothing of pass 1, and
-// its CTAs start as pass 1's leave their SMs; pass 3 is resident before pass 2 ends.
+// Part 2 (mma.sync, 8 to 32 rows a sequence and head): a stream-K walk over the pages past
+// the shared ones and the new tokens; each segment leaves its state.  The parts were two
+// kernels first; between them an SM stood idle for about 9 us (part 1's states, 133 KB a CTA,
+// drain before a CTA's place is free, then part 2's launch and plan).  In one kernel part 2's
+// plan is made by a spare warp during part 1, and its first loads pass the draining states.
+// merge_kernel: merges each row's states and writes bf16; it also appends the new rows.
 #include "decode_tile.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
@@ -28,7 +27,7 @@
 namespace hsa {
 namespace {
 
-// ------------------------------------------------------------------ groups, both passes
+// ------------------------------------------------------------------ groups
 
 // A group's shared whole pages, or 0 (nothing is shared).
 __device__ __forceinline__ int group_pages(const SharedParams &p, int g)
@@ -66,7 +65,7 @@ __device__ __forceinline__ int group_of(const SharedParams &p, int b)
 
 __device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
 
-// ------------------------------------------------------------------ pass 1: shared pages
+// ------------------------------------------------------------------ part 1: shared pages
 //
 // A step is one 64-key page.  Each query tile has two 64-column S regions in TMEM, so that
 // the next page's scores are there when the softmax warps finish a page.
@@ -84,7 +83,7 @@ constexpr int kQHalf = kQBytes / 2;
 constexpr int kPageBytes = kTileKeys * kD * 2;  // 16 KB: two blocks of 64 rows x 64 columns
 constexpr int kPageHalf = kPageBytes / 2;
 constexpr int kRing = 5;
-constexpr int kSharedThreads = 352;         // producer, issuers 1 and 10, softmax warps 2 .. 9
+constexpr int kAttendThreads = 384;         // producer 0, issuers 1 and 10, softmax 2 .. 9, plan 11
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;             // S: tile t, region h at 128 t + 64 h; O_t at 256 + 128 t
 // A segment's states, by octets of rows: m[8], l[8], then o as [dim / 4][8 rows][4], so
@@ -93,17 +92,6 @@ constexpr uint32_t kColO = 256;             // S: tile t, region h at 128 t + 64
 constexpr int kOctFloats = 16 + 8 * kD;
 constexpr int kSlotFloats = 2 * kBM / 8 * kOctFloats;
 
-struct SharedSmem {
-    alignas(1024) uint8_t q[2][kQBytes];
-    alignas(1024) uint8_t ring[kRing][2][kPageBytes];
-    alignas(8) uint64_t q_full, q_empty;
-    uint64_t full[kRing], empty[kRing];
-    uint64_t s_full[2][2], p_full[2][2];    // [query tile][region]
-    uint64_t pv_done[2], o_empty[2], done[2];
-    uint32_t tmem_base;
-    int32_t g0, unit0;
-    int64_t item0, N;
-};
 
 // a / b of non-negative numbers that mostly fit 32 bits
 __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
@@ -170,6 +158,382 @@ __device__ __forceinline__ bool page_ok(const SharedParams &p, int seq, int page
     return true;
 }
 
+// ------------------------------------------------------ part 2: own pages and new tokens
+//
+// What a sequence holds past the shared pages is often short (a question on a document), so
+// the work is cut over many small streams instead of CTAs: four groups of MT warps a CTA,
+// each with a range of 32-key items, a ring of stages and softmax states of its own, which
+// loads its own tiles (lane 0, one item's stage refilled as it is done with) and writes its
+// own state at the end of a (sequence, head) unit.  No barrier joins the groups, so one
+// group's start and end of a unit hides under the others' tiles.  The T new tokens are the
+// unit's last keys: their rows are written into the staged tile that they fall in.
+
+constexpr int kKT = 32;                         // keys an item: half a page
+constexpr int kGroups = 4;
+constexpr int kDepth = 3;                       // stages a group
+constexpr int kHalfTile = kKT * kD * 2;         // 8 KB: K or V of an item
+constexpr int kItemBytes = 2 * kHalfTile;
+// A unit counts kUnitCost items more than it has keys for: starting and leaving one (query
+// rows, new rows, state) takes a group about as long, and without it the streams that cross
+// many short units ended last (a batch of 1 .. 1024 own tokens: 28 us the median stream, 46
+// the last).  Those items, the unit's first, do nothing.
+constexpr int kUnitCost = 2;
+constexpr int kInfoCap = 128;                   // sequences whose lengths are kept in shared memory
+
+struct OwnSmem {
+    alignas(8) uint64_t full[kGroups][kDepth];
+    alignas(8) uint64_t empty[kGroups][kDepth];  // MT = 2: the second warp is done with it
+    int32_t ok[kGroups][kDepth];                 // the item's cached keys were loaded
+    int2 info[kInfoCap];                         // (c, fp) of a sequence
+    int32_t first_b[kGroups], first_before[kGroups];
+    int32_t total_items, share;
+};
+
+// Position in a stream: sequence b, head h, item j of n; c cached tokens past the first
+// page `fp` that is the sequence's own.
+struct OwnWalk {
+    int b, h, j, n, c, fp;
+    __device__ __forceinline__ int key0() const { return (j - kUnitCost) * kKT; }  // < 0: no keys
+};
+
+// c and fp of sequence b, from the inputs.
+__device__ __forceinline__ int2 own_info(const SharedParams &p, bool share, int b)
+{
+    const int fp = share ? group_pages(p, group_of(p, b)) : 0;
+    return make_int2(max(0, clamp_len(__ldg(p.d.cached_len + b)) - fp * kTileKeys), fp);
+}
+
+__device__ __forceinline__ int own_items(const SharedParams &p, int c)
+{
+    return kUnitCost + (c + p.d.T + kKT - 1) / kKT;
+}
+
+__device__ __forceinline__ void own_load(const SharedParams &p, const OwnSmem &sh, OwnWalk &w)
+{
+    const int2 v = w.b < kInfoCap ? sh.info[w.b] : own_info(p, sh.share != 0, w.b);
+    w.c = v.x;
+    w.fp = v.y;
+    w.n = own_items(p, w.c);
+}
+
+__device__ __forceinline__ void own_next(const SharedParams &p, const OwnSmem &sh, OwnWalk &w)
+{
+    if (++w.j == w.n) {
+        w.j = 0;
+        if (++w.h == p.d.Hkv) {
+            w.h = 0;
+            ++w.b;
+            if (w.b < p.d.B)
+                own_load(p, sh, w);
+        }
+    }
+}
+
+// Block-table entry of item w (-1: past the table); only read where it has cached keys.
+__device__ __forceinline__ int own_entry(const SharedParams &p, const OwnWalk &w)
+{
+    const int k0 = w.key0(), page = w.fp + k0 / kTileKeys;
+    if (k0 < 0 || k0 >= w.c || page >= p.d.max_blocks)
+        return -1;
+    return __ldg(p.d.block_tables + (int64_t)w.b * p.d.max_blocks + page);
+}
+
+// Floats of an own segment's state: m[R], l[R], o[R][128] for R = G T rows, m and l padded
+// to 16 bytes.
+__host__ __device__ inline int own_pad(int rows) { return (rows + 3) & ~3; }
+__host__ __device__ inline int own_slot_floats(int rows) { return 2 * own_pad(rows) + rows * kD; }
+
+// Part 2's plan, by one warp: the items before each sequence, and where this CTA's streams
+// begin.
+__device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int lane)
+{
+    const DecodeParams &d = p.d;
+    const bool share = groups_ok(p, lane);
+    OwnPlan *const plan = reinterpret_cast<OwnPlan *>(d.ws + p.own_plan_off);
+    int total = 0;
+    for (int base = 0; base < d.B; base += 32) {
+        const int b = base + lane;
+        int n = 0;
+        if (b < d.B) {
+            const int2 v = own_info(p, share, b);
+            if (b < kInfoCap)
+                sh.info[b] = v;
+            n = own_items(p, v.x);
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += u;
+        }
+        if (blockIdx.x == 0 && b < d.B)  // for the merge
+            plan->before[b] = total + incl - n;
+        total += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int64_t N = (int64_t)total * d.Hkv;
+    const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
+    if (lane == 0) {
+        sh.share = share;
+        sh.total_items = total;
+        if (blockIdx.x == 0) {
+            plan->N = N;
+            plan->C = C;
+        }
+    }
+    // second walk: the sequences that hold the first items of this CTA's streams
+    int64_t at[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+        at[i] = min(N, cut((int64_t)i * gridDim.x + blockIdx.x, N, C));
+    __syncwarp();
+    int before = 0;
+    for (int base = 0; base < d.B; base += 32) {
+        const int b = base + lane;
+        int n = 0;
+        if (b < d.B)
+            n = own_items(p, b < kInfoCap ? sh.info[b].x : own_info(p, share, b).x);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += u;
+        }
+        const int lo = before + incl - n;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+            if (n > 0 && (int64_t)lo * d.Hkv <= at[i] && (int64_t)(lo + n) * d.Hkv > at[i]) {
+                sh.first_b[i] = b;
+                sh.first_before[i] = lo;
+            }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// The streams of this CTA: group grp, warp mt of its MT.
+template <int MT>
+__device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                        const SharedParams &p, OwnSmem &sh,
+                                        uint8_t (*stages)[kDepth][kItemBytes], int grp, int mt,
+                                        int lane)
+{
+    const DecodeParams &d = p.d;
+    const int64_t N = (int64_t)sh.total_items * d.Hkv;
+    const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
+    // streams 0 .. gridDim - 1 on different CTAs: few items still use every SM
+    const int64_t stream = (int64_t)grp * gridDim.x + blockIdx.x;
+    const int64_t i0 = min(N, cut(stream, N, C)), i1 = min(N, cut(stream + 1, N, C));
+    if (i0 >= i1)
+        return;
+    OwnWalk w;
+    w.b = sh.first_b[grp];
+    own_load(p, sh, w);
+    {
+        const int64_t off = i0 - (int64_t)sh.first_before[grp] * d.Hkv;
+        w.h = (int)div_pos(off, w.n);
+        w.j = (int)(off - (int64_t)w.h * w.n);
+    }
+
+    // ---- loads: item li of the stream, kDepth items ahead of the products ------------
+    const uint64_t pol = policy_evict_first();
+    OwnWalk lw = w;
+    int64_t li = i0;
+    int lst = 0;
+    uint32_t lph = 0;  // parity of the stage's next empty phase (MT = 2)
+    auto skip = [&] {  // to an item with keys
+        while (li < i1 && lw.key0() < 0) {
+            ++li;
+            if (li < i1)
+                own_next(p, sh, lw);
+        }
+    };
+    skip();
+    int entry = li < i1 ? own_entry(p, lw) : -1;
+    bool timed_out = false;
+    auto load = [&](bool refill) {  // the group's first warp
+        if (li >= i1)
+            return;
+        if (MT == 2 && refill && !timed_out && !mbar_wait(&sh.empty[grp][lst], lph)) {
+            set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+            timed_out = true;
+        }
+        if (lane == 0) {
+            const int k0 = lw.key0();
+            bool ok = k0 < lw.c && !timed_out;
+            if (ok && (entry < 0 || entry >= d.num_blocks)) {
+                set_err(d.dev_err, lw.fp + k0 / kTileKeys >= d.max_blocks ? HSA_DEVERR_BAD_PAGE
+                                                                         : HSA_DEVERR_BAD_BLOCK);
+                ok = false;
+            }
+            uint64_t *const full = &sh.full[grp][lst];
+            sh.ok[grp][lst] = ok;
+            if (ok) {
+                uint8_t *const dst = stages[grp][lst];
+                const int32_t r = (entry * d.Hkv + lw.h) * kTileKeys + k0 % kTileKeys;
+                mbar_arrive_expect_tx(full, kItemBytes);
+                tma_load_2d(dst, &tmK, full, 0, r, pol);
+                tma_load_2d(dst + kHalfTile / 2, &tmK, full, 64, r, pol);
+                tma_load_2d(dst + kHalfTile, &tmV, full, 0, r, pol);
+                tma_load_2d(dst + kHalfTile + kHalfTile / 2, &tmV, full, 64, r, pol);
+            } else {
+                mbar_arrive(full);
+            }
+        }
+        __syncwarp();
+        ++li;
+        if (li < i1) {
+            own_next(p, sh, lw);
+            skip();
+            if (li < i1)
+                entry = own_entry(p, lw);  // used at the next load
+        }
+        if (++lst == kDepth) {
+            lst = 0;
+            lph ^= refill ? 1 : 0;
+        }
+    };
+    if (mt == 0)
+        for (int i = 0; i < kDepth; ++i)
+            load(false);
+
+    // ---- products ---------------------------------------------------------------------
+    const int g = lane >> 2, tq = lane & 3;
+    const int q_r0 = mt * 16 + g, q_r1 = q_r0 + 8;
+    const int t0 = q_r0 / d.G, t1 = q_r1 / d.G;
+    const bool v0 = t0 < d.T, v1 = t1 < d.T;
+    const int Hq = d.G * d.Hkv, rows = d.G * d.T;
+    RowState st;
+    uint32_t qa[kD / 16][4];
+    int stg = 0;
+    uint32_t ph = 0;
+    const int pad = own_pad(rows);
+    bool fresh = true;
+    for (int64_t i = i0; i < i1; ++i) {
+        if (w.key0() < 0) {
+            if (i == i1 - 1 && lane < 16 && mt * 16 + lane < rows) {  // the share holds no keys
+                float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
+                                    (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
+                part[mt * 16 + lane] = -INFINITY;
+                part[pad + mt * 16 + lane] = 0.f;
+            }
+            own_next(p, sh, w);
+            continue;
+        }
+        if (fresh) {
+            fresh = false;
+            st.m[0] = st.m[1] = -INFINITY;
+            st.l[0] = st.l[1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < kD / 8; ++n)
+                st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
+            const __nv_bfloat16 *q0 =
+                d.q + ((int64_t)(w.b * d.T + t0) * Hq + w.h * d.G + q_r0 % d.G) * kD;
+            const __nv_bfloat16 *q1 =
+                d.q + ((int64_t)(w.b * d.T + t1) * Hq + w.h * d.G + q_r1 % d.G) * kD;
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                const int c0 = ks * 16 + 2 * tq;
+                qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
+                qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
+                qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
+                qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
+            }
+        }
+        if (!timed_out && !mbar_wait(&sh.full[grp][stg], ph)) {
+            set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
+            timed_out = true;
+        }
+        uint8_t *const base = stages[grp][stg];
+        // keys 0 .. cached - 1 of the item are cached ones, key news + t is new token t
+        const int news = w.c - w.key0();
+        const int cached = !timed_out && sh.ok[grp][stg] ? min(kKT, news) : 0;
+        if (cached < kKT) {
+            // the new tokens' rows; V rows of no key may hold anything, and 0 x NaN is NaN:
+            // they become 0 (their scores are masked).  Both warps of a pair write the same.
+            for (int e = lane; e < (kKT - cached) * (kD / 8); e += 32) {
+                const int key = cached + e / (kD / 8), col = (e % (kD / 8)) * 8, t = key - news;
+                uint4 vv = make_uint4(0, 0, 0, 0);
+                uint8_t *const at = base + swz128_offset(key, col, kKT);
+                if (t >= 0 && t < d.T) {
+                    const int64_t src = ((int64_t)(w.b * d.T + t) * d.Hkv + w.h) * kD + col;
+                    vv = __ldg(reinterpret_cast<const uint4 *>(d.v_new + src));
+                    *reinterpret_cast<uint4 *>(at) = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
+                }
+                *reinterpret_cast<uint4 *>(at + kHalfTile) = vv;
+            }
+            fence_proxy_async_smem();  // before the stage's next TMA write
+            __syncwarp();
+        }
+        {
+            const int T = d.T;
+            auto vis = [&](int rr, int key) -> bool {
+                const int t = rr == g ? t0 : t1;
+                return t < T && (key < cached || (key >= news && key - news <= t));
+            };
+            const uint32_t sK = smem_u32(base);
+            run_tile<kKT / 8>(st, qa, sK, sK + kHalfTile, kKT, 0, d.scale_log2, cached == kKT, v0, v1, vis);
+        }
+        __syncwarp();
+        if (MT == 2 && mt == 1 && lane == 0)
+            mbar_arrive(&sh.empty[grp][stg]);
+        if (mt == 0)
+            load(true);
+        if (++stg == kDepth) {
+            stg = 0;
+            ph ^= 1;
+        }
+        const bool last = w.j == w.n - 1 || i == i1 - 1;
+        if (last) {
+            // ---- the segment's state, from the registers ------------------------------
+            fresh = true;
+            float l0 = st.l[0], l1 = st.l[1];
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+            float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
+                                (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
+            if (tq == 0) {
+                if (v0) {
+                    part[q_r0] = st.m[0];
+                    part[pad + q_r0] = l0;
+                }
+                if (v1) {
+                    part[q_r1] = st.m[1];
+                    part[pad + q_r1] = l1;
+                }
+            }
+            float *const o0 = part + 2 * pad + q_r0 * kD + 2 * tq;
+#pragma unroll
+            for (int n = 0; n < kD / 8; ++n) {
+                if (v0)
+                    *reinterpret_cast<float2 *>(o0 + n * 8) = make_float2(st.o[n][0], st.o[n][1]);
+                if (v1)
+                    *reinterpret_cast<float2 *>(o0 + 8 * kD + n * 8) =
+                        make_float2(st.o[n][2], st.o[n][3]);
+            }
+        }
+        own_next(p, sh, w);
+    }
+}
+
+struct AttendSmem {
+    // part 2's stages lie over these
+    alignas(1024) uint8_t q[2][kQBytes];
+    alignas(1024) uint8_t ring[kRing][2][kPageBytes];
+    alignas(8) uint64_t q_full, q_empty;
+    uint64_t full[kRing], empty[kRing];
+    uint64_t s_full[2][2], p_full[2][2];    // [query tile][region]
+    uint64_t pv_done[2], o_empty[2], done[2];
+    uint32_t tmem_base;
+    int32_t g0, unit0;
+    int64_t item0, N;
+    OwnSmem own;
+};
+static_assert(kGroups * kDepth * kItemBytes <= 2 * kQBytes + 2 * kRing * kPageBytes, "part 2's stages");
+static_assert(sizeof(AttendSmem) + 1024 <= 232448, "shared memory");
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -192,12 +556,15 @@ struct RingPos {
     }
 };
 
-__global__ void __launch_bounds__(kSharedThreads, 1)
-    shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ SharedParams p)
+// MT: 16-row m-tiles of a sequence's G T query rows (1 or 2), a warp each in part 2.
+template <int MT>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK32,
+                  const __grid_constant__ CUtensorMap tmV32, const __grid_constant__ SharedParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    SharedSmem &sh = *reinterpret_cast<SharedSmem *>(align_smem_1024(smem_raw));
+    AttendSmem &sh = *reinterpret_cast<AttendSmem *>(align_smem_1024(smem_raw));
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
 
@@ -217,12 +584,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             mbar_init(&sh.o_empty[t], 4 * 32);
             mbar_init(&sh.done[t], 1);
         }
+        for (int i = 0; i < kGroups; ++i)
+            for (int s = 0; s < kDepth; ++s) {
+                mbar_init(&sh.own.full[i][s], 1);
+                mbar_init(&sh.own.empty[i][s], 1);
+            }
         fence_barrier_init();
     }
     if (tid == 64) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmK32);
+        tma_prefetch_desc(&tmV32);
     }
     if (warp == 1) {
         __syncwarp();
@@ -298,21 +672,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     tc_fence_after();
     const int64_t N = sh.N;
     const int64_t C = min(N, (int64_t)gridDim.x);
-    if ((int64_t)blockIdx.x >= C) {
-        if (warp == 1)
-            tmem_dealloc(sh.tmem_base, kTmemCols);
-        return;
-    }
     SegWalk w{};
-    w.it = cut(blockIdx.x, N, C);
-    w.i1 = cut((int64_t)blockIdx.x + 1, N, C);
-    w.item0 = sh.item0;
-    w.g = sh.g0;
-    w.unit0 = sh.unit0;
-    load_group(p, w);
+    if ((int64_t)blockIdx.x < C) {  // else no segments
+        w.it = cut(blockIdx.x, N, C);
+        w.i1 = cut((int64_t)blockIdx.x + 1, N, C);
+        w.item0 = sh.item0;
+        w.g = sh.g0;
+        w.unit0 = sh.unit0;
+        load_group(p, w);
+    }
     const uint32_t tmem = sh.tmem_base;
 
-    if (warp == 0) {
+    if (warp == 11) {
+        own_plan(p, sh.own, lane);
+    } else if (warp == 0) {
         // ================================================================ producer
         if (lane == 0) {
             const uint64_t pol_first = policy_evict_first(), pol_keep = policy_evict_last();
@@ -656,416 +1029,110 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
     }
 
+    // ---- part 2: every read of part 1's shared memory and TMEM is done ------------------
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    const int ow = warp - 2;  // warps 2 .. 5 or 2 .. 9
+    if (ow >= 0 && ow < kGroups * MT)
+        own_run<MT>(tmK32, tmV32, p, sh.own,
+                    reinterpret_cast<uint8_t(*)[kDepth][kItemBytes]>(&sh.q[0][0]), ow / MT, ow % MT,
+                    lane);
 }
 
-// ------------------------------------------------------ pass 2: own pages and new tokens
-//
-// What a sequence holds past the shared pages is often short (a question on a document), so
-// the work is cut over many small streams instead of CTAs: four groups of MT warps a CTA,
-// each with a range of 32-key items, a ring of stages and softmax states of its own, which
-// loads its own tiles (lane 0, one item's stage refilled as it is done with) and writes its
-// own state at the end of a (sequence, head) unit.  No barrier joins the groups, so one
-// group's start and end of a unit hides under the others' tiles.  The T new tokens are the
-// unit's last keys: their rows are written into the staged tile that they fall in.
+// ------------------------------------------------------------------------ merge, append
 
-constexpr int kKT = 32;                         // keys an item: half a page
-constexpr int kGroups = 4;
-constexpr int kDepth = 3;                       // stages a group
-constexpr int kHalfTile = kKT * kD * 2;         // 8 KB: K or V of an item
-constexpr int kItemBytes = 2 * kHalfTile;
-constexpr int kInfoCap = 1024;                  // sequences whose lengths are kept in shared memory
-constexpr int kOwnMaxThreads = kGroups * 2 * 32;
+constexpr int kMergeParts = 2;                       // threads that share a row's states
+constexpr int kMergeThreads = kMergeParts * 8 * 32;  // x eight rows x 32 pieces of four dimensions
+constexpr int kMergeBatch = 8;                       // states whose loads are in flight together
 
-struct OwnSmem {
-    alignas(1024) uint8_t stage[kGroups][kDepth][kItemBytes];  // [K lo|K hi|V lo|V hi]
-    alignas(8) uint64_t full[kGroups][kDepth];
-    alignas(8) uint64_t empty[kGroups][kDepth];  // MT = 2: the second warp is done with it
-    int32_t ok[kGroups][kDepth];                 // the item's cached keys were loaded
-    int2 info[kInfoCap];                         // (c, fp) of a sequence
-    int32_t scan[kOwnMaxThreads];
-    int32_t first_b[kGroups], first_before[kGroups];
-    int32_t total_items, share;
-};
-
-// Position in a stream: sequence b, head h, item j of n; c cached tokens past the first
-// page `fp` that is the sequence's own.
-struct OwnWalk {
-    int b, h, j, n, c, fp;
-};
-
-// c and fp of sequence b, from the inputs.
-__device__ __forceinline__ int2 own_info(const SharedParams &p, bool share, int b)
+// A row has one state for each part of a unit's pages that a CTA or stream took: tens of
+// them for a long prefix, and a thread that reads them one batch after another waits an L2
+// latency a batch.  Two threads take every other state each and join in shared memory.
+__global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_constant__ SharedParams p)
 {
-    const int fp = share ? group_pages(p, group_of(p, b)) : 0;
-    return make_int2(max(0, clamp_len(__ldg(p.d.cached_len + b)) - fp * kTileKeys), fp);
-}
-
-__device__ __forceinline__ int own_items(const SharedParams &p, int c)
-{
-    return (c + p.d.T + kKT - 1) / kKT;
-}
-
-__device__ __forceinline__ void own_load(const SharedParams &p, const OwnSmem &sh, OwnWalk &w)
-{
-    const int2 v = w.b < kInfoCap ? sh.info[w.b] : own_info(p, sh.share != 0, w.b);
-    w.c = v.x;
-    w.fp = v.y;
-    w.n = own_items(p, w.c);
-}
-
-__device__ __forceinline__ void own_next(const SharedParams &p, const OwnSmem &sh, OwnWalk &w)
-{
-    if (++w.j == w.n) {
-        w.j = 0;
-        if (++w.h == p.d.Hkv) {
-            w.h = 0;
-            ++w.b;
-            if (w.b < p.d.B)
-                own_load(p, sh, w);
-        }
-    }
-}
-
-// Block-table entry of item w (-1: past the table); only read where it has cached keys.
-__device__ __forceinline__ int own_entry(const SharedParams &p, const OwnWalk &w)
-{
-    const int page = w.fp + w.j / (kTileKeys / kKT);
-    if (w.j * kKT >= w.c || page >= p.d.max_blocks)
-        return -1;
-    return __ldg(p.d.block_tables + (int64_t)w.b * p.d.max_blocks + page);
-}
-
-// Floats of an own segment's state: m[R], l[R], o[R][128] for R = G T rows, m and l padded
-// to 16 bytes.
-__host__ __device__ inline int own_pad(int rows) { return (rows + 3) & ~3; }
-__host__ __device__ inline int own_slot_floats(int rows) { return 2 * own_pad(rows) + rows * kD; }
-
-// MT: 16-row m-tiles of a sequence's G T query rows (1 or 2), a warp each.
-template <int MT>
-__global__ void __launch_bounds__(kGroups *MT * 32, 1)
-    own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const __grid_constant__ SharedParams p)
-{
-    extern __shared__ uint8_t smem_raw[];
-    OwnSmem &sh = *reinterpret_cast<OwnSmem *>(align_smem_1024(smem_raw));
-    constexpr int kThr = kGroups * MT * 32;
-    const int tid = threadIdx.x;
-    const int warp = tid >> 5, lane = tid & 31;
-    const int grp = warp / MT, mt = warp % MT;
-    const DecodeParams &d = p.d;
-
-    if (tid == 0) {
-        for (int i = 0; i < kGroups; ++i)
-            for (int s = 0; s < kDepth; ++s) {
-                mbar_init(&sh.full[i][s], 1);
-                mbar_init(&sh.empty[i][s], 1);
-            }
-        fence_barrier_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-    }
-    // Pass 1's CTAs signal only after their own wait, so everything queued before pass 1
-    // has completed here: q, the new rows, lengths, tables and pool are final.  Nothing
-    // here reads what pass 1 writes; the wait before the exit keeps pass 3 behind it.
-    grid_launch_dependents();
-    if (warp == 0) {
-        const bool ok = groups_ok(p, lane);
-        if (lane == 0)
-            sh.share = ok;
-    }
-    __syncthreads();
-    const bool share = sh.share != 0;
-
-    // ---- items before each sequence; a stream an equal contiguous range ----------
-    const int per = (d.B + kThr - 1) / kThr;
-    const int b_lo = min(d.B, tid * per), b_hi = min(d.B, b_lo + per);
-    {
-        int local = 0;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const int2 v = own_info(p, share, b);
-            if (b < kInfoCap)
-                sh.info[b] = v;
-            local += own_items(p, v.x);
-        }
-        sh.scan[tid] = local;
-        __syncthreads();
-        if (warp == 0) {
-            constexpr int kPer = kThr / 32;
-            int v[kPer];
-            int sum = 0;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                v[j] = sh.scan[lane * kPer + j];
-                sum += v[j];
-            }
-            int incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += u;
-            }
-            int acc = incl - sum;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                sh.scan[lane * kPer + j] = acc;
-                acc += v[j];
-            }
-            if (lane == 31)
-                sh.total_items = incl;
-        }
-        __syncthreads();
-    }
-    const int64_t N = (int64_t)sh.total_items * d.Hkv;
-    const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
-    // streams 0 .. gridDim - 1 on different CTAs: few items still use every SM
-    const int64_t stream = (int64_t)grp * gridDim.x + blockIdx.x;
-    const int64_t i0 = min(N, cut(stream, N, C)), i1 = min(N, cut(stream + 1, N, C));
-    {
-        OwnPlan *const plan = reinterpret_cast<OwnPlan *>(d.ws + p.own_plan_off);
-        int before = sh.scan[tid];
-        for (int b = b_lo; b < b_hi; ++b) {
-            const int n = own_items(p, b < kInfoCap ? sh.info[b].x : own_info(p, share, b).x);
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                const int64_t at = min(N, cut((int64_t)i * gridDim.x + blockIdx.x, N, C));
-                if ((int64_t)(before + n) * d.Hkv > at && (int64_t)before * d.Hkv <= at) {
-                    sh.first_b[i] = b;
-                    sh.first_before[i] = before;
-                }
-            }
-            if (blockIdx.x == 0)  // for pass 3
-                plan->before[b] = before;
-            before += n;
-        }
-        if (blockIdx.x == 0 && tid == 0) {
-            plan->N = N;
-            plan->C = C;
-        }
-        __syncthreads();
-    }
-    if (i0 >= i1) {
-        grid_dependency_wait();  // every CTA's exit stays ordered after pass 1
-        return;
-    }
-    OwnWalk w;
-    w.b = sh.first_b[grp];
-    own_load(p, sh, w);
-    {
-        const int64_t off = i0 - (int64_t)sh.first_before[grp] * d.Hkv;
-        w.h = (int)div_pos(off, w.n);
-        w.j = (int)(off - (int64_t)w.h * w.n);
-    }
-
-    // ---- loads: item li of the stream, kDepth items ahead of the products ------------
-    const uint64_t pol = policy_evict_first();
-    OwnWalk lw = w;
-    int64_t li = i0;
-    int lst = 0;
-    uint32_t lph = 0;  // parity of the stage's next empty phase (MT = 2)
-    int entry = own_entry(p, lw);
-    bool timed_out = false;
-    auto load = [&](bool refill) {  // the group's first warp
-        if (li >= i1)
-            return;
-        if (MT == 2 && refill && !timed_out && !mbar_wait(&sh.empty[grp][lst], lph)) {
-            set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
-            timed_out = true;
-        }
-        if (lane == 0) {
-            bool ok = lw.j * kKT < lw.c && !timed_out;
-            if (ok && (entry < 0 || entry >= d.num_blocks)) {
-                set_err(d.dev_err, lw.fp + lw.j / (kTileKeys / kKT) >= d.max_blocks
-                                       ? HSA_DEVERR_BAD_PAGE
-                                       : HSA_DEVERR_BAD_BLOCK);
-                ok = false;
-            }
-            uint64_t *const full = &sh.full[grp][lst];
-            sh.ok[grp][lst] = ok;
-            if (ok) {
-                uint8_t *const dst = sh.stage[grp][lst];
-                const int32_t r = (entry * d.Hkv + lw.h) * kTileKeys + lw.j * kKT % kTileKeys;
-                mbar_arrive_expect_tx(full, kItemBytes);
-                tma_load_2d(dst, &tmK, full, 0, r, pol);
-                tma_load_2d(dst + kHalfTile / 2, &tmK, full, 64, r, pol);
-                tma_load_2d(dst + kHalfTile, &tmV, full, 0, r, pol);
-                tma_load_2d(dst + kHalfTile + kHalfTile / 2, &tmV, full, 64, r, pol);
-            } else {
-                mbar_arrive(full);
-            }
-        }
-        __syncwarp();
-        ++li;
-        if (li < i1) {
-            own_next(p, sh, lw);
-            entry = own_entry(p, lw);  // used at the next load
-        }
-        if (++lst == kDepth) {
-            lst = 0;
-            lph ^= refill ? 1 : 0;
-        }
-    };
-    if (mt == 0)
-        for (int i = 0; i < kDepth; ++i)
-            load(false);
-
-    // ---- products ---------------------------------------------------------------------
-    const int g = lane >> 2, tq = lane & 3;
-    const int q_r0 = mt * 16 + g, q_r1 = q_r0 + 8;
-    const int t0 = q_r0 / d.G, t1 = q_r1 / d.G;
-    const bool v0 = t0 < d.T, v1 = t1 < d.T;
-    const int Hq = d.G * d.Hkv, rows = d.G * d.T;
-    RowState st;
-    uint32_t qa[kD / 16][4];
-    int stg = 0;
-    uint32_t ph = 0;
-    bool fresh = true;
-    for (int64_t i = i0; i < i1; ++i) {
-        if (fresh) {
-            fresh = false;
-            st.m[0] = st.m[1] = -INFINITY;
-            st.l[0] = st.l[1] = 0.f;
-#pragma unroll
-            for (int n = 0; n < kD / 8; ++n)
-                st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
-            const __nv_bfloat16 *q0 =
-                d.q + ((int64_t)(w.b * d.T + t0) * Hq + w.h * d.G + q_r0 % d.G) * kD;
-            const __nv_bfloat16 *q1 =
-                d.q + ((int64_t)(w.b * d.T + t1) * Hq + w.h * d.G + q_r1 % d.G) * kD;
-#pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-                const int c0 = ks * 16 + 2 * tq;
-                qa[ks][0] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0)) : 0u;
-                qa[ks][1] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0)) : 0u;
-                qa[ks][2] = v0 ? __ldg(reinterpret_cast<const uint32_t *>(q0 + c0 + 8)) : 0u;
-                qa[ks][3] = v1 ? __ldg(reinterpret_cast<const uint32_t *>(q1 + c0 + 8)) : 0u;
-            }
-        }
-        if (!timed_out && !mbar_wait(&sh.full[grp][stg], ph)) {
-            set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
-            timed_out = true;
-        }
-        uint8_t *const base = sh.stage[grp][stg];
-        // keys 0 .. cached - 1 of the item are cached ones, key news + t is new token t
-        const int news = w.c - w.j * kKT;
-        const int cached = !timed_out && sh.ok[grp][stg] ? min(kKT, news) : 0;
-        if (cached < kKT) {
-            // the new tokens' rows; V rows of no key may hold anything, and 0 x NaN is NaN:
-            // they become 0 (their scores are masked).  Both warps of a pair write the same.
-            for (int e = lane; e < (kKT - cached) * (kD / 8); e += 32) {
-                const int key = cached + e / (kD / 8), col = (e % (kD / 8)) * 8, t = key - news;
-                uint4 vv = make_uint4(0, 0, 0, 0);
-                uint8_t *const at = base + swz128_offset(key, col, kKT);
-                if (t >= 0 && t < d.T) {
-                    const int64_t src = ((int64_t)(w.b * d.T + t) * d.Hkv + w.h) * kD + col;
-                    vv = __ldg(reinterpret_cast<const uint4 *>(d.v_new + src));
-                    *reinterpret_cast<uint4 *>(at) = __ldg(reinterpret_cast<const uint4 *>(d.k_new + src));
-                }
-                *reinterpret_cast<uint4 *>(at + kHalfTile) = vv;
-            }
-            fence_proxy_async_smem();  // before the stage's next TMA write
-            __syncwarp();
-        }
-        {
-            const int T = d.T;
-            auto vis = [&](int rr, int key) -> bool {
-                const int t = rr == g ? t0 : t1;
-                return t < T && (key < cached || (key >= news && key - news <= t));
-            };
-            const uint32_t sK = smem_u32(base);
-            run_tile<kKT / 8>(st, qa, sK, sK + kHalfTile, kKT, 0, d.scale_log2, cached == kKT, v0, v1, vis);
-        }
-        __syncwarp();
-        if (MT == 2 && mt == 1 && lane == 0)
-            mbar_arrive(&sh.empty[grp][stg]);
-        if (mt == 0)
-            load(true);
-        if (++stg == kDepth) {
-            stg = 0;
-            ph ^= 1;
-        }
-        const bool last = w.j == w.n - 1 || i == i1 - 1;
-        if (last) {
-            // ---- the segment's state, from the registers ------------------------------
-            fresh = true;
-            float l0 = st.l[0], l1 = st.l[1];
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            const int pad = own_pad(rows);
-            float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
-                                (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
-            if (tq == 0) {
-                if (v0) {
-                    part[q_r0] = st.m[0];
-                    part[pad + q_r0] = l0;
-                }
-                if (v1) {
-                    part[q_r1] = st.m[1];
-                    part[pad + q_r1] = l1;
-                }
-            }
-            float *const o0 = part + 2 * pad + q_r0 * kD + 2 * tq;
-#pragma unroll
-            for (int n = 0; n < kD / 8; ++n) {
-                if (v0)
-                    *reinterpret_cast<float2 *>(o0 + n * 8) = make_float2(st.o[n][0], st.o[n][1]);
-                if (v1)
-                    *reinterpret_cast<float2 *>(o0 + 8 * kD + n * 8) =
-                        make_float2(st.o[n][2], st.o[n][3]);
-            }
-        }
-        own_next(p, sh, w);
-    }
-    grid_dependency_wait();
-}
-
-// ---------------------------------------------------------------- pass 3: merge, append
-
-constexpr int kMergeThreads = 256;  // eight rows x 32 pieces of four dimensions
-constexpr int kMergeBatch = 8;      // states whose loads are in flight together
-
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ SharedParams p)
-{
+    __shared__ float2 join_ml[kMergeParts][kMergeThreads / kMergeParts];
+    __shared__ float4 join_o[kMergeParts][kMergeThreads / kMergeParts];
     const DecodeParams &d = p.d;
     const int tid = threadIdx.x;
+    const int part = tid / (kMergeThreads / kMergeParts), id = tid % (kMergeThreads / kMergeParts);
     const int RT = d.G * d.T, Hq = d.G * d.Hkv;
     const int64_t rows = (int64_t)d.B * RT;
     const int h = blockIdx.x % d.Hkv;
-    const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + (tid & 7);
-    const int d4 = tid >> 3;
+    const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + (id & 7);
+    const int d4 = id >> 3;
     const bool on = r < rows;
     grid_launch_dependents();
-    // inputs, final since before pass 1
-    const int b = on ? (int)(r / RT) : 0, rr = (int)(r % RT);
+    // inputs, final since before this call
+    const int b = on ? (int)div_pos(r, RT) : 0, rr = (int)(r - (int64_t)b * RT);
     const int g = group_of(p, b);
     const int seq0 = __ldg(p.cu_group + g), seq1 = __ldg(p.cu_group + g + 1);
     grid_dependency_wait();
 
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // n states at m (l at m + l_at, o at m + o_at), `step` floats apart
-    auto take = [&](const float *m0, int l_at, int o_at, int64_t step, int n) {
-        for (int c0 = 0; c0 < n; c0 += kMergeBatch) {
+    if (on) {
+        const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
+        const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
+        const SharedGroup *const gp = &plan->group[g];
+        const int64_t oN = __ldcg(&own->N), oC = __ldcg(&own->C);
+        const int before = __ldcg(&own->before[b]);
+        const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : -1;
+        const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
+        const int64_t item0 = __ldcg(&gp->item0);
+        const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
+        // the sequence's own states: streams c_lo .. c_hi of part 2
+        const float *own_s;
+        int own_n, own_step = own_slot_floats(RT), own_l = own_pad(RT);
+        const int own_o = 2 * own_l - rr + rr * kD + 4 * d4;
+        {
+            const int n = (next < 0 ? (int)div_pos(oN, d.Hkv) : next) - before;
+            const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
+            const int64_t c_lo = div_pos((s0 + 1) * oC - 1, oN), c_hi = div_pos((s0 + n) * oC - 1, oN);
+            own_n = (int)(c_hi - c_lo) + 1;
+            own_s = reinterpret_cast<const float *>(d.ws + p.own_off) +
+                    (c_lo + (int64_t)b * d.Hkv + h) * own_step + rr;
+        }
+        // the shared segments' states
+        const float *sh_s = own_s;
+        int sh_n = 0, sh_step = 0, sh_o = 0;
+        if (N > 0 && pages > 0) {
+            const int64_t rg = r - (int64_t)seq0 * RT;  // row of the group
+            const int pair = (int)(rg / (2 * kBM)), row = (int)(rg % (2 * kBM));
+            const int un = h * pairs + pair;
+            const int64_t s0 = item0 + (int64_t)un * pages;
+            const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s0 + pages) * C - 1, N);
+            sh_s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
+                   (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + (row & 7);
+            sh_n = (int)(c_hi - c_lo) + 1;
+            sh_o = 16 - (row & 7) + (d4 * 8 + (row & 7)) * 4;
+            sh_step = kSlotFloats;
+            // a unit of one query tile left two states a row, 128 rows apart
+            if ((int64_t)(seq1 - seq0) * RT - (int64_t)pair * 2 * kBM <= kBM) {
+                sh_n *= 2;
+                sh_step /= 2;
+            }
+        }
+        const int n = own_n + sh_n;
+        for (int c0 = part; c0 < n; c0 += kMergeParts * kMergeBatch) {
             float m[kMergeBatch], l[kMergeBatch];
             float4 x[kMergeBatch];
 #pragma unroll
             for (int i = 0; i < kMergeBatch; ++i) {
+                const int c = c0 + i * kMergeParts;
                 m[i] = -INFINITY;
                 l[i] = 0.f;
                 x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c0 + i < n) {
-                    const float *s = m0 + (c0 + i) * step;
+                if (c < n) {
+                    const bool is_own = c < own_n;
+                    const float *s = is_own ? own_s + (int64_t)c * own_step
+                                            : sh_s + (int64_t)(c - own_n) * sh_step;
                     m[i] = __ldcg(s);
-                    l[i] = __ldcg(s + l_at);
-                    x[i] = __ldcg(reinterpret_cast<const float4 *>(s + o_at));
+                    l[i] = __ldcg(s + (is_own ? own_l : 8));
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(s + (is_own ? own_o : sh_o)));
                 }
             }
             float M1 = M;
@@ -1093,44 +1160,27 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
                 o.w += x[i].w * f;
             }
         }
-    };
-    if (on) {
-        const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
-        const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
-        const SharedGroup *const gp = &plan->group[g];
-        const int64_t oN = __ldcg(&own->N), oC = __ldcg(&own->C);
-        const int before = __ldcg(&own->before[b]);
-        const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : (int)(oN / d.Hkv);
-        const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
-        const int64_t item0 = __ldcg(&gp->item0);
-        const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
-        // the sequence's own states: streams c_lo .. c_hi of pass 2
-        {
-            const int n = next - before;
-            const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
-            const int64_t c_lo = div_pos((s0 + 1) * oC - 1, oN), c_hi = div_pos((s0 + n) * oC - 1, oN);
-            const int step = own_slot_floats(RT), pad = own_pad(RT);
-            const float *s = reinterpret_cast<const float *>(d.ws + p.own_off) +
-                             (c_lo + b * d.Hkv + h) * step;
-            take(s + rr, pad, 2 * pad - rr + rr * kD + 4 * d4, step, (int)(c_hi - c_lo) + 1);
-        }
-        // the shared segments' states
-        if (N > 0 && pages > 0) {
-            const int64_t rg = r - (int64_t)seq0 * RT;  // row of the group
-            const int pair = (int)(rg / (2 * kBM)), row = (int)(rg % (2 * kBM));
-            const int un = h * pairs + pair;
-            const int64_t s0 = item0 + (int64_t)un * pages;
-            const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s0 + pages) * C - 1, N);
-            const float *s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
-                             (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + (row & 7);
-            const int n = (int)(c_hi - c_lo) + 1;
-            const int o_at = 16 - (row & 7) + (d4 * 8 + (row & 7)) * 4;
-            // a unit of one query tile left two states a row, 128 rows apart
-            const bool split = (int64_t)(seq1 - seq0) * RT - (int64_t)pair * 2 * kBM <= kBM;
-            if (split)
-                take(s, 8, o_at, kSlotFloats / 2, 2 * n);
-            else
-                take(s, 8, o_at, kSlotFloats, n);
+    }
+    join_ml[part][id] = make_float2(M, L);
+    join_o[part][id] = o;
+    __syncthreads();
+    if (part == 0 && on) {
+#pragma unroll
+        for (int i = 1; i < kMergeParts; ++i)
+            M = fmaxf(M, join_ml[i][id].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kMergeParts; ++i) {
+            const float2 ml = join_ml[i][id];
+            const float4 x = join_o[i][id];
+            const float f = fast_exp2(ml.x - base);
+            L += ml.y * f;
+            o.x += x.x * f;
+            o.y += x.y * f;
+            o.z += x.z * f;
+            o.w += x.w * f;
         }
         const float inv = L > 0.f ? 1.f / L : 0.f;
         const int t = rr / d.G, hh = rr % d.G;
@@ -1192,7 +1242,7 @@ SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv,
     l.own_plan = l.plan + pad256(sizeof(SharedPlan) + (size_t)n_groups * sizeof(SharedGroup));
     l.slots = l.own_plan + pad256(sizeof(OwnPlan) + (size_t)B * sizeof(int32_t));
     // segments in order move on by a CTA, a unit or both, so (CTA, unit)'s slot is
-    // CTA + unit; units of pass 1: 256 rows of a group and a KV head
+    // CTA + unit; units of part 1: 256 rows of a group and a KV head
     const size_t units = ((size_t)B * T * G / (2 * kBM) + (n_groups < B ? n_groups : B)) * Hkv;
     l.own = l.slots + pad256((ctas + units) * kSlotFloats * sizeof(float));
     l.total = l.own + ((size_t)ctas * kGroups + (size_t)B * Hkv) * own_slot_floats(G * T) * sizeof(float);
@@ -1203,34 +1253,24 @@ cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
                           const CUtensorMap &tmK32, const CUtensorMap &tmV32,
                           const SharedParams &p, int ctas, cudaStream_t stream)
 {
-    const size_t smem1 = sizeof(SharedSmem) + 1024, smem2 = sizeof(OwnSmem) + 1024;
+    const size_t smem = sizeof(AttendSmem) + 1024;
     const int MT = (p.d.G * p.d.T + 15) / 16;
-    auto own = MT == 1 ? own_kernel<1> : own_kernel<2>;
-    // the opt-in shared-memory sizes are set once per process
-    static bool attr_set[3] = {false, false, false};
-    if (!attr_set[0]) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
-        if (e != cudaSuccess)
-            return e;
-        attr_set[0] = true;
-    }
-    if (!attr_set[MT]) {
+    auto attend = MT == 1 ? attend_kernel<1> : attend_kernel<2>;
+    // the opt-in shared-memory size is set once per process
+    static bool attr_set[2] = {false, false};
+    if (!attr_set[MT - 1]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem2);
+            cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;
-        attr_set[MT] = true;
+        attr_set[MT - 1] = true;
     }
-    cudaError_t e = launch_dependent(shared_kernel, (unsigned)ctas, kSharedThreads, smem1, stream,
-                                     tmK, tmV, tmQ, p);
-    if (e == cudaSuccess)
-        e = launch_dependent(own, (unsigned)ctas, kGroups * MT * 32, smem2, stream, tmK32, tmV32, p);
-    if (e == cudaSuccess) {
-        const int64_t octs = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8;
-        e = launch_dependent(merge_kernel, (unsigned)(octs * p.d.Hkv), kMergeThreads, 0, stream, p);
-    }
-    return e;
+    const cudaError_t e = launch_dependent(attend, (unsigned)ctas, kAttendThreads, smem, stream, tmK,
+                                           tmV, tmQ, tmK32, tmV32, p);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t octs = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8;
+    return launch_dependent(merge_kernel, (unsigned)(octs * p.d.Hkv), kMergeThreads, 0, stream, p);
 }
 
 }  // namespace hsa

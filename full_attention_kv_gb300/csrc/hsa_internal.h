@@ -57,19 +57,19 @@ hsa_status decode_host_check(const hsa_pools *pools, int32_t layer, const void *
 cudaError_t launch_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const DecodeParams &p,
                           int ctas, cudaStream_t stream);
 
-// Decode over shared prefixes (decode_shared.cu): what its three passes leave one another
+// Decode over shared prefixes (decode_shared.cu): what its parts leave the merge
 // in the workspace.
 struct SharedGroup {
-    int64_t item0;               // first item (page) of the group in pass 1's item space
+    int64_t item0;               // first item (page) of the group in part 1's item space
     int32_t unit0;               // units of the groups before it
     int32_t pairs, pages;        // 256-row units a KV head; shared pages (items a unit)
 };
 struct SharedPlan {
-    int64_t N, C;                // pass 1's items, and the CTAs they were cut over
+    int64_t N, C;                // part 1's items, and the CTAs they were cut over
     SharedGroup group[1];        // [n_groups]
 };
 struct OwnPlan {
-    int64_t N, C;                // pass 2's, and its streams
+    int64_t N, C;                // part 2's, and its streams
     int32_t before[1];           // [B]: own items (of one head) of the sequences before
 };
 struct SharedLayout {            // byte offsets in the workspace
