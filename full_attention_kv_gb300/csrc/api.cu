@@ -573,11 +573,10 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     if (n_groups == 0 || !pools->layer_is_full[layer] || layer_fp8(pools, layer))
         return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
                              workspace, ws_bytes, max_ctas, dev_err, stream, options);
-    int ctas = device_sms();
-    if (ctas <= 0)
+    const int sms = device_sms();
+    if (sms <= 0)
         return HSA_CUDA_ERROR;
-    if (max_ctas > 0 && ctas > max_ctas)
-        ctas = max_ctas;
+    const int ctas = max_ctas > 0 ? std::min(sms, max_ctas) : sms;
     const int Hkv = pools->Hkv, G = pools->Hq / Hkv;
     const hsa::SharedLayout lay = hsa::shared_layout(hsa::decode_counter_bytes(B, Hkv), ctas, B, T,
                                                      G, Hkv, n_groups);
@@ -617,7 +616,7 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     p.slot_off = (int64_t)lay.slots;
     p.own_off = (int64_t)lay.own;
     p.n_groups = n_groups;
-    return hsa::launch_shared(tmK, tmV, tmQ, tmK32, tmV32, p, ctas,
+    return hsa::launch_shared(tmK, tmV, tmQ, tmK32, tmV32, p, ctas, sms,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HSA_OK
                : HSA_CUDA_ERROR;

@@ -411,11 +411,16 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
     bool fresh = true;
     for (int64_t i = i0; i < i1; ++i) {
         if (w.key0() < 0) {
-            if (i == i1 - 1 && lane < 16 && mt * 16 + lane < rows) {  // the share holds no keys
+            if (i == i1 - 1) {  // the share holds no keys
                 float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
                                     (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
-                part[mt * 16 + lane] = -INFINITY;
-                part[pad + mt * 16 + lane] = 0.f;
+                for (int e = lane; e < min(16, rows - mt * 16); e += 32) {
+                    part[mt * 16 + e] = -INFINITY;
+                    part[pad + mt * 16 + e] = 0.f;
+                }
+                for (int e = lane; e < min(16, rows - mt * 16) * (kD / 4); e += 32)
+                    reinterpret_cast<float4 *>(part + 2 * pad + mt * 16 * kD)[e] =
+                        make_float4(0.f, 0.f, 0.f, 0.f);
             }
             own_next(p, sh, w);
             continue;
@@ -888,11 +893,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 if (row_ok) {
                     oct[row & 7] = -INFINITY;
                     oct[8 + (row & 7)] = 0.f;
+                    for (int i = 0; i < kD / 4; ++i)
+                        reinterpret_cast<float4 *>(oct + 16)[i * 8 + (row & 7)] =
+                            make_float4(0.f, 0.f, 0.f, 0.f);
                 }
                 continue;
             }
-            // a member may hold less than the shared pages
-            int hi_row = 0;
+            // a member may hold less than the shared pages; a row of no member (padding, not
+            // written) sees every key, so that it takes no part in the choice below
+            int hi_row = 0x7fffffff;
             if (row_ok)
                 hi_row = clamp_len(__ldg(p.d.cached_len + w.seq0 + r / p.d.G / p.d.T));
             float m_used = -INFINITY, l = 0.f;
@@ -908,7 +917,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 }
                 tc_fence_after();
                 const int hi = entry >= 0 && entry < p.d.num_blocks ? hi_row - n * kTileKeys : 0;
-                const bool whole = hi >= kTileKeys;
+                // the whole warp, which stores to TMEM together, takes one way or the other
+                const bool whole = __all_sync(0xffffffffu, hi >= kTileKeys);
                 // ---- the row's 64 scores: one TMEM read, kept in registers ----------
                 uint32_t r32[2][32];
                 tmem_ld32(lane_addr + col_s, r32[0]);
@@ -943,30 +953,52 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 m_used = m_new;
                 const float base = m_used == -INFINITY ? 0.f : m_used;
                 // ---- P = 2^(s scale log2e - m) as bf16 pairs over S ---------------------
-                // whole pages: the row sum takes the unrounded P (64 keys: bf16's
-                // rounding averages out); partial ones the rounded P that PV multiplies
+                // whole pages: the row sum takes the unrounded P (64 keys: bf16's rounding
+                // averages out); partial ones the rounded P that PV multiplies.  Two loops: a
+                // test of `whole` inside one costs the hot path the other's instructions.
                 const uint64_t sc2 = f2_make(p.d.scale_log2, p.d.scale_log2);
                 const uint64_t nb2 = f2_make(-base, -base);
-                uint64_t acc2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-                float accr = 0.f;
+                float sum;
+                auto exp_pair = [&](int c2, int i, float &p0, float &p1) {
+                    float x0, x1;
+                    f2_split(f2_fma(f2_make(__uint_as_float(r32[c2][2 * i]),
+                                            __uint_as_float(r32[c2][2 * i + 1])),
+                                    sc2, nb2),
+                             x0, x1);
+                    p0 = fast_exp2(x0);
+                    p1 = fast_exp2(x1);
+                };
+                if (whole) {
+                    uint64_t acc2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
 #pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2) {
-                    uint32_t pk[16];
+                    for (int c2 = 0; c2 < 2; ++c2) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t x2 = f2_fma(f2_make(__uint_as_float(r32[c2][2 * i]),
-                                                           __uint_as_float(r32[c2][2 * i + 1])),
-                                                   sc2, nb2);
-                        float x0, x1;
-                        f2_split(x2, x0, x1);
-                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        pk[i] = pack_bf16(p0, p1);
-                        if (whole)
+                        for (int i = 0; i < 16; ++i) {
+                            float p0, p1;
+                            exp_pair(c2, i, p0, p1);
+                            pk[i] = pack_bf16(p0, p1);
                             acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
-                        else
-                            accr += bf16_lo(pk[i]) + bf16_hi(pk[i]);
+                        }
+                        tmem_st16(lane_addr + col_s + c2 * 16, pk);
                     }
-                    tmem_st16(lane_addr + col_s + c2 * 16, pk);
+                    float a0, a1;
+                    f2_split(f2_add(acc2[0], acc2[1]), a0, a1);
+                    sum = a0 + a1;
+                } else {
+                    sum = 0.f;
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float p0, p1;
+                            exp_pair(c2, i, p0, p1);
+                            pk[i] = pack_bf16(p0, p1);
+                            sum += bf16_lo(pk[i]) + bf16_hi(pk[i]);
+                        }
+                        tmem_st16(lane_addr + col_s + c2 * 16, pk);
+                    }
                 }
                 // The previous page's PV is done before O is rescaled (and is waited for at
                 // every page: a parity wait must see every phase).  The segment's first PV
@@ -988,11 +1020,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         tmem_st32(lane_addr + col_o + c4 * 32, o32);
                     }
                 }
-                {
-                    float a0, a1;
-                    f2_split(f2_add(acc2[0], acc2[1]), a0, a1);
-                    l = l * alpha + ((a0 + a1) + accr);
-                }
+                l = l * alpha + sum;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[t][h]);
@@ -1045,35 +1073,68 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
 // ------------------------------------------------------------------------ merge, append
 
-constexpr int kMergeParts = 2;                       // threads that share a row's states
-constexpr int kMergeThreads = kMergeParts * 8 * 32;  // x eight rows x 32 pieces of four dimensions
-constexpr int kMergeBatch = 8;                       // states whose loads are in flight together
+constexpr int kMergeThreads = 256;  // eight rows x 32 pieces of four dimensions
+constexpr int kMergeSpread = 200 * 1024;  // shared memory an SM has for its merge CTAs, spread below
+constexpr int kMergeCap = 32;       // states whose weights are kept at a time
+constexpr int kMergeBatch = 8;      // states whose loads are in flight together
 
-// A row has one state for each part of a unit's pages that a CTA or stream took: tens of
-// them for a long prefix, and a thread that reads them one batch after another waits an L2
-// latency a batch.  Two threads take every other state each and join in shared memory.
-__global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_constant__ SharedParams p)
+// Loads that read where `on` and give 0 elsewhere, and stay where they are written, so that a
+// batch of them is in flight together.
+__device__ __forceinline__ float4 load4_if(const float *p, bool on)
 {
-    __shared__ float2 join_ml[kMergeParts][kMergeThreads / kMergeParts];
-    __shared__ float4 join_o[kMergeParts][kMergeThreads / kMergeParts];
+    float4 v;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "mov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+                 "mov.f32 %2, 0f00000000;\n\tmov.f32 %3, 0f00000000;\n\t"
+                 "@q ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p), "r"((uint32_t)on)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float load_if(const float *p, bool on, float other)
+{
+    float v;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\tmov.f32 %0, %3;\n\t"
+                 "@q ld.global.cg.f32 %0, [%1];\n\t}"
+                 : "=f"(v)
+                 : "l"(p), "r"((uint32_t)on), "f"(other)
+                 : "memory");
+    return v;
+}
+
+// A row has a state for each part of its unit's pages that a CTA or a stream took.  A warp
+// (eight rows, sixteen dimensions) collects its rows' m and l 32 states at a time, four lanes
+// a row, turns them into weights, and reads o with the weights at hand.  Bound by the length
+// of its instruction stream and the latency of its reads (0.6 us each from L2), not by their
+// 20 to 30 MB: pointers step instead of being computed a state (that version ran 4000
+// instructions a warp, 10 us), and four CTAs fit on an SM.
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_constant__ SharedParams p)
+{
+    __shared__ float wt_all[kMergeThreads / 32][kMergeCap][8];
     const DecodeParams &d = p.d;
     const int tid = threadIdx.x;
-    const int part = tid / (kMergeThreads / kMergeParts), id = tid % (kMergeThreads / kMergeParts);
+    float(&wt)[kMergeCap][8] = wt_all[tid >> 5];
     const int RT = d.G * d.T, Hq = d.G * d.Hkv;
     const int64_t rows = (int64_t)d.B * RT;
     const int h = blockIdx.x % d.Hkv;
-    const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + (id & 7);
-    const int d4 = id >> 3;
+    const int oct_row = tid & 7, d4 = tid >> 3;
+    const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + oct_row;
     const bool on = r < rows;
     grid_launch_dependents();
-    // inputs, final since before this call
+    // inputs, final since before the attend kernel
     const int b = on ? (int)div_pos(r, RT) : 0, rr = (int)(r - (int64_t)b * RT);
     const int g = group_of(p, b);
     const int seq0 = __ldg(p.cu_group + g), seq1 = __ldg(p.cu_group + g + 1);
     grid_dependency_wait();
 
-    float M = -INFINITY, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // own states: own_n from own_s on; shared segments' states: sh_n from sh_s on.  l and o
+    // of a state are l_at and o_at floats past its m.
+    int own_n = 0, sh_n = 0, sh_step = kSlotFloats, sh_o = 0;
+    const int own_step = own_slot_floats(RT), own_l = own_pad(RT);
+    const int own_o = 2 * own_l - rr + rr * kD + 4 * d4;
+    const float *own_s = nullptr, *sh_s = nullptr;
     if (on) {
         const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
         const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
@@ -1084,10 +1145,6 @@ __global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_co
         const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
         const int64_t item0 = __ldcg(&gp->item0);
         const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
-        // the sequence's own states: streams c_lo .. c_hi of part 2
-        const float *own_s;
-        int own_n, own_step = own_slot_floats(RT), own_l = own_pad(RT);
-        const int own_o = 2 * own_l - rr + rr * kD + 4 * d4;
         {
             const int n = (next < 0 ? (int)div_pos(oN, d.Hkv) : next) - before;
             const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
@@ -1096,12 +1153,9 @@ __global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_co
             own_s = reinterpret_cast<const float *>(d.ws + p.own_off) +
                     (c_lo + (int64_t)b * d.Hkv + h) * own_step + rr;
         }
-        // the shared segments' states
-        const float *sh_s = own_s;
-        int sh_n = 0, sh_step = 0, sh_o = 0;
         if (N > 0 && pages > 0) {
-            const int64_t rg = r - (int64_t)seq0 * RT;  // row of the group
-            const int pair = (int)(rg / (2 * kBM)), row = (int)(rg % (2 * kBM));
+            const int rg = (int)(r - (int64_t)seq0 * RT);  // row of the group
+            const int pair = rg / (2 * kBM), row = rg % (2 * kBM);
             const int un = h * pairs + pair;
             const int64_t s0 = item0 + (int64_t)un * pages;
             const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s0 + pages) * C - 1, N);
@@ -1109,79 +1163,74 @@ __global__ void __launch_bounds__(kMergeThreads, 1) merge_kernel(const __grid_co
                    (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + (row & 7);
             sh_n = (int)(c_hi - c_lo) + 1;
             sh_o = 16 - (row & 7) + (d4 * 8 + (row & 7)) * 4;
-            sh_step = kSlotFloats;
             // a unit of one query tile left two states a row, 128 rows apart
-            if ((int64_t)(seq1 - seq0) * RT - (int64_t)pair * 2 * kBM <= kBM) {
+            if ((seq1 - seq0) * RT - pair * 2 * kBM <= kBM) {
                 sh_n *= 2;
                 sh_step /= 2;
             }
         }
-        const int n = own_n + sh_n;
-        for (int c0 = part; c0 < n; c0 += kMergeParts * kMergeBatch) {
-            float m[kMergeBatch], l[kMergeBatch];
-            float4 x[kMergeBatch];
-#pragma unroll
-            for (int i = 0; i < kMergeBatch; ++i) {
-                const int c = c0 + i * kMergeParts;
-                m[i] = -INFINITY;
-                l[i] = 0.f;
-                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c < n) {
-                    const bool is_own = c < own_n;
-                    const float *s = is_own ? own_s + (int64_t)c * own_step
-                                            : sh_s + (int64_t)(c - own_n) * sh_step;
-                    m[i] = __ldcg(s);
-                    l[i] = __ldcg(s + (is_own ? own_l : 8));
-                    x[i] = __ldcg(reinterpret_cast<const float4 *>(s + (is_own ? own_o : sh_o)));
-                }
-            }
+    }
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // merges n states from s on, `step` floats apart, their l and o at l_at and o_at
+    auto take = [&](const float *s, int64_t step, int l_at, int o_at, int n) {
+        const int n_warp = __reduce_max_sync(0xffffffffu, n);
+        const float *sm = s + (d4 & 3) * step, *so = s + o_at;
+        for (int base = 0; base < n_warp; base += kMergeCap) {
+            float m[kMergeCap / 4], l[kMergeCap / 4];
             float M1 = M;
 #pragma unroll
-            for (int i = 0; i < kMergeBatch; ++i)
+            for (int i = 0; i < kMergeCap / 4; ++i) {
+                const bool some = base + 4 * i + (d4 & 3) < n;
+                m[i] = load_if(sm, some, -INFINITY);
+                l[i] = load_if(sm + l_at, some, 0.f);
+                sm += 4 * step;
+            }
+#pragma unroll
+            for (int i = 0; i < kMergeCap / 4; ++i)
                 M1 = fmaxf(M1, m[i]);
-            if (M1 == -INFINITY)
-                continue;
-            const float a = fast_exp2(M - M1);
+            // the row's four lanes: 8 and 16 apart
+            M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, 8));
+            M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, 16));
+            const float top = M1 == -INFINITY ? 0.f : M1;
+            const float a = fast_exp2(M - top);
             M = M1;
             L *= a;
+#pragma unroll
+            for (int i = 0; i < kMergeCap / 4; ++i) {
+                const float f = fast_exp2(m[i] - top);
+                L += l[i] * f;
+                wt[4 * i + (d4 & 3)][oct_row] = f;
+            }
+            __syncwarp();
             o.x *= a;
             o.y *= a;
             o.z *= a;
             o.w *= a;
+            for (int c0 = base; c0 < min(base + kMergeCap, n_warp); c0 += kMergeBatch) {
+                float4 x[kMergeBatch];
 #pragma unroll
-            for (int i = 0; i < kMergeBatch; ++i) {
-                if (m[i] == -INFINITY)
-                    continue;  // a state of no keys: its o was not written
-                const float f = fast_exp2(m[i] - M1);
-                L += l[i] * f;
-                o.x += x[i].x * f;
-                o.y += x[i].y * f;
-                o.z += x[i].z * f;
-                o.w += x[i].w * f;
+                for (int i = 0; i < kMergeBatch; ++i) {
+                    x[i] = load4_if(so, c0 + i < n);
+                    so += step;
+                }
+#pragma unroll
+                for (int i = 0; i < kMergeBatch; ++i) {
+                    const float f = wt[c0 - base + i][oct_row];
+                    o.x += x[i].x * f;
+                    o.y += x[i].y * f;
+                    o.z += x[i].z * f;
+                    o.w += x[i].w * f;
+                }
             }
+            __syncwarp();
         }
-    }
-    join_ml[part][id] = make_float2(M, L);
-    join_o[part][id] = o;
-    __syncthreads();
-    if (part == 0 && on) {
-#pragma unroll
-        for (int i = 1; i < kMergeParts; ++i)
-            M = fmaxf(M, join_ml[i][id].x);
-        const float base = M == -INFINITY ? 0.f : M;
-        L = 0.f;
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kMergeParts; ++i) {
-            const float2 ml = join_ml[i][id];
-            const float4 x = join_o[i][id];
-            const float f = fast_exp2(ml.x - base);
-            L += ml.y * f;
-            o.x += x.x * f;
-            o.y += x.y * f;
-            o.z += x.z * f;
-            o.w += x.w * f;
-        }
+    };
+    take(own_s, own_step, own_l, own_o, own_n);
+    take(sh_s, sh_step, 8, sh_o, sh_n);
+    L += __shfl_xor_sync(0xffffffffu, L, 8);
+    L += __shfl_xor_sync(0xffffffffu, L, 16);
+    if (on) {
         const float inv = L > 0.f ? 1.f / L : 0.f;
         const int t = rr / d.G, hh = rr % d.G;
         *reinterpret_cast<uint2 *>(d.out + ((int64_t)(b * d.T + t) * Hq + h * d.G + hh) * kD + 4 * d4) =
@@ -1251,7 +1300,7 @@ SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv,
 
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
                           const CUtensorMap &tmK32, const CUtensorMap &tmV32,
-                          const SharedParams &p, int ctas, cudaStream_t stream)
+                          const SharedParams &p, int ctas, int sms, cudaStream_t stream)
 {
     const size_t smem = sizeof(AttendSmem) + 1024;
     const int MT = (p.d.G * p.d.T + 15) / 16;
@@ -1263,14 +1312,24 @@ cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
             cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;
+        const cudaError_t m = cudaFuncSetAttribute(
+            merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSpread);
+        if (m != cudaSuccess)
+            return m;
         attr_set[MT - 1] = true;
     }
     const cudaError_t e = launch_dependent(attend, (unsigned)ctas, kAttendThreads, smem, stream, tmK,
                                            tmV, tmQ, tmK32, tmV32, p);
     if (e != cudaSuccess)
         return e;
-    const int64_t octs = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8;
-    return launch_dependent(merge_kernel, (unsigned)(octs * p.d.Hkv), kMergeThreads, 0, stream, p);
+    // Merge CTAs start while attend CTAs still hold most SMs, and would pile up on the first
+    // ones to come free, whose 64 bytes a cycle then bound them (128 CTAs, 40 states a row:
+    // 11 us on a quarter of the SMs, 5 us spread).  Shared memory that they do not use keeps
+    // an SM to its share of the grid.
+    const int64_t grid = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8 * p.d.Hkv;
+    const int64_t share = (grid + sms - 1) / sms;
+    const size_t spread = share <= 4 ? (size_t)kMergeSpread / share : 0;
+    return launch_dependent(merge_kernel, (unsigned)grid, kMergeThreads, spread, stream, p);
 }
 
 }  // namespace hsa

@@ -87,7 +87,7 @@ SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv,
 // tmK, tmV: boxes of a page; tmK32, tmV32: of half a page
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
                           const CUtensorMap &tmK32, const CUtensorMap &tmV32,
-                          const SharedParams &p, int ctas, cudaStream_t stream);
+                          const SharedParams &p, int ctas, int sms, cudaStream_t stream);
 
 struct AppendParams {
     const uint4 *k_new;          // [ntok, Hkv, d] as 16-byte chunks
