@@ -400,9 +400,44 @@ class Rope:
                                scale=float(scale),
                                inv_freq=ctypes.cast(self._inv, ctypes.POINTER(ctypes.c_double)),
                                axis_of_pair=ctypes.cast(self._axis, ctypes.POINTER(ctypes.c_uint8)))
+        self.ref = ctypes.byref(self.c)
 
-    def ref(self):
-        return ctypes.byref(self.c)
+
+# Small calls are bound by the host (a decode step's rotation is 3 us on the GPU), so the
+# entry points below test everything a tensor has to be in one expression and go through
+# the checks that name the fault only where that fails.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _good(t, dtype, shape):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda \
+        and t.is_contiguous()
+
+
+def _expect(t, name, dtype, shape):
+    if not _good(t, dtype, shape):
+        _need(t, name, dtype)
+        _shape(t, name, shape)
+
+
+def _need_rank(t, name, dtype, ndim):
+    if not isinstance(t, torch.Tensor) or t.dim() != ndim:
+        _need(t, name, dtype, ndim=ndim)
+
+
+def _place(stream, *ts):
+    """One device for all, the current one; -> its stream (an int or None)."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            _same_device(ts[0], *ts)
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError("tensors on cuda:%d, but the current device is cuda:%d"
+                         % (dev, torch.cuda.current_device()))
+    if stream is None and dev >= 0 and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _head_rows(t, name, heads, d, n=None):
@@ -410,35 +445,30 @@ def _head_rows(t, name, heads, d, n=None):
     contiguous: dense, or a slice of wider rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d or \
-            (n is not None and t.shape[0] != n):
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != d or \
+            (n is not None and shape[0] != n):
         raise ValueError("%s must have shape %s, got %s" % (
-            name, ("n" if n is None else n, "heads" if heads is None else heads, d),
-            tuple(t.shape)))
+            name, ("n" if n is None else n, "heads" if heads is None else heads, d), tuple(shape)))
     s0, s1, s2 = t.stride()
-    width = t.shape[1] * d
-    if t.shape[0] <= 1:
+    width = shape[1] * d
+    if shape[0] <= 1:
         s0 = width
-    if s2 != 1 or (s1 != d and t.shape[1] > 1) or s0 < width or s0 % 8:
+    if s2 != 1 or (s1 != d and shape[1] > 1) or s0 < width or s0 % 8:
         raise ValueError("%s: a token's heads must be contiguous and its stride a multiple of 8, "
                          "got strides %s" % (name, tuple(t.stride())))
     return s0
 
 
 def _positions(rope, positions, n):
-    _need(positions, "positions", torch.int32)
-    if tuple(positions.shape) != (rope.n_axes, n) and not (
-            rope.n_axes == 1 and tuple(positions.shape) == (n,)):
-        raise ValueError("positions must have shape %s, got %s" % ((rope.n_axes, n),
-                                                                   tuple(positions.shape)))
-
-
-def _current_device(t):
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError("tensors on %s, but the current device is cuda:%d"
-                         % (t.device, torch.cuda.current_device()))
+    if not _good(positions, torch.int32, (rope.n_axes, n)):
+        _need(positions, "positions", torch.int32)
+        if tuple(positions.shape) != (rope.n_axes, n) and not (
+                rope.n_axes == 1 and tuple(positions.shape) == (n,)):
+            raise ValueError("positions must have shape %s, got %s" % ((rope.n_axes, n),
+                                                                       tuple(positions.shape)))
 
 
 def hsa_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
@@ -450,24 +480,30 @@ def hsa_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
         raise ValueError("give q, k or both")
     n, d = some.shape[0], some.shape[-1]
     Hq = Hkv = qs = ks = 0
+    qp = kp = qo = ko = None
     if q is not None:
         qs, Hq = _head_rows(q, "q", None, d, n), q.shape[1]
-        q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _need(q_out, "q_out", torch.bfloat16)
-        _shape(q_out, "q_out", (n, Hq, d))
+        if q_out is None:
+            q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
+        else:
+            _expect(q_out, "q_out", torch.bfloat16, (n, Hq, d))
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    else:
+        q_out = None
     if k is not None:
         ks, Hkv = _head_rows(k, "k", None, d, n), k.shape[1]
-        k_out = torch.empty((n, Hkv, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
-        _need(k_out, "k_out", torch.bfloat16)
-        _shape(k_out, "k_out", (n, Hkv, d))
+        if k_out is None:
+            k_out = torch.empty((n, Hkv, d), dtype=k.dtype, device=k.device)
+        else:
+            _expect(k_out, "k_out", torch.bfloat16, (n, Hkv, d))
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    else:
+        k_out = None
     _positions(rope, positions, n)
-    _same_device(positions, q, k, q_out if q is not None else None,
-                 k_out if k is not None else None)
-    _current_device(positions)
-    s = lib().hsa_rope(rope.ref(), _ptr(q), qs, _ptr(k), ks, _ptr(positions), n, Hq, Hkv, d,
-                       _ptr(q_out) if q is not None else None,
-                       _ptr(k_out) if k is not None else None, _stream(stream))
-    _check("hsa_rope", s)
+    stream = _place(stream, positions, q, k, q_out, k_out)
+    s = lib().hsa_rope(rope.ref, qp, qs, kp, ks, positions.data_ptr(), n, Hq, Hkv, d, qo, ko, stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_rope", s)
     return q_out, k_out
 
 
@@ -477,41 +513,47 @@ def hsa_rope_kv_append(pool, layer, rope, q, k_new, v_new, cu_tokens, seq_idx, s
     None: keys alone), k_new and v_new [ntok, Hkv, d] as in hsa_rope; positions [n_axes,
     ntok] int32, or None: each token's cache position on every axis.  k_out=False leaves
     the turned keys out (they go to the pool alone)."""
-    n = k_new.shape[0] if isinstance(k_new, torch.Tensor) else 0
-    ks = _head_rows(k_new, "k_new", pool.Hkv, pool.d)
-    vs = _head_rows(v_new, "v_new", pool.Hkv, pool.d, n)
+    Hq, Hkv, d = pool.Hq, pool.Hkv, pool.d
+    ks = _head_rows(k_new, "k_new", Hkv, d)
+    n = k_new.shape[0]
+    vs = _head_rows(v_new, "v_new", Hkv, d, n)
     qs = 0
+    qp = qo = ko = pos = None
     if q is not None:
-        qs = _head_rows(q, "q", pool.Hq, pool.d, n)
+        qs = _head_rows(q, "q", Hq, d, n)
         if q_out is None:
-            q_out = torch.empty((n, pool.Hq, pool.d), dtype=q.dtype, device=q.device)
-        _need(q_out, "q_out", torch.bfloat16)
-        _shape(q_out, "q_out", (n, pool.Hq, pool.d))
+            q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
+        else:
+            _expect(q_out, "q_out", torch.bfloat16, (n, Hq, d))
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     else:
         q_out = None
     if k_out is False:
         k_out = None
     else:
         if k_out is None:
-            k_out = torch.empty((n, pool.Hkv, pool.d), dtype=k_new.dtype, device=k_new.device)
-        _need(k_out, "k_out", torch.bfloat16)
-        _shape(k_out, "k_out", (n, pool.Hkv, pool.d))
-    for nm, t in (("cu_tokens", cu_tokens), ("seq_idx", seq_idx), ("start_pos", start_pos)):
-        _need(t, nm, torch.int32, ndim=1)
+            k_out = torch.empty((n, Hkv, d), dtype=k_new.dtype, device=k_new.device)
+        else:
+            _expect(k_out, "k_out", torch.bfloat16, (n, Hkv, d))
+        ko = k_out.data_ptr()
+    if not isinstance(seq_idx, torch.Tensor) or seq_idx.dim() != 1:
+        _need(seq_idx, "seq_idx", torch.int32, ndim=1)
     R = seq_idx.shape[0]
-    if cu_tokens.shape[0] != R + 1 or start_pos.shape[0] != R:
-        raise ValueError("cu_tokens must be [R+1] and start_pos [R]")
+    _expect(seq_idx, "seq_idx", torch.int32, (R,))
+    _expect(cu_tokens, "cu_tokens", torch.int32, (R + 1,))
+    _expect(start_pos, "start_pos", torch.int32, (R,))
     if positions is not None:
         _positions(rope, positions, n)
+        pos = positions.data_ptr()
     _need_err(dev_err)
-    _same_device(k_new, q, v_new, cu_tokens, seq_idx, start_pos, positions, q_out, k_out, dev_err,
-                 pool.block_tables)
-    _current_device(k_new)
-    s = lib().hsa_rope_kv_append(pool.ref(), int(layer), rope.ref(), _ptr(q), qs, _ptr(k_new), ks,
-                                 _ptr(v_new), vs, _ptr(positions), _ptr(cu_tokens), _ptr(seq_idx),
-                                 _ptr(start_pos), R, n, _ptr(q_out), _ptr(k_out), _ptr(dev_err),
-                                 _stream(stream))
-    _check("hsa_rope_kv_append", s)
+    stream = _place(stream, k_new, q, v_new, cu_tokens, seq_idx, start_pos, positions, q_out, k_out,
+                    dev_err, pool.block_tables)
+    s = lib().hsa_rope_kv_append(pool.ref(), int(layer), rope.ref, qp, qs, k_new.data_ptr(), ks,
+                                 v_new.data_ptr(), vs, pos, cu_tokens.data_ptr(),
+                                 seq_idx.data_ptr(), start_pos.data_ptr(), R, n, qo, ko,
+                                 None if dev_err is None else dev_err.data_ptr(), stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_rope_kv_append", s)
     return q_out, k_out
 
 
@@ -618,33 +660,37 @@ def hsa_decode_attn_shared(pool, layer, q, k_new, v_new, cached_len, cu_group, s
     shares the pages of its first shared_len[g] tokens (cu_group [n_groups + 1] and shared_len
     [n_groups], device int32): hsa_decode_attn's results, with a full layer's shared pages
     read once a group."""
-    _need(q, "q", torch.bfloat16, ndim=4)
-    _need(k_new, "k_new", torch.bfloat16, ndim=4)
-    _need(v_new, "v_new", torch.bfloat16, ndim=4)
-    for nm, t in (("cached_len", cached_len), ("cu_group", cu_group), ("shared_len", shared_len)):
-        _need(t, nm, torch.int32, ndim=1)
-    B, T = q.shape[0], q.shape[1]
-    _decode_shapes(pool, q, k_new, v_new, cached_len)
-    n_groups = shared_len.shape[0]
-    _shape(cu_group, "cu_group", (n_groups + 1,))
+    _need_rank(q, "q", torch.bfloat16, 4)
+    _need_rank(shared_len, "shared_len", torch.int32, 1)
+    B, T, n_groups = q.shape[0], q.shape[1], shared_len.shape[0]
+    Hq, Hkv, d = pool.Hq, pool.Hkv, pool.d
+    _expect(q, "q", torch.bfloat16, (B, T, Hq, d))
+    _expect(k_new, "k_new", torch.bfloat16, (B, T, Hkv, d))
+    _expect(v_new, "v_new", torch.bfloat16, (B, T, Hkv, d))
+    _expect(cached_len, "cached_len", torch.int32, (B,))
+    _expect(cu_group, "cu_group", torch.int32, (n_groups + 1,))
+    _expect(shared_len, "shared_len", torch.int32, (n_groups,))
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, ndim=4)
-    _shape(out, "out", q.shape)
+    else:
+        _expect(out, "out", torch.bfloat16, (B, T, Hq, d))
     if workspace is None:
         workspace = decode_shared_workspace(pool, B, T, n_groups, device=q.device)
-    _need(workspace, "workspace", torch.uint8)
+    else:
+        _need(workspace, "workspace", torch.uint8)
     _need_err(dev_err)
-    _same_device(q, out, workspace, dev_err, cu_group, shared_len, pool.block_tables)
-    _current_device(q)
+    stream = _place(stream, q, k_new, v_new, cached_len, cu_group, shared_len, out, workspace,
+                    dev_err, pool.block_tables)
     opts = (HSA_DECODE_APPEND if append else 0) | \
         (HSA_DECODE_EARLY_POOL_READ if early_pool_read else 0)
-    s = lib().hsa_decode_attn_shared(pool.ref(), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                     _ptr(cached_len), _ptr(cu_group), _ptr(shared_len), n_groups,
-                                     B, T, float(scale), _ptr(out), _ptr(workspace),
-                                     workspace.numel(), int(max_ctas), opts, _ptr(dev_err),
-                                     _stream(stream))
-    _check("hsa_decode_attn_shared", s)
+    s = lib().hsa_decode_attn_shared(pool.ref(), int(layer), q.data_ptr(), k_new.data_ptr(),
+                                     v_new.data_ptr(), cached_len.data_ptr(), cu_group.data_ptr(),
+                                     shared_len.data_ptr(), n_groups, B, T, float(scale),
+                                     out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                     int(max_ctas), opts,
+                                     None if dev_err is None else dev_err.data_ptr(), stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_decode_attn_shared", s)
     return out
 
 

@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;  // head quads whose loads are in flight together
+constexpr int kBatch = 5;  // head quads whose loads are in flight together
+constexpr int kBlocks = 2; // blocks an SM
 
 enum Kind { kRope = 0, kAppend = 1, kAppendFp8 = 2 };
 
@@ -171,12 +172,137 @@ __device__ __forceinline__ void store_fp8(const float (&a)[8], const float (&b)[
     }
 }
 
+// Values of an FP8 layer, 16 keys of one KV head at a time.  V pages are stored transposed (64
+// bytes of keys a dimension), so a token on its own is 128 single-byte stores, each a 32-byte
+// sector's worth of traffic; a group of 16 aligned positions is one 16-byte store a dimension.
+// A half warp's worth of consecutive tokens (16) is an item; those that begin a group --
+// position a multiple of 16, or the request's first token -- are handled one after another,
+// through a tile of shared memory.  A group that is not whole, at a request's ends, is read,
+// and its other bytes, keys of the same sequence, are written back as they were.  The loops are kept short: a version with the
+// group in registers ran 3000 straight instructions, which came in from a cold instruction
+// cache at about 10 cycles each.
+constexpr int kVKeys = 16;
+constexpr int kVPitch = 33;  // 8-byte pieces a row of the tile: its columns on different banks
+
+template <bool E5>
+__device__ __forceinline__ void append_v_group(const RopeParams &p, uint2 (&tile)[kVKeys][kVPitch],
+                                               int64_t chunk, int h, int lane)
+{
+    {
+        const int tok = (int)min((int64_t)p.n, chunk * kVKeys + (lane % kVKeys));
+        // ---- this lane's token: its row, and whether it begins a group -------------------
+        int64_t row = -1;
+        int cnt = 0;
+        if (tok < p.n && lane < kVKeys) {
+            int lo = 0, hi = p.R;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(p.cu_tokens + mid) <= tok)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int first = __ldg(p.cu_tokens + lo), last = __ldg(p.cu_tokens + lo + 1);
+            const int64_t pos = (int64_t)__ldg(p.start_pos + lo) + (tok - first);
+            if (tok >= first && tok < last && pos >= 0 && (pos % kVKeys == 0 || tok == first)) {
+                int err = 0;  // flagged with the keys
+                row = pool_row(p, __ldg(p.seq_idx + lo), pos, &err);
+                cnt = (int)min((int64_t)(last - tok), kVKeys - pos % kVKeys);
+            }
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, row >= 0);
+        while (todo) {
+            const int who = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int64_t grow = __shfl_sync(0xffffffffu, row, who);
+            const int n = __shfl_sync(0xffffffffu, cnt, who);
+            const int gtok = __shfl_sync(0xffffffffu, tok, who);
+            const int off = (int)(grow & 63), key0 = off % kVKeys;  // the group's first key there
+            const int64_t page = (grow >> 6) + h;
+            // ---- key k of the group is token gtok + k - key0: rows to shared memory ----------
+            {
+                uint2 x[kVKeys];
+#pragma unroll
+                for (int k = 0; k < kVKeys; ++k) {
+                    const int t = k - key0;
+                    x[k] = make_uint2(0, 0);
+                    if (t >= 0 && t < n)
+                        x[k] = __ldcs(reinterpret_cast<const uint2 *>(
+                                          p.v + (int64_t)(gtok + t) * p.v_stride + h * 16) + lane);
+                }
+#pragma unroll
+                for (int k = 0; k < kVKeys; ++k)
+                    tile[k][lane] = x[k];
+            }
+            __syncwarp();
+            // ---- lanes k and k + 16 take half of key k's magnitudes each ----------------------
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint2 x = tile[lane % kVKeys][lane / kVKeys * 16 + i];
+                amax = fmax3(amax, fmaxf(fabsf(bf16_lo(x.x)), fabsf(bf16_hi(x.x))),
+                             fmaxf(fabsf(bf16_lo(x.y)), fabsf(bf16_hi(x.y))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+            const float scale = __fdiv_rn(amax, E5 ? 57344.0f : 448.0f);
+            uint8_t *const base = reinterpret_cast<uint8_t *>(p.v_dst);
+            float *const scales = reinterpret_cast<float *>(base + fp8_codes_bytes(p.num_blocks, p.Hkv));
+            if (lane >= key0 && lane < key0 + n)  // lanes 16 .. 31 hold copies
+                scales[page * 64 + (off - key0) + lane] = amax > 0.f ? scale : 0.f;
+            // ---- codes, a dimension a lane: byte perm16(k) of sixteen is key k's -------------
+            uint32_t mine[4];  // the bytes of the group's keys
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                mine[w] = 0;
+#pragma unroll
+                for (int l = 0; l < kVKeys; ++l)
+                    if (perm16(l) / 4 == w && l >= key0 && l < key0 + n)
+                        mine[w] |= 0xffu << (8 * (perm16(l) % 4));
+            }
+            const uint16_t *const col = reinterpret_cast<const uint16_t *>(&tile[0][0]) + lane;
+            constexpr int kPitch = 4 * kVPitch;  // 16-bit values a row
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                uint32_t word[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    word[w] = 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = 2 * w + 8 * e;  // word w: keys 2w, 2w + 1, 2w + 8, 2w + 9
+                        const float s0 = __shfl_sync(0xffffffffu, scale, k);
+                        const float s1 = __shfl_sync(0xffffffffu, scale, k + 1);
+                        const float u = __uint_as_float((uint32_t)col[k * kPitch + 32 * j] << 16);
+                        const float v = __uint_as_float((uint32_t)col[(k + 1) * kPitch + 32 * j] << 16);
+                        const float a = s0 > 0.f ? __fdiv_rn(u, s0) : 0.f;
+                        const float b = s1 > 0.f ? __fdiv_rn(v, s1) : 0.f;
+                        word[w] |= (E5 ? f32x2_to_e5m2x2(a, b) : f32x2_to_e4m3x2(a, b)) << (16 * e);
+                    }
+                }
+                uint4 *const at = reinterpret_cast<uint4 *>(
+                    base + (page * 128 + 32 * j + lane) * 64 + (off - key0));
+                if (n < kVKeys) {
+                    const uint4 was = *at;  // the neighbours' bytes, of the same sequence
+                    word[0] = (word[0] & mine[0]) | (was.x & ~mine[0]);
+                    word[1] = (word[1] & mine[1]) | (was.y & ~mine[1]);
+                    word[2] = (word[2] & mine[2]) | (was.z & ~mine[2]);
+                    word[3] = (word[3] & mine[3]) | (was.w & ~mine[3]);
+                }
+                *at = make_uint4(word[0], word[1], word[2], word[3]);
+            }
+            __syncwarp();
+        }
+    }
+}
+
 // One warp an item: a token and a slice of its head quads (q heads, k heads, then, when
-// appending, v heads).
+// appending, v heads).  With v_apart the v heads of an FP8 layer are items of their own, ahead
+// of the tokens: 16 tokens of a KV head.
 template <int KIND, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeParams p)
 {
     __shared__ uint4 stage_all[KIND == kAppendFp8 ? kWarps * 32 : 1];
+    __shared__ uint2 tiles[KIND == kAppendFp8 ? kWarps : 1][kVKeys][kVPitch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = lane & 7, hl = lane >> 3;
     const bool rot = c < p.rot16;
@@ -194,16 +320,47 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
     }
     const int qq = (p.Hq + 3) >> 2, kq = (p.Hkv + 3) >> 2;
-    const int nq = qq + kq + (KIND == kRope ? 0 : kq);
+    const int nq = qq + kq + (KIND == kRope || p.v_apart ? 0 : kq);
     const int slices = (nq + p.quads - 1) / p.quads;
-    const int64_t items = (int64_t)p.n * slices;
+    const int64_t v_items =
+        KIND == kAppendFp8 && p.v_apart ? ((int64_t)p.n + kVKeys - 1) / kVKeys * p.Hkv : 0;
+    const int64_t items = v_items + (int64_t)p.n * slices;
     uint8_t *const stage =
         reinterpret_cast<uint8_t *>(stage_all) + (KIND == kAppendFp8 ? (warp * 4 + hl) * 128 : 0);
     grid_dependency_wait();
     for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
          it += (int64_t)gridDim.x * kWarps) {
-        const int tok = (int)(it / slices);
-        const int q0 = (int)(it % slices) * p.quads, q1 = min(nq, q0 + p.quads);
+        if constexpr (KIND == kAppendFp8) {
+            if (it < v_items) {
+                if (p.fp8 == 2)
+                    append_v_group<true>(p, tiles[warp], it / p.Hkv, (int)(it % p.Hkv), lane);
+                else
+                    append_v_group<false>(p, tiles[warp], it / p.Hkv, (int)(it % p.Hkv), lane);
+                continue;
+            }
+        }
+        const int64_t ti = it - v_items;
+        const int tok = (int)(ti / slices);
+        const int q0 = (int)(ti % slices) * p.quads, q1 = min(nq, q0 + p.quads);
+        // head quad qd: q (part 0), k (1) or v (2), its first head h
+        uint4 wa[kBatch], wb[kBatch];
+        auto load = [&](int qb, bool want_v) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int qd = qb + u;
+                const int part = qd < qq ? 0 : (qd < qq + kq ? 1 : 2);
+                const int h = 4 * (qd - (part == 0 ? 0 : (part == 1 ? qq : qq + kq))) + hl;
+                const uint4 *src = part == 0   ? p.q + (int64_t)tok * p.q_stride
+                                   : part == 1 ? p.k + (int64_t)tok * p.k_stride
+                                               : p.v + (int64_t)tok * p.v_stride;
+                wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
+                if (qd < q1 && h < (part == 0 ? p.Hq : p.Hkv) && (part < 2 || want_v)) {
+                    wa[u] = __ldcs(src + h * 16 + ca);
+                    wb[u] = __ldcs(src + h * 16 + cb);
+                }
+            }
+        };
+        load(q0, true);  // ahead of the reads that say where the token belongs
         // ---- the token's request and pool row -------------------------------------
         int64_t row = -1, first_pos = 0;
         bool skip = false;
@@ -246,21 +403,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
         // ---- the head quads -----------------------------------------------------------
         for (int qb = q0; qb < q1; qb += kBatch) {
-            uint4 wa[kBatch], wb[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int qd = qb + u;
-                const int part = qd < qq ? 0 : (qd < qq + kq ? 1 : 2);
-                const int h = 4 * (qd - (part == 0 ? 0 : (part == 1 ? qq : qq + kq))) + hl;
-                const uint4 *src = part == 0   ? p.q + (int64_t)tok * p.q_stride
-                                   : part == 1 ? p.k + (int64_t)tok * p.k_stride
-                                               : p.v + (int64_t)tok * p.v_stride;
-                wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
-                if (qd < q1 && h < (part == 0 ? p.Hq : p.Hkv) && (part < 2 || row >= 0)) {
-                    wa[u] = __ldcs(src + h * 16 + ca);
-                    wb[u] = __ldcs(src + h * 16 + cb);
-                }
-            }
+            if (qb > q0)
+                load(qb, row >= 0);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int qd = qb + u;
@@ -320,21 +464,29 @@ cudaError_t launch(const RopeParams &p, unsigned blocks, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return p.interleaved ? cudaLaunchKernelEx(&cfg, rope_kernel<KIND, true>, p)
-                         : cudaLaunchKernelEx(&cfg, rope_kernel<KIND, false>, p);
+    return cudaLaunchKernelEx(&cfg, p.interleaved ? rope_kernel<KIND, true> : rope_kernel<KIND, false>,
+                              p);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(RopeParams &p, bool append, int sms, cudaStream_t stream)
 {
-    const int nq = (p.Hq + 3) / 4 + (p.Hkv + 3) / 4 * (append ? 2 : 1);
+    // An FP8 layer's values by groups of keys, where the requests are long enough to have whole
+    // groups and many enough to fill the SMs: 8 requests of 700 tokens 32 us against 53 with
+    // a token's values beside its keys, 8 of 100 tokens 20 against 12, 32 of one 66 against 5
+    p.v_apart = append && p.fp8 && p.n >= 2048 && p.n >= 32 * (int64_t)p.R;
+    const int nq = (p.Hq + 3) / 4 + (p.Hkv + 3) / 4 * (append && !p.v_apart ? 2 : 1);
     if (p.n == 0 || nq == 0)
         return cudaSuccess;
-    p.quads = nq;
+    // few tokens: their heads spread over the warps that two blocks an SM have (32 tokens:
+    // 2.4 us against 4.0 with a warp a token)
+    const int64_t spread = (int64_t)sms * kBlocks * kWarps / p.n;
+    p.quads = spread > 1 ? (int32_t)((nq + spread - 1) / spread) : nq;
     const int64_t slices = (nq + p.quads - 1) / p.quads;
-    int64_t blocks = ((int64_t)p.n * slices + kWarps - 1) / kWarps;
-    blocks = blocks < (int64_t)sms * 8 ? blocks : (int64_t)sms * 8;
+    const int64_t v_items = p.v_apart ? ((int64_t)p.n + kVKeys - 1) / kVKeys * p.Hkv : 0;
+    int64_t blocks = ((int64_t)p.n * slices + v_items + kWarps - 1) / kWarps;
+    blocks = blocks < (int64_t)sms * kBlocks ? blocks : (int64_t)sms * kBlocks;
     if (!append)
         return launch<kRope>(p, (unsigned)blocks, stream);
     return p.fp8 ? launch<kAppendFp8>(p, (unsigned)blocks, stream)
