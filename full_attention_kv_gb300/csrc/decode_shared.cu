@@ -106,11 +106,31 @@ __device__ __forceinline__ int64_t cut(int64_t c, int64_t N, int64_t C)
     return c * q + div_pos(c * (N - q * C), C);
 }
 
+// A page of a unit in pair mode counts two items, one of a unit in split mode (a group's
+// last 128 rows or fewer) one: with equal items the CTAs that drew split units were done
+// after 31 us and the others after 57 (three groups of 352 to 704 rows).  A page belongs to
+// the CTA that holds its first item.
+__host__ __device__ inline int page_items(int rows) { return rows <= kBM ? 1 : 2; }
+
+// A group's items for one head: units of 256 rows, the last one's weight by its rows.
+__host__ __device__ inline int64_t head_items(int pairs, int pages, int rows)
+{
+    return pairs > 0 ? (int64_t)pages * (2 * (pairs - 1) + page_items(rows - (pairs - 1) * 2 * kBM)) : 0;
+}
+
+// Parts that N items are cut into: of two items at least, so that every part of a unit
+// between its first page's and its last page's holds a page.
+__host__ __device__ inline int64_t item_parts(int64_t N, int64_t ctas)
+{
+    return N < 2 * ctas ? (N + 1) / 2 : ctas;
+}
+
 // A CTA's walk over the segments of its item range: every role runs its own copy.
 struct SegWalk {
     int64_t it, i1, item0;  // next item, end, first item of group g
+    int64_t per_head;       // the group's items a head
     int g, unit0;           // group, units before it
-    int pairs, pages;       // the group's 256-row units a head, pages (items) a unit
+    int pairs, pages;       // the group's 256-row units a head, pages a unit
     int seq0, ntok;
     // the current segment: pages n0 .. n1 - 1
     int h, pair, n0, n1, unit, rows;
@@ -123,30 +143,34 @@ __device__ __forceinline__ void load_group(const SharedParams &p, SegWalk &w)
     w.ntok = (__ldg(p.cu_group + w.g + 1) - w.seq0) * p.d.T;
     w.pages = group_pages(p, w.g);
     w.pairs = w.pages > 0 ? (w.ntok * p.d.G + 2 * kBM - 1) / (2 * kBM) : 0;
+    w.per_head = head_items(w.pairs, w.pages, w.ntok * p.d.G);
 }
 
 __device__ __forceinline__ bool next_seg(const SharedParams &p, SegWalk &w)
 {
-    if (w.it >= w.i1)
-        return false;
-    int64_t n = (int64_t)w.pairs * p.d.Hkv * w.pages;
-    while (w.it >= w.item0 + n) {
-        w.item0 += n;
-        w.unit0 += w.pairs * p.d.Hkv;
-        ++w.g;
-        load_group(p, w);
-        n = (int64_t)w.pairs * p.d.Hkv * w.pages;
+    while (w.it < w.i1) {
+        while (w.it >= w.item0 + w.per_head * p.d.Hkv) {
+            w.item0 += w.per_head * p.d.Hkv;
+            w.unit0 += w.pairs * p.d.Hkv;
+            ++w.g;
+            load_group(p, w);
+        }
+        const int64_t off = w.it - w.item0;
+        w.h = (int)div_pos(off, w.per_head);
+        const int64_t in_head = off - w.h * w.per_head;
+        w.pair = min((int)div_pos(in_head, 2 * w.pages), w.pairs - 1);
+        w.unit = w.unit0 + w.h * w.pairs + w.pair;
+        w.rows = w.ntok * p.d.G - w.pair * 2 * kBM;
+        const int wt = page_items(w.rows);
+        const int64_t o0 = in_head - (int64_t)w.pair * 2 * w.pages;  // items into the unit
+        const int64_t o1 = min((int64_t)w.pages * wt, o0 + (w.i1 - w.it));
+        w.it += o1 - o0;
+        w.n0 = (int)((o0 + wt - 1) / wt);
+        w.n1 = (int)((o1 + wt - 1) / wt);
+        if (w.n0 < w.n1)
+            return true;
     }
-    const int64_t off = w.it - w.item0;
-    const int u = (int)div_pos(off, w.pages);
-    w.n0 = (int)(off - (int64_t)u * w.pages);
-    w.n1 = (int)min((int64_t)w.pages, w.n0 + (w.i1 - w.it));
-    w.h = u / w.pairs;
-    w.pair = u - w.h * w.pairs;
-    w.unit = w.unit0 + u;
-    w.rows = w.ntok * p.d.G - w.pair * 2 * kBM;
-    w.it += w.n1 - w.n0;
-    return true;
+    return false;
 }
 
 __device__ __forceinline__ bool page_ok(const SharedParams &p, int seq, int page, int *blk)
@@ -187,6 +211,7 @@ struct OwnSmem {
     int2 info[kInfoCap];                         // (c, fp) of a sequence
     int32_t first_b[kGroups], first_before[kGroups];
     int32_t total_items, share;
+    alignas(8) uint64_t ready;                   // the plan is made
 };
 
 // Position in a stream: sequence b, head h, item j of n; c cached tokens past the first
@@ -311,6 +336,19 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
     }
 }
 
+// The position of a stream's first item.
+__device__ __forceinline__ OwnWalk own_start(const SharedParams &p, const OwnSmem &sh, int grp,
+                                             int64_t i0)
+{
+    OwnWalk w;
+    w.b = sh.first_b[grp];
+    own_load(p, sh, w);
+    const int64_t off = i0 - (int64_t)sh.first_before[grp] * p.d.Hkv;
+    w.h = (int)div_pos(off, w.n);
+    w.j = (int)(off - (int64_t)w.h * w.n);
+    return w;
+}
+
 // The streams of this CTA: group grp, warp mt of its MT.
 template <int MT>
 __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMap &tmV,
@@ -326,14 +364,7 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
     const int64_t i0 = min(N, cut(stream, N, C)), i1 = min(N, cut(stream + 1, N, C));
     if (i0 >= i1)
         return;
-    OwnWalk w;
-    w.b = sh.first_b[grp];
-    own_load(p, sh, w);
-    {
-        const int64_t off = i0 - (int64_t)sh.first_before[grp] * d.Hkv;
-        w.h = (int)div_pos(off, w.n);
-        w.j = (int)(off - (int64_t)w.h * w.n);
-    }
+    OwnWalk w = own_start(p, sh, grp, i0);
 
     // ---- loads: item li of the stream, kDepth items ahead of the products ------------
     const uint64_t pol = policy_evict_first();
@@ -589,6 +620,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             mbar_init(&sh.o_empty[t], 4 * 32);
             mbar_init(&sh.done[t], 1);
         }
+        mbar_init(&sh.own.ready, 1);
         for (int i = 0; i < kGroups; ++i)
             for (int s = 0; s < kDepth; ++s) {
                 mbar_init(&sh.own.full[i][s], 1);
@@ -624,7 +656,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 w.g = base + lane;
                 if (w.g < p.n_groups)
                     load_group(p, w);
-                const int64_t n = (int64_t)w.pairs * p.d.Hkv * w.pages;
+                const int64_t n = w.per_head * p.d.Hkv;
                 const int un = w.pairs * p.d.Hkv;
                 int64_t incl = n;
                 int uincl = un;
@@ -659,7 +691,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
             if (walk == 0) {
                 N = total;
-                C = min(N, (int64_t)gridDim.x);
+                C = item_parts(N, gridDim.x);
                 i0 = blockIdx.x < C ? cut(blockIdx.x, N, C) : N;
                 if (lane == 0)
                     sh.N = N;
@@ -676,7 +708,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     __syncthreads();
     tc_fence_after();
     const int64_t N = sh.N;
-    const int64_t C = min(N, (int64_t)gridDim.x);
+    const int64_t C = item_parts(N, gridDim.x);
     SegWalk w{};
     if ((int64_t)blockIdx.x < C) {  // else no segments
         w.it = cut(blockIdx.x, N, C);
@@ -690,7 +722,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
     if (warp == 11) {
         own_plan(p, sh.own, lane);
-    } else if (warp == 0) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.own.ready);
+        return;
+    }
+    if (warp == 0) {
         // ================================================================ producer
         if (lane == 0) {
             const uint64_t pol_first = policy_evict_first(), pol_keep = policy_evict_last();
@@ -1059,16 +1096,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
     // ---- part 2: every read of part 1's shared memory and TMEM is done ------------------
     tc_fence_before();
-    __syncthreads();
+    named_bar_sync(1, kAttendThreads - 32);  // all but the plan's warp
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
     const int ow = warp - 2;  // warps 2 .. 5 or 2 .. 9
-    if (ow >= 0 && ow < kGroups * MT)
+    if (ow < 0 || ow >= kGroups * MT)
+        return;
+    if (mbar_wait_sleep(&sh.own.ready, 0))
         own_run<MT>(tmK32, tmV32, p, sh.own,
                     reinterpret_cast<uint8_t(*)[kDepth][kItemBytes]>(&sh.q[0][0]), ow / MT, ow % MT,
                     lane);
+    else if (lane == 0)
+        set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------ merge, append
@@ -1110,9 +1151,15 @@ __device__ __forceinline__ float load_if(const float *p, bool on, float other)
 // of its instruction stream and the latency of its reads (0.6 us each from L2), not by their
 // 20 to 30 MB: pointers step instead of being computed a state (that version ran 4000
 // instructions a warp, 10 us), and four CTAs fit on an SM.
+struct MergeRow {  // a row's states: own_n from own_s on, sh_n from sh_s on, sh_step floats apart
+    const float *own_s, *sh_s;
+    int32_t own_n, sh_n, sh_step, sh_row;
+};
+
 __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_constant__ SharedParams p)
 {
     __shared__ float wt_all[kMergeThreads / 32][kMergeCap][8];
+    __shared__ MergeRow merge_rows[8];
     const DecodeParams &d = p.d;
     const int tid = threadIdx.x;
     float(&wt)[kMergeCap][8] = wt_all[tid >> 5];
@@ -1123,53 +1170,64 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
     const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + oct_row;
     const bool on = r < rows;
     grid_launch_dependents();
-    // inputs, final since before the attend kernel
     const int b = on ? (int)div_pos(r, RT) : 0, rr = (int)(r - (int64_t)b * RT);
-    const int g = group_of(p, b);
-    const int seq0 = __ldg(p.cu_group + g), seq1 = __ldg(p.cu_group + g + 1);
-    grid_dependency_wait();
-
-    // own states: own_n from own_s on; shared segments' states: sh_n from sh_s on.  l and o
-    // of a state are l_at and o_at floats past its m.
-    int own_n = 0, sh_n = 0, sh_step = kSlotFloats, sh_o = 0;
-    const int own_step = own_slot_floats(RT), own_l = own_pad(RT);
-    const int own_o = 2 * own_l - rr + rr * kD + 4 * d4;
-    const float *own_s = nullptr, *sh_s = nullptr;
-    if (on) {
-        const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
-        const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
-        const SharedGroup *const gp = &plan->group[g];
-        const int64_t oN = __ldcg(&own->N), oC = __ldcg(&own->C);
-        const int before = __ldcg(&own->before[b]);
-        const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : -1;
-        const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
-        const int64_t item0 = __ldcg(&gp->item0);
-        const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
-        {
-            const int n = (next < 0 ? (int)div_pos(oN, d.Hkv) : next) - before;
-            const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
-            const int64_t c_lo = div_pos((s0 + 1) * oC - 1, oN), c_hi = div_pos((s0 + n) * oC - 1, oN);
-            own_n = (int)(c_hi - c_lo) + 1;
-            own_s = reinterpret_cast<const float *>(d.ws + p.own_off) +
-                    (c_lo + (int64_t)b * d.Hkv + h) * own_step + rr;
-        }
-        if (N > 0 && pages > 0) {
-            const int rg = (int)(r - (int64_t)seq0 * RT);  // row of the group
-            const int pair = rg / (2 * kBM), row = rg % (2 * kBM);
-            const int un = h * pairs + pair;
-            const int64_t s0 = item0 + (int64_t)un * pages;
-            const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s0 + pages) * C - 1, N);
-            sh_s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
-                   (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + (row & 7);
-            sh_n = (int)(c_hi - c_lo) + 1;
-            sh_o = 16 - (row & 7) + (d4 * 8 + (row & 7)) * 4;
-            // a unit of one query tile left two states a row, 128 rows apart
-            if ((seq1 - seq0) * RT - pair * 2 * kBM <= kBM) {
-                sh_n *= 2;
-                sh_step /= 2;
+    // ---- where the eight rows' states are: a thread a row, for all of the CTA ---------------
+    if (tid < 8) {
+        MergeRow mr{};
+        // inputs, final since before the attend kernel
+        const int g = group_of(p, b);
+        const int seq0 = __ldg(p.cu_group + g), seq1 = __ldg(p.cu_group + g + 1);
+        grid_dependency_wait();
+        if (on) {
+            const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
+            const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
+            const SharedGroup *const gp = &plan->group[g];
+            const int64_t oN = __ldcg(&own->N), oC = __ldcg(&own->C);
+            const int before = __ldcg(&own->before[b]);
+            const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : -1;
+            const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
+            const int64_t item0 = __ldcg(&gp->item0);
+            const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
+            {
+                const int n = (next < 0 ? (int)div_pos(oN, d.Hkv) : next) - before;
+                const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
+                const int64_t c_lo = div_pos((s0 + 1) * oC - 1, oN);
+                const int64_t c_hi = div_pos((s0 + n) * oC - 1, oN);
+                mr.own_n = (int)(c_hi - c_lo) + 1;
+                mr.own_s = reinterpret_cast<const float *>(d.ws + p.own_off) +
+                           (c_lo + (int64_t)b * d.Hkv + h) * own_slot_floats(RT) + rr;
+            }
+            if (N > 0 && pages > 0) {
+                const int rg = (int)(r - (int64_t)seq0 * RT);  // row of the group
+                const int pair = rg / (2 * kBM), row = rg % (2 * kBM);
+                const int un = h * pairs + pair;
+                const int group_rows = (seq1 - seq0) * RT;
+                const int wt = page_items(group_rows - pair * 2 * kBM);
+                // the parts that hold the first items of the unit's first and last page
+                const int64_t s0 =
+                    item0 + h * head_items(pairs, pages, group_rows) + (int64_t)pair * 2 * pages;
+                const int64_t s1 = s0 + (int64_t)(pages - 1) * wt;
+                const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s1 + 1) * C - 1, N);
+                mr.sh_row = row & 7;
+                mr.sh_s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
+                          (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + mr.sh_row;
+                mr.sh_n = (int)(c_hi - c_lo) + 1;
+                mr.sh_step = kSlotFloats;
+                // a unit in split mode left two states a row, 128 rows apart
+                if (wt == 1) {
+                    mr.sh_n *= 2;
+                    mr.sh_step /= 2;
+                }
             }
         }
+        merge_rows[tid] = mr;
     }
+    __syncthreads();
+    // l and o of a state are l_at and o_at floats past its m
+    const MergeRow mr = merge_rows[oct_row];
+    const int own_step = own_slot_floats(RT), own_l = own_pad(RT);
+    const int own_o = 2 * own_l - rr + rr * kD + 4 * d4;
+    const int sh_o = 16 - mr.sh_row + (d4 * 8 + mr.sh_row) * 4;
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // merges n states from s on, `step` floats apart, their l and o at l_at and o_at
@@ -1193,7 +1251,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
             M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, 8));
             M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, 16));
             const float top = M1 == -INFINITY ? 0.f : M1;
-            const float a = fast_exp2(M - top);
+            const float a = fast_exp2(M - top);  // M = -inf: o and L are 0
             M = M1;
             L *= a;
 #pragma unroll
@@ -1226,8 +1284,15 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
             __syncwarp();
         }
     };
-    take(own_s, own_step, own_l, own_o, own_n);
-    take(sh_s, sh_step, 8, sh_o, sh_n);
+    // the first own state as it is, its reads in flight with the first of the others'; the sum
+    // is spread over the row's four lanes
+    const float m0 = load_if(mr.own_s, on, -INFINITY);
+    const float l0 = load_if(mr.own_s + own_l, on, 0.f);
+    o = load4_if(mr.own_s + own_o, on);
+    M = m0;
+    L = (d4 & 3) == 0 ? l0 : 0.f;
+    take(mr.sh_s, mr.sh_step, 8, sh_o, mr.sh_n);
+    take(mr.own_s + own_step, own_step, own_l, own_o, mr.own_n - 1);
     L += __shfl_xor_sync(0xffffffffu, L, 8);
     L += __shfl_xor_sync(0xffffffffu, L, 16);
     if (on) {
@@ -1237,7 +1302,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     }
     if (d.flags & kDecodeAppend) {
-        // every read of the pool is done: the new rows, one 16-byte chunk of K and V a thread
+        // (behind the barrier, so behind the wait) every read of the pool is done: the new rows, one 16-byte chunk of K and V a thread
         const int64_t chunks = (int64_t)d.B * d.T * d.Hkv * (kD / 8);
         for (int64_t e = (int64_t)blockIdx.x * kMergeThreads + tid; e < chunks;
              e += (int64_t)gridDim.x * kMergeThreads) {

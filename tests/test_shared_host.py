@@ -68,47 +68,58 @@ def test_shared_binding_checks(fake):
     assert len(fake.calls) == done
 
 
-@pytest.mark.parametrize("seed", range(40))
+@pytest.mark.parametrize("seed", range(60))
 def test_segments_cover_the_items_and_slots_are_their_own(seed):
-    """Pass 1's split: every (unit, page) in exactly one segment; a segment's slot, CTA +
-    unit, is its own and inside the workspace's count; and the range of CTAs that pass 2
-    computes for a unit is the one that wrote it."""
+    """Part 1's split: every (unit, page) in exactly one segment; a segment's slot, CTA + unit,
+    is its own and inside the workspace's count; and the range of CTAs that the merge computes
+    for a unit is the one that wrote it."""
     rng = random.Random(seed)
     G, T, Hkv = rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 3, 4]), rng.choice([1, 2, 4, 8])
     members = [rng.choice([0, 1, 2, 5, 40, 300]) for _ in range(rng.randint(1, 40))]
     pages = [rng.choice([0, 0, 1, 2, 3, 17, 200]) for _ in members]
     ctas = rng.choice([1, 2, 13, 152])
     B = sum(members)
+    weight = lambda rows: 1 if rows <= 128 else 2  # noqa: E731
     groups, item0, unit0 = [], 0, 0
     for m, pg in zip(members, pages):
-        kt = pg
-        pairs = (m * T * G + 255) // 256 if kt else 0
-        groups.append((item0, unit0, pairs, kt))
-        item0 += pairs * Hkv * kt
+        rows = m * T * G
+        pairs = (rows + 255) // 256 if pg else 0
+        head = pg * (2 * (pairs - 1) + weight(rows - (pairs - 1) * 256)) if pairs else 0
+        groups.append((item0, unit0, pairs, pg, rows, head))
+        item0 += head * Hkv
         unit0 += pairs * Hkv
     N, slots = item0, ctas + (B * T * G // 256 + min(len(members), B)) * Hkv
     if N == 0:
         return
-    C = min(N, ctas)
+    C = (N + 1) // 2 if N < 2 * ctas else ctas
     wrote, used = {}, set()
     for c in range(C):
         it, i1 = c * N // C, (c + 1) * N // C
         while it < i1:
-            g = next(k for k, (s, _, pr, kt) in enumerate(groups) if s <= it < s + pr * Hkv * kt)
-            s, u0, pr, kt = groups[g]
-            u, n0 = divmod(it - s, kt)
-            n1 = min(kt, n0 + i1 - it)
+            g = next(k for k, x in enumerate(groups) if x[0] <= it < x[0] + x[5] * Hkv)
+            s, u0, pr, pg, rows, head = groups[g]
+            h, in_head = divmod(it - s, head)
+            pair = min(in_head // (2 * pg), pr - 1)
+            wt = weight(rows - pair * 256)
+            o0 = in_head - pair * 2 * pg
+            o1 = min(pg * wt, o0 + i1 - it)
+            it += o1 - o0
+            n0, n1 = -(-o0 // wt), -(-o1 // wt)
+            if n0 == n1:
+                continue
+            u = h * pr + pair
             slot = c + u0 + u
             assert slot not in used and slot < slots
             used.add(slot)
             wrote.setdefault((g, u), []).append((c, n0, n1, slot))
-            it += n1 - n0
-    for g, (s, u0, pr, kt) in enumerate(groups):
+    for g, (s, u0, pr, pg, rows, head) in enumerate(groups):
         for u in range(pr * Hkv):
             segs = wrote[(g, u)]
-            assert segs[0][1] == 0 and segs[-1][2] == kt
+            assert segs[0][1] == 0 and segs[-1][2] == pg
             assert all(a[2] == b[1] for a, b in zip(segs, segs[1:]))
-            a = s + u * kt
-            lo, hi = ((a + 1) * C - 1) // N, ((a + kt) * C - 1) // N
+            h, pair = divmod(u, pr)
+            a = s + h * head + pair * 2 * pg
+            b = a + (pg - 1) * weight(rows - pair * 256)
+            lo, hi = ((a + 1) * C - 1) // N, ((b + 1) * C - 1) // N
             assert [x[0] for x in segs] == list(range(lo, hi + 1))
             assert [x[3] for x in segs] == [c + u0 + u for c in range(lo, hi + 1)]
