@@ -84,6 +84,7 @@ constexpr int kPageBytes = kTileKeys * kD * 2;  // 16 KB: two blocks of 64 rows 
 constexpr int kPageHalf = kPageBytes / 2;
 constexpr int kRing = 5;
 constexpr int kAttendThreads = 384;         // producer 0, issuers 1 and 10, softmax 2 .. 9, plan 11
+constexpr float kFar = 60.0f;               // log2 units that P may lie above 1 before O is rescaled at once
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;             // S: tile t, region h at 128 t + 64 h; O_t at 256 + 128 t
 // A segment's states, by octets of rows: m[8], l[8], then o as [dim / 4][8 rows][4], so
@@ -614,10 +615,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         for (int t = 0; t < 2; ++t) {
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&sh.s_full[t][h], 1);
-                mbar_init(&sh.p_full[t][h], 4 * 32);
+                mbar_init(&sh.p_full[t][h], 4);  // its warps
             }
             mbar_init(&sh.pv_done[t], 1);
-            mbar_init(&sh.o_empty[t], 4 * 32);
+            mbar_init(&sh.o_empty[t], 4);
             mbar_init(&sh.done[t], 1);
         }
         mbar_init(&sh.own.ready, 1);
@@ -941,7 +942,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             int hi_row = 0x7fffffff;
             if (row_ok)
                 hi_row = clamp_len(__ldg(p.d.cached_len + w.seq0 + r / p.d.G / p.d.T));
-            float m_used = -INFINITY, l = 0.f;
+            // O and l are in units of 2^m_used; m_want is the next page's m_used
+            float m_used = -INFINITY, m_want = -INFINITY, l = 0.f;
             const int32_t *const table = p.d.block_tables + (int64_t)w.seq0 * p.d.max_blocks;
             int entry = __ldg(table + first);
             for (int n = first; n < w.n1; n += step, ++c) {
@@ -961,42 +963,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 tmem_ld32(lane_addr + col_s, r32[0]);
                 tmem_ld32(lane_addr + col_s + 32, r32[1]);
                 tmem_wait_ld();
-                if (!whole) {
-#pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c2 * 32 + i >= hi)
-                                r32[c2][i] = __float_as_uint(-INFINITY);
+                // this page's PV-before test, whose answer is wanted after the exponents
+                const bool pv_early = c == 0 || mbar_try_wait(&sh.pv_done[t], (c - 1) & 1);
+                // a raise of the running maximum that the last page asked for
+                float alpha = 1.f;
+                bool resc = false;
+                if (m_want != m_used) {
+                    alpha = m_used == -INFINITY ? 1.f : fast_exp2(m_used - m_want);
+                    resc = m_used != -INFINITY;
+                    m_used = m_want;
                 }
-                // ---- row max (three-input max, four chains) ---------------------------
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        m4[0] = fmax3(m4[0], __uint_as_float(r32[c2][i + 0]), __uint_as_float(r32[c2][i + 1]));
-                        m4[1] = fmax3(m4[1], __uint_as_float(r32[c2][i + 2]), __uint_as_float(r32[c2][i + 3]));
-                        m4[2] = fmax3(m4[2], __uint_as_float(r32[c2][i + 4]), __uint_as_float(r32[c2][i + 5]));
-                        m4[3] = fmax3(m4[3], __uint_as_float(r32[c2][i + 6]), __uint_as_float(r32[c2][i + 7]));
-                    }
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.d.scale_log2;
-                // ---- running max, raised only when it grows by more than 2^8 -----------
-                float m_new = m_used;
-                if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleSlack))
-                    m_new = mx;
-                const bool resc = m_used != -INFINITY && m_new != m_used;
-                const float alpha = resc ? fast_exp2(m_used - m_new) : 1.0f;
-                m_used = m_new;
-                const float base = m_used == -INFINITY ? 0.f : m_used;
-                // ---- P = 2^(s scale log2e - m) as bf16 pairs over S ---------------------
-                // whole pages: the row sum takes the unrounded P (64 keys: bf16's rounding
-                // averages out); partial ones the rounded P that PV multiplies.  Two loops: a
-                // test of `whole` inside one costs the hot path the other's instructions.
                 const uint64_t sc2 = f2_make(p.d.scale_log2, p.d.scale_log2);
-                const uint64_t nb2 = f2_make(-base, -base);
-                float sum;
-                auto exp_pair = [&](int c2, int i, float &p0, float &p1) {
+                uint32_t pk[2][16];  // P = 2^(s scale log2e - m) as bf16 pairs
+                float sum = 0.f;
+                auto exp_pair = [&](int c2, int i, uint64_t nb2, float &p0, float &p1) {
                     float x0, x1;
                     f2_split(f2_fma(f2_make(__uint_as_float(r32[c2][2 * i]),
                                             __uint_as_float(r32[c2][2 * i + 1])),
@@ -1004,43 +984,84 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                              x0, x1);
                     p0 = fast_exp2(x0);
                     p1 = fast_exp2(x1);
+                    pk[c2][i] = pack_bf16(p0, p1);
                 };
-                if (whole) {
+                auto row_max = [&] {  // three-input maximum, four chains
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                m4[e] = fmax3(m4[e], __uint_as_float(r32[c2][i + 2 * e]),
+                                              __uint_as_float(r32[c2][i + 2 * e + 1]));
+                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.d.scale_log2;
+                };
+                // The usual page -- all of its keys seen, a maximum there from pages before --
+                // takes that maximum as it is, so that no exponent waits for this page's.  P may
+                // then reach 2^kFar, which costs no precision (bf16's is relative, and the sum
+                // and O are fp32); a maximum more than kRescaleSlack higher is taken up with
+                // the next page.
+                bool done = false;
+                if (whole && __all_sync(0xffffffffu, m_used != -INFINITY)) {
+                    const uint64_t nb2 = f2_make(-m_used, -m_used);
                     uint64_t acc2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2) {
-                        uint32_t pk[16];
+                    for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float p0, p1;
-                            exp_pair(c2, i, p0, p1);
-                            pk[i] = pack_bf16(p0, p1);
+                            exp_pair(c2, i, nb2, p0, p1);
+                            // (the row sum takes the unrounded P of a whole page: over 64 keys
+                            // bf16's rounding averages out)
                             acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
                         }
-                        tmem_st16(lane_addr + col_s + c2 * 16, pk);
-                    }
+                    const float mx = row_max();
                     float a0, a1;
                     f2_split(f2_add(acc2[0], acc2[1]), a0, a1);
                     sum = a0 + a1;
-                } else {
+                    m_want = mx > m_used + kRescaleSlack ? mx : m_used;
+                    done = __all_sync(0xffffffffu, mx <= m_used + kFar);
+                }
+                if (!done) {
+                    // a segment's first page, keys that a row does not see, a leap of the scores:
+                    // the maximum first; the row sum takes the rounded P that PV multiplies, so
+                    // that a row of few keys gets no error proportional to |O|
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c2 * 32 + i >= hi)
+                                r32[c2][i] = __float_as_uint(-INFINITY);
+                    const float mx = row_max();
+                    if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleSlack)) {
+                        if (m_used != -INFINITY) {
+                            alpha *= fast_exp2(m_used - mx);
+                            resc = true;
+                        }
+                        m_used = mx;
+                    }
+                    m_want = m_used;
+                    const float base = m_used == -INFINITY ? 0.f : m_used;
+                    const uint64_t nb2 = f2_make(-base, -base);
                     sum = 0.f;
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2) {
-                        uint32_t pk[16];
+                    for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float p0, p1;
-                            exp_pair(c2, i, p0, p1);
-                            pk[i] = pack_bf16(p0, p1);
-                            sum += bf16_lo(pk[i]) + bf16_hi(pk[i]);
+                            exp_pair(c2, i, nb2, p0, p1);
+                            sum += bf16_lo(pk[c2][i]) + bf16_hi(pk[c2][i]);
                         }
-                        tmem_st16(lane_addr + col_s + c2 * 16, pk);
-                    }
                 }
+                tmem_st16(lane_addr + col_s, pk[0]);
+                tmem_st16(lane_addr + col_s + 16, pk[1]);
                 // The previous page's PV is done before O is rescaled (and is waited for at
                 // every page: a parity wait must see every phase).  The segment's first PV
                 // overwrites O, so its first page rescales nothing.
-                if (c > 0 && !mbar_wait_sleep(&sh.pv_done[t], (c - 1) & 1)) {
+                if (!__all_sync(0xffffffffu, pv_early) &&
+                    !mbar_wait_sleep(&sh.pv_done[t], (c - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -1060,7 +1081,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 l = l * alpha + sum;
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sh.p_full[t][h]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.p_full[t][h]);
                 entry = next_entry;
             }
             // ---- the segment's state -----------------------------------------------
@@ -1088,7 +1111,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive(&sh.o_empty[t]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.o_empty[t]);
         }
         if (!ok)
             set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
