@@ -189,7 +189,7 @@ struct Rows {
 bool rows_ok(const void *ptr, int64_t stride, int32_t n, int32_t heads, Rows *r)
 {
     const int64_t row = (int64_t)heads * 128;
-    if (!ptr || !aligned16(ptr) || stride < 0 || stride % 8 != 0)
+    if (!ptr || !aligned16(ptr) || stride < 0 || stride % 8 != 0 || stride > (int64_t(1) << 31))
         return false;
     r->stride = stride ? stride : row;
     if (n > 1 && r->stride < row)

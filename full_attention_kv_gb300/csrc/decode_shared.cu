@@ -226,7 +226,10 @@ struct OwnWalk {
 __device__ __forceinline__ int2 own_info(const SharedParams &p, bool share, int b)
 {
     const int fp = share ? group_pages(p, group_of(p, b)) : 0;
-    return make_int2(max(0, clamp_len(__ldg(p.d.cached_len + b)) - fp * kTileKeys), fp);
+    // a length past the block table counts up to the first page that is not there
+    const int64_t most = ((int64_t)p.d.max_blocks + 1) * kTileKeys;
+    const int c = (int)min((int64_t)clamp_len(__ldg(p.d.cached_len + b)), most);
+    return make_int2(max(0, c - fp * kTileKeys), fp);
 }
 
 __device__ __forceinline__ int own_items(const SharedParams &p, int c)

@@ -202,7 +202,8 @@ __device__ __forceinline__ void append_v_group(const RopeParams &p, uint2 (&tile
                 else
                     hi = mid;
             }
-            const int first = __ldg(p.cu_tokens + lo), last = __ldg(p.cu_tokens + lo + 1);
+            // (offsets past the tokens there are must not lead past the rows of v)
+            const int first = __ldg(p.cu_tokens + lo), last = min(p.n, __ldg(p.cu_tokens + lo + 1));
             const int64_t pos = (int64_t)__ldg(p.start_pos + lo) + (tok - first);
             if (tok >= first && tok < last && pos >= 0 && (pos % kVKeys == 0 || tok == first)) {
                 int err = 0;  // flagged with the keys

@@ -176,7 +176,7 @@ typedef struct hsa_rope_params {
  * otherwise hsa_rope_kv_append does both in one launch.
  *  q  [n, Hq, d] bf16, k [n, Hkv, d] bf16: the heads of a token are contiguous, tokens are
  *     q_stride / k_stride elements apart (0 = dense; else a multiple of 8, at least one
- *     token's heads), so slices of a QKV projection's rows serve.
+ *     token's heads, at most 2^31), so slices of a QKV projection's rows serve.
  *  q_out, k_out  dense; q_out may be q itself and k_out k itself when those are dense, and
  *     must not overlap an input or each other otherwise (HSA_INVALID_ARG).
  *  positions     device int32 [n_axes, n]
@@ -199,6 +199,9 @@ hsa_status hsa_rope(const hsa_rope_params *rope, const void *q, int64_t q_stride
  *                   (start_pos[r] + i) on every axis
  * An FP8 layer quantises the turned fp32 values (one rounding); hsa_rope followed by
  * hsa_kv_append would round them to bf16 first.  bf16 pools get the same bits either way.
+ * Long appends to an FP8 layer write V codes in groups of 16 positions: of a group that the
+ * request does not fill, the other positions' codes (of the same sequence) are written back
+ * as they were, so no other stream may write them meanwhile.
  * A token of no request, or at a negative cache position, is skipped whole and flagged
  * (HSA_DEVERR_BAD_LEN): its rows of q_out and k_out stay as they were.  A token whose
  * pool row cannot be reached is flagged and not appended, but its q_out and k_out rows are
@@ -293,7 +296,9 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
  *  shared_len  device int32 [n_groups]: tokens whose pages the group shares (>= 0).  Their
  *              whole pages, shared_len[g] / 64, have to be the same block-table entries in
  *              every row of the group (they are read through its first row) as far as a
- *              member's cached tokens go; a part of a page is each sequence's own.
+ *              member's cached tokens go; a part of a page is each sequence's own.  A member
+ *              may have fewer cached tokens than shared_len (it sees its own), but must not
+ *              append then: its new rows would land in a shared page.
  *  n_groups    0 is hsa_decode_attn_ex.  Groups may be empty or of one sequence.
  *  options     as in hsa_decode_attn_ex.  The appended rows go to each sequence's own pages.
  *  workspace   at least hsa_decode_shared_workspace_bytes() bytes, with the rules of

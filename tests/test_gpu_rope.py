@@ -354,3 +354,46 @@ def test_rope_on_another_stream_and_in_a_graph():
         s.synchronize()
         assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
         assert torch.equal(pool.k[0], want_pool.k[0]) and torch.equal(pool.v[0], want_pool.v[0])
+
+
+@pytest.mark.parametrize("layer", ["full", "e4m3", "e5m2"])
+def test_append_with_offsets_past_the_tokens(layer):
+    """cu_tokens that end past ntok: the tokens that are there are appended, and nothing is read
+    behind them (a long FP8 append gathers the values of 16 positions at a time)."""
+    hsa = _hsa()
+    n = 2100
+    tables = torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40)
+    rows = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v = _heads(_gen(40), n, 16, 2, False)
+    rope, inv, ax = _rope(hsa, 128, 1, False)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pools = [_pool(hsa, layer, tables, rows, 40, 16, 2, 41) for _ in range(2)]
+    err = i32(0)
+    for pool, end in zip(pools, (n, n + 300)):
+        hsa.hsa_rope_kv_append(pool, 0, rope, None, k, v, i32(0, end), i32(0), i32(5), k_out=False, dev_err=err)
+    assert int(err) == 0
+    assert torch.equal(pools[0].k[0], pools[1].k[0]) and torch.equal(pools[0].v[0], pools[1].v[0])
+
+
+@pytest.mark.parametrize("layer", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("counts,starts", [([2048], [0]), ([700, 3, 1500, 40], [9, 62, 16, 1000]), ([2500], [4001])])
+def test_long_fp8_append_equals_short_ones(layer, counts, starts):
+    """The grouped way of long appends and the token by token way of short ones: every byte of
+    the layer, stale rows among them."""
+    hsa = _hsa()
+    cu, seq, start, tables, rows, nb = _requests(42, counts, starts)
+    n = sum(counts)
+    q, k, v = _heads(_gen(43), n, 16, 2, True)
+    v[5, 1] = 0
+    v[n - 1, 0, 3] = 300.0
+    rope, inv, ax = _rope(hsa, 64, 1, True)
+    a, b = (_pool(hsa, layer, tables, rows, nb, 16, 2, 44) for _ in range(2))
+    hsa.hsa_rope_kv_append(a, 0, rope, None, k, v, cu, seq, start, k_out=False)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for r, c in enumerate(counts):
+        for lo in range(0, c, 999):
+            hi = min(c, lo + 999)
+            at = slice(int(cu[r]) + lo, int(cu[r]) + hi)
+            hsa.hsa_rope_kv_append(b, 0, rope, None, k[at], v[at], i32([0, hi - lo]), seq[r:r + 1].contiguous(),
+                                   i32([starts[r] + lo]), k_out=False)
+    assert torch.equal(a.k[0], b.k[0]) and torch.equal(a.v[0], b.v[0])

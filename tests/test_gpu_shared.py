@@ -172,6 +172,20 @@ def test_shared_peaked_scores():
     c.check(c.run())
 
 
+def test_shared_scores_that_leap():
+    """Scores that rise by hundreds from page to page, and fall back: P is never out of
+    range, and the maximum of the pages before is given up in time."""
+    hsa = _hsa()
+    for order in (1, -1):
+        c = Case(hsa, [3], [64 * 30], [20], 1, 16, 2, seed=21, sharp=0.0)
+        c.q[:] = torch.randn(1, generator=_gen(22), device="cuda").bfloat16().abs() + 1
+        for i in range(30):
+            level = torch.tensor(float(abs((i * order) % 30 - 7) * 2), device="cuda")
+            blk = int(c.table[0, i])
+            c.kp[blk] = (torch.randn(2, PAGE, D, generator=_gen(100 + i), device="cuda") * 0.05 + level / 2).bfloat16()
+        c.check(c.run())
+
+
 def test_shared_rows_past_the_end_may_be_nan():
     """Rows of a sequence's last page past its length hold NaN and infinities."""
     hsa = _hsa()
@@ -204,6 +218,20 @@ def test_shared_appends_like_the_append():
         assert int(c.err) == 0
 
 
+def test_shared_workspace_serves_the_plain_call():
+    """One workspace, the calls in turn: each leaves it as the other wants it."""
+    hsa = _hsa()
+    c = Case(hsa, *CASES["long tails"], seed=14)
+    ws = hsa.decode_workspace(c.pool, c.B, c.T)
+    want = hsa.hsa_decode_attn(c.pool, 0, c.q, c.k, c.v, c.cl, SCALE, workspace=ws)
+    first = c.run()
+    for _ in range(3):
+        plain = hsa.hsa_decode_attn(c.pool, 0, c.q, c.k, c.v, c.cl, SCALE, workspace=c.ws)
+        assert torch.equal(plain, want)
+        assert torch.equal(c.run(), first)
+    c.check(first)
+
+
 def test_shared_offsets_out_of_order_share_nothing():
     hsa = _hsa()
     for bad in ([0, 3, 2, 5], [1, 2, 3, 5], [0, 2, 3, 4], [0, -1, 3, 5], [0, 9, 3, 5]):
@@ -226,6 +254,15 @@ def test_shared_lengths_out_of_range():
     c.sl = _i32([2 ** 31 - 1])
     out = c.run()
     assert int(c.err) & hsa.HSA_DEVERR_BAD_PAGE
+    c.check(out)
+    # a cached length far past the block table: its pages, and the flag
+    c = Case(hsa, [1, 1], [640, 64], [5, 700], 2, 16, 2, seed=8)
+    width = c.table.shape[1]
+    c.table[:] = torch.arange(width, dtype=torch.int32, device="cuda") % c.kp.shape[0]
+    c.cl = _i32([2 ** 31 - 1, c.cached[1]])
+    out = c.run()
+    assert int(c.err) == hsa.HSA_DEVERR_BAD_PAGE
+    c.cached[0] = width * PAGE
     c.check(out)
     # negative cached lengths count as none
     c = Case(hsa, [2], [0], [0], 1, 16, 2, seed=8)
