@@ -272,6 +272,14 @@ __device__ __forceinline__ int own_entry(const SharedParams &p, const OwnWalk &w
 __host__ __device__ inline int own_pad(int rows) { return (rows + 3) & ~3; }
 __host__ __device__ inline int own_slot_floats(int rows) { return 2 * own_pad(rows) + rows * kD; }
 
+// The stream of this CTA's group grp.  Streams 0 .. gridDim - 1 are on different CTAs, so that
+// few items still use every SM, and the first on the last CTA: where part 1 has fewer parts
+// than there are CTAs, the two parts' work is on different ones.
+__device__ __forceinline__ int64_t own_stream(int grp)
+{
+    return (int64_t)grp * gridDim.x + (gridDim.x - 1 - blockIdx.x);
+}
+
 // Part 2's plan, by one warp: the items before each sequence, and where this CTA's streams
 // begin.
 __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int lane)
@@ -314,7 +322,7 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
     int64_t at[kGroups];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
-        at[i] = min(N, cut((int64_t)i * gridDim.x + blockIdx.x, N, C));
+        at[i] = min(N, cut(own_stream(i), N, C));
     __syncwarp();
     int before = 0;
     for (int base = 0; base < d.B; base += 32) {
@@ -363,8 +371,7 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
     const DecodeParams &d = p.d;
     const int64_t N = (int64_t)sh.total_items * d.Hkv;
     const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
-    // streams 0 .. gridDim - 1 on different CTAs: few items still use every SM
-    const int64_t stream = (int64_t)grp * gridDim.x + blockIdx.x;
+    const int64_t stream = own_stream(grp);
     const int64_t i0 = min(N, cut(stream, N, C)), i1 = min(N, cut(stream + 1, N, C));
     if (i0 >= i1)
         return;
