@@ -177,10 +177,10 @@ __device__ __forceinline__ void store_fp8(const float (&a)[8], const float (&b)[
 // sector's worth of traffic; a group of 16 aligned positions is one 16-byte store a dimension.
 // A half warp's worth of consecutive tokens (16) is an item; those that begin a group --
 // position a multiple of 16, or the request's first token -- are handled one after another,
-// through a tile of shared memory.  A group that is not whole, at a request's ends, is read,
-// and its other bytes, keys of the same sequence, are written back as they were.  The loops are kept short: a version with the
-// group in registers ran 3000 straight instructions, which came in from a cold instruction
-// cache at about 10 cycles each.
+// through a tile of shared memory.  Of a group that is not whole, at a request's ends, only the
+// request's own bytes are written: the others may be another request's of the same call.  The
+// loops are kept short: a version with the group in registers ran 3000 straight instructions,
+// which came in from a cold instruction cache at about 10 cycles each.
 constexpr int kVKeys = 16;
 constexpr int kVPitch = 33;  // 8-byte pieces a row of the tile: its columns on different banks
 
@@ -251,15 +251,6 @@ __device__ __forceinline__ void append_v_group(const RopeParams &p, uint2 (&tile
             if (lane >= key0 && lane < key0 + n)  // lanes 16 .. 31 hold copies
                 scales[page * 64 + (off - key0) + lane] = amax > 0.f ? scale : 0.f;
             // ---- codes, a dimension a lane: byte perm16(k) of sixteen is key k's -------------
-            uint32_t mine[4];  // the bytes of the group's keys
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                mine[w] = 0;
-#pragma unroll
-                for (int l = 0; l < kVKeys; ++l)
-                    if (perm16(l) / 4 == w && l >= key0 && l < key0 + n)
-                        mine[w] |= 0xffu << (8 * (perm16(l) % 4));
-            }
             const uint16_t *const col = reinterpret_cast<const uint16_t *>(&tile[0][0]) + lane;
             constexpr int kPitch = 4 * kVPitch;  // 16-bit values a row
 #pragma unroll 1
@@ -280,16 +271,15 @@ __device__ __forceinline__ void append_v_group(const RopeParams &p, uint2 (&tile
                         word[w] |= (E5 ? f32x2_to_e5m2x2(a, b) : f32x2_to_e4m3x2(a, b)) << (16 * e);
                     }
                 }
-                uint4 *const at = reinterpret_cast<uint4 *>(
-                    base + (page * 128 + 32 * j + lane) * 64 + (off - key0));
-                if (n < kVKeys) {
-                    const uint4 was = *at;  // the neighbours' bytes, of the same sequence
-                    word[0] = (word[0] & mine[0]) | (was.x & ~mine[0]);
-                    word[1] = (word[1] & mine[1]) | (was.y & ~mine[1]);
-                    word[2] = (word[2] & mine[2]) | (was.z & ~mine[2]);
-                    word[3] = (word[3] & mine[3]) | (was.w & ~mine[3]);
+                uint8_t *const at = base + (page * 128 + 32 * j + lane) * 64 + (off - key0);
+                if (n == kVKeys) {
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(word[0], word[1], word[2], word[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kVKeys; ++k)
+                        if (k >= key0 && k < key0 + n)
+                            at[perm16(k)] = (uint8_t)(word[perm16(k) / 4] >> (8 * (perm16(k) % 4)));
                 }
-                *at = make_uint4(word[0], word[1], word[2], word[3]);
             }
             __syncwarp();
         }

@@ -199,9 +199,6 @@ hsa_status hsa_rope(const hsa_rope_params *rope, const void *q, int64_t q_stride
  *                   (start_pos[r] + i) on every axis
  * An FP8 layer quantises the turned fp32 values (one rounding); hsa_rope followed by
  * hsa_kv_append would round them to bf16 first.  bf16 pools get the same bits either way.
- * Long appends to an FP8 layer write V codes in groups of 16 positions: of a group that the
- * request does not fill, the other positions' codes (of the same sequence) are written back
- * as they were, so no other stream may write them meanwhile.
  * A token of no request, or at a negative cache position, is skipped whole and flagged
  * (HSA_DEVERR_BAD_LEN): its rows of q_out and k_out stay as they were.  A token whose
  * pool row cannot be reached is flagged and not appended, but its q_out and k_out rows are

@@ -397,3 +397,31 @@ def test_long_fp8_append_equals_short_ones(layer, counts, starts):
             hsa.hsa_rope_kv_append(b, 0, rope, None, k[at], v[at], i32([0, hi - lo]), seq[r:r + 1].contiguous(),
                                    i32([starts[r] + lo]), k_out=False)
     assert torch.equal(a.k[0], b.k[0]) and torch.equal(a.v[0], b.v[0])
+
+
+@pytest.mark.parametrize("layer", LAYERS)
+def test_a_sequence_in_many_requests_of_one_call(layer):
+    """One call that names a sequence many times, its ranges end to end (they meet inside groups
+    of 16 positions): every byte as from one request."""
+    hsa = _hsa()
+    counts = [17, 5, 70, 1, 30, 64, 41] * 9 + [50]
+    n = sum(counts)
+    assert n >= 2048 and n >= 32 * len(counts)
+    cu, starts = [0], [7]
+    for c in counts:
+        cu.append(cu[-1] + c)
+        starts.append(starts[-1] + c)
+    tables = torch.randperm(40, generator=_gen(50), device="cuda").int().view(1, 40).contiguous()
+    rows = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v = _heads(_gen(51), n, 16, 2, True)
+    rope, inv, ax = _rope(hsa, 128, 1, False)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    a, b = (_pool(hsa, layer, tables, rows, 40, 16, 2, 52) for _ in range(2))
+    tail = slice(n - 100, n)           # a ring of 128 slots holds the last tokens alone
+    if layer == "ring":
+        cu, starts = [0, 17, 22, 92, 93, 100], [7, 24, 29, 99, 100, 107]
+        q, k, v, n = q[tail], k[tail], v[tail], 100
+    one = hsa.hsa_rope_kv_append(a, 0, rope, q, k, v, i32(cu), i32([0] * (len(cu) - 1)), i32(starts[:len(cu) - 1]))
+    two = hsa.hsa_rope_kv_append(b, 0, rope, q, k, v, i32([0, n]), i32([0]), i32([7]))
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    assert torch.equal(a.k[0], b.k[0]) and torch.equal(a.v[0], b.v[0])
