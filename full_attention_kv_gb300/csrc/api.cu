@@ -616,6 +616,9 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     p.slot_off = (int64_t)lay.slots;
     p.own_off = (int64_t)lay.own;
     p.n_groups = n_groups;
+    if (!hsa::shared_fits(p))
+        return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                             workspace, ws_bytes, max_ctas, dev_err, stream, options);
     return hsa::launch_shared(tmK, tmV, tmQ, tmK32, tmV32, p, ctas, sms,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HSA_OK

@@ -275,9 +275,16 @@ __host__ __device__ inline int own_slot_floats(int rows) { return 2 * own_pad(ro
 // The stream of this CTA's group grp.  Streams 0 .. gridDim - 1 are on different CTAs, so that
 // few items still use every SM, and the first on the last CTA: where part 1 has fewer parts
 // than there are CTAs, the two parts' work is on different ones.
-__device__ __forceinline__ int64_t own_stream(int grp)
+__device__ __forceinline__ int own_stream(int grp)
 {
-    return (int64_t)grp * gridDim.x + (gridDim.x - 1 - blockIdx.x);
+    return grp * (int)gridDim.x + ((int)gridDim.x - 1 - (int)blockIdx.x);
+}
+
+// First item of stream c <= C of N: cut() in 32 bits (shared_fits bounds N, and C < 2^16).
+__device__ __forceinline__ int own_cut(int c, int N, int C)
+{
+    const uint32_t q = (uint32_t)N / (uint32_t)C;
+    return (int)(c * q + c * ((uint32_t)N - q * C) / (uint32_t)C);
 }
 
 // Part 2's plan, by one warp: the items before each sequence, and where this CTA's streams
@@ -308,8 +315,7 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
             plan->before[b] = total + incl - n;
         total += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const int64_t N = (int64_t)total * d.Hkv;
-    const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
+    const int N = total * d.Hkv, C = min(N, (int)gridDim.x * kGroups);
     if (lane == 0) {
         sh.share = share;
         sh.total_items = total;
@@ -319,10 +325,10 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
         }
     }
     // second walk: the sequences that hold the first items of this CTA's streams
-    int64_t at[kGroups];
+    int at[kGroups];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
-        at[i] = min(N, cut(own_stream(i), N, C));
+        at[i] = own_stream(i) < C ? own_cut(own_stream(i), N, C) : N;
     __syncwarp();
     int before = 0;
     for (int base = 0; base < d.B; base += 32) {
@@ -340,7 +346,7 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
         const int lo = before + incl - n;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
-            if (n > 0 && (int64_t)lo * d.Hkv <= at[i] && (int64_t)(lo + n) * d.Hkv > at[i]) {
+            if (n > 0 && lo * d.Hkv <= at[i] && (lo + n) * d.Hkv > at[i]) {
                 sh.first_b[i] = b;
                 sh.first_before[i] = lo;
             }
@@ -350,14 +356,14 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
 
 // The position of a stream's first item.
 __device__ __forceinline__ OwnWalk own_start(const SharedParams &p, const OwnSmem &sh, int grp,
-                                             int64_t i0)
+                                             int i0)
 {
     OwnWalk w;
     w.b = sh.first_b[grp];
     own_load(p, sh, w);
-    const int64_t off = i0 - (int64_t)sh.first_before[grp] * p.d.Hkv;
-    w.h = (int)div_pos(off, w.n);
-    w.j = (int)(off - (int64_t)w.h * w.n);
+    const int off = i0 - sh.first_before[grp] * p.d.Hkv;
+    w.h = off / w.n;
+    w.j = off - w.h * w.n;
     return w;
 }
 
@@ -369,18 +375,17 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
                                         int lane)
 {
     const DecodeParams &d = p.d;
-    const int64_t N = (int64_t)sh.total_items * d.Hkv;
-    const int64_t C = min(N, (int64_t)gridDim.x * kGroups);
-    const int64_t stream = own_stream(grp);
-    const int64_t i0 = min(N, cut(stream, N, C)), i1 = min(N, cut(stream + 1, N, C));
-    if (i0 >= i1)
+    const int N = sh.total_items * d.Hkv, C = min(N, (int)gridDim.x * kGroups);
+    const int stream = own_stream(grp);
+    if (stream >= C)
         return;
+    const int i0 = own_cut(stream, N, C), i1 = own_cut(stream + 1, N, C);
     OwnWalk w = own_start(p, sh, grp, i0);
 
     // ---- loads: item li of the stream, kDepth items ahead of the products ------------
     const uint64_t pol = policy_evict_first();
     OwnWalk lw = w;
-    int64_t li = i0;
+    int li = i0;
     int lst = 0;
     uint32_t lph = 0;  // parity of the stage's next empty phase (MT = 2)
     auto skip = [&] {  // to an item with keys
@@ -392,17 +397,17 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
     };
     skip();
     int entry = li < i1 ? own_entry(p, lw) : -1;
-    bool timed_out = false;
     auto load = [&](bool refill) {  // the group's first warp
         if (li >= i1)
             return;
-        if (MT == 2 && refill && !timed_out && !mbar_wait(&sh.empty[grp][lst], lph)) {
+        if (MT == 2 && refill && !mbar_wait(&sh.empty[grp][lst], lph)) {
             set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
-            timed_out = true;
+            li = i1;  // no more loads: the products then give up on their own
+            return;
         }
         if (lane == 0) {
             const int k0 = lw.key0();
-            bool ok = k0 < lw.c && !timed_out;
+            bool ok = k0 < lw.c;
             if (ok && (entry < 0 || entry >= d.num_blocks)) {
                 set_err(d.dev_err, lw.fp + k0 / kTileKeys >= d.max_blocks ? HSA_DEVERR_BAD_PAGE
                                                                          : HSA_DEVERR_BAD_BLOCK);
@@ -450,12 +455,12 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
     int stg = 0;
     uint32_t ph = 0;
     const int pad = own_pad(rows);
-    bool fresh = true;
-    for (int64_t i = i0; i < i1; ++i) {
+    bool fresh = true, timed_out = false;
+    for (int i = i0; i < i1; ++i) {
         if (w.key0() < 0) {
             if (i == i1 - 1) {  // the share holds no keys
                 float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
-                                    (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
+                                    (int64_t)(stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
                 for (int e = lane; e < min(16, rows - mt * 16); e += 32) {
                     part[mt * 16 + e] = -INFINITY;
                     part[pad + mt * 16 + e] = 0.f;
@@ -490,6 +495,9 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
         if (!timed_out && !mbar_wait(&sh.full[grp][stg], ph)) {
             set_err(d.dev_err, HSA_DEVERR_TIMEOUT);
             timed_out = true;
+            li = i1;
+            for (int s = 0; s < kDepth; ++s)  // no TMA write may be in flight when the CTA exits
+                mbar_wait(&sh.full[grp][s], s < stg ? ph ^ 1 : ph);
         }
         uint8_t *const base = stages[grp][stg];
         // keys 0 .. cached - 1 of the item are cached ones, key news + t is new token t
@@ -540,7 +548,7 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
             float *const part = reinterpret_cast<float *>(d.ws + p.own_off) +
-                                (stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
+                                (int64_t)(stream + w.b * d.Hkv + w.h) * own_slot_floats(rows);
             if (tq == 0) {
                 if (v0) {
                     part[q_r0] = st.m[0];
@@ -1396,6 +1404,12 @@ SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv,
     l.own = l.slots + pad256((ctas + units) * kSlotFloats * sizeof(float));
     l.total = l.own + ((size_t)ctas * kGroups + (size_t)B * Hkv) * own_slot_floats(G * T) * sizeof(float);
     return l;
+}
+
+bool shared_fits(const SharedParams &p)
+{
+    const int64_t items = kUnitCost + ((int64_t)p.d.max_blocks + 1) * (kTileKeys / kKT) + p.d.T;
+    return items * p.d.B * p.d.Hkv < (int64_t)1 << 31;
 }
 
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,

@@ -304,7 +304,8 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
  * Offsets out of order are flagged (HSA_DEVERR_BAD_LEN) and nothing is shared then: every
  * sequence reads its own pages, with the same results.  A negative shared_len is flagged and
  * taken as 0, one past the block table (HSA_DEVERR_BAD_PAGE) as its width.  Sliding layers
- * (a ring is its sequence's own) and FP8 layers run hsa_decode_attn_ex.
+ * (a ring is its sequence's own) and FP8 layers run hsa_decode_attn_ex, as do block tables
+ * with room for 2^31 half pages and more over all sequences and KV heads.
  */
 size_t hsa_decode_shared_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
                                          int32_t n_groups);

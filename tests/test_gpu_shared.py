@@ -427,3 +427,33 @@ def test_a_run_of_the_operators_together():
                 vals[layer][i] = torch.cat((vals[layer][i], v[i:i + 1].double()))
                 near(out[i], attend(q64[i:i + 1], keys[layer][i], vals[layer][i], window))
     assert int(err) == 0
+
+
+def test_shared_with_a_very_wide_block_table():
+    """Room for 2^31 half pages (here 64 rows of 2^21 entries, 8 KV heads): the plain call's
+    results, and with one entry less a row the shared kernels' own."""
+    hsa = _hsa()
+    g = _gen(14)
+    B, hq, hkv, wide = 64, 16, 8, 2 ** 21
+    q = torch.randn(B, 1, hq, D, generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn(B, 1, hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    cl = _i32([130 + b for b in range(B)])
+    cu, sl = _i32([0, B]), _i32([128])
+    outs = {}
+    for width in (4, wide - 3, wide):
+        table = torch.zeros(B, width, dtype=torch.int32, device="cuda")
+        table[:, 1] = 1
+        table[:, 2] = 2 + torch.arange(B, dtype=torch.int32, device="cuda")
+        table[:, 3] = 66 + torch.arange(B, dtype=torch.int32, device="cuda")
+        pool = hsa.DualPool.allocate([True], 130, B, table, torch.zeros(B, dtype=torch.int32, device="cuda"), hq, hkv)
+        h = _gen(15)
+        for t in (pool.k[0], pool.v[0]):
+            t.copy_(torch.randn(t.shape, generator=h, device="cuda").bfloat16())
+        plain = hsa.hsa_decode_attn(pool, 0, q, k, v, cl, SCALE)
+        ws = hsa.decode_shared_workspace(pool, B, 1, 1)
+        outs[width] = hsa.hsa_decode_attn_shared(pool, 0, q, k, v, cl, cu, sl, SCALE, workspace=ws)
+        if width == wide:
+            assert torch.equal(outs[width], plain)
+        del table, pool
+    assert torch.equal(outs[4], outs[wide - 3])
+    assert float((outs[4].float() - outs[wide].float()).abs().max()) < 0.05
