@@ -100,11 +100,12 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
     return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// First item of part c of N items cut into C equal parts: floor(c N / C)
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t N, int64_t C)
+// First item of part c <= C of N items cut into C equal parts: floor(c N / C).  (shared_fits
+// bounds N, and C < 2^16.)
+__device__ __forceinline__ int cut(int c, int N, int C)
 {
-    const int64_t q = div_pos(N, C);
-    return c * q + div_pos(c * (N - q * C), C);
+    const uint32_t q = (uint32_t)N / (uint32_t)C;
+    return (int)(c * q + c * ((uint32_t)N - q * C) / (uint32_t)C);
 }
 
 // A page of a unit in pair mode counts two items, one of a unit in split mode (a group's
@@ -114,24 +115,24 @@ __device__ __forceinline__ int64_t cut(int64_t c, int64_t N, int64_t C)
 __host__ __device__ inline int page_items(int rows) { return rows <= kBM ? 1 : 2; }
 
 // A group's items for one head: units of 256 rows, the last one's weight by its rows.
-__host__ __device__ inline int64_t head_items(int pairs, int pages, int rows)
+__host__ __device__ inline int head_items(int pairs, int pages, int rows)
 {
-    return pairs > 0 ? (int64_t)pages * (2 * (pairs - 1) + page_items(rows - (pairs - 1) * 2 * kBM)) : 0;
+    return pairs > 0 ? pages * (2 * (pairs - 1) + page_items(rows - (pairs - 1) * 2 * kBM)) : 0;
 }
 
 // Parts that N items are cut into: of two items at least, so that every part of a unit
 // between its first page's and its last page's holds a page.
-__host__ __device__ inline int64_t item_parts(int64_t N, int64_t ctas)
+__host__ __device__ inline int item_parts(int N, int ctas)
 {
     return N < 2 * ctas ? (N + 1) / 2 : ctas;
 }
 
 // A CTA's walk over the segments of its item range: every role runs its own copy.
 struct SegWalk {
-    int64_t it, i1, item0;  // next item, end, first item of group g
-    int64_t per_head;       // the group's items a head
-    int g, unit0;           // group, units before it
-    int pairs, pages;       // the group's 256-row units a head, pages a unit
+    int it, i1, item0;  // next item, end, first item of group g
+    int per_head;       // the group's items a head
+    int g, unit0;       // group, units before it
+    int pairs, pages;   // the group's 256-row units a head, pages a unit
     int seq0, ntok;
     // the current segment: pages n0 .. n1 - 1
     int h, pair, n0, n1, unit, rows;
@@ -156,18 +157,18 @@ __device__ __forceinline__ bool next_seg(const SharedParams &p, SegWalk &w)
             ++w.g;
             load_group(p, w);
         }
-        const int64_t off = w.it - w.item0;
-        w.h = (int)div_pos(off, w.per_head);
-        const int64_t in_head = off - w.h * w.per_head;
-        w.pair = min((int)div_pos(in_head, 2 * w.pages), w.pairs - 1);
+        const uint32_t off = w.it - w.item0;
+        w.h = (int)(off / (uint32_t)w.per_head);
+        const int in_head = (int)(off - w.h * w.per_head);
+        w.pair = min((int)((uint32_t)in_head / (2u * w.pages)), w.pairs - 1);
         w.unit = w.unit0 + w.h * w.pairs + w.pair;
         w.rows = w.ntok * p.d.G - w.pair * 2 * kBM;
         const int wt = page_items(w.rows);
-        const int64_t o0 = in_head - (int64_t)w.pair * 2 * w.pages;  // items into the unit
-        const int64_t o1 = min((int64_t)w.pages * wt, o0 + (w.i1 - w.it));
+        const int o0 = in_head - w.pair * 2 * w.pages;  // items into the unit
+        const int o1 = min(w.pages * wt, o0 + (w.i1 - w.it));
         w.it += o1 - o0;
-        w.n0 = (int)((o0 + wt - 1) / wt);
-        w.n1 = (int)((o1 + wt - 1) / wt);
+        w.n0 = (o0 + wt - 1) >> (wt - 1);  // wt is 1 or 2
+        w.n1 = (o1 + wt - 1) >> (wt - 1);
         if (w.n0 < w.n1)
             return true;
     }
@@ -280,13 +281,6 @@ __device__ __forceinline__ int own_stream(int grp)
     return grp * (int)gridDim.x + ((int)gridDim.x - 1 - (int)blockIdx.x);
 }
 
-// First item of stream c <= C of N: cut() in 32 bits (shared_fits bounds N, and C < 2^16).
-__device__ __forceinline__ int own_cut(int c, int N, int C)
-{
-    const uint32_t q = (uint32_t)N / (uint32_t)C;
-    return (int)(c * q + c * ((uint32_t)N - q * C) / (uint32_t)C);
-}
-
 // Part 2's plan, by one warp: the items before each sequence, and where this CTA's streams
 // begin.
 __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int lane)
@@ -328,7 +322,7 @@ __device__ __forceinline__ void own_plan(const SharedParams &p, OwnSmem &sh, int
     int at[kGroups];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
-        at[i] = own_stream(i) < C ? own_cut(own_stream(i), N, C) : N;
+        at[i] = own_stream(i) < C ? cut(own_stream(i), N, C) : N;
     __syncwarp();
     int before = 0;
     for (int base = 0; base < d.B; base += 32) {
@@ -379,7 +373,7 @@ __device__ __forceinline__ void own_run(const CUtensorMap &tmK, const CUtensorMa
     const int stream = own_stream(grp);
     if (stream >= C)
         return;
-    const int i0 = own_cut(stream, N, C), i1 = own_cut(stream + 1, N, C);
+    const int i0 = cut(stream, N, C), i1 = cut(stream + 1, N, C);
     OwnWalk w = own_start(p, sh, grp, i0);
 
     // ---- loads: item li of the stream, kDepth items ahead of the products ------------
@@ -582,8 +576,7 @@ struct AttendSmem {
     uint64_t s_full[2][2], p_full[2][2];    // [query tile][region]
     uint64_t pv_done[2], o_empty[2], done[2];
     uint32_t tmem_base;
-    int32_t g0, unit0;
-    int64_t item0, N;
+    int32_t g0, unit0, item0, N;
     OwnSmem own;
 };
 static_assert(kGroups * kDepth * kItemBytes <= 2 * kQBytes + 2 * kRing * kPageBytes, "part 2's stages");
@@ -666,22 +659,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     if (warp == 0) {
         const bool ok = groups_ok(p, lane);
         SharedPlan *const plan = reinterpret_cast<SharedPlan *>(p.d.ws + p.plan_off);
-        int64_t N = 0, C = 0, i0 = 0;
+        int N = 0, C = 0, i0 = 0;
         for (int walk = 0; walk < 2; ++walk) {  // 0: the sums, 1: the group that holds i0
-            int64_t total = 0;
-            int units = 0;
+            int total = 0, units = 0;
             for (int base = 0; ok && base < p.n_groups; base += 32) {
                 SegWalk w{};
                 w.g = base + lane;
                 if (w.g < p.n_groups)
                     load_group(p, w);
-                const int64_t n = w.per_head * p.d.Hkv;
-                const int un = w.pairs * p.d.Hkv;
-                int64_t incl = n;
-                int uincl = un;
+                const int n = w.per_head * p.d.Hkv, un = w.pairs * p.d.Hkv;
+                int incl = n, uincl = un;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+                    const int a = __shfl_up_sync(0xffffffffu, incl, o);
                     const int b = __shfl_up_sync(0xffffffffu, uincl, o);
                     if (lane >= o) {
                         incl += a;
@@ -711,7 +701,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (walk == 0) {
                 N = total;
                 C = item_parts(N, gridDim.x);
-                i0 = blockIdx.x < C ? cut(blockIdx.x, N, C) : N;
+                i0 = (int)blockIdx.x < C ? cut(blockIdx.x, N, C) : N;
                 if (lane == 0)
                     sh.N = N;
                 if (blockIdx.x == 0 && lane == 0) {
@@ -726,12 +716,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int64_t N = sh.N;
-    const int64_t C = item_parts(N, gridDim.x);
+    const int N = sh.N, C = item_parts(N, gridDim.x);
     SegWalk w{};
-    if ((int64_t)blockIdx.x < C) {  // else no segments
+    if ((int)blockIdx.x < C) {  // else no segments
         w.it = cut(blockIdx.x, N, C);
-        w.i1 = cut((int64_t)blockIdx.x + 1, N, C);
+        w.i1 = cut((int)blockIdx.x + 1, N, C);
         w.item0 = sh.item0;
         w.g = sh.g0;
         w.unit0 = sh.unit0;
@@ -752,7 +741,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const uint64_t pol_first = policy_evict_first(), pol_keep = policy_evict_last();
             bool ok = true;
             RingPos rp{0, 0};
-            int64_t fills = 0;
+            int fills = 0;
             int sc = 0;
             while (ok && next_seg(p, w)) {
                 const int nq = w.split() ? 1 : 2;
@@ -805,10 +794,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (!ok)
                 set_err(p.d.dev_err, HSA_DEVERR_TIMEOUT);
             // drain: no TMA write may still be in flight when the CTA exits
-            for (int64_t s = 0; s < kRing && s < fills; ++s) {
-                const int64_t last = s + ((fills - 1 - s) / kRing) * kRing;
-                mbar_wait_sleep(&sh.full[s], (uint32_t)((last / kRing) & 1));
-            }
+            for (int s = 0; s < kRing && s < fills; ++s)
+                mbar_wait_sleep(&sh.full[s], (fills - 1 - s) / kRing & 1);
             if (sc > 0)
                 mbar_wait_sleep(&sh.q_full, (sc - 1) & 1);
         }
@@ -1248,7 +1235,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
                 const int wt = page_items(group_rows - pair * 2 * kBM);
                 // the parts that hold the first items of the unit's first and last page
                 const int64_t s0 =
-                    item0 + h * head_items(pairs, pages, group_rows) + (int64_t)pair * 2 * pages;
+                    item0 + (int64_t)h * head_items(pairs, pages, group_rows) + (int64_t)pair * 2 * pages;
                 const int64_t s1 = s0 + (int64_t)(pages - 1) * wt;
                 const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s1 + 1) * C - 1, N);
                 mr.sh_row = row & 7;
@@ -1408,8 +1395,11 @@ SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv,
 
 bool shared_fits(const SharedParams &p)
 {
-    const int64_t items = kUnitCost + ((int64_t)p.d.max_blocks + 1) * (kTileKeys / kKT) + p.d.T;
-    return items * p.d.B * p.d.Hkv < (int64_t)1 << 31;
+    const DecodeParams &d = p.d;
+    const int64_t groups = p.n_groups < d.B ? p.n_groups : d.B;
+    const int64_t units = (int64_t)d.B * d.T * d.G / (2 * kBM) + groups;
+    const int64_t own = kUnitCost + ((int64_t)d.max_blocks + 1) * (kTileKeys / kKT) + d.T;
+    return units * 2 * d.max_blocks * d.Hkv < (int64_t)1 << 31 && own * d.B * d.Hkv < (int64_t)1 << 31;
 }
 
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,

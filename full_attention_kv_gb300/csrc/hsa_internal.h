@@ -84,7 +84,8 @@ struct SharedParams {
 };
 
 SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv, int n_groups);
-// Whether part 2's items, at the longest that the block table has room for, count to below 2^31.
+// Whether the items of both parts, at the longest that the block table has room for, count to
+// below 2^31.
 bool shared_fits(const SharedParams &p);
 // tmK, tmV: boxes of a page; tmK32, tmV32: of half a page
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
