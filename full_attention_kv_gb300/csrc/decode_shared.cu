@@ -94,18 +94,24 @@ constexpr int kOctFloats = 16 + 8 * kD;
 constexpr int kSlotFloats = 2 * kBM / 8 * kOctFloats;
 
 
-// a / b of non-negative numbers that mostly fit 32 bits
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
-{
-    return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // First item of part c <= C of N items cut into C equal parts: floor(c N / C).  (shared_fits
 // bounds N, and C < 2^16.)
 __device__ __forceinline__ int cut(int c, int N, int C)
 {
     const uint32_t q = (uint32_t)N / (uint32_t)C;
     return (int)(c * q + c * ((uint32_t)N - q * C) / (uint32_t)C);
+}
+
+// The part that holds item s: the c with cut(c) <= s < cut(c + 1), from a guess that is off by
+// one at most.
+__device__ __forceinline__ int part_of(int s, int N, int C)
+{
+    int c = min((int)((float)s * ((float)C / (float)N)), C - 1);
+    if (cut(c, N, C) > s)
+        --c;
+    else if (cut(c + 1, N, C) <= s)
+        ++c;
+    return c;
 }
 
 // A page of a unit in pair mode counts two items, one of a unit in split mode (a group's
@@ -1194,13 +1200,13 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
     const int tid = threadIdx.x;
     float(&wt)[kMergeCap][8] = wt_all[tid >> 5];
     const int RT = d.G * d.T, Hq = d.G * d.Hkv;
-    const int64_t rows = (int64_t)d.B * RT;
+    const int rows = d.B * RT;
     const int h = blockIdx.x % d.Hkv;
     const int oct_row = tid & 7, d4 = tid >> 3;
-    const int64_t r = (int64_t)(blockIdx.x / d.Hkv) * 8 + oct_row;
+    const int r = (int)(blockIdx.x / d.Hkv) * 8 + oct_row;
     const bool on = r < rows;
     grid_launch_dependents();
-    const int b = on ? (int)div_pos(r, RT) : 0, rr = (int)(r - (int64_t)b * RT);
+    const int b = on ? r / RT : 0, rr = r - b * RT;
     // ---- where the eight rows' states are: a thread a row, for all of the CTA ---------------
     if (tid < 8) {
         MergeRow mr{};
@@ -1212,36 +1218,33 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
             const OwnPlan *const own = reinterpret_cast<const OwnPlan *>(d.ws + p.own_plan_off);
             const SharedPlan *const plan = reinterpret_cast<const SharedPlan *>(d.ws + p.plan_off);
             const SharedGroup *const gp = &plan->group[g];
-            const int64_t oN = __ldcg(&own->N), oC = __ldcg(&own->C);
+            const int oN = __ldcg(&own->N), oC = __ldcg(&own->C);
             const int before = __ldcg(&own->before[b]);
             const int next = b + 1 < d.B ? __ldcg(&own->before[b + 1]) : -1;
-            const int64_t N = __ldcg(&plan->N), C = __ldcg(&plan->C);
-            const int64_t item0 = __ldcg(&gp->item0);
+            const int N = __ldcg(&plan->N), C = __ldcg(&plan->C);
+            const int item0 = __ldcg(&gp->item0);
             const int unit0 = __ldcg(&gp->unit0), pairs = __ldcg(&gp->pairs), pages = __ldcg(&gp->pages);
             {
-                const int n = (next < 0 ? (int)div_pos(oN, d.Hkv) : next) - before;
-                const int64_t s0 = (int64_t)before * d.Hkv + (int64_t)h * n;
-                const int64_t c_lo = div_pos((s0 + 1) * oC - 1, oN);
-                const int64_t c_hi = div_pos((s0 + n) * oC - 1, oN);
-                mr.own_n = (int)(c_hi - c_lo) + 1;
+                const int n = (next < 0 ? oN / d.Hkv : next) - before;
+                const int s0 = before * d.Hkv + h * n;
+                const int c_lo = part_of(s0, oN, oC), c_hi = part_of(s0 + n - 1, oN, oC);
+                mr.own_n = c_hi - c_lo + 1;
                 mr.own_s = reinterpret_cast<const float *>(d.ws + p.own_off) +
-                           (c_lo + (int64_t)b * d.Hkv + h) * own_slot_floats(RT) + rr;
+                           (int64_t)(c_lo + b * d.Hkv + h) * own_slot_floats(RT) + rr;
             }
             if (N > 0 && pages > 0) {
-                const int rg = (int)(r - (int64_t)seq0 * RT);  // row of the group
+                const int rg = r - seq0 * RT;  // row of the group
                 const int pair = rg / (2 * kBM), row = rg % (2 * kBM);
                 const int un = h * pairs + pair;
                 const int group_rows = (seq1 - seq0) * RT;
                 const int wt = page_items(group_rows - pair * 2 * kBM);
                 // the parts that hold the first items of the unit's first and last page
-                const int64_t s0 =
-                    item0 + (int64_t)h * head_items(pairs, pages, group_rows) + (int64_t)pair * 2 * pages;
-                const int64_t s1 = s0 + (int64_t)(pages - 1) * wt;
-                const int64_t c_lo = div_pos((s0 + 1) * C - 1, N), c_hi = div_pos((s1 + 1) * C - 1, N);
+                const int s0 = item0 + h * head_items(pairs, pages, group_rows) + pair * 2 * pages;
+                const int c_lo = part_of(s0, N, C), c_hi = part_of(s0 + (pages - 1) * wt, N, C);
                 mr.sh_row = row & 7;
                 mr.sh_s = reinterpret_cast<const float *>(d.ws + p.slot_off) +
-                          (c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + mr.sh_row;
-                mr.sh_n = (int)(c_hi - c_lo) + 1;
+                          (int64_t)(c_lo + unit0 + un) * kSlotFloats + row / 8 * kOctFloats + mr.sh_row;
+                mr.sh_n = c_hi - c_lo + 1;
                 mr.sh_step = kSlotFloats;
                 // a unit in split mode left two states a row, 128 rows apart
                 if (wt == 1) {
@@ -1261,7 +1264,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // merges n states from s on, `step` floats apart, their l and o at l_at and o_at
-    auto take = [&](const float *s, int64_t step, int l_at, int o_at, int n) {
+    auto take = [&](const float *s, int step, int l_at, int o_at, int n) {
         const int n_warp = __reduce_max_sync(0xffffffffu, n);
         const float *sm = s + (d4 & 3) * step, *so = s + o_at;
         for (int base = 0; base < n_warp; base += kMergeCap) {
@@ -1332,28 +1335,24 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     }
     if (d.flags & kDecodeAppend) {
-        // (behind the barrier, so behind the wait) every read of the pool is done: the new rows, one 16-byte chunk of K and V a thread
-        const int64_t chunks = (int64_t)d.B * d.T * d.Hkv * (kD / 8);
-        for (int64_t e = (int64_t)blockIdx.x * kMergeThreads + tid; e < chunks;
-             e += (int64_t)gridDim.x * kMergeThreads) {
-            const int ch = (int)(e % (kD / 8));
-            const int64_t th = e / (kD / 8);
-            const int hk = (int)(th % d.Hkv);
-            const int64_t bt = th / d.Hkv;
-            const int sb = (int)(bt / d.T);
-            const int64_t pos = (int64_t)clamp_len(__ldg(d.cached_len + sb)) + bt % d.T;
-            if (pos / kTileKeys >= d.max_blocks) {
-                set_err(d.dev_err, HSA_DEVERR_BAD_PAGE);
-                continue;
-            }
-            int blk = 0;
-            if (!page_ok(p, sb, (int)(pos / kTileKeys), &blk)) {
-                set_err(d.dev_err, HSA_DEVERR_BAD_BLOCK);
-                continue;
-            }
-            const int64_t to = (((int64_t)blk * d.Hkv + hk) * kTileKeys + pos % kTileKeys) * (kD / 8) + ch;
-            d.k_dst[to] = __ldg(reinterpret_cast<const uint4 *>(d.k_new) + e);
-            d.v_dst[to] = __ldg(reinterpret_cast<const uint4 *>(d.v_new) + e);
+        // (behind the barrier, so behind the wait: every read of the pool is done) the new rows,
+        // one 16-byte chunk of K and V a thread; the grid has threads enough for all
+        constexpr int kChunks = kD / 8;
+        const int th = (int)blockIdx.x * (kMergeThreads / kChunks) + tid / kChunks, ch = tid % kChunks;
+        if (th >= d.B * d.T * d.Hkv)
+            return;
+        const int bt = th / d.Hkv, hk = th - bt * d.Hkv, sb = bt / d.T;
+        const int64_t pos = (int64_t)clamp_len(__ldg(d.cached_len + sb)) + bt % d.T;
+        int blk = 0;
+        if (pos / kTileKeys >= d.max_blocks) {
+            set_err(d.dev_err, HSA_DEVERR_BAD_PAGE);
+        } else if (!page_ok(p, sb, (int)(pos / kTileKeys), &blk)) {
+            set_err(d.dev_err, HSA_DEVERR_BAD_BLOCK);
+        } else {
+            const int64_t from = (int64_t)th * kChunks + ch;
+            const int64_t to = (((int64_t)blk * d.Hkv + hk) * kTileKeys + pos % kTileKeys) * kChunks + ch;
+            d.k_dst[to] = __ldg(reinterpret_cast<const uint4 *>(d.k_new) + from);
+            d.v_dst[to] = __ldg(reinterpret_cast<const uint4 *>(d.v_new) + from);
         }
     }
 }
@@ -1399,7 +1398,8 @@ bool shared_fits(const SharedParams &p)
     const int64_t groups = p.n_groups < d.B ? p.n_groups : d.B;
     const int64_t units = (int64_t)d.B * d.T * d.G / (2 * kBM) + groups;
     const int64_t own = kUnitCost + ((int64_t)d.max_blocks + 1) * (kTileKeys / kKT) + d.T;
-    return units * 2 * d.max_blocks * d.Hkv < (int64_t)1 << 31 && own * d.B * d.Hkv < (int64_t)1 << 31;
+    return units * 2 * d.max_blocks * d.Hkv < (int64_t)1 << 31 && own * d.B * d.Hkv < (int64_t)1 << 31 &&
+           (int64_t)d.B * d.T * d.G * d.Hkv < (int64_t)1 << 30;
 }
 
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,

@@ -60,16 +60,16 @@ cudaError_t launch_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
 // Decode over shared prefixes (decode_shared.cu): what its parts leave the merge
 // in the workspace.
 struct SharedGroup {
-    int64_t item0;               // first item (page) of the group in part 1's item space
+    int32_t item0;               // first item of the group in part 1's item space
     int32_t unit0;               // units of the groups before it
     int32_t pairs, pages;        // 256-row units a KV head; shared pages (items a unit)
 };
 struct SharedPlan {
-    int64_t N, C;                // part 1's items, and the CTAs they were cut over
+    int32_t N, C;                // part 1's items, and the CTAs they were cut over
     SharedGroup group[1];        // [n_groups]
 };
 struct OwnPlan {
-    int64_t N, C;                // part 2's, and its streams
+    int32_t N, C;                // part 2's, and its streams
     int32_t before[1];           // [B]: own items (of one head) of the sequences before
 };
 struct SharedLayout {            // byte offsets in the workspace
@@ -84,8 +84,8 @@ struct SharedParams {
 };
 
 SharedLayout shared_layout(size_t start, int ctas, int B, int T, int G, int Hkv, int n_groups);
-// Whether the items of both parts, at the longest that the block table has room for, count to
-// below 2^31.
+// Whether the items of both parts, at the longest that the block table has room for, and the
+// merge's rows and threads count to below 2^31.
 bool shared_fits(const SharedParams &p);
 // tmK, tmV: boxes of a page; tmK32, tmV32: of half a page
 cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const CUtensorMap &tmQ,
