@@ -88,8 +88,8 @@ __device__ __forceinline__ int find_request(const int32_t *cu, int R, int tok, i
 }
 
 // Destination row of cache position pos of sequence seq (units of one head's rows), or
-// -1 with *err set.
-__device__ __forceinline__ int64_t pool_row(const RopeParams &p, int seq, int64_t pos, int *err)
+// -1 with *err set.  (A start and an offset of 31 bits each: the sum has 32.)
+__device__ __forceinline__ int64_t pool_row(const RopeParams &p, int seq, uint32_t pos, int *err)
 {
     if (seq < 0 || seq >= p.batch) {
         *err = HSA_DEVERR_BAD_SEQ;
@@ -101,10 +101,10 @@ __device__ __forceinline__ int64_t pool_row(const RopeParams &p, int seq, int64_
             *err = HSA_DEVERR_BAD_RING;
             return -1;
         }
-        return (int64_t)rr * p.Hkv * p.W + pos % p.W;
+        return (int64_t)rr * p.Hkv * p.W + pos % (uint32_t)p.W;
     }
-    const int64_t page = pos / 64;
-    if (page >= p.max_blocks) {
+    const uint32_t page = pos / 64;
+    if (page >= (uint32_t)p.max_blocks) {
         *err = HSA_DEVERR_BAD_PAGE;
         return -1;
     }
@@ -186,10 +186,10 @@ constexpr int kVPitch = 33;  // 8-byte pieces a row of the tile: its columns on 
 
 template <bool E5>
 __device__ __forceinline__ void append_v_group(const RopeParams &p, uint2 (&tile)[kVKeys][kVPitch],
-                                               int64_t chunk, int h, int lane)
+                                               uint32_t chunk, int h, int lane)
 {
     {
-        const int tok = (int)min((int64_t)p.n, chunk * kVKeys + (lane % kVKeys));
+        const int tok = (int)min((uint32_t)p.n, chunk * kVKeys + (lane % kVKeys));
         // ---- this lane's token: its row, and whether it begins a group -------------------
         int64_t row = -1;
         int cnt = 0;
@@ -207,7 +207,7 @@ __device__ __forceinline__ void append_v_group(const RopeParams &p, uint2 (&tile
             const int64_t pos = (int64_t)__ldg(p.start_pos + lo) + (tok - first);
             if (tok >= first && tok < last && pos >= 0 && (pos % kVKeys == 0 || tok == first)) {
                 int err = 0;  // flagged with the keys
-                row = pool_row(p, __ldg(p.seq_idx + lo), pos, &err);
+                row = pool_row(p, __ldg(p.seq_idx + lo), (uint32_t)pos, &err);
                 cnt = (int)min((int64_t)(last - tok), kVKeys - pos % kVKeys);
             }
         }
@@ -313,24 +313,24 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     const int qq = (p.Hq + 3) >> 2, kq = (p.Hkv + 3) >> 2;
     const int nq = qq + kq + (KIND == kRope || p.v_apart ? 0 : kq);
     const int slices = (nq + p.quads - 1) / p.quads;
-    const int64_t v_items =
-        KIND == kAppendFp8 && p.v_apart ? ((int64_t)p.n + kVKeys - 1) / kVKeys * p.Hkv : 0;
-    const int64_t items = v_items + (int64_t)p.n * slices;
+    // items count in 32 bits (launch_rope): a 64-bit division an item is 70 instructions
+    const uint32_t v_items =
+        KIND == kAppendFp8 && p.v_apart ? ((uint32_t)p.n + kVKeys - 1) / kVKeys * p.Hkv : 0;
+    const uint32_t items = v_items + (uint32_t)p.n * slices;
     uint8_t *const stage =
         reinterpret_cast<uint8_t *>(stage_all) + (KIND == kAppendFp8 ? (warp * 4 + hl) * 128 : 0);
     grid_dependency_wait();
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
-         it += (int64_t)gridDim.x * kWarps) {
+    for (uint32_t it = blockIdx.x * kWarps + warp; it < items; it += gridDim.x * kWarps) {
         if constexpr (KIND == kAppendFp8) {
             if (it < v_items) {
                 if (p.fp8 == 2)
-                    append_v_group<true>(p, tiles[warp], it / p.Hkv, (int)(it % p.Hkv), lane);
+                    append_v_group<true>(p, tiles[warp], it / p.Hkv, it % p.Hkv, lane);
                 else
-                    append_v_group<false>(p, tiles[warp], it / p.Hkv, (int)(it % p.Hkv), lane);
+                    append_v_group<false>(p, tiles[warp], it / p.Hkv, it % p.Hkv, lane);
                 continue;
             }
         }
-        const int64_t ti = it - v_items;
+        const uint32_t ti = it - v_items;
         const int tok = (int)(ti / slices);
         const int q0 = (int)(ti % slices) * p.quads, q1 = min(nq, q0 + p.quads);
         // head quad qd: q (part 0), k (1) or v (2), its first head h
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
                 skip = true;
             } else if (!p.ring_mode || tok - first >= (last - first) - p.W) {
                 // (an earlier ring token is overwritten later in this same request)
-                row = pool_row(p, seq, first_pos, &err);
+                row = pool_row(p, seq, (uint32_t)first_pos, &err);
             }
             if (err && lane == 0 && q0 == 0)
                 set_err(p.dev_err, err);
@@ -466,7 +466,8 @@ cudaError_t launch_rope(RopeParams &p, bool append, int sms, cudaStream_t stream
     // An FP8 layer's values by groups of keys, where the requests are long enough to have whole
     // groups and many enough to fill the SMs: 8 requests of 700 tokens 32 us against 53 with
     // a token's values beside its keys, 8 of 100 tokens 20 against 12, 32 of one 66 against 5
-    p.v_apart = append && p.fp8 && p.n >= 2048 && p.n >= 32 * (int64_t)p.R;
+    p.v_apart = append && p.fp8 && p.n >= 2048 && p.n >= 32 * (int64_t)p.R &&
+                (int64_t)p.n * p.Hkv < (int64_t)1 << 31;
     const int nq = (p.Hq + 3) / 4 + (p.Hkv + 3) / 4 * (append && !p.v_apart ? 2 : 1);
     if (p.n == 0 || nq == 0)
         return cudaSuccess;
