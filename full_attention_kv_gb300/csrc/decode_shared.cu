@@ -20,6 +20,18 @@
 // drain before a CTA's place is free, then part 2's launch and plan).  In one kernel part 2's
 // plan is made by a spare warp during part 1, and its first loads pass the draining states.
 // merge_kernel: merges each row's states and writes bf16; it also appends the new rows.
+//
+// What bounds it (152 SMs; measured peaks 6.8 TB/s and 1.94 PFLOP/s; whole calls): many rows a
+// page, the tensor cores (128 sequences on a document of 65600 tokens, 32 / 4 heads, 131 us:
+// 1.05 PFLOP/s); few rows a page, the reads (12 pairs on prompts of 1000 to 40000 tokens, 87 us:
+// 5.6 TB/s); between them the two parts one after the other and their seams (32 sequences on
+// 32768 tokens with 64 to 4096 of their own, 55 us: 3.6 TB/s); four samples of one prompt of
+// 2048 tokens, latency (15 us).  decode.cu takes 1750, 238, 279 and 230 us for the four.
+// Part 2 beside part 1 instead of after it (warps of its own, registers shared out by
+// setmaxnreg) measured 141 us for the document and 87 against 80 for 48 verified drafts: its
+// mma.sync products share the tensor cores, and it has half of the stages.
+// Items and parts are counted in 32 bits: 64-bit divisions and the registers they held cost
+// the document 11 us and the four samples 4.
 #include "decode_tile.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
@@ -72,8 +84,12 @@ __device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
 //   pair mode (129 .. 256 rows): query tiles A and B, one warpgroup each, every page
 //   split mode (up to 128 rows): one query tile; the warpgroups, with S and O regions of
 //     their own, take the pages in turn and leave two states a row
-// Each warpgroup has an issuing warp of its own: an issuer spends about half of a step in
-// the latency of its waits and commits, and two of them keep the tensor cores fed.
+// Each warpgroup has an issuing warp of its own: an issuer spends about a third of a step in
+// the latency of its waits and commits, and two of them keep the tensor cores fed.  A step of
+// a pair takes about 1550 cycles.  Its products take about 1440: 64 cycles for a k-step of PV,
+// and 58 for one of S, whose arithmetic takes 32 but which reads 6 KB of shared memory.  (S of
+// two pages at a time reads less, but leaves TMEM one region a tile and the softmax waiting:
+// 131 us against 109 for part 1 of the document.)  The softmax warps take about 1180.
 // K and V pages pass through a ring of two-page stages in the order of their use: with L = 2
 // (pair) or 4 (split) pages of scores ahead, [K0 K1] .. [K(L-2) K(L-1)], then [V(n) K(n+L)].
 
@@ -92,7 +108,6 @@ constexpr uint32_t kColO = 256;             // S: tile t, region h at 128 t + 64
 // 16-byte pieces) both move whole 128-byte lines.
 constexpr int kOctFloats = 16 + 8 * kD;
 constexpr int kSlotFloats = 2 * kBM / 8 * kOctFloats;
-
 
 // First item of part c <= C of N items cut into C equal parts: floor(c N / C).  (shared_fits
 // bounds N, and C < 2^16.)
@@ -809,7 +824,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         // ================================================================ MMA issuers
         // The whole warp runs the loop and one elected lane issues, so that control flow
         // and descriptors stay uniform across the warp (an issuing branch of lane 0 alone
-        // took 1.3 times as long a step).
+        // took 1.3 times as long a step, products in a loop that is not unrolled 1.4 times).
         const int t = warp == 10;
         const uint32_t id_s = idesc_bf16_f32(kBM, kTileKeys, 0, 0);
         const uint32_t id_pv = idesc_bf16_f32(kBM, kD, 0, 1);
@@ -827,11 +842,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         auto issue_s = [&](uint32_t qa, int h, int b, int e) {
             const uint32_t kb = k_lo + (2 * b + e) * (kPageBytes >> 4);
             const uint32_t col = tmem + t * 128 + h * 64;
+            const bool one = elect_one();
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) {
                 const uint64_t qd = desc_join(qa + (ks >> 2) * (kQHalf >> 4) + (ks & 3) * 2, dhi);
                 const uint64_t kd = desc_join(kb + (ks >> 2) * (kPageHalf >> 4) + (ks & 3) * 2, dhi);
-                if (elect_one()) {
+                if (one) {
                     if (ks == 0)
                         tc_mma_ss_k<0>(col, qd, kd, id_s);
                     else
@@ -845,10 +861,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         auto issue_pv = [&](int h, int b, bool first) {
             const uint32_t vb = v_lo + 2 * b * (kPageBytes >> 4);
             const uint32_t o = tmem + kColO + t * 128, a = tmem + t * 128 + h * 64;
+            const bool one = elect_one();
 #pragma unroll
             for (int ks = 0; ks < kTileKeys / 16; ++ks) {
                 const uint64_t vd = desc_join(vb + ks * (2048 >> 4), dhi);
-                if (elect_one()) {
+                if (one) {
                     if (ks == 0)
                         tc_mma_ts(o, a, vd, id_pv, first ? 0u : 1u);
                     else
@@ -1185,7 +1202,7 @@ __device__ __forceinline__ float load_if(const float *p, bool on, float other)
 // (eight rows, sixteen dimensions) collects its rows' m and l 32 states at a time, four lanes
 // a row, turns them into weights, and reads o with the weights at hand.  Bound by the length
 // of its instruction stream and the latency of its reads (0.6 us each from L2), not by their
-// 20 to 30 MB: pointers step instead of being computed a state (that version ran 4000
+// bytes (7 to 11 us for 8 to 26 MB of states): pointers step instead of being computed a state (that version ran 4000
 // instructions a warp, 10 us), and four CTAs fit on an SM.
 struct MergeRow {  // a row's states: own_n from own_s on, sh_n from sh_s on, sh_step floats apart
     const float *own_s, *sh_s;

@@ -23,6 +23,14 @@
 // pair never crosses lanes; chunks past rot_dim go to the remaining lanes.  A warp takes
 // four heads at a time and reads 128 contiguous bytes of each.  Each lane computes two of
 // a token's 64 angles and the warp exchanges them by shuffles, once for all heads.
+//
+// What bounds it: the reads and writes, each head once (measured copy 6.8 TB/s): 20011 tokens
+// of 32 / 4 heads in 60 us, 6.2 TB/s; with the pool 34985 tokens in 121 us, 6.2 TB/s; a ring,
+// whose 128 rows a request are few of the 7897, 29 us, 5.1 TB/s.  Five head quads in flight
+// a warp and two blocks an SM: ten quads or three blocks were no faster.  An FP8 layer is bound
+// by instructions (divisions, codes, the transposed V; 20 million a call of 7447 tokens, issued
+// in 48% of the cycles): 42 to 45 us, 3.5 TB/s.  32 tokens take 2.4 us alone and 3.5 with the pool, less
+// than the host's call.
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
