@@ -880,24 +880,25 @@ def _ctx_desc(cfg):
 
 
 # DRAM bytes per launch of a kernel from an ncu capture, keyed by (workload, kernel)
-# and by the code digest (code_digest) of the source the capture was taken on; a
+# and by the code digests (code_digest) of the sources the capture was taken on; a
 # kernel whose source has changed since reports None.  Captures of fewer
 # sequences / requests are scaled to the full launch by the units processed.
+_DECODE = "9bab9c32a1d53c3e b682c9e692da2f5e"
 TRAFFIC = {
-    # decode_kernel, full layer: 389.2 MB on 4 sequences, scaled by units
-    ("decode", "full"): ("decode.cu", "4f3057adad2ada52", 2829665666),
+    # decode_kernel, full layer: 389.3 MB on 4 sequences, scaled by units
+    ("decode", "full"): ("decode.cu decode_tile.cuh", _DECODE, 2830372955),
     # decode_kernel, sliding layer: full-size launch (32 sequences)
-    ("decode", "sliding"): ("decode.cu", "4f3057adad2ada52", 8786944),
+    ("decode", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 8786944),
     # decode_kernel, FP8 full layer: 202.1 MB (E4M3 and E5M2) on 4
     # sequences, scaled by units
-    ("decode", "full_fp8"): ("decode.cu", "4f3057adad2ada52", 1469597851),
-    ("decode", "full_e5m2"): ("decode.cu", "4f3057adad2ada52", 1469201390),
+    ("decode", "full_fp8"): ("decode.cu decode_tile.cuh", _DECODE, 1469048761),
+    ("decode", "full_e5m2"): ("decode.cu decode_tile.cuh", _DECODE, 1469834239),
     # decode_kernel, full layer: 1.608 GB on 1 sequence, scaled by units
-    ("long", "full"): ("decode.cu", "4f3057adad2ada52", 5674878985),
-    ("long", "sliding"): ("decode.cu", "4f3057adad2ada52", 1169664),
+    ("long", "full"): ("decode.cu decode_tile.cuh", _DECODE, 5674991021),
+    ("long", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 1169920),
     # decode_kernel, full layer, T = 4: 1.658 GB on 8 sequences, scaled by units
-    ("mtp", "full"): ("decode.cu", "4f3057adad2ada52", 11699016334),
-    ("mtp", "sliding"): ("decode.cu", "4f3057adad2ada52", 14617344),
+    ("mtp", "full"): ("decode.cu decode_tile.cuh", _DECODE, 11699113876),
+    ("mtp", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 14617088),
     # prefill_kernel, full layer: 4.985 GB on 2 requests, scaled by flops
     ("prefill", "full"): ("prefill.cu", "7128fc2d6f16d75e", 15703684589),
     # prefill_swa_kernel, sliding layer: full-size launch
@@ -924,7 +925,8 @@ def _traffic(name, key):
     t = TRAFFIC.get((name, key))
     if not t:
         return None
-    digest = code_digest(os.path.join(ROOT, "full_attention_kv_gb300", "csrc", t[0]))
+    csrc = os.path.join(ROOT, "full_attention_kv_gb300", "csrc")
+    digest = " ".join(code_digest(os.path.join(csrc, f)) for f in t[0].split())
     return t[2] if t[1] == digest else None
 
 

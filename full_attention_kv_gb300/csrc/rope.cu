@@ -29,8 +29,8 @@
 // whose 128 rows a request are few of the 7897, 29 us, 5.1 TB/s.  Five head quads in flight
 // a warp and two blocks an SM: ten quads or three blocks were no faster.  An FP8 layer is bound
 // by instructions (divisions, codes, the transposed V; 20 million a call of 7447 tokens, issued
-// in 48% of the cycles): 42 to 45 us, 3.5 TB/s.  32 tokens take 2.4 us alone and 3.5 with the pool, less
-// than the host's call.
+// in 48% of the cycles): 42 to 45 us, 3.5 TB/s.  32 tokens take 2.4 us alone and 3.5 with the
+// pool, less than the host's call.
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
