@@ -84,8 +84,10 @@ __device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
 //   pair mode (129 .. 256 rows): query tiles A and B, one warpgroup each, every page
 //   split mode (up to 128 rows): one query tile; the warpgroups, with S and O regions of
 //     their own, take the pages in turn and leave two states a row
-// Each warpgroup has an issuing warp of its own: an issuer spends about a third of a step in
-// the latency of its waits and commits, and two of them keep the tensor cores fed.  A step of
+// Each warpgroup has an issuing warp of its own: one warp issues a product in about 90 cycles
+// and spends a third of a step in the latency of its waits and commits, and two of them keep
+// the tensor cores fed (one for both tiles, S of one between PV of the other: 186 us against
+// 131 for the document; a third for PV: 135).  A step of
 // a pair takes about 1550 cycles.  Its products take about 1440: 64 cycles for a k-step of PV,
 // and 58 for one of S, whose arithmetic takes 32 but which reads 6 KB of shared memory.  (S of
 // two pages at a time reads less, but leaves TMEM one region a tile and the softmax waiting:
