@@ -1170,7 +1170,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 // ------------------------------------------------------------------------ merge, append
 
 constexpr int kMergeThreads = 256;  // eight rows x 32 pieces of four dimensions
-constexpr int kMergeSpread = 200 * 1024;  // shared memory an SM has for its merge CTAs, spread below
 constexpr int kMergeCap = 32;       // states whose weights are kept at a time
 constexpr int kMergeBatch = 8;      // states whose loads are in flight together
 
@@ -1211,10 +1210,24 @@ struct MergeRow {  // a row's states: own_n from own_s on, sh_n from sh_s on, sh
     int32_t own_n, sh_n, sh_step, sh_row;
 };
 
-__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_constant__ SharedParams p)
+constexpr int kMergeStatic = kMergeThreads / 32 * kMergeCap * 8 * 4 + 8 * sizeof(MergeRow);
+
+// Dynamic shared memory with which `share` merge CTAs fill an SM: 228 KB, of which each CTA has
+// 1 KB taken off and its static arrays.
+__host__ __device__ constexpr int merge_spread(int share)
+{
+    return (228 * 1024 / share - 1024 - kMergeStatic) & ~127;
+}
+
+// CTAS: on an SM.  Four have the registers to keep a batch's loads in flight; five are for
+// grids of more than four an SM (48 sequences x 4 tokens: 72 us against 74, four samples 16
+// against 15).
+template <int CTAS>
+__global__ void __launch_bounds__(kMergeThreads, CTAS) merge_kernel(const __grid_constant__ SharedParams p)
 {
     __shared__ float wt_all[kMergeThreads / 32][kMergeCap][8];
     __shared__ MergeRow merge_rows[8];
+    static_assert(sizeof(wt_all) + sizeof(merge_rows) == kMergeStatic, "static arrays");
     const DecodeParams &d = p.d;
     const int tid = threadIdx.x;
     float(&wt)[kMergeCap][8] = wt_all[tid >> 5];
@@ -1436,7 +1449,7 @@ cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
         if (e != cudaSuccess)
             return e;
         const cudaError_t m = cudaFuncSetAttribute(
-            merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSpread);
+            merge_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge_spread(1));
         if (m != cudaSuccess)
             return m;
         attr_set[MT - 1] = true;
@@ -1451,8 +1464,10 @@ cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
     // an SM to its share of the grid.
     const int64_t grid = ((int64_t)p.d.B * p.d.G * p.d.T + 7) / 8 * p.d.Hkv;
     const int64_t share = (grid + sms - 1) / sms;
-    const size_t spread = share <= 4 ? (size_t)kMergeSpread / share : 0;
-    return launch_dependent(merge_kernel, (unsigned)grid, kMergeThreads, spread, stream, p);
+    if (share > 4)
+        return launch_dependent(merge_kernel<5>, (unsigned)grid, kMergeThreads, 0, stream, p);
+    return launch_dependent(merge_kernel<4>, (unsigned)grid, kMergeThreads,
+                            (size_t)merge_spread((int)share), stream, p);
 }
 
 }  // namespace hsa
