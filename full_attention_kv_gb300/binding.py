@@ -408,6 +408,7 @@ class Rope:
 # the checks that name the fault only where that fails.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _good(t, dtype, shape):
@@ -416,9 +417,19 @@ def _good(t, dtype, shape):
 
 
 def _expect(t, name, dtype, shape):
-    if not _good(t, dtype, shape):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
         _need(t, name, dtype)
         _shape(t, name, shape)
+
+
+def _err_ptr(t):
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()
+            and t.numel() >= 1):
+        _need_err(t)
+    return t.data_ptr()
 
 
 def _need_rank(t, name, dtype, ndim):
@@ -432,7 +443,7 @@ def _place(stream, *ts):
     for t in ts:
         if t is not None and t.get_device() != dev:
             _same_device(ts[0], *ts)
-    if dev >= 0 and dev != torch.cuda.current_device():
+    if dev >= 0 and dev != _raw_device():
         raise ValueError("tensors on cuda:%d, but the current device is cuda:%d"
                          % (dev, torch.cuda.current_device()))
     if stream is None and dev >= 0 and _raw_stream is not None:
@@ -545,13 +556,12 @@ def hsa_rope_kv_append(pool, layer, rope, q, k_new, v_new, cu_tokens, seq_idx, s
     if positions is not None:
         _positions(rope, positions, n)
         pos = positions.data_ptr()
-    _need_err(dev_err)
+    err = _err_ptr(dev_err)
     stream = _place(stream, k_new, q, v_new, cu_tokens, seq_idx, start_pos, positions, q_out, k_out,
                     dev_err, pool.block_tables)
     s = lib().hsa_rope_kv_append(pool.ref(), int(layer), rope.ref, qp, qs, k_new.data_ptr(), ks,
                                  v_new.data_ptr(), vs, pos, cu_tokens.data_ptr(),
-                                 seq_idx.data_ptr(), start_pos.data_ptr(), R, n, qo, ko,
-                                 None if dev_err is None else dev_err.data_ptr(), stream)
+                                 seq_idx.data_ptr(), start_pos.data_ptr(), R, n, qo, ko, err, stream)
     if s != HSA_OK:
         raise HsaError("hsa_rope_kv_append", s)
     return q_out, k_out
@@ -678,7 +688,7 @@ def hsa_decode_attn_shared(pool, layer, q, k_new, v_new, cached_len, cu_group, s
         workspace = decode_shared_workspace(pool, B, T, n_groups, device=q.device)
     else:
         _need(workspace, "workspace", torch.uint8)
-    _need_err(dev_err)
+    err = _err_ptr(dev_err)
     stream = _place(stream, q, k_new, v_new, cached_len, cu_group, shared_len, out, workspace,
                     dev_err, pool.block_tables)
     opts = (HSA_DECODE_APPEND if append else 0) | \
@@ -687,8 +697,7 @@ def hsa_decode_attn_shared(pool, layer, q, k_new, v_new, cached_len, cu_group, s
                                      v_new.data_ptr(), cached_len.data_ptr(), cu_group.data_ptr(),
                                      shared_len.data_ptr(), n_groups, B, T, float(scale),
                                      out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                     int(max_ctas), opts,
-                                     None if dev_err is None else dev_err.data_ptr(), stream)
+                                     int(max_ctas), opts, err, stream)
     if s != HSA_OK:
         raise HsaError("hsa_decode_attn_shared", s)
     return out
