@@ -390,7 +390,8 @@ size_t hsa_decode_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T)
     const int hkv = pools ? pools->Hkv : 0;
     if (B < 0 || hkv <= 0)
         return 0;
-    return hsa::decode_workspace_bytes(std::max(sms > 0 ? sms : 1, B * hkv), B, hkv);
+    return hsa::decode_workspace_bytes(std::max(sms > 0 ? sms : 1, B * hkv),
+                                       hsa::decode_counted(pools, B), hkv);
 }
 
 }  // extern "C"
@@ -422,14 +423,10 @@ hsa_status decode_host_check(const hsa_pools *pools, int32_t layer, const void *
     return HSA_OK;
 }
 
-}  // namespace hsa
-
-namespace {
-
-hsa_status decode_common(const hsa_pools *pools, int32_t layer, const void *q, const void *k_new,
-                         const void *v_new, const int32_t *cached_len, int32_t B, int32_t T,
-                         float scale, void *out, void *workspace, size_t ws_bytes,
-                         int32_t max_ctas, int32_t *dev_err, void *stream, int32_t options)
+hsa_status decode_attn(const hsa_pools *pools, int32_t layer, const void *q, const void *k_new,
+                       const void *v_new, const int32_t *cached_len, int32_t B, int32_t T,
+                       float scale, void *out, void *workspace, size_t ws_bytes, int32_t max_ctas,
+                       int32_t *dev_err, void *stream, int32_t options, int32_t counted)
 {
     if (options & ~(HSA_DECODE_APPEND | HSA_DECODE_EARLY_POOL_READ))
         return HSA_INVALID_ARG;
@@ -454,7 +451,9 @@ hsa_status decode_common(const hsa_pools *pools, int32_t layer, const void *q, c
     }
     if (max_ctas > 0 && ctas > max_ctas)
         ctas = max_ctas;
-    const size_t need = hsa::decode_workspace_bytes(ctas, B, pools->Hkv);
+    if (counted == 0)
+        counted = hsa::decode_counted(pools, B);
+    const size_t need = hsa::decode_workspace_bytes(ctas, counted, pools->Hkv);
     if (!workspace || ws_bytes < need || !aligned16(workspace))
         return HSA_INVALID_ARG;
 
@@ -482,7 +481,8 @@ hsa_status decode_common(const hsa_pools *pools, int32_t layer, const void *q, c
     p.block_tables = pools->block_tables;
     p.ring_row = pools->ring_row;
     p.out = static_cast<__nv_bfloat16 *>(out);
-    p.ws = static_cast<uint8_t *>(workspace);
+    p.ws = static_cast<uint8_t *>(workspace) + hsa::decode_counter_bytes(counted, pools->Hkv) -
+           hsa::decode_counter_bytes(B, pools->Hkv);
     p.dev_err = dev_err;
     p.k_dst = static_cast<uint4 *>(pools->k[layer]);
     p.v_dst = static_cast<uint4 *>(pools->v[layer]);
@@ -503,7 +503,7 @@ hsa_status decode_common(const hsa_pools *pools, int32_t layer, const void *q, c
                : HSA_CUDA_ERROR;
 }
 
-}  // namespace
+}  // namespace hsa
 
 extern "C" {
 
@@ -512,8 +512,8 @@ hsa_status hsa_decode_attn(const hsa_pools *pools, int32_t layer, const void *q,
                            int32_t B, int32_t T, float scale, void *out, void *workspace,
                            size_t ws_bytes, int32_t max_ctas, int32_t *dev_err, void *stream)
 {
-    return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out, workspace,
-                         ws_bytes, max_ctas, dev_err, stream, 0);
+    return hsa::decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                            workspace, ws_bytes, max_ctas, dev_err, stream, 0, 0);
 }
 
 hsa_status hsa_decode_attn_append(const hsa_pools *pools, int32_t layer, const void *q,
@@ -522,8 +522,8 @@ hsa_status hsa_decode_attn_append(const hsa_pools *pools, int32_t layer, const v
                                   void *out, void *workspace, size_t ws_bytes, int32_t max_ctas,
                                   int32_t *dev_err, void *stream)
 {
-    return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out, workspace,
-                         ws_bytes, max_ctas, dev_err, stream, HSA_DECODE_APPEND);
+    return hsa::decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                            workspace, ws_bytes, max_ctas, dev_err, stream, HSA_DECODE_APPEND, 0);
 }
 
 hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void *q,
@@ -532,8 +532,8 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
                               size_t ws_bytes, int32_t max_ctas, int32_t options,
                               int32_t *dev_err, void *stream)
 {
-    return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out, workspace,
-                         ws_bytes, max_ctas, dev_err, stream, options);
+    return hsa::decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                            workspace, ws_bytes, max_ctas, dev_err, stream, options, 0);
 }
 
 size_t hsa_decode_shared_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
@@ -542,11 +542,11 @@ size_t hsa_decode_shared_workspace_bytes(const hsa_pools *pools, int32_t B, int3
     const size_t plain = hsa_decode_workspace_bytes(pools, B, T);
     if (plain == 0 || T < 1 || n_groups < 0 || pools->Hq <= 0)
         return 0;
-    const int sms = std::max(device_sms(), 1);
-    // behind the plain call's counters, which have to stay zero
-    return std::max(plain, hsa::shared_layout(hsa::decode_counter_bytes(B, pools->Hkv), sms, B, T,
-                                              pools->Hq / pools->Hkv, pools->Hkv, n_groups)
-                               .total);
+    const int sms = std::max(device_sms(), 1), Hkv = pools->Hkv;
+    // behind the plain calls' counters, which have to stay zero
+    const size_t start = hsa::decode_counter_bytes(hsa::decode_counted(pools, B), Hkv);
+    return std::max(
+        plain, hsa::shared_layout(start, sms, B, T, pools->Hq / Hkv, Hkv, n_groups).total);
 }
 
 hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const void *q,
@@ -571,15 +571,15 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     if (n_groups > 0 && (!cu_group || !shared_len))
         return HSA_INVALID_ARG;
     if (n_groups == 0 || !pools->layer_is_full[layer] || layer_fp8(pools, layer))
-        return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
-                             workspace, ws_bytes, max_ctas, dev_err, stream, options);
+        return hsa::decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                                workspace, ws_bytes, max_ctas, dev_err, stream, options, 0);
     const int sms = device_sms();
     if (sms <= 0)
         return HSA_CUDA_ERROR;
     const int ctas = max_ctas > 0 ? std::min(sms, max_ctas) : sms;
     const int Hkv = pools->Hkv, G = pools->Hq / Hkv;
-    const hsa::SharedLayout lay = hsa::shared_layout(hsa::decode_counter_bytes(B, Hkv), ctas, B, T,
-                                                     G, Hkv, n_groups);
+    const hsa::SharedLayout lay = hsa::shared_layout(
+        hsa::decode_counter_bytes(hsa::decode_counted(pools, B), Hkv), ctas, B, T, G, Hkv, n_groups);
     if (!workspace || ws_bytes < lay.total || !aligned16(workspace))
         return HSA_INVALID_ARG;
     CUtensorMap tmK, tmV, tmK32, tmV32, tmQ;
@@ -617,8 +617,8 @@ hsa_status hsa_decode_attn_shared(const hsa_pools *pools, int32_t layer, const v
     p.own_off = (int64_t)lay.own;
     p.n_groups = n_groups;
     if (!hsa::shared_fits(p))
-        return decode_common(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
-                             workspace, ws_bytes, max_ctas, dev_err, stream, options);
+        return hsa::decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out,
+                                workspace, ws_bytes, max_ctas, dev_err, stream, options, 0);
     return hsa::launch_shared(tmK, tmV, tmQ, tmK32, tmV32, p, ctas, sms,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HSA_OK

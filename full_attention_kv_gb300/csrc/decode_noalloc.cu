@@ -87,6 +87,6 @@ extern "C" hsa_status hsa_decode_attn_noalloc(const hsa_pools *pools, int32_t la
     const size_t cnt_bytes = hsa::decode_counter_bytes(B, pools->Hkv);
     if (cudaMemsetAsync(scratch, 0, cnt_bytes, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return HSA_CUDA_ERROR;
-    return hsa_decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out, scratch,
-                           kScratchBytes, ctas, dev_err, stream);
+    return hsa::decode_attn(pools, layer, q, k_new, v_new, cached_len, B, T, scale, out, scratch,
+                            kScratchBytes, ctas, dev_err, stream, 0, B);
 }

@@ -42,13 +42,26 @@ constexpr int32_t kDecodeEarly = 8;   // sliding layer: walk and load the ring b
 constexpr int32_t kDecodeE5M2 = 16;   // with kDecodeFp8: the codes are E5M2 (else E4M3)
 static_assert(sizeof(DecodeParams) <= 128, "keep the decode parameter struct <= 128 bytes");
 
-// Bytes of the arrival-counter region at the start of a decode workspace.
+// Bytes of the arrival counters of B sequences.  A workspace begins with room for those of
+// the pools' whole batch (decode_counted), so that no call's states lie where another call,
+// of more sequences, counts arrivals.  A kernel is handed the end of that room less its own
+// batch's counters, and finds its partial states right behind them.
 __host__ __device__ inline size_t decode_counter_bytes(int B, int Hkv)
 {
     return ((size_t)B * Hkv * sizeof(int32_t) + 255) & ~size_t(255);
 }
 
-size_t decode_workspace_bytes(int num_sms, int B, int Hkv);
+size_t decode_workspace_bytes(int num_sms, int counted, int Hkv);
+inline int decode_counted(const hsa_pools *pools, int B)
+{
+    return pools->batch > B ? pools->batch : B;
+}
+// hsa_decode_attn_ex on a workspace that holds counters for `counted` >= B sequences
+// (counted = 0: of the pools' batch).
+hsa_status decode_attn(const hsa_pools *pools, int32_t layer, const void *q, const void *k_new,
+                       const void *v_new, const int32_t *cached_len, int32_t B, int32_t T,
+                       float scale, void *out, void *workspace, size_t ws_bytes, int32_t max_ctas,
+                       int32_t *dev_err, void *stream, int32_t options, int32_t counted);
 // Every host-side check of a decode call except the workspace's (api.cu); HSA_OK
 // with *done = true means there is nothing to do (B = 0).
 hsa_status decode_host_check(const hsa_pools *pools, int32_t layer, const void *q,

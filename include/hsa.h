@@ -225,9 +225,12 @@ hsa_status hsa_rope_kv_append(const hsa_pools *pools, int32_t layer, const hsa_r
  *  Full layers split each sequence's pages across all SMs (flash-decoding) and
  *  merge the partial softmax states in the same kernel; that needs `workspace`
  *  of at least hsa_decode_workspace_bytes() bytes, ZERO-FILLED ONCE after
- *  allocation (every call leaves it zeroed again).  Calls sharing one workspace
- *  must not run concurrently.  After a call that set any bit in *dev_err, zero
- *  the workspace again before reusing it.
+ *  allocation (every call leaves its arrival counters, at the start, zeroed again; the
+ *  rest may hold anything).  The counters have room for pools->batch sequences, so one
+ *  workspace serves calls of any B up to the one it was sized for, in any order, on any
+ *  pools with the same batch and Hkv.  Calls sharing one workspace must not run
+ *  concurrently.  After a call that set any bit in *dev_err, zero the workspace again
+ *  before reusing it.
  *  max_ctas: 0 = one persistent CTA per SM (the default); > 0 caps the CTA count
  *  (results do not depend on it beyond rounding).
  */
@@ -299,7 +302,8 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
  *  n_groups    0 is hsa_decode_attn_ex.  Groups may be empty or of one sequence.
  *  options     as in hsa_decode_attn_ex.  The appended rows go to each sequence's own pages.
  *  workspace   at least hsa_decode_shared_workspace_bytes() bytes, with the rules of
- *              hsa_decode_attn's; a workspace of one serves hsa_decode_attn_ex too.
+ *              hsa_decode_attn's; it serves calls of fewer sequences, tokens and groups, and
+ *              hsa_decode_attn_ex's, in any order.
  *  scale       > 0
  * Offsets out of order are flagged (HSA_DEVERR_BAD_LEN) and nothing is shared then: every
  * sequence reads its own pages, with the same results.  A negative shared_len is flagged and
