@@ -41,11 +41,19 @@ namespace {
 
 // ------------------------------------------------------------------ groups
 
-// A group's shared whole pages, or 0 (nothing is shared).
+__device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
+
+// A group's shared whole pages, or 0 (nothing is shared): as many as the first member, whose
+// row they are read through, has cached.  Behind its own tokens a row may hold anything, and
+// so may a page that nobody has written; a later member's further pages are its own.
+// (Offsets in order.)
 __device__ __forceinline__ int group_pages(const SharedParams &p, int g)
 {
-    const int len = __ldg(p.shared_len + g);
-    return len > 0 ? min(len / kTileKeys, p.d.max_blocks) : 0;
+    const int b = __ldg(p.cu_group + g);
+    if (b >= __ldg(p.cu_group + g + 1))
+        return 0;
+    const int len = min(__ldg(p.shared_len + g), __ldg(p.d.cached_len + b));
+    return min(clamp_len(len) / kTileKeys, p.d.max_blocks);
 }
 
 // Whether cu_group is 0 = cu[0] <= cu[1] <= ... <= cu[n] = B.  Called by a whole warp.
@@ -74,8 +82,6 @@ __device__ __forceinline__ int group_of(const SharedParams &p, int b)
     }
     return lo;
 }
-
-__device__ __forceinline__ int clamp_len(int c) { return c < 0 ? 0 : c; }
 
 // ------------------------------------------------------------------ part 1: shared pages
 //

@@ -295,10 +295,13 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
  *              = B: group g is sequences cu_group[g] .. cu_group[g + 1] - 1
  *  shared_len  device int32 [n_groups]: tokens whose pages the group shares (>= 0).  Their
  *              whole pages, shared_len[g] / 64, have to be the same block-table entries in
- *              every row of the group (they are read through its first row) as far as a
- *              member's cached tokens go; a part of a page is each sequence's own.  A member
- *              may have fewer cached tokens than shared_len (it sees its own), but must not
- *              append then: its new rows would land in a shared page.
+ *              every row of the group as far as that member's cached tokens go; a part of a
+ *              page is each sequence's own.  A member may have fewer cached tokens than
+ *              shared_len (it sees its own), but must not append then: its new rows would
+ *              land in a shared page.  The pages are read through the first member's row and
+ *              shared as far as its cached tokens go, the others' further ones as their own:
+ *              put a member that holds them all first.  Values of the shared pages have to be
+ *              finite, also for a member that does not see them (it multiplies them by 0).
  *  n_groups    0 is hsa_decode_attn_ex.  Groups may be empty or of one sequence.
  *  options     as in hsa_decode_attn_ex.  The appended rows go to each sequence's own pages.
  *  workspace   at least hsa_decode_shared_workspace_bytes() bytes, with the rules of

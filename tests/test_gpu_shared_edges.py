@@ -1,0 +1,44 @@
+"""Shared-prefix decode at the edges of its contract: members of unlike lengths and pages that
+nobody has written.  Limits as in test_gpu_shared."""
+import pytest
+import torch
+
+import test_gpu_shared as base
+
+pytestmark = pytest.mark.gpu
+
+D, PAGE, SCALE = base.D, base.PAGE, base.SCALE
+
+
+@pytest.mark.parametrize("max_ctas", [0, 2])
+@pytest.mark.parametrize("past", ["absent", "stale"])
+def test_a_first_member_that_holds_less(past, max_ctas):
+    """Rows agree as far as a member's cached tokens go; behind its own, a short member's row
+    holds -1 or another sequence's block.  The first member is one of the short ones."""
+    hsa = base._hsa()
+    for own in ([-640, 5, -100, 130], [-300, 0, 64, -640], [-1, 70, 1, 2], [-64, -128, -63, 9]):
+        for T in (1, 3):
+            c = base.Case(hsa, [4, 2], [640, 200], own, T, 16, 2, seed=len(own) + T)
+            for i, n in enumerate(c.cached):
+                # a block of other values, and where there is no such block, none
+                c.table[i, (n + T + PAGE - 1) // PAGE:] = -1 if past == "absent" else c.spare
+            out = c.run(max_ctas=max_ctas)
+            assert int(c.err) == 0
+            c.check(out)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_members_that_all_hold_less_see_no_unwritten_page(T):
+    """Nobody holds the last shared pages: they may hold anything, NaN and infinities too."""
+    hsa = base._hsa()
+    c = base.Case(hsa, [3, 2], [640, 256], [-100, -300, -193, -70, -256], T, 32, 4, seed=4)
+    written = torch.zeros(c.kp.shape[0], PAGE, dtype=torch.bool, device="cuda")
+    for i, n in enumerate(c.cached):
+        for at in range(0, n, PAGE):
+            written[int(c.table[i, at // PAGE]), :n - at] = True
+    hole = ~written[:, None, :, None]
+    c.kp.masked_fill_(hole, float("nan"))
+    c.vp.masked_fill_(hole, float("inf"))
+    c.vp[..., 1::2].masked_fill_(hole, float("nan"))
+    c.check(c.run())
+    assert int(c.err) == 0
