@@ -807,9 +807,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         if (e == 1 && !has_y)
                             break;
                         if (blk[e] < 0 || blk[e] >= p.d.num_blocks) {
-                            // page 0 as a stand-in, masked by the softmax warps
+                            // behind the pool's last row: zeros, which the softmax warps mask
                             set_err(p.d.dev_err, HSA_DEVERR_BAD_BLOCK);
-                            blk[e] = 0;
+                            blk[e] = p.d.num_blocks;
                         }
                         const CUtensorMap *const map = e == 0 && j >= 0 ? &tmV : &tmK;
                         const int32_t row = (blk[e] * p.d.Hkv + w.h) * kTileKeys;

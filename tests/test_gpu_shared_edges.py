@@ -1,5 +1,5 @@
-"""Shared-prefix decode at the edges of its contract: members of unlike lengths and pages that
-nobody has written.  Limits as in test_gpu_shared."""
+"""Shared-prefix decode at the edges of its contract: members of unlike lengths, pages that
+nobody has written, entries that are not there.  Limits as in test_gpu_shared."""
 import pytest
 import torch
 
@@ -42,3 +42,21 @@ def test_members_that_all_hold_less_see_no_unwritten_page(T):
     c.vp[..., 1::2].masked_fill_(hole, float("nan"))
     c.check(c.run())
     assert int(c.err) == 0
+
+
+def test_bad_entries_read_no_block():
+    """The keys of an entry outside the pool are absent: no block stands in for them, whatever
+    block 0 holds."""
+    hsa = base._hsa()
+    c = base.Case(hsa, [3, 40], [640, 450], [5, 130], 1, 16, 2, seed=10)
+    # block 0 takes the place of the spare one
+    c.kp[c.spare], c.vp[c.spare] = c.kp[0].clone(), c.vp[0].clone()
+    c.table[c.table == 0] = c.spare
+    c.kp[0], c.vp[0] = float("nan"), float("nan")
+    c.table[:3, 4] = -1
+    c.table[:3, 9] = c.kp.shape[0]
+    c.table[3:, 6] = 10 ** 9
+    c.table[3:, 0] = 2 ** 31 - 1
+    out = c.run()
+    assert int(c.err) == hsa.HSA_DEVERR_BAD_BLOCK
+    c.check(out)
