@@ -108,7 +108,9 @@ constexpr int kPageBytes = kTileKeys * kD * 2;  // 16 KB: two blocks of 64 rows 
 constexpr int kPageHalf = kPageBytes / 2;
 constexpr int kRing = 5;
 constexpr int kAttendThreads = 384;         // producer 0, issuers 1 and 10, softmax 2 .. 9, plan 11
-constexpr float kFar = 60.0f;               // log2 units that P may lie above 1 before O is rescaled at once
+// Log2 units that P may lie above 1 before O is rescaled at once: more than usual pages rise,
+// and few enough that O has room for values up to 2^127 / 2^16 less the keys' count.
+constexpr float kFar = 16.0f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;             // S: tile t, region h at 128 t + 64 h; O_t at 256 + 128 t
 // A segment's states, by octets of rows: m[8], l[8], then o as [dim / 4][8 rows][4], so
@@ -1037,7 +1039,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 // The usual page -- all of its keys seen, a maximum there from pages before --
                 // takes that maximum as it is, so that no exponent waits for this page's.  P may
                 // then reach 2^kFar, which costs no precision (bf16's is relative, and the sum
-                // and O are fp32); a maximum more than kRescaleSlack higher is taken up with
+                // and O are fp32), only headroom; a maximum more than kRescaleSlack higher is taken up with
                 // the next page.
                 bool done = false;
                 if (whole && __all_sync(0xffffffffu, m_used != -INFINITY)) {

@@ -1,5 +1,6 @@
 """Shared-prefix decode at the edges of its contract: members of unlike lengths, pages that
-nobody has written, entries that are not there.  Limits as in test_gpu_shared."""
+nobody has written, entries that are not there, values near the top of bf16's range.  Limits
+as in test_gpu_shared."""
 import pytest
 import torch
 
@@ -60,3 +61,24 @@ def test_bad_entries_read_no_block():
     out = c.run()
     assert int(c.err) == hsa.HSA_DEVERR_BAD_BLOCK
     c.check(out)
+
+
+@pytest.mark.parametrize("max_ctas", [0, 1])
+def test_large_values_behind_a_leap_of_the_scores(max_ctas):
+    """Scores 2^12 to 2^56 above those of the pages before, on values of 1e30: a weight that
+    is held above 1 for a page must leave fp32 room for them."""
+    hsa = base._hsa()
+    for leap in (12, 20, 56):
+        for members in (3, 40):  # one tile of rows, two
+            c = base.Case(hsa, [members], [64 * 30], [20, 3], 1, 16, 2, seed=31, sharp=0.0)
+            c.q[:] = 1
+            c.kp.mul_(0.02)
+            # a key of all u scores 128 u D^-1/2, log2 e times that in powers of two
+            u = leap / (D * SCALE * 1.4427)
+            for i in range(7, 30):
+                c.kp[int(c.table[0, i])] += u
+            for x in (c.vp, c.v):
+                x.mul_(1e30)
+            out = c.run(max_ctas=max_ctas)
+            assert bool(out.isfinite().all())
+            c.check(out)
