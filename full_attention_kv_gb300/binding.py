@@ -172,6 +172,31 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _made(make, ref, stream):
+    """make(), a tensor for a call whose kernels run on `stream`: its memory, and what fills
+    it, belong to that stream, so that neither work still queued on the current stream nor
+    the memory's next use there can meet the kernels.  (The current stream counts as a user
+    of it, as the caller may read the result there.)"""
+    if stream is None or not ref.is_cuda:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=ref.device) if int(stream) else \
+            torch.cuda.default_stream(ref.device)
+    here = torch.cuda.current_stream(ref.device)
+    if stream.cuda_stream == here.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
+def _empty(shape, like, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    return _made(lambda: torch.empty(shape, dtype=like.dtype, device=like.device), like, stream)
+
+
 def _need(t, name, dtype, device=None, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -495,7 +520,7 @@ def hsa_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
     if q is not None:
         qs, Hq = _head_rows(q, "q", None, d, n), q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
+            q_out = _empty((n, Hq, d), q, stream)
         else:
             _expect(q_out, "q_out", torch.bfloat16, (n, Hq, d))
         qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -504,7 +529,7 @@ def hsa_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
     if k is not None:
         ks, Hkv = _head_rows(k, "k", None, d, n), k.shape[1]
         if k_out is None:
-            k_out = torch.empty((n, Hkv, d), dtype=k.dtype, device=k.device)
+            k_out = _empty((n, Hkv, d), k, stream)
         else:
             _expect(k_out, "k_out", torch.bfloat16, (n, Hkv, d))
         kp, ko = k.data_ptr(), k_out.data_ptr()
@@ -533,7 +558,7 @@ def hsa_rope_kv_append(pool, layer, rope, q, k_new, v_new, cu_tokens, seq_idx, s
     if q is not None:
         qs = _head_rows(q, "q", Hq, d, n)
         if q_out is None:
-            q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
+            q_out = _empty((n, Hq, d), q, stream)
         else:
             _expect(q_out, "q_out", torch.bfloat16, (n, Hq, d))
         qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -543,7 +568,7 @@ def hsa_rope_kv_append(pool, layer, rope, q, k_new, v_new, cu_tokens, seq_idx, s
         k_out = None
     else:
         if k_out is None:
-            k_out = torch.empty((n, Hkv, d), dtype=k_new.dtype, device=k_new.device)
+            k_out = _empty((n, Hkv, d), k_new, stream)
         else:
             _expect(k_out, "k_out", torch.bfloat16, (n, Hkv, d))
         ko = k_out.data_ptr()
@@ -599,11 +624,11 @@ def hsa_decode_attn(pool, layer, q, k_new, v_new, cached_len, scale, out=None, w
     B, T = q.shape[0], q.shape[1]
     _decode_shapes(pool, q, k_new, v_new, cached_len)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q, stream)
     _need(out, "out", torch.bfloat16, ndim=4)
     _shape(out, "out", q.shape)
     if workspace is None:
-        workspace = decode_workspace(pool, B, T, device=q.device)
+        workspace = _made(lambda: decode_workspace(pool, B, T, device=q.device), q, stream)
     _need(workspace, "workspace", torch.uint8)
     _need_err(dev_err)
     _same_device(q, out, workspace, dev_err)
@@ -681,11 +706,12 @@ def hsa_decode_attn_shared(pool, layer, q, k_new, v_new, cached_len, cu_group, s
     _expect(cu_group, "cu_group", torch.int32, (n_groups + 1,))
     _expect(shared_len, "shared_len", torch.int32, (n_groups,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q, stream)
     else:
         _expect(out, "out", torch.bfloat16, (B, T, Hq, d))
     if workspace is None:
-        workspace = decode_shared_workspace(pool, B, T, n_groups, device=q.device)
+        workspace = _made(lambda: decode_shared_workspace(pool, B, T, n_groups, device=q.device), q,
+                          stream)
     else:
         _need(workspace, "workspace", torch.uint8)
     err = _err_ptr(dev_err)
@@ -718,7 +744,7 @@ def hsa_prefill_attn(pool, layer, q, k_new, v_new, cu_rows, prefix_len, seq_idx,
     _shape(cu_rows, "cu_rows", (R + 1,))
     _shape(prefix_len, "prefix_len", (R,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q, stream)
     _need(out, "out", torch.bfloat16, ndim=3)
     _shape(out, "out", q.shape)
     _need_err(dev_err)
@@ -762,7 +788,7 @@ def hsa_window_safe_len(match_len, swa_slot_pos, W, out=None, stream=None):
     if swa_slot_pos.shape != (n, W):
         raise ValueError("swa_slot_pos must be [n, W]")
     if out is None:
-        out = torch.empty_like(match_len)
+        out = _empty(match_len.shape, match_len, stream)
     _need(out, "out", torch.int32)
     _shape(out, "out", match_len.shape)
     _same_device(match_len, swa_slot_pos, out)
@@ -780,7 +806,7 @@ def hsa_window_safe_len_bitmap(match_len, live_off, live, W, out=None, stream=No
     if live_off.shape[0] != n + 1:
         raise ValueError("live_off must be [n+1]")
     if out is None:
-        out = torch.empty_like(match_len)
+        out = _empty(match_len.shape, match_len, stream)
     _need(out, "out", torch.int32)
     _shape(out, "out", match_len.shape)
     _same_device(match_len, live_off, live, out)
