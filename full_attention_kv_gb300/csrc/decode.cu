@@ -1423,10 +1423,7 @@ cudaError_t launch_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
     const bool fp8 = (p.flags & kDecodeFp8) != 0;
     const bool ring = (p.flags & kDecodeRing) != 0;
     const size_t smem = (ring ? sizeof(SharedStorage<true>) : sizeof(SharedStorage<false>)) + 1024;
-    // the opt-in shared-memory size is set once per process (the API is not a stream
-    // operation, but setting it once keeps graph capture free of extra calls)
-    static bool attr_set[10] = {false, false, false, false, false,
-                                false, false, false, false, false};
+    static SmemOptIn opt[10];
     void (*kern)(CUtensorMap, CUtensorMap, DecodeParams);
     int which;
     constexpr int C4 = kConsumerWarps;
@@ -1449,13 +1446,9 @@ cudaError_t launch_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
         kern = MT == 1 ? decode_kernel<1, 0, false, C4> : decode_kernel<2, 0, false, C4>;
         which = MT - 1;
     }
-    if (!attr_set[which]) {
-        cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-        attr_set[which] = true;
-    }
+    const cudaError_t e = opt[which].set(kern, smem);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(((sw ? kSwWarps : kConsumerWarps) + 1) * 32);

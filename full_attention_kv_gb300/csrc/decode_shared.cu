@@ -1449,20 +1449,13 @@ cudaError_t launch_shared(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
     const size_t smem = sizeof(AttendSmem) + 1024;
     const int MT = (p.d.G * p.d.T + 15) / 16;
     auto attend = MT == 1 ? attend_kernel<1> : attend_kernel<2>;
-    // the opt-in shared-memory size is set once per process
-    static bool attr_set[2] = {false, false};
-    if (!attr_set[MT - 1]) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-        const cudaError_t m = cudaFuncSetAttribute(
-            merge_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, merge_spread(1));
-        if (m != cudaSuccess)
-            return m;
-        attr_set[MT - 1] = true;
-    }
-    const cudaError_t e = launch_dependent(attend, (unsigned)ctas, kAttendThreads, smem, stream, tmK,
+    static SmemOptIn attend_opt[2], merge_opt;
+    cudaError_t e = attend_opt[MT - 1].set(attend, smem);
+    if (e == cudaSuccess)
+        e = merge_opt.set(merge_kernel<4>, (size_t)merge_spread(1));
+    if (e != cudaSuccess)
+        return e;
+    e = launch_dependent(attend, (unsigned)ctas, kAttendThreads, smem, stream, tmK,
                                            tmV, tmQ, tmK32, tmV32, p);
     if (e != cudaSuccess)
         return e;

@@ -7,11 +7,38 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/hsa.h"
 
 struct __nv_bfloat16;
 
 namespace hsa {
+
+// A kernel's opt-in to its dynamic shared memory, which the runtime keeps for each device: set
+// at the kernel's first call on a device (it is not a stream operation, but later calls, the
+// captured ones among them, then make none).  Host threads may meet here: both then set it.
+class SmemOptIn {
+    std::atomic<uint64_t> done{0};  // bit = device; devices past 63 set it at every call
+
+public:
+    template <typename Kernel>
+    cudaError_t set(Kernel kern, size_t bytes)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return e;
+        const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit)
+            return cudaSuccess;
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess)
+            done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // The decode parameter struct is passed by value and kept at <= 128 bytes: on
 // sm_103a the decode kernel measured 19% slower with the same code when this

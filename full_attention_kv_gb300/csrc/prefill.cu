@@ -525,14 +525,10 @@ cudaError_t launch_prefill(const CUtensorMap &tmPK, const CUtensorMap &tmPV,
                            const CUtensorMap &tmQ, const PrefillParams &p, cudaStream_t stream)
 {
     const size_t smem = prefill_smem_bytes();
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-        attr_set = true;
-    }
+    static SmemOptIn opt;
+    const cudaError_t e = opt.set(prefill_kernel, smem);
+    if (e != cudaSuccess)
+        return e;
     // tiles_per_req_bound bounds the number of 128-row tiles; a CTA takes a pair of
     // them, and each request may end on an odd tile
     const int64_t pairs = ((int64_t)p.tiles_per_req_bound + p.R + 1) / 2;

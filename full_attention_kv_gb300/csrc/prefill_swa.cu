@@ -644,14 +644,10 @@ cudaError_t launch_prefill_swa(const CUtensorMap &tmQ, const CUtensorMap &tmNK, 
                                int sms, cudaStream_t stream)
 {
     const size_t smem = sizeof(SwaSmem) + 1024;
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_swa_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-        attr_set = true;
-    }
+    static SmemOptIn opt;
+    const cudaError_t e = opt.set(prefill_swa_kernel, smem);
+    if (e != cudaSuccess)
+        return e;
     // tiles_per_req_bound bounds sum_r ceil(C_r / 128); a tile here holds 128 / G rows
     const int64_t tiles = ((int64_t)p.rows / (kBM / p.G) + p.R) * p.Hkv;
     const int64_t ctas = tiles < sms ? tiles : sms;

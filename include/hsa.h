@@ -30,10 +30,7 @@
  *    appending first would overwrite ring slots the earlier queries still need.
  *  - Query head h uses KV head h / (Hq / Hkv).  A sliding-window query at
  *    position p attends positions max(0, p-W+1) .. p (W keys including itself).
- *  - One device per process: the kernels' shared-memory opt-in is set once, on the
- *    device current at a kernel's first call.  In a process that drives several
- *    GPUs a call on another device may be refused with HSA_CUDA_ERROR (the launch
- *    fails; nothing runs).
+ *  - A call runs on the current device, which has to be its tensors' and its stream's.
  */
 #ifndef HSA_H
 #define HSA_H

@@ -87,3 +87,34 @@ def test_memory_made_for_a_call_on_another_stream(name, kind):
             torch.cuda.synchronize()
             for a, b in zip(kept, want):
                 assert torch.equal(a, b)
+
+
+def test_two_host_threads_at_once():
+    """Every call from two threads, each on a stream and a workspace of its own."""
+    import threading
+    hsa = base._hsa()
+    cases = [base.Case(hsa, *base.CASES[n], seed=4) for n in ("three tokens", "odd pages")]
+    want = [c.run() for c in cases]
+    plain = [hsa.hsa_decode_attn(c.pool, 0, c.q, c.k, c.v, c.cl, SCALE) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w, p):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(50):
+                    a = c.run()
+                    b = hsa.hsa_decode_attn(c.pool, 0, c.q, c.k, c.v, c.cl, SCALE)
+                s.synchronize()
+                if not torch.equal(a, w) or not torch.equal(b, p):
+                    bad.append("values")
+        except Exception as e:  # noqa: BLE001 - told by the test's thread
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(cases, want, plain)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
