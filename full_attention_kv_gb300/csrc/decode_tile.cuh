@@ -1,5 +1,5 @@
-// decode_tile.cuh -- the tensor-core key tile and the row append that the decode kernels
-// share (decode.cu, decode_shared.cu).
+// decode_tile.cuh -- the tensor-core key tile that the decode kernels share (decode.cu,
+// decode_shared.cu).
 #pragma once
 
 #include "hsa_device.cuh"
@@ -11,7 +11,6 @@ namespace {
 constexpr int kTileKeys = 64;
 constexpr int kD = 128;
 constexpr int kMaxRows = 32;                    // G * T
-constexpr int kNewRows = 16;                    // new-token tile (T <= 4 used)
 
 // Per-warp attention state for one m-tile of 16 query rows.
 struct RowState {
@@ -174,59 +173,6 @@ __device__ __forceinline__ void run_tile(RowState &st, const uint32_t (&qa)[kD /
     }
     st.l[0] += sum0;
     st.l[1] += sum1;
-}
-
-// Append the T new K/V rows of unit (b, h) to this layer's pool or ring.  Called by
-// the CTA that completes the unit, after every read of the unit has finished.  With
-// new_k / new_v (the rows this CTA staged in shared memory, bf16, 128-byte swizzle)
-// the rows are copied from there instead of being read again from k_new / v_new.
-__device__ __forceinline__ void append_unit(const DecodeParams &p, int b, int h, int c, int tid,
-                                            int nthreads, const uint8_t *new_k = nullptr,
-                                            const uint8_t *new_v = nullptr)
-{
-    constexpr int kChunks = kD * 2 / 16;  // 16-byte chunks per row
-    const int total = 2 * p.T * kChunks;
-    const bool ring = (p.flags & kDecodeRing) != 0;
-    int rr = 0;
-    if (ring) {
-        rr = __ldg(p.ring_row + b);
-        if (rr < 0 || rr >= p.n_ring_rows) {
-            if (tid == 0)
-                set_err(p.dev_err, HSA_DEVERR_BAD_RING);
-            return;
-        }
-    }
-    for (int e = tid; e < total; e += nthreads) {
-        const int kv = e / (p.T * kChunks);
-        const int t = (e / kChunks) % p.T;
-        const int ch = e % kChunks;
-        const int64_t pos = (int64_t)c + t;
-        int64_t dst_row;
-        if (ring) {
-            dst_row = ((int64_t)rr * p.Hkv + h) * p.W + pos % p.W;
-        } else {
-            const int64_t page = pos / kTileKeys;
-            if (page >= p.max_blocks) {
-                set_err(p.dev_err, HSA_DEVERR_BAD_PAGE);
-                continue;
-            }
-            const int blk = __ldg(p.block_tables + (int64_t)b * p.max_blocks + page);
-            if (blk < 0 || blk >= p.num_blocks) {
-                set_err(p.dev_err, HSA_DEVERR_BAD_BLOCK);
-                continue;
-            }
-            dst_row = ((int64_t)blk * p.Hkv + h) * kTileKeys + pos % kTileKeys;
-        }
-        uint4 *to = kv ? p.v_dst : p.k_dst;
-        if (new_k) {
-            to[dst_row * kChunks + ch] = *reinterpret_cast<const uint4 *>(
-                (kv ? new_v : new_k) + swz128_offset(t, ch * 8, kNewRows));
-        } else {
-            const int64_t src = ((int64_t)(b * p.T + t) * p.Hkv + h) * kChunks + ch;
-            const uint4 *from = reinterpret_cast<const uint4 *>(kv ? p.v_new : p.k_new);
-            to[dst_row * kChunks + ch] = __ldg(from + src);
-        }
-    }
 }
 
 }  // namespace
