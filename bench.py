@@ -883,26 +883,26 @@ def _ctx_desc(cfg):
 # and by the code digests (code_digest) of the sources the capture was taken on; a
 # kernel whose source has changed since reports None.  Captures of fewer
 # sequences / requests are scaled to the full launch by the units processed.
-_DECODE = "9bab9c32a1d53c3e b682c9e692da2f5e"
+_DECODE = "90c3dea9ca848311 f7f26a4c41071a96"
 TRAFFIC = {
-    # decode_kernel, full layer: 389.3 MB on 4 sequences, scaled by units
-    ("decode", "full"): ("decode.cu decode_tile.cuh", _DECODE, 2830372955),
+    # decode_kernel, full layer: 389.2 MB on 4 sequences, scaled by units
+    ("decode", "full"): ("decode.cu decode_tile.cuh", _DECODE, 2829862807),
     # decode_kernel, sliding layer: full-size launch (32 sequences)
-    ("decode", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 8786944),
+    ("decode", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 8786688),
     # decode_kernel, FP8 full layer: 202.1 MB (E4M3 and E5M2) on 4
     # sequences, scaled by units
-    ("decode", "full_fp8"): ("decode.cu decode_tile.cuh", _DECODE, 1469048761),
-    ("decode", "full_e5m2"): ("decode.cu decode_tile.cuh", _DECODE, 1469834239),
+    ("decode", "full_fp8"): ("decode.cu decode_tile.cuh", _DECODE, 1469519652),
+    ("decode", "full_e5m2"): ("decode.cu decode_tile.cuh", _DECODE, 1469037569),
     # decode_kernel, full layer: 1.608 GB on 1 sequence, scaled by units
-    ("long", "full"): ("decode.cu decode_tile.cuh", _DECODE, 5674991021),
+    ("long", "full"): ("decode.cu decode_tile.cuh", _DECODE, 5674942702),
     ("long", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 1169920),
     # decode_kernel, full layer, T = 4: 1.658 GB on 8 sequences, scaled by units
-    ("mtp", "full"): ("decode.cu decode_tile.cuh", _DECODE, 11699113876),
-    ("mtp", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 14617088),
-    # prefill_kernel, full layer: 4.985 GB on 2 requests, scaled by flops
-    ("prefill", "full"): ("prefill.cu", "7128fc2d6f16d75e", 15703684589),
+    ("mtp", "full"): ("decode.cu decode_tile.cuh", _DECODE, 11699437769),
+    ("mtp", "sliding"): ("decode.cu decode_tile.cuh", _DECODE, 14617344),
+    # prefill_kernel, full layer: 4.478 GB on 2 requests, scaled by flops
+    ("prefill", "full"): ("prefill.cu", "11b48e7dcc95ecbd", 14108166903),
     # prefill_swa_kernel, sliding layer: full-size launch
-    ("prefill", "sliding"): ("prefill_swa.cu", "40cbea755aac5f81", 808964352),
+    ("prefill", "sliding"): ("prefill_swa.cu", "51d0e44debaecf1b", 808864512),
     # append_kernel, full-size launches (writes still held in L2 at the kernel's end
     # reach DRAM after it)
     ("prefill", "append_full"): ("append.cu", "436d89e400666e68", 143246080),
