@@ -176,7 +176,8 @@ struct RopeParams {
     int32_t R, batch, max_blocks, num_blocks, n_ring_rows, W;
     int32_t ring_mode;
     int32_t fp8;                 // 0 bf16, 1 E4M3, 2 E5M2
-    int32_t v_apart;             // FP8: the values by a kernel of their own (set by launch_rope)
+    int32_t v_apart;             // FP8: the values as items of their own, 16 tokens of a KV
+                                 // head each, ahead of the tokens (set by launch_rope)
 };
 
 cudaError_t launch_rope(RopeParams &p, bool append, int sms, cudaStream_t stream);

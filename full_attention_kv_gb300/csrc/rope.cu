@@ -472,10 +472,16 @@ cudaError_t launch(const RopeParams &p, unsigned blocks, cudaStream_t stream)
 cudaError_t launch_rope(RopeParams &p, bool append, int sms, cudaStream_t stream)
 {
     // An FP8 layer's values by groups of keys, where the requests are long enough to have whole
-    // groups and many enough to fill the SMs: 8 requests of 700 tokens 32 us against 53 with
-    // a token's values beside its keys, 8 of 100 tokens 20 against 12, 32 of one 66 against 5
-    p.v_apart = append && p.fp8 && p.n >= 2048 && p.n >= 32 * (int64_t)p.R &&
-                (int64_t)p.n * p.Hkv < (int64_t)1 << 31;
+    // groups and their tokens and heads many enough to fill the SMs.  us by groups, and with a
+    // token's values beside its keys:
+    //   one request, 2 KV heads: 1500 tokens 18 and 18, 2900 23 and 29; 4 heads: 1024 tokens 20
+    //   and 18, 1500 23 and 25, 4096 33 and 45; 8 heads: 700 tokens 21 and 18, 1500 21 and 35
+    //   16 requests, 4 heads: 96 tokens each 27 and 25, 128 31 and 27, 256 37 and 43; 8 heads:
+    //   64 tokens 29 and 23, 96 31 and 35
+    //   64 requests, 4 heads: 32 tokens each 33 and 25, 64 39 and 45
+    const int64_t fill = (int64_t)p.n * (p.Hkv + 4);
+    p.v_apart = append && p.fp8 && fill >= (p.n >= 300 * (int64_t)p.R ? 12000 : 18000) &&
+                p.n >= 32 * (int64_t)p.R && (int64_t)p.n * p.Hkv < (int64_t)1 << 31;
     const int nq = (p.Hq + 3) / 4 + (p.Hkv + 3) / 4 * (append && !p.v_apart ? 2 : 1);
     if (p.n == 0 || nq == 0)
         return cudaSuccess;
