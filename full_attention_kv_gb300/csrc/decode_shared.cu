@@ -22,11 +22,13 @@
 // merge_kernel: merges each row's states and writes bf16; it also appends the new rows.
 //
 // What bounds it (152 SMs; measured peaks 6.8 TB/s and 1.94 PFLOP/s; whole calls): many rows a
-// page, the tensor cores (128 sequences on a document of 65600 tokens, 32 / 4 heads, 131 us:
-// 1.05 PFLOP/s); few rows a page, the reads (12 pairs on prompts of 1000 to 40000 tokens, 87 us:
-// 5.6 TB/s); between them the two parts one after the other and their seams (32 sequences on
-// 32768 tokens with 64 to 4096 of their own, 55 us: 3.6 TB/s); four samples of one prompt of
-// 2048 tokens, latency (15 us).  decode.cu takes 1750, 238, 279 and 230 us for the four.
+// page, the tensor cores (128 sequences on a document of 65600 tokens, 32 / 4 heads, 130 us:
+// 1.07 PFLOP/s); few rows a page, the reads (32 sequences in 12 groups of 1 to 5 on prompts of
+// 1000 to 40000 tokens, 88 us: 5.5 TB/s); between them the two parts one after the other and
+// their seams (32 sequences on 32768 tokens with 64 to 4096 of their own, 56 us: 3.6 TB/s); four
+// samples of one prompt of 2048 tokens, latency (15 us).  decode.cu takes 1750, 234, 279 and
+// 224 us for the four; the last is its merge, which takes a unit's states one after the other
+// (8 units over 152 CTAs; 39 us over 16).
 // Part 2 beside part 1 instead of after it (warps of its own, registers shared out by
 // setmaxnreg) measured 141 us for the document and 87 against 80 for 48 verified drafts: its
 // mma.sync products share the tensor cores, and it has half of the stages.
@@ -141,8 +143,8 @@ __device__ __forceinline__ int part_of(int s, int N, int C)
 
 // A page of a unit in pair mode counts two items, one of a unit in split mode (a group's
 // last 128 rows or fewer) one: with equal items the CTAs that drew split units were done
-// after 31 us and the others after 57 (three groups of 352 to 704 rows).  A page belongs to
-// the CTA that holds its first item.
+// after 31 us and the others after 57 (three groups of 96, 352 and 1088 rows).  A page belongs
+// to the CTA that holds its first item.
 __host__ __device__ inline int page_items(int rows) { return rows <= kBM ? 1 : 2; }
 
 // A group's items for one head: units of 256 rows, the last one's weight by its rows.
@@ -1051,8 +1053,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         for (int i = 0; i < 16; ++i) {
                             float p0, p1;
                             exp_pair(c2, i, nb2, p0, p1);
-                            // (the row sum takes the unrounded P of a whole page: over 64 keys
-                            // bf16's rounding averages out)
+                            // (The row sum takes P before its rounding to bf16: unpacking the
+                            // rounded pairs took the document from 129 to 134 us.  Over many
+                            // keys the roundings average out; a row whose weight is on one key
+                            // is off by that key's, 2^-8 of itself at most.)
                             acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
                         }
                     const float mx = row_max();

@@ -431,9 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float base = m_used == -INFINITY ? 0.f : m_used;
             // ---- P = 2^(s scale log2e - m) as bf16 pairs, from the registers ------
             // group c4's 16 P columns land on S columns 16 c4 .. 16 c4 + 15, all read
-            // above.  On whole tiles the row sum takes the unrounded P (128 keys: the
-            // bf16 rounding averages out, relative error ~2^-12.5); on partial tiles
-            // it takes the bf16-rounded P the PV MMA uses, so rows with few keys get
+            // above.  On whole tiles the row sum takes the unrounded P (over 128 keys of
+            // like weight the bf16 rounding averages out, relative error ~2^-12.5; a row
+            // whose weight is on one key is off by that key's, 2^-8 at most); on partial
+            // tiles it takes the bf16-rounded P the PV MMA uses, so rows with few keys get
             // no scale error proportional to |O|.
             const uint64_t sc2 = f2_make(p.scale_log2, p.scale_log2);
             const uint64_t nb2 = f2_make(-base, -base);

@@ -15,8 +15,9 @@
 // million tokens.  Only its fraction of a turn matters, so the host gives inv_freq / 2 pi
 // as a 64-bit binary fraction F of a turn and the kernel takes the low 64 bits of
 // pos * F: the whole turns fall off the top, exactly, and the top 32 bits are the angle
-// to 2^-32 of a turn for every 32-bit position, negative ones too.  One integer
-// multiply; cos and sin then see an argument in [-1, 1] half turns.
+// to 2^-31 of a turn for every 32-bit position, negative ones too.  One integer
+// multiply; cos and sin then see an fp32 argument in [-1, 1] half turns, whose rounding is
+// 2^-26 of a turn at most.
 //
 // Layout: eight lanes take a head, lane c its 16-byte chunks c and c + rot_dim / 16, which
 // hold both sides of each of its eight pairs (or, interleaved, eight whole pairs), so a
@@ -26,11 +27,13 @@
 //
 // What bounds it: the reads and writes, each head once (measured copy 6.8 TB/s): 20011 tokens
 // of 32 / 4 heads in 60 us, 6.2 TB/s; with the pool 34985 tokens in 121 us, 6.2 TB/s; a ring,
-// whose 128 rows a request are few of the 7897, 29 us, 5.1 TB/s.  Five head quads in flight
+// whose 128 rows a request are few of the 7897, 29 us, 5.2 TB/s.  Five head quads in flight
 // a warp and two blocks an SM: ten quads or three blocks were no faster.  An FP8 layer is bound
-// by instructions (divisions, codes, the transposed V; 20 million a call of 7447 tokens, issued
-// in 48% of the cycles): 42 to 45 us, 3.5 TB/s.  32 tokens take 2.4 us alone and 3.5 with the
-// pool, less than the host's call.
+// by latency: 7447 tokens take 43 us, 3.5 TB/s, with 28% of the DRAM's cycles in use and
+// instructions (divisions, codes, the transposed V; 20 million) issued in 48%, as 16 warps an SM
+// wait for their loads and for each other's results, and as the last of a warp's four items
+// leaves others idle.  32 tokens take 2.4 us alone and 3.5 with the pool, less than the host's
+// call.
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"

@@ -23,7 +23,8 @@
  *    pool, a position past the block table, a ring row outside the ring) are
  *    OR-ed into *dev_err (device int32, caller zeroes it) as HSA_DEVERR_* bits;
  *    the offending item is skipped or its keys treated as absent, never trapped.
- *  - Attention calls never modify the pools; only hsa_kv_append does.
+ *  - Attention calls never modify the pools; only the appends do (hsa_kv_append,
+ *    hsa_rope_kv_append, and a decode call that is asked to append).
  *  - Attention reads pool positions < cached/prefix length only; the current
  *    step's new tokens are read from k_new/v_new.  For several new tokens on a
  *    sliding layer (MTP verify, prefill chunks) call append AFTER attention:
@@ -147,9 +148,10 @@ hsa_status hsa_kv_append(const hsa_pools *pools, int32_t layer, const void *k_ne
  *   (x, y) -> scale * (x cos t - y sin t, y cos t + x sin t)
  * Values past rot_dim pass unchanged (not scaled).  Text has one axis; an image's or a
  * video's tokens have several (time, height, width), each with a section of the pairs.
- * Angles are exact to 2^-31 of a turn at every int32 position (not an fp32 product);
- * the turn itself is fp32, rounded once to bf16.  Positions may be negative: negated
- * positions undo a rotation (scale 1).
+ * Whole turns are taken off to within 2^-31 of a turn at every int32 position (not by an
+ * fp32 product); the rest is rounded to fp32, 2^-26 of a turn at most, and the rotation is
+ * fp32, rounded once to bf16.  Positions may be negative: negated positions undo a rotation
+ * (scale 1).
  *  rot_dim       a multiple of 16 in [16, d] (else HSA_UNSUPPORTED_SHAPE)
  *  n_axes        1 .. 4
  *  interleaved   0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)
@@ -199,7 +201,8 @@ hsa_status hsa_rope(const hsa_rope_params *rope, const void *q, int64_t q_stride
  * A token of no request, or at a negative cache position, is skipped whole and flagged
  * (HSA_DEVERR_BAD_LEN): its rows of q_out and k_out stay as they were.  A token whose
  * pool row cannot be reached is flagged and not appended, but its q_out and k_out rows are
- * written.  On a sliding layer with several new tokens append only after attention.
+ * written.  ntok = 0 or R = 0: nothing is done.  On a sliding layer with several new tokens
+ * append only after attention.
  */
 hsa_status hsa_rope_kv_append(const hsa_pools *pools, int32_t layer, const hsa_rope_params *rope,
                               const void *q, int64_t q_stride, const void *k_new,
@@ -287,7 +290,11 @@ hsa_status hsa_decode_attn_ex(const hsa_pools *pools, int32_t layer, const void 
  * Decode / MTP-verify attention of a batch whose groups of sequences share their first
  * pages (a system prompt, a document, several samples of one prompt: what the prefix tree
  * hands out).  Same results as hsa_decode_attn_ex, beyond rounding; on a bf16 full layer
- * the shared pages are read once for a group instead of once for each sequence.
+ * the shared pages are read once for a group instead of once for each sequence.  Rounding:
+ * over shared pages a row's sum takes weights that the products round to bf16, so a row whose
+ * weight is on few keys may be off by a further 2^-8 of itself.  Range: weights reach 2^16
+ * between two updates of a row's maximum (2^8 in hsa_decode_attn_ex), so a value times the
+ * number of keys has to stay below 2^111.
  *  cu_group    device int32 [n_groups + 1], 0 = cu_group[0] <= ... <= cu_group[n_groups]
  *              = B: group g is sequences cu_group[g] .. cu_group[g + 1] - 1
  *  shared_len  device int32 [n_groups]: tokens whose pages the group shares (>= 0).  Their
