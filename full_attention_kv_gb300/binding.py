@@ -32,7 +32,7 @@ HSA_DEVERR_TIMEOUT = 32
 EXPORTS = ("hsa_kv_append", "hsa_rope", "hsa_rope_kv_append", "hsa_decode_workspace_bytes", "hsa_decode_attn",
            "hsa_decode_attn_append", "hsa_decode_attn_ex", "hsa_decode_attn_noalloc",
            "hsa_decode_shared_workspace_bytes", "hsa_decode_attn_shared",
-           "hsa_prefill_attn",
+           "hsa_prefill_attn", "hsa_kv_select", "hsa_kv_compact",
            "hsa_swa_prefetch",
            "hsa_window_safe_len", "hsa_window_safe_len_bitmap", "hsa_status_string")
 # every symbol include/hsa_tree.h declares
@@ -124,6 +124,10 @@ def lib():
         L.hsa_prefill_attn.restype = ctypes.c_int
         L.hsa_prefill_attn.argtypes = [pp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32, vp,
                                        vp, vp]
+        L.hsa_kv_select.restype = ctypes.c_int
+        L.hsa_kv_select.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.hsa_kv_compact.restype = ctypes.c_int
+        L.hsa_kv_compact.argtypes = [pp, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, vp, vp]
         L.hsa_swa_prefetch.restype = ctypes.c_int
         L.hsa_swa_prefetch.argtypes = [pp, i32, vp, vp, i32, vp, vp, i32, vp, vp]
         L.hsa_window_safe_len.restype = ctypes.c_int
@@ -755,6 +759,80 @@ def hsa_prefill_attn(pool, layer, q, k_new, v_new, cu_rows, prefix_len, seq_idx,
                                _stream(stream))
     _check("hsa_prefill_attn", s)
     return out
+
+
+def _weight_rows(w, name, rows, heads):
+    """w_stride of weights [rows, heads, w_stride] (fp32, w_stride a multiple of 4)."""
+    _need_rank(w, name, torch.float32, 3)
+    n = w.shape[2]
+    _expect(w, name, torch.float32, (w.shape[0] if rows is None else rows,
+                                     w.shape[1] if heads is None else heads, n))
+    if n % 4:
+        raise ValueError("%s: the row length must be a multiple of 4, got %d" % (name, n))
+    return n
+
+
+def hsa_kv_select(w, kv_len, seq_idx, budget, sinks=0, recent=0, reach=0, keep=None, new_len=None,
+                  dev_err=None, stream=None):
+    """The positions of a budget that stay -> (keep [R, heads, budget] int32, ascending, -1
+    past new_len; new_len [R] int32).  w [batch, heads, w_stride] fp32: request r is row
+    seq_idx[r], of kv_len[r] positions.  The first `sinks` and the last `recent` always stay;
+    the others by the largest weight among a position and `reach` neighbours on each side."""
+    stride = _weight_rows(w, "w", None, None)
+    _need_rank(seq_idx, "seq_idx", torch.int32, 1)
+    R, heads, budget = seq_idx.shape[0], w.shape[1], int(budget)
+    _expect(seq_idx, "seq_idx", torch.int32, (R,))
+    _expect(kv_len, "kv_len", torch.int32, (R,))
+    if budget < 0:
+        raise ValueError("budget must not be negative")
+    if keep is None:
+        keep = _empty((R, heads, budget), seq_idx, stream)
+    else:
+        _expect(keep, "keep", torch.int32, (R, heads, budget))
+    if new_len is None:
+        new_len = _empty((R,), seq_idx, stream)
+    else:
+        _expect(new_len, "new_len", torch.int32, (R,))
+    err = _err_ptr(dev_err)
+    stream = _place(stream, w, kv_len, seq_idx, keep, new_len, dev_err)
+    s = lib().hsa_kv_select(w.data_ptr(), stride, w.shape[0], heads, kv_len.data_ptr(),
+                            seq_idx.data_ptr(), R, budget, int(sinks), int(recent), int(reach),
+                            keep.data_ptr(), new_len.data_ptr(), err, stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_kv_select", s)
+    return keep, new_len
+
+
+def hsa_kv_compact(pool, layer, keep, new_len, seq_idx, dst_tables, w=None, w_dst=None, dev_err=None,
+                   stream=None):
+    """Copy the K and V rows of a full layer at keep [R, Hkv or 1, budget] (positions of
+    sequence seq_idx[r], the first new_len[r] of them) to positions 0, 1, ... of the pages
+    dst_tables [R, dst_blocks] int32, and the weights w [batch, Hkv, w_stride] to w_dst."""
+    _need_rank(keep, "keep", torch.int32, 3)
+    _need_rank(dst_tables, "dst_tables", torch.int32, 2)
+    R, heads, budget = keep.shape
+    if heads != 1 and heads != pool.Hkv:
+        raise ValueError("keep must have %d heads or one, got %d" % (pool.Hkv, heads))
+    _expect(keep, "keep", torch.int32, (R, heads, budget))
+    _expect(new_len, "new_len", torch.int32, (R,))
+    _expect(seq_idx, "seq_idx", torch.int32, (R,))
+    _expect(dst_tables, "dst_tables", torch.int32, (R, dst_tables.shape[1]))
+    wp = wd = None
+    stride = 0
+    if (w is None) != (w_dst is None):
+        raise ValueError("give w and w_dst, or neither")
+    if w is not None:
+        batch = pool.block_tables.shape[0]
+        stride = _weight_rows(w, "w", batch, pool.Hkv)
+        _expect(w_dst, "w_dst", torch.float32, (batch, pool.Hkv, stride))
+        wp, wd = w.data_ptr(), w_dst.data_ptr()
+    err = _err_ptr(dev_err)
+    stream = _place(stream, keep, new_len, seq_idx, dst_tables, w, w_dst, dev_err, pool.block_tables)
+    s = lib().hsa_kv_compact(pool.ref(), int(layer), keep.data_ptr(), heads, budget,
+                             new_len.data_ptr(), seq_idx.data_ptr(), R, dst_tables.data_ptr(),
+                             dst_tables.shape[1], wp, wd, stride, err, stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_kv_compact", s)
 
 
 def hsa_swa_prefetch(pool, layer, host_k, host_v, host_row, seq_idx, dev_err=None, stream=None):

@@ -704,6 +704,106 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
     return e == cudaSuccess ? HSA_OK : HSA_CUDA_ERROR;
 }
 
+// The weights' rows of an eviction call: fp32, w_stride a multiple of 4.
+static hsa_status check_weights(const float *w_prev, float decay, const float *w, int32_t w_stride)
+{
+    if (w_stride < 0 || w_stride % 4 != 0 || !std::isfinite(decay))
+        return HSA_INVALID_ARG;
+    return w && aligned16(w) && aligned16(w_prev) ? HSA_OK : HSA_INVALID_ARG;
+}
+
+hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_t heads,
+                         const int32_t *kv_len, const int32_t *seq_idx, int32_t R,
+                         int32_t budget, int32_t sinks, int32_t recent, int32_t reach,
+                         int32_t *keep, int32_t *new_len, int32_t *dev_err, void *stream)
+{
+    if (R < 0 || batch < 0 || heads < 1 || budget < 0 || sinks < 0 || recent < 0 || reach < 0 ||
+        (int64_t)sinks + recent > budget)
+        return HSA_INVALID_ARG;
+    if (reach > 7)
+        return HSA_UNSUPPORTED_SHAPE;
+    if (R == 0)
+        return HSA_OK;
+    const hsa_status st = check_weights(nullptr, 1.f, w, w_stride);
+    if (st != HSA_OK)
+        return st;
+    if (!kv_len || !seq_idx || !new_len || (!keep && budget > 0) || (int64_t)R * heads > (1 << 27))
+        return HSA_INVALID_ARG;
+    hsa::SelectParams p{};
+    p.w = w;
+    p.kv_len = kv_len;
+    p.seq_idx = seq_idx;
+    p.keep = keep;
+    p.new_len = new_len;
+    p.dev_err = dev_err;
+    p.w_stride = w_stride;
+    p.batch = batch;
+    p.heads = heads;
+    p.R = R;
+    p.budget = budget;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.reach = reach;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return HSA_CUDA_ERROR;
+    return hsa::launch_select(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
+}
+
+hsa_status hsa_kv_compact(const hsa_pools *pools, int32_t layer, const int32_t *keep,
+                          int32_t heads, int32_t budget, const int32_t *new_len,
+                          const int32_t *seq_idx, int32_t R, const int32_t *dst_tables,
+                          int32_t dst_blocks, const float *w, float *w_dst, int32_t w_stride,
+                          int32_t *dev_err, void *stream)
+{
+    const hsa_status st = check_pools(pools, layer);
+    if (st != HSA_OK)
+        return st;
+    if (!pools->layer_is_full[layer] || (heads != 1 && heads != pools->Hkv))
+        return HSA_UNSUPPORTED_SHAPE;
+    if (R < 0 || budget < 0 || dst_blocks < 0 || w_stride < 0 || (w == nullptr) != (w_dst == nullptr))
+        return HSA_INVALID_ARG;
+    if (w) {  // rows of every sequence: no part of one in the other
+        const hsa_status sw = check_weights(w, 1.f, w_dst, w_stride);
+        if (sw != HSA_OK)
+            return sw;
+        const int64_t n = (int64_t)pools->batch * pools->Hkv * w_stride;
+        if (w < w_dst + n && w_dst < w + n)
+            return HSA_INVALID_ARG;
+    }
+    if (R == 0 || budget == 0)
+        return HSA_OK;
+    if (!keep || !new_len || !seq_idx || !dst_tables ||
+        (int64_t)R * pools->Hkv * ((budget + 63) / 64) > INT32_MAX)
+        return HSA_INVALID_ARG;
+    hsa::CompactParams p{};
+    p.k = static_cast<uint4 *>(pools->k[layer]);
+    p.v = static_cast<uint4 *>(pools->v[layer]);
+    p.keep = keep;
+    p.new_len = new_len;
+    p.seq_idx = seq_idx;
+    p.block_tables = pools->block_tables;
+    p.dst_tables = dst_tables;
+    p.w = w;
+    p.w_dst = w_dst;
+    p.dev_err = dev_err;
+    p.heads = heads;
+    p.budget = budget;
+    p.R = R;
+    p.dst_blocks = dst_blocks;
+    p.w_stride = w_stride;
+    p.batch = pools->batch;
+    p.max_blocks = pools->max_blocks;
+    p.num_blocks = pools->num_blocks;
+    p.Hkv = pools->Hkv;
+    p.fp8 = layer_fp8(pools, layer) ? 1 : 0;
+    return hsa::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
+}
+
 hsa_status hsa_swa_prefetch(const hsa_pools *pools, int32_t layer, const void *host_k,
                             const void *host_v, int32_t n_host_rows, const int32_t *host_row,
                             const int32_t *seq_idx, int32_t n, int32_t *dev_err, void *stream)

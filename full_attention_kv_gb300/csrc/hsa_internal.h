@@ -217,6 +217,68 @@ cudaError_t launch_prefill_swa(const CUtensorMap &tmQ, const CUtensorMap &tmNewK
                                const CUtensorMap &tmRingV, const PrefillParams &p, int sms,
                                cudaStream_t stream);
 
+// Eviction by accumulated weight.
+struct WeighParams {             // decode_weights.cu
+    const __nv_bfloat16 *q;      // [B, T, Hq, d]
+    const __nv_bfloat16 *k_new;  // [B, T, Hkv, d]
+    const __nv_bfloat16 *v_new;
+    const int32_t *cached_len;   // [B]
+    const int32_t *block_tables; // [batch, max_blocks]
+    __nv_bfloat16 *out;          // [B, T, Hq, d]
+    const float *w_prev;         // [B, Hkv, w_stride] or null
+    float *w;
+    float *part;                 // workspace: partial states, slot by slot
+    float *score;                // workspace: [B, Hkv, w_stride, srow] scores in log2 units
+    int32_t *dev_err;
+    uint4 *k_pool, *v_pool;      // this layer's pools (FP8 scales; the append)
+    int32_t max_blocks, num_blocks, B, Hkv, w_stride;
+    int32_t T, G, srow;          // srow: G T rounded up to even
+    int32_t append, fp8;         // fp8: 0 bf16, 1 E4M3, 2 E5M2
+    float scale_log2, decay;
+};
+struct WeighLayout {             // byte offsets in the workspace
+    size_t part, score, total;
+};
+WeighLayout weigh_layout(int ctas, int B, int T, int G, int Hkv, int w_stride);
+cudaError_t launch_weigh(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &p,
+                         int ctas, int sms, cudaStream_t stream);
+
+struct PromptParams {            // prefill_weights.cu
+    const int32_t *cu_rows;      // [R+1]
+    const int32_t *kv_len;       // [R]
+    const int32_t *seq_idx;      // [R]
+    const int32_t *block_tables;
+    const float *w_prev;         // [batch, Hkv, w_stride] or null
+    float *w;
+    float2 *part;                // workspace: (m, l) of each slot's rows
+    int32_t *dev_err;
+    int32_t R, rows, window, Hkv, G, batch, max_blocks, num_blocks, w_stride;
+    float scale_log2, decay;
+};
+size_t prompt_workspace_bytes(int ctas, int R, int Hkv, int G, int window);
+cudaError_t launch_prompt_weights(const CUtensorMap &tmK, const CUtensorMap &tmQ,
+                                  const PromptParams &p, int ctas, cudaStream_t stream);
+
+struct SelectParams {            // kv_select.cu
+    const float *w;              // [batch, heads, w_stride]
+    const int32_t *kv_len, *seq_idx;
+    int32_t *keep, *new_len, *dev_err;
+    int32_t w_stride, batch, heads, R, budget, sinks, recent, reach;
+    int32_t held;                // keys a CTA keeps in shared memory (set by launch_select)
+};
+cudaError_t launch_select(SelectParams &p, int sms, cudaStream_t stream);
+
+struct CompactParams {           // kv_compact.cu
+    uint4 *k, *v;                // the layer's pools
+    const int32_t *keep, *new_len, *seq_idx, *block_tables, *dst_tables;
+    const float *w;
+    float *w_dst;
+    int32_t *dev_err;
+    int32_t heads, budget, R, dst_blocks, w_stride;
+    int32_t batch, max_blocks, num_blocks, Hkv, fp8;
+};
+cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream);
+
 struct SwaPrefetchParams {
     const uint4 *host_k;         // pinned host ring rows [n_host_rows, Hkv, W, d] (device-visible)
     const uint4 *host_v;

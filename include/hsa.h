@@ -24,7 +24,7 @@
  *    OR-ed into *dev_err (device int32, caller zeroes it) as HSA_DEVERR_* bits;
  *    the offending item is skipped or its keys treated as absent, never trapped.
  *  - Attention calls never modify the pools; only the appends do (hsa_kv_append,
- *    hsa_rope_kv_append, and a decode call that is asked to append).
+ *    hsa_rope_kv_append, and a decode call that is asked to append), and hsa_kv_compact.
  *  - Attention reads pool positions < cached/prefix length only; the current
  *    step's new tokens are read from k_new/v_new.  For several new tokens on a
  *    sliding layer (MTP verify, prefill chunks) call append AFTER attention:
@@ -368,6 +368,68 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
                             const int32_t *prefix_len, const int32_t *seq_idx, int32_t R,
                             int32_t rows, int32_t max_chunk, float scale, void *out,
                             int32_t *dev_err, void *stream);
+
+/*
+ * Eviction from a full layer by accumulated attention weight (the pages have no counterpart:
+ * their full layers keep every token).  A sliding layer's ring evicts by position alone; a
+ * full layer grows with its sequence, and these calls bound it: hsa_prefill_weights and
+ * hsa_decode_attn_weights sum the softmax weight that each cached key gets, hsa_kv_select
+ * chooses the positions of a budget, and hsa_kv_compact moves their rows to pages of their
+ * own, after which the sequence goes on as one of that many cached tokens.  Keys keep the
+ * rotation they were appended with: give later tokens their own positions (`positions` of
+ * hsa_rope_kv_append), not the cache's.
+ *
+ * Weights are fp32 rows w[sequence][KV head][w_stride], one value a cache position, w_stride a
+ * multiple of 4 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and the query
+ * heads of the KV head of exp(scale q.k - lse), lse the query's log of the sum over every key
+ * that it sees.  Both calls write w[j] = decay * w_prev[j] + sum; w_prev (same layout) may be
+ * w itself, or NULL: nothing before.  Positions that are new in the call count nothing from
+ * w_prev.  Entries past a sequence's tokens are left as they were.  Sums are fp32, in an
+ * order that does not change from call to call.
+ */
+
+/*
+ * The positions that stay.  Request r is row seq_idx[r] of w ([batch, heads, w_stride]), with
+ * kv_len[r] positions.  For each of the `heads` rows, of n > budget positions stay the first
+ * `sinks`, the last `recent` (sinks + recent <= budget) and, of the others, those of the
+ * largest score until the budget is full: a position's score is the largest weight among
+ * itself and its `reach` neighbours on each side (0 .. 7), NaN counting as -infinity and -0 as
+ * 0; of equal scores the lowest position.  Of n <= budget positions all stay.
+ *  keep     int32 [R, heads, budget]: the positions, ascending; -1 past new_len[r]
+ *  new_len  int32 [R]: min(kv_len[r], budget)
+ * heads is Hkv where every KV head keeps its own, or 1 for weights that the caller has summed.
+ * kv_len[r] outside 0 .. w_stride (HSA_DEVERR_BAD_LEN) and a bad sequence (HSA_DEVERR_BAD_SEQ)
+ * are flagged: nothing stays of them (new_len 0).
+ */
+hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_t heads,
+                         const int32_t *kv_len, const int32_t *seq_idx, int32_t R,
+                         int32_t budget, int32_t sinks, int32_t recent, int32_t reach,
+                         int32_t *keep, int32_t *new_len, int32_t *dev_err, void *stream);
+
+/*
+ * Moves the rows that stay.  For request r and each KV head h, the K and V rows of sequence
+ * seq_idx[r] (through block_tables) at positions keep[r][h][i], i < new_len[r], are copied to
+ * position i of the pages dst_tables[r] ([R, dst_blocks] int32, physical blocks); an FP8
+ * layer's codes and scales as they are.  Any full layer (a sliding one:
+ * HSA_UNSUPPORTED_SHAPE).  The destination pages are the caller's to hand out, and no request
+ * of the call may read or write them otherwise: a sequence's old pages, which other sequences
+ * may share, stay as they were.  Once every full layer is compacted, the destination pages
+ * become the sequence's row of the block table and new_len[r] its cached tokens.
+ *  keep     int32 [R, heads, budget] as hsa_kv_select gives them, heads = Hkv or 1 (one
+ *           list for every head; else HSA_UNSUPPORTED_SHAPE)
+ *  w, w_dst [batch, Hkv, w_stride] or both NULL: the weights moved along, w_dst[seq][h][i] =
+ *           w[seq][h][keep[r][h][i]]; must not overlap
+ * Rows of a destination page at new_len[r] and past it are left as they were.  Flagged, and
+ * not copied: a position outside the block table (HSA_DEVERR_BAD_PAGE; a negative one, or
+ * new_len[r] outside 0 .. budget, HSA_DEVERR_BAD_LEN), a bad block on either side
+ * (HSA_DEVERR_BAD_BLOCK), a destination past dst_blocks (HSA_DEVERR_BAD_PAGE), a bad sequence
+ * (HSA_DEVERR_BAD_SEQ).  A weight is copied if its position and its place lie below w_stride.
+ */
+hsa_status hsa_kv_compact(const hsa_pools *pools, int32_t layer, const int32_t *keep,
+                          int32_t heads, int32_t budget, const int32_t *new_len,
+                          const int32_t *seq_idx, int32_t R, const int32_t *dst_tables,
+                          int32_t dst_blocks, const float *w, float *w_dst, int32_t w_stride,
+                          int32_t *dev_err, void *stream);
 
 /*
  * Layerwise SWA-KV prefetch [youleyou s2 "KVCache系统重构": the SWA layers' KV is

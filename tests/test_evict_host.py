@@ -1,0 +1,109 @@
+"""Host side of the eviction entry points, without a GPU: refusals of the C ABI and of the
+binding, and the order of the selection kernel's keys."""
+import ctypes
+import math
+import struct
+
+import pytest
+import torch
+
+import test_binding_host as host
+import test_cabi as cabi
+from full_attention_kv_gb300 import binding
+
+fake = host.fake
+M = 1 << 20
+
+
+def _f32(*shape):
+    return torch.zeros(shape, dtype=torch.float32)
+
+
+def test_select_arguments_refused():
+    import full_attention_kv_gb300 as hsa
+    L = hsa.lib()
+    INV, OK = hsa.HSA_INVALID_ARG, hsa.HSA_OK
+    base = dict(w=M, stride=64, batch=4, heads=2, n=256, seq=256, R=2, budget=16, sinks=4, recent=8, reach=1,
+                keep=2 * M, new=256)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return L.hsa_kv_select(a["w"], a["stride"], a["batch"], a["heads"], a["n"], a["seq"], a["R"], a["budget"],
+                               a["sinks"], a["recent"], a["reach"], a["keep"], a["new"], None, None)
+    for kw in (dict(w=None), dict(w=M + 4), dict(stride=62), dict(stride=-4), dict(batch=-1), dict(heads=0),
+               dict(n=None), dict(seq=None), dict(R=-1), dict(budget=-1), dict(sinks=-1), dict(recent=-1),
+               dict(reach=-1), dict(sinks=9), dict(keep=None), dict(new=None), dict(R=1 << 27),
+               dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1)):
+        assert call(**kw) == INV, kw
+    assert call(reach=8) == hsa.HSA_UNSUPPORTED_SHAPE
+    assert call(R=0, w=None, n=None, seq=None, keep=None, new=None) == OK
+
+
+def test_compact_arguments_refused():
+    import full_attention_kv_gb300 as hsa
+    L = hsa.lib()
+    INV, SHAPE, OK = hsa.HSA_INVALID_ARG, hsa.HSA_UNSUPPORTED_SHAPE, hsa.HSA_OK
+    base = dict(p=ctypes.byref(cabi._pools(hsa)), layer=1, keep=M, heads=4, budget=64, new=256, seq=256, R=2, dst=512,
+                blocks=1, w=2 * M, wd=3 * M, stride=64)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return L.hsa_kv_compact(a["p"], a["layer"], a["keep"], a["heads"], a["budget"], a["new"], a["seq"], a["R"], a["dst"],
+                                a["blocks"], a["w"], a["wd"], a["stride"], None, None)
+    assert call(layer=0) == SHAPE  # a ring evicts by position
+    assert call(heads=2) == SHAPE and call(heads=0) == SHAPE
+    for kw in (dict(p=None), dict(layer=2), dict(keep=None), dict(budget=-1), dict(new=None), dict(seq=None), dict(R=-1),
+               dict(dst=None), dict(blocks=-1), dict(w=None), dict(wd=None), dict(w=2 * M + 4), dict(wd=3 * M + 8),
+               dict(stride=63), dict(stride=-4), dict(wd=2 * M), dict(wd=2 * M + 16), dict(wd=2 * M - 16),
+               dict(R=1 << 30)):
+        assert call(**kw) == INV, kw
+    assert call(R=0, keep=None, dst=None) == OK and call(budget=0) == OK
+    for change, layer, status in cabi._BAD_POOLS:
+        p = ctypes.byref(cabi._pools(hsa, **dict(change)))
+        assert call(p=p, layer=layer) in (getattr(hsa, status), SHAPE), (change, layer)
+
+
+def test_select_and_compact_binding_checks(fake):
+    i32 = host._i32
+    w = _f32(4, 2, 64)
+    keep, new = binding.hsa_kv_select(w, i32(3), i32(3), 16, sinks=1, recent=2, reach=3, stream=0)
+    name, a = fake.calls[-1]
+    assert name == "hsa_kv_select" and a[1:4] == (64, 4, 2) and a[6:11] == (3, 16, 1, 2, 3)
+    assert keep.shape == (3, 2, 16) and new.shape == (3,)
+    pool = host._pool()
+    binding.hsa_kv_compact(pool, 1, keep, new, i32(3), i32(3, 5), w=w, w_dst=w.clone(), stream=0)
+    name, a = fake.calls[-1]
+    assert name == "hsa_kv_compact" and a[3:5] == (2, 16) and a[7] == 3 and a[9] == 5 and a[12] == 64
+    binding.hsa_kv_compact(pool, 1, keep[:, :1].contiguous(), new, i32(3), i32(3, 5), stream=0)
+    assert fake.calls[-1][1][3] == 1 and fake.calls[-1][1][10] is None
+    done = len(fake.calls)
+    for args, kw in [((w, i32(2), i32(3), 16), {}), ((_f32(4, 2, 62), i32(3), i32(3), 16), {}), ((w[0], i32(3), i32(3), 16), {}),
+                     ((w, i32(3), i32(3), -1), {}), ((w, i32(3), i32(3), 16), dict(keep=i32(3, 2, 15))),
+                     ((w, i32(3), i32(3), 16), dict(new_len=i32(4))), ((w[:, :, ::2], i32(3), i32(3), 16), {})]:
+        with pytest.raises(ValueError):
+            binding.hsa_kv_select(*args, stream=0, **kw)
+    with pytest.raises(TypeError):
+        binding.hsa_kv_select(w.double(), i32(3), i32(3), 16, stream=0)
+    for kw in (dict(keep=i32(3, 3, 16)), dict(new=i32(2)), dict(seq=i32(4)), dict(dst=i32(2, 5)), dict(w=w), dict(wd=w),
+               dict(w=_f32(3, 2, 64), wd=_f32(3, 2, 64)), dict(w=w, wd=_f32(4, 2, 60)), dict(w=_f32(4, 1, 64), wd=_f32(4, 1, 64))):
+        with pytest.raises(ValueError):
+            binding.hsa_kv_compact(pool, 1, kw.get("keep", keep), kw.get("new", new), kw.get("seq", i32(3)),
+                                   kw.get("dst", i32(3, 5)), w=kw.get("w"), w_dst=kw.get("wd"), stream=0)
+    assert len(fake.calls) == done
+
+
+def _key(x):
+    """The kernel's integer of an fp32 value."""
+    x = -math.inf if math.isnan(x) else x + 0.0
+    u = struct.unpack("<I", struct.pack("<f", x))[0]
+    return u ^ (0xffffffff if u >> 31 else 0x80000000)
+
+
+def test_key_order():
+    tiny = 2.0 ** -149
+    v = [-math.inf, -3.4e38, -1.0, -2.0 ** -126, -tiny, 0.0, tiny, 2.0 ** -126, 1e-4, 1.0, 1.0 + 2.0 ** -23, 3.4e38, math.inf]
+    keys = [_key(x) for x in v]
+    assert keys == sorted(set(keys)) and keys[0] > 0
+    assert _key(-0.0) == _key(0.0) and _key(math.nan) == _key(-math.inf)
+    # of the lowest key's digit nothing reaches the mark of a position that does not compete
+    assert (keys[0] >> 21 << 21) - 1 > 0
