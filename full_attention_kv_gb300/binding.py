@@ -32,6 +32,7 @@ HSA_DEVERR_TIMEOUT = 32
 EXPORTS = ("hsa_kv_append", "hsa_rope", "hsa_rope_kv_append", "hsa_decode_workspace_bytes", "hsa_decode_attn",
            "hsa_decode_attn_append", "hsa_decode_attn_ex", "hsa_decode_attn_noalloc",
            "hsa_decode_shared_workspace_bytes", "hsa_decode_attn_shared",
+           "hsa_decode_weights_workspace_bytes", "hsa_decode_attn_weights",
            "hsa_prefill_attn", "hsa_kv_select", "hsa_kv_compact",
            "hsa_swa_prefetch",
            "hsa_window_safe_len", "hsa_window_safe_len_bitmap", "hsa_status_string")
@@ -124,6 +125,11 @@ def lib():
         L.hsa_prefill_attn.restype = ctypes.c_int
         L.hsa_prefill_attn.argtypes = [pp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32, vp,
                                        vp, vp]
+        L.hsa_decode_weights_workspace_bytes.restype = sz
+        L.hsa_decode_weights_workspace_bytes.argtypes = [pp, i32, i32, i32]
+        L.hsa_decode_attn_weights.restype = ctypes.c_int
+        L.hsa_decode_attn_weights.argtypes = [pp, i32, vp, vp, vp, vp, i32, i32, f32, vp, vp, f32, vp,
+                                              i32, vp, sz, i32, i32, vp, vp]
         L.hsa_kv_select.restype = ctypes.c_int
         L.hsa_kv_select.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
         L.hsa_kv_compact.restype = ctypes.c_int
@@ -770,6 +776,55 @@ def _weight_rows(w, name, rows, heads):
     if n % 4:
         raise ValueError("%s: the row length must be a multiple of 4, got %d" % (name, n))
     return n
+
+
+def hsa_decode_weights_workspace_bytes(pool, B, T, w_stride):
+    return int(lib().hsa_decode_weights_workspace_bytes(pool.ref(), int(B), int(T), int(w_stride)))
+
+
+def decode_weights_workspace(pool, B, T, w_stride, device="cuda"):
+    """Workspace for hsa_decode_attn_weights (allocate once, reuse; any contents)."""
+    n = hsa_decode_weights_workspace_bytes(pool, B, T, w_stride)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def hsa_decode_attn_weights(pool, layer, q, k_new, v_new, cached_len, scale, w, w_prev=None, decay=1.0,
+                            out=None, workspace=None, max_ctas=0, dev_err=None, stream=None,
+                            append=False):
+    """Decode attention over a full layer that also weighs its keys: w [B, Hkv, w_stride] fp32
+    becomes decay * w_prev + the softmax weight that the step's queries give each position
+    (w_prev: the same shape, w itself, or None: nothing before).  -> out [B, T, Hq, d]."""
+    _need_rank(q, "q", torch.bfloat16, 4)
+    B, T = q.shape[0], q.shape[1]
+    Hq, Hkv, d = pool.Hq, pool.Hkv, pool.d
+    _expect(q, "q", torch.bfloat16, (B, T, Hq, d))
+    _expect(k_new, "k_new", torch.bfloat16, (B, T, Hkv, d))
+    _expect(v_new, "v_new", torch.bfloat16, (B, T, Hkv, d))
+    _expect(cached_len, "cached_len", torch.int32, (B,))
+    stride = _weight_rows(w, "w", B, Hkv)
+    prev = None
+    if w_prev is not None:
+        _expect(w_prev, "w_prev", torch.float32, (B, Hkv, stride))
+        prev = w_prev.data_ptr()
+    if out is None:
+        out = _empty(q.shape, q, stream)
+    else:
+        _expect(out, "out", torch.bfloat16, (B, T, Hq, d))
+    if workspace is None:
+        workspace = _made(lambda: decode_weights_workspace(pool, B, T, stride, device=q.device), q, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    err = _err_ptr(dev_err)
+    stream = _place(stream, q, k_new, v_new, cached_len, w, w_prev, out, workspace, dev_err,
+                    pool.block_tables)
+    s = lib().hsa_decode_attn_weights(pool.ref(), int(layer), q.data_ptr(), k_new.data_ptr(),
+                                      v_new.data_ptr(), cached_len.data_ptr(), B, T, float(scale),
+                                      out.data_ptr(), prev, float(decay), w.data_ptr(), stride,
+                                      workspace.data_ptr(), workspace.numel(), int(max_ctas),
+                                      HSA_DECODE_APPEND if append else 0, err, stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_decode_attn_weights", s)
+    return out
 
 
 def hsa_kv_select(w, kv_len, seq_idx, budget, sinks=0, recent=0, reach=0, keep=None, new_len=None,

@@ -707,9 +707,99 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
 // The weights' rows of an eviction call: fp32, w_stride a multiple of 4.
 static hsa_status check_weights(const float *w_prev, float decay, const float *w, int32_t w_stride)
 {
-    if (w_stride < 0 || w_stride % 4 != 0 || !std::isfinite(decay))
+    if (w_stride < 0 || w_stride % 4 != 0 || w_stride > (1 << 30) || !std::isfinite(decay))
         return HSA_INVALID_ARG;
     return w && aligned16(w) && aligned16(w_prev) ? HSA_OK : HSA_INVALID_ARG;
+}
+
+// n floats at a and at b: apart, or (own) the same ones.
+static bool floats_apart(const float *a, const float *b, int64_t n, bool own)
+{
+    return (own && a == b) || a + n <= b || b + n <= a;
+}
+
+size_t hsa_decode_weights_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
+                                          int32_t w_stride)
+{
+    if (!pools || pools->Hkv <= 0 || pools->Hq <= 0 || B < 0 || T < 1 || w_stride < 0)
+        return 0;
+    return hsa::weigh_layout(std::max(device_sms(), 1), B, T, pools->Hq / pools->Hkv, pools->Hkv,
+                             w_stride).total;
+}
+
+hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const void *q,
+                                   const void *k_new, const void *v_new,
+                                   const int32_t *cached_len, int32_t B, int32_t T, float scale,
+                                   void *out, const float *w_prev, float decay, float *w,
+                                   int32_t w_stride, void *workspace, size_t ws_bytes,
+                                   int32_t max_ctas, int32_t options, int32_t *dev_err,
+                                   void *stream)
+{
+    if (options & ~HSA_DECODE_APPEND)
+        return HSA_INVALID_ARG;
+    bool done = false;
+    hsa_status st = hsa::decode_host_check(pools, layer, q, k_new, v_new, cached_len, B, T, out,
+                                           max_ctas, &done);
+    if (st != HSA_OK)
+        return st;
+    if (!pools->layer_is_full[layer])
+        return HSA_UNSUPPORTED_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return HSA_INVALID_ARG;
+    if (done)
+        return HSA_OK;
+    st = check_weights(w_prev, decay, w, w_stride);
+    if (st != HSA_OK)
+        return st;
+    const int Hkv = pools->Hkv, G = pools->Hq / Hkv;
+    if (w_prev && !floats_apart(w_prev, w, (int64_t)B * Hkv * w_stride, true))
+        return HSA_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return HSA_CUDA_ERROR;
+    const int ctas = max_ctas > 0 ? std::min(sms, max_ctas) : sms;
+    const hsa::WeighLayout lay = hsa::weigh_layout(ctas, B, T, G, Hkv, w_stride);
+    if (!workspace || ws_bytes < lay.total || !aligned16(workspace))
+        return HSA_INVALID_ARG;
+    CUtensorMap tmK, tmV;
+    const int fmt = layer_fp8(pools, layer);
+    const uint64_t rows = (uint64_t)pools->num_blocks * Hkv * pools->page_size;
+    if (fmt) {
+        if (!encode_2d_u8(&tmK, pools->k[layer], 128, rows, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_2d_u8(&tmV, pools->v[layer], 64, rows * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B))
+            return HSA_CUDA_ERROR;
+    } else if (!encode_2d(&tmK, pools->k[layer], 128, rows, 128, 64, 64) ||
+               !encode_2d(&tmV, pools->v[layer], 128, rows, 128, 64, 64)) {
+        return HSA_CUDA_ERROR;
+    }
+    hsa::WeighParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    p.cached_len = cached_len;
+    p.block_tables = pools->block_tables;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.w_prev = w_prev;
+    p.w = w;
+    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + lay.part);
+    p.score = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + lay.score);
+    p.dev_err = dev_err;
+    p.k_pool = static_cast<uint4 *>(pools->k[layer]);
+    p.v_pool = static_cast<uint4 *>(pools->v[layer]);
+    p.max_blocks = pools->max_blocks;
+    p.num_blocks = pools->num_blocks;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.w_stride = w_stride;
+    p.T = T;
+    p.G = G;
+    p.append = (options & HSA_DECODE_APPEND) != 0;
+    p.fp8 = fmt == HSA_KV_E5M2 ? 2 : fmt ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.decay = decay;
+    return hsa::launch_weigh(tmK, tmV, p, ctas, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
 }
 
 hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_t heads,
@@ -769,8 +859,7 @@ hsa_status hsa_kv_compact(const hsa_pools *pools, int32_t layer, const int32_t *
         const hsa_status sw = check_weights(w, 1.f, w_dst, w_stride);
         if (sw != HSA_OK)
             return sw;
-        const int64_t n = (int64_t)pools->batch * pools->Hkv * w_stride;
-        if (w < w_dst + n && w_dst < w + n)
+        if (!floats_apart(w, w_dst, (int64_t)pools->batch * pools->Hkv * w_stride, false))
             return HSA_INVALID_ARG;
     }
     if (R == 0 || budget == 0)

@@ -380,13 +380,42 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  * hsa_rope_kv_append), not the cache's.
  *
  * Weights are fp32 rows w[sequence][KV head][w_stride], one value a cache position, w_stride a
- * multiple of 4 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and the query
+ * multiple of 4, at most 2^30 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and the query
  * heads of the KV head of exp(scale q.k - lse), lse the query's log of the sum over every key
  * that it sees.  Both calls write w[j] = decay * w_prev[j] + sum; w_prev (same layout) may be
  * w itself, or NULL: nothing before.  Positions that are new in the call count nothing from
  * w_prev.  Entries past a sequence's tokens are left as they were.  Sums are fp32, in an
  * order that does not change from call to call.
  */
+
+/*
+ * Decode / MTP-verify attention that also weighs the cached keys.  Arguments and output as
+ * hsa_decode_attn_ex's on a full layer, bf16 or FP8 (a sliding layer: HSA_UNSUPPORTED_SHAPE);
+ * sequence b's weights are row b of w, its new tokens' at cached_len[b] + t.
+ *  decay      finite
+ *  w_stride   cached_len[b] + T have to fit: a sequence whose tokens do not is flagged
+ *             (HSA_DEVERR_BAD_LEN) and left out, its rows of out and w as they were, and not
+ *             appended
+ *  workspace  at least hsa_decode_weights_workspace_bytes() bytes for this B, T and w_stride;
+ *             its contents do not matter before or after.  It holds every score in fp32:
+ *             4 * T * Hq * B * w_stride bytes (T and Hq / Hkv's product rounded up to a
+ *             power of two) and the partial states.  Calls sharing one must
+ *             not run concurrently.
+ *  max_ctas   as in hsa_decode_attn
+ *  options    HSA_DECODE_APPEND (other bits: HSA_INVALID_ARG)
+ *  scale      > 0
+ * A key whose page cannot be read is absent (flagged as in hsa_decode_attn): its weight is 0.
+ */
+size_t hsa_decode_weights_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
+                                          int32_t w_stride);
+
+hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const void *q,
+                                   const void *k_new, const void *v_new,
+                                   const int32_t *cached_len, int32_t B, int32_t T, float scale,
+                                   void *out, const float *w_prev, float decay, float *w,
+                                   int32_t w_stride, void *workspace, size_t ws_bytes,
+                                   int32_t max_ctas, int32_t options, int32_t *dev_err,
+                                   void *stream);
 
 /*
  * The positions that stay.  Request r is row seq_idx[r] of w ([batch, heads, w_stride]), with

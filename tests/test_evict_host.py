@@ -92,6 +92,54 @@ def test_select_and_compact_binding_checks(fake):
     assert len(fake.calls) == done
 
 
+def test_decode_weights_arguments_refused():
+    import full_attention_kv_gb300 as hsa
+    L = hsa.lib()
+    INV, SHAPE, OK = hsa.HSA_INVALID_ARG, hsa.HSA_UNSUPPORTED_SHAPE, hsa.HSA_OK
+    base = dict(p=ctypes.byref(cabi._pools(hsa)), layer=1, q=M, k=2 * M, v=3 * M, c=256, B=2, T=1, scale=0.1, out=4 * M,
+                prev=5 * M, decay=1.0, w=6 * M, stride=256, ws=7 * M, bytes=1 << 40, ctas=0, opt=0)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return L.hsa_decode_attn_weights(a["p"], a["layer"], a["q"], a["k"], a["v"], a["c"], a["B"], a["T"], a["scale"], a["out"],
+                                         a["prev"], a["decay"], a["w"], a["stride"], a["ws"], a["bytes"], a["ctas"], a["opt"],
+                                         None, None)
+    for kw in (dict(p=None), dict(layer=2), dict(q=None), dict(k=None), dict(v=None), dict(c=None), dict(out=None), dict(w=None),
+               dict(q=M + 8), dict(out=4 * M + 2), dict(w=6 * M + 4), dict(prev=5 * M + 4), dict(B=-1), dict(B=3), dict(T=0),
+               dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(decay=math.nan),
+               dict(decay=-math.inf), dict(stride=255), dict(stride=-4), dict(stride=(1 << 30) + 4), dict(ctas=-1),
+               dict(opt=2), dict(opt=4), dict(prev=6 * M + 16), dict(prev=6 * M - 16)):
+        assert call(**kw) == INV, kw
+    assert call(layer=0) == SHAPE and call(T=5) == SHAPE
+    assert call(B=0) == OK
+    p = cabi._pools(hsa)
+    size = lambda B, T, n: L.hsa_decode_weights_workspace_bytes(ctypes.byref(p), B, T, n)  # noqa: E731
+    assert size(2, 1, 1024) >= 4 * 2 * 32 * 1024 and size(2, 4, 1024) >= 4 * size(2, 1, 1024) // 2
+    assert size(-1, 1, 4) == 0 and size(1, 0, 4) == 0 and size(1, 1, -4) == 0
+    assert L.hsa_decode_weights_workspace_bytes(None, 1, 1, 4) == 0
+
+
+def test_decode_weights_binding_checks(fake, monkeypatch):
+    monkeypatch.setattr(binding, "decode_weights_workspace", lambda *a, **k: torch.zeros(64, dtype=torch.uint8))
+    pool, i32, bf = host._pool(), host._i32, host._bf
+    B, T = 3, 2
+    q, k, v, cl, w = bf(B, T, host.Hq, 128), bf(B, T, host.Hkv, 128), bf(B, T, host.Hkv, 128), i32(B), _f32(B, host.Hkv, 64)
+    binding.hsa_decode_attn_weights(pool, 1, q, k, v, cl, 0.1, w, w_prev=w, append=True, stream=0)
+    name, a = fake.calls[-1]
+    assert name == "hsa_decode_attn_weights" and a[6:8] == (B, T) and a[13] == 64 and a[17] == binding.HSA_DECODE_APPEND
+    binding.hsa_decode_attn_weights(pool, 1, q, k, v, cl, 0.1, w, stream=0)
+    assert fake.calls[-1][1][10] is None and fake.calls[-1][1][17] == 0
+    done = len(fake.calls)
+    for kw in (dict(q=q[:, :, :-1]), dict(k=k[:-1]), dict(v=v[:, :1]), dict(cl=i32(2)), dict(w=_f32(B, host.Hkv, 62)),
+               dict(w=_f32(2, host.Hkv, 64)), dict(w=w[0]), dict(prev=_f32(B, host.Hkv, 60)), dict(out=bf(B, T, host.Hq, 64))):
+        with pytest.raises(ValueError):
+            binding.hsa_decode_attn_weights(pool, 1, kw.get("q", q), kw.get("k", k), kw.get("v", v), kw.get("cl", cl), 0.1,
+                                            kw.get("w", w), w_prev=kw.get("prev"), out=kw.get("out"), stream=0)
+    with pytest.raises(TypeError):
+        binding.hsa_decode_attn_weights(pool, 1, q, k, v, cl, 0.1, w.double(), stream=0)
+    assert len(fake.calls) == done
+
+
 def _key(x):
     """The kernel's integer of an fp32 value."""
     x = -math.inf if math.isnan(x) else x + 0.0
