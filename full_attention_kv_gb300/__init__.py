@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     hsa_decode_shared_workspace_bytes,
     fp8_code, hsa_decode_attn_append, hsa_decode_attn_noalloc, hsa_decode_workspace_bytes,
     hsa_kv_append, hsa_kv_compact, hsa_kv_select, decode_weights_workspace, hsa_decode_attn_weights,
-    hsa_decode_weights_workspace_bytes,
+    hsa_decode_weights_workspace_bytes, hsa_prefill_weights, hsa_prefill_weights_workspace_bytes,
+    prefill_weights_workspace,
     hsa_prefill_attn, hsa_rope, hsa_rope_kv_append, hsa_swa_prefetch, hsa_window_safe_len, hsa_window_safe_len_bitmap, lib,
     status_string)

@@ -33,6 +33,7 @@ EXPORTS = ("hsa_kv_append", "hsa_rope", "hsa_rope_kv_append", "hsa_decode_worksp
            "hsa_decode_attn_append", "hsa_decode_attn_ex", "hsa_decode_attn_noalloc",
            "hsa_decode_shared_workspace_bytes", "hsa_decode_attn_shared",
            "hsa_decode_weights_workspace_bytes", "hsa_decode_attn_weights",
+           "hsa_prefill_weights_workspace_bytes", "hsa_prefill_weights",
            "hsa_prefill_attn", "hsa_kv_select", "hsa_kv_compact",
            "hsa_swa_prefetch",
            "hsa_window_safe_len", "hsa_window_safe_len_bitmap", "hsa_status_string")
@@ -130,6 +131,11 @@ def lib():
         L.hsa_decode_attn_weights.restype = ctypes.c_int
         L.hsa_decode_attn_weights.argtypes = [pp, i32, vp, vp, vp, vp, i32, i32, f32, vp, vp, f32, vp,
                                               i32, vp, sz, i32, i32, vp, vp]
+        L.hsa_prefill_weights_workspace_bytes.restype = sz
+        L.hsa_prefill_weights_workspace_bytes.argtypes = [pp, i32, i32]
+        L.hsa_prefill_weights.restype = ctypes.c_int
+        L.hsa_prefill_weights.argtypes = [pp, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, f32, vp, i32,
+                                          vp, sz, vp, vp]
         L.hsa_kv_select.restype = ctypes.c_int
         L.hsa_kv_select.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
         L.hsa_kv_compact.restype = ctypes.c_int
@@ -825,6 +831,50 @@ def hsa_decode_attn_weights(pool, layer, q, k_new, v_new, cached_len, scale, w, 
     if s != HSA_OK:
         raise HsaError("hsa_decode_attn_weights", s)
     return out
+
+
+def hsa_prefill_weights_workspace_bytes(pool, R, window):
+    return int(lib().hsa_prefill_weights_workspace_bytes(pool.ref(), int(R), int(window)))
+
+
+def prefill_weights_workspace(pool, R, window, device="cuda"):
+    """Workspace for hsa_prefill_weights (allocate once, reuse; any contents)."""
+    n = hsa_prefill_weights_workspace_bytes(pool, R, window)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def hsa_prefill_weights(pool, layer, q, cu_rows, kv_len, seq_idx, window, scale, w, w_prev=None,
+                        decay=1.0, workspace=None, dev_err=None, stream=None):
+    """After a chunk's append: w [batch, Hkv, w_stride] fp32, rows seq_idx, becomes decay * w_prev
+    + the softmax weight that the last `window` queries of each request give every position of
+    its sequence's kv_len[r] tokens.  q [rows, Hq, d], cu_rows [R + 1] as in hsa_prefill_attn
+    -> w."""
+    _need_rank(q, "q", torch.bfloat16, 3)
+    _need_rank(seq_idx, "seq_idx", torch.int32, 1)
+    R, rows = seq_idx.shape[0], q.shape[0]
+    _expect(q, "q", torch.bfloat16, (rows, pool.Hq, pool.d))
+    _expect(cu_rows, "cu_rows", torch.int32, (R + 1,))
+    _expect(kv_len, "kv_len", torch.int32, (R,))
+    _expect(seq_idx, "seq_idx", torch.int32, (R,))
+    batch = pool.block_tables.shape[0]
+    stride = _weight_rows(w, "w", batch, pool.Hkv)
+    prev = None
+    if w_prev is not None:
+        _expect(w_prev, "w_prev", torch.float32, (batch, pool.Hkv, stride))
+        prev = w_prev.data_ptr()
+    if workspace is None:
+        workspace = _made(lambda: prefill_weights_workspace(pool, R, window, device=q.device), q, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    err = _err_ptr(dev_err)
+    stream = _place(stream, q, cu_rows, kv_len, seq_idx, w, w_prev, workspace, dev_err, pool.block_tables)
+    s = lib().hsa_prefill_weights(pool.ref(), int(layer), q.data_ptr(), cu_rows.data_ptr(),
+                                  kv_len.data_ptr(), seq_idx.data_ptr(), R, rows, int(window),
+                                  float(scale), prev, float(decay), w.data_ptr(), stride,
+                                  workspace.data_ptr(), workspace.numel(), err, stream)
+    if s != HSA_OK:
+        raise HsaError("hsa_prefill_weights", s)
+    return w
 
 
 def hsa_kv_select(w, kv_len, seq_idx, budget, sinks=0, recent=0, reach=0, keep=None, new_len=None,

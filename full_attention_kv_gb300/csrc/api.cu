@@ -802,6 +802,75 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
                : HSA_CUDA_ERROR;
 }
 
+size_t hsa_prefill_weights_workspace_bytes(const hsa_pools *pools, int32_t R, int32_t window)
+{
+    if (!pools || pools->Hkv <= 0 || pools->Hq <= 0 || R < 0 || window < 1)
+        return 0;
+    return hsa::prompt_workspace_bytes(std::max(device_sms(), 1), R, pools->Hkv,
+                                       pools->Hq / pools->Hkv, std::min(window, 64));
+}
+
+hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void *q,
+                               const int32_t *cu_rows, const int32_t *kv_len,
+                               const int32_t *seq_idx, int32_t R, int32_t rows, int32_t window,
+                               float scale, const float *w_prev, float decay, float *w,
+                               int32_t w_stride, void *workspace, size_t ws_bytes,
+                               int32_t *dev_err, void *stream)
+{
+    hsa_status st = check_pools(pools, layer);
+    if (st != HSA_OK)
+        return st;
+    if (!pools->layer_is_full[layer] || layer_fp8(pools, layer) || window > 64)
+        return HSA_UNSUPPORTED_SHAPE;
+    if (R < 0 || rows < 0 || window < 1 || !(scale > 0.f) || !std::isfinite(scale))
+        return HSA_INVALID_ARG;
+    if (R == 0 || rows == 0)
+        return HSA_OK;
+    st = check_weights(w_prev, decay, w, w_stride);
+    if (st != HSA_OK)
+        return st;
+    const int Hkv = pools->Hkv, G = pools->Hq / Hkv;
+    if (!q || !aligned16(q) || !cu_rows || !kv_len || !seq_idx ||
+        (w_prev && !floats_apart(w_prev, w, (int64_t)pools->batch * Hkv * w_stride, true)))
+        return HSA_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return HSA_CUDA_ERROR;
+    if (!workspace || !aligned16(workspace) ||
+        ws_bytes < hsa::prompt_workspace_bytes(sms, R, Hkv, G, window))
+        return HSA_INVALID_ARG;
+    CUtensorMap tmK, tmQ;
+    const uint64_t prow = (uint64_t)pools->num_blocks * Hkv * pools->page_size;
+    // boxes of a page, and of 128 / G queries x the G heads of one KV head
+    if (!encode_2d(&tmK, pools->k[layer], 128, prow, 128, 64, 64) ||
+        !encode_3d(&tmQ, q, 128, pools->Hq, rows, 64, 128 / G, G))
+        return HSA_CUDA_ERROR;
+    hsa::PromptParams p{};
+    p.cu_rows = cu_rows;
+    p.kv_len = kv_len;
+    p.seq_idx = seq_idx;
+    p.block_tables = pools->block_tables;
+    p.w_prev = w_prev;
+    p.w = w;
+    p.part = static_cast<float2 *>(workspace);
+    p.dev_err = dev_err;
+    p.R = R;
+    p.rows = rows;
+    p.window = window;
+    p.Hkv = Hkv;
+    p.G = G;
+    p.batch = pools->batch;
+    p.max_blocks = pools->max_blocks;
+    p.num_blocks = pools->num_blocks;
+    p.w_stride = w_stride;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.decay = decay;
+    return hsa::launch_prompt_weights(tmK, tmQ, p, sms, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? HSA_OK
+               : HSA_CUDA_ERROR;
+}
+
 hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_t heads,
                          const int32_t *kv_len, const int32_t *seq_idx, int32_t R,
                          int32_t budget, int32_t sinks, int32_t recent, int32_t reach,

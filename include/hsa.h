@@ -418,6 +418,30 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
                                    void *stream);
 
 /*
+ * The weight that a prompt's last queries put on every cached key.  Called after the append:
+ * request r is sequence seq_idx[r] with kv_len[r] tokens in the pool, the newest of them rows
+ * cu_rows[r] .. cu_rows[r+1]-1 of q ([rows, Hq, d] bf16, as given to hsa_prefill_attn); the
+ * last min(window, number of rows) of those weigh, row i of n rows seeing the positions up to
+ * kv_len[r] - n + i.  The weights are row seq_idx[r] of w ([pools->batch, Hkv, w_stride]).
+ *  window     1 .. 64 (else HSA_UNSUPPORTED_SHAPE)
+ *  workspace  at least hsa_prefill_weights_workspace_bytes(); as above
+ *  decay finite, scale > 0
+ * bf16 full layers (a sliding or FP8 layer: HSA_UNSUPPORTED_SHAPE, as prefill itself refuses
+ * FP8).  A sequence may appear in at most one request per call.  A request without rows is left
+ * out.  So is one that is flagged: offsets out of order or past `rows`, more rows than
+ * kv_len[r], kv_len[r] negative or past w_stride (HSA_DEVERR_BAD_LEN), a bad sequence
+ * (HSA_DEVERR_BAD_SEQ).  A key whose page cannot be read is flagged and absent.
+ */
+size_t hsa_prefill_weights_workspace_bytes(const hsa_pools *pools, int32_t R, int32_t window);
+
+hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void *q,
+                               const int32_t *cu_rows, const int32_t *kv_len,
+                               const int32_t *seq_idx, int32_t R, int32_t rows, int32_t window,
+                               float scale, const float *w_prev, float decay, float *w,
+                               int32_t w_stride, void *workspace, size_t ws_bytes,
+                               int32_t *dev_err, void *stream);
+
+/*
  * The positions that stay.  Request r is row seq_idx[r] of w ([batch, heads, w_stride]), with
  * kv_len[r] positions.  For each of the `heads` rows, of n > budget positions stay the first
  * `sinks`, the last `recent` (sinks + recent <= budget) and, of the others, those of the

@@ -140,6 +140,45 @@ def test_decode_weights_binding_checks(fake, monkeypatch):
     assert len(fake.calls) == done
 
 
+def test_prefill_weights_arguments_refused():
+    import full_attention_kv_gb300 as hsa
+    L = hsa.lib()
+    INV, SHAPE, OK = hsa.HSA_INVALID_ARG, hsa.HSA_UNSUPPORTED_SHAPE, hsa.HSA_OK
+    base = dict(p=ctypes.byref(cabi._pools(hsa)), layer=1, q=M, cu=256, n=256, seq=256, R=2, rows=40, window=16, scale=0.1,
+                prev=5 * M, decay=1.0, w=6 * M, stride=256, ws=7 * M, bytes=1 << 40)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return L.hsa_prefill_weights(a["p"], a["layer"], a["q"], a["cu"], a["n"], a["seq"], a["R"], a["rows"], a["window"],
+                                     a["scale"], a["prev"], a["decay"], a["w"], a["stride"], a["ws"], a["bytes"], None, None)
+    for kw in (dict(p=None), dict(layer=2), dict(q=None), dict(q=M + 8), dict(cu=None), dict(n=None), dict(seq=None), dict(R=-1),
+               dict(rows=-1), dict(window=0), dict(window=-1), dict(scale=0.0), dict(scale=math.nan), dict(decay=math.nan),
+               dict(w=None), dict(w=6 * M + 4), dict(prev=5 * M + 4), dict(stride=255), dict(stride=-4), dict(prev=6 * M + 16),
+               dict(stride=(1 << 30) + 4)):
+        assert call(**kw) == INV, kw
+    assert call(layer=0) == SHAPE and call(window=65) == SHAPE
+    assert call(p=ctypes.byref(cabi._pools(hsa, fp8=[0, 1]))) == SHAPE
+    assert call(R=0, q=None, w=None) == OK and call(rows=0, q=None) == OK
+    size = lambda R, n: L.hsa_prefill_weights_workspace_bytes(base["p"], R, n)  # noqa: E731
+    assert size(2, 16) > 0 and size(2, 64) == 4 * size(2, 16) and size(-1, 4) == 0 and size(1, 0) == 0
+
+
+def test_prefill_weights_binding_checks(fake, monkeypatch):
+    monkeypatch.setattr(binding, "prefill_weights_workspace", lambda *a, **k: torch.zeros(64, dtype=torch.uint8))
+    pool, i32, bf = host._pool(), host._i32, host._bf
+    q, w = bf(40, host.Hq, 128), _f32(4, host.Hkv, 64)
+    binding.hsa_prefill_weights(pool, 1, q, i32(3), i32(2), i32(2), 16, 0.1, w, w_prev=w, decay=0.5, stream=0)
+    name, a = fake.calls[-1]
+    assert name == "hsa_prefill_weights" and a[6:9] == (2, 40, 16) and a[13] == 64 and a[10] == w.data_ptr()
+    done = len(fake.calls)
+    for kw in (dict(q=q[:, :-1].contiguous()), dict(q=q[0]), dict(cu=i32(2)), dict(n=i32(3)), dict(seq=i32(3)),
+               dict(w=_f32(3, host.Hkv, 64)), dict(w=_f32(4, host.Hkv, 63)), dict(prev=_f32(4, host.Hkv, 60))):
+        with pytest.raises(ValueError):
+            binding.hsa_prefill_weights(pool, 1, kw.get("q", q), kw.get("cu", i32(3)), kw.get("n", i32(2)), kw.get("seq", i32(2)),
+                                        16, 0.1, kw.get("w", w), w_prev=kw.get("prev"), stream=0)
+    assert len(fake.calls) == done
+
+
 def _key(x):
     """The kernel's integer of an fp32 value."""
     x = -math.inf if math.isnan(x) else x + 0.0
