@@ -806,8 +806,7 @@ size_t hsa_prefill_weights_workspace_bytes(const hsa_pools *pools, int32_t R, in
 {
     if (!pools || pools->Hkv <= 0 || pools->Hq <= 0 || R < 0 || window < 1)
         return 0;
-    return hsa::prompt_workspace_bytes(std::max(device_sms(), 1), R, pools->Hkv,
-                                       pools->Hq / pools->Hkv, std::min(window, 64));
+    return hsa::prompt_workspace_bytes(std::max(device_sms(), 1), R, pools->Hkv);
 }
 
 hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void *q,
@@ -837,7 +836,7 @@ hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void
     if (sms <= 0)
         return HSA_CUDA_ERROR;
     if (!workspace || !aligned16(workspace) ||
-        ws_bytes < hsa::prompt_workspace_bytes(sms, R, Hkv, G, window))
+        ws_bytes < hsa::prompt_workspace_bytes(sms, R, Hkv))
         return HSA_INVALID_ARG;
     CUtensorMap tmK, tmQ;
     const uint64_t prow = (uint64_t)pools->num_blocks * Hkv * pools->page_size;

@@ -615,15 +615,6 @@ struct AttendSmem {
 static_assert(kGroups * kDepth * kItemBytes <= 2 * kQBytes + 2 * kRing * kPageBytes, "part 2's stages");
 static_assert(sizeof(AttendSmem) + 1024 <= 232448, "shared memory");
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r));
-    return r != 0;
-}
-
 // Position in the ring: buffer and the parity of its current phase.
 struct RingPos {
     int b;

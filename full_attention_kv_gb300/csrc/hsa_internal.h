@@ -255,7 +255,7 @@ struct PromptParams {            // prefill_weights.cu
     int32_t R, rows, window, Hkv, G, batch, max_blocks, num_blocks, w_stride;
     float scale_log2, decay;
 };
-size_t prompt_workspace_bytes(int ctas, int R, int Hkv, int G, int window);
+size_t prompt_workspace_bytes(int ctas, int R, int Hkv);
 cudaError_t launch_prompt_weights(const CUtensorMap &tmK, const CUtensorMap &tmQ,
                                   const PromptParams &p, int ctas, cudaStream_t stream);
 

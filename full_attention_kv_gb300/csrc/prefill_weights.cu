@@ -10,14 +10,15 @@
 // Pass 1 takes the rows as TMEM lanes (S = Q K^T, 128 rows x 128 keys): a thread owns a row, keeps
 // its running maximum and sum over the keys, and leaves them in the workspace.  Pass 2 takes the
 // keys as lanes (S^T = K Q^T, the same tiles in shared memory with A and B exchanged): a thread
-// owns a key, and the sum over rows is its own.  Neither sums across threads.
+// owns a key, and the sum over a tile's rows is its own.  Neither sums across threads.
 //
 // Both: persistent, one CTA an SM; the 128-key tiles (two pages) of all (request, KV head) units
 // laid end to end and cut into equal ranges.  Warp 0 loads Q (up to four tiles of 128 rows) at a
-// unit's start and streams K; one thread of warp 1 issues the MMAs into four TMEM slots of 128
-// columns, two a warpgroup; warps 2-5 and 6-9 are the two warpgroups, which take a unit's row
-// tiles in turn (pass 1; key tiles in turn where there is one row tile) or key tiles (pass 2).
-// The states of a unit's CTAs lie side by side, and their order is fixed: so are the sums.
+// unit's start and streams K; warps 1 and 2 issue the MMAs into four TMEM slots of 128 columns, one
+// a warpgroup; the four warpgroups of warps 4-19 take the (key tile, row tile) pairs in turn, a
+// unit's row tiles (1, 2 or 4 of them in the count: three as four) always the same ones.  In pass 2 the warpgroups of a key tile hand
+// their sums to the first of them through shared memory.
+// The states of a unit's CTAs lie side by side, and every order of summation is fixed.
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
 
@@ -30,17 +31,20 @@ constexpr int kHalfBytes = kBlock * 128;   // 128 rows x 64 bf16 (one swizzle co
 constexpr int kTileBytes = 2 * kHalfBytes; // 32 KB
 constexpr int kTiles = 6;                  // Q tiles and K stages together
 constexpr int kMaxStages = 4;
-constexpr int kMaxRowTiles = 4;
-constexpr int kThreads = 320;
+constexpr int kGroups = 4;                  // warpgroups, and TMEM slots
+constexpr int kIssuers = 2;
+constexpr int kThreads = 128 + kGroups * 128;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kSlack = 8.0f;             // a running maximum may lag by so much (log2 units)
+constexpr float kSlack = 60.0f;            // a running maximum may lag by so much (log2 units)
 
 struct alignas(1024) PromptSmem {
     uint8_t tile[kTiles][kTileBytes];
-    alignas(16) float neg_lse[2][kMaxRowTiles * kBlock];  // pass 2: a copy a warpgroup
+    alignas(16) float neg_lse[kGroups][kBlock];  // pass 2: of each warpgroup's rows
+    float sum[kGroups][2][kBlock];               // pass 2: its keys' sums, for the first one
     alignas(8) uint64_t q_full, q_empty, done;
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
-    uint64_t s_full[4], s_empty[4];
+    uint64_t s_full[kGroups], s_empty[kGroups];
+    uint64_t sum_full[kGroups][2], sum_free[kGroups][2];
     int32_t scan[kThreads];
     int32_t first_r, before, total;
     uint32_t tmem_base;
@@ -79,24 +83,28 @@ __device__ __forceinline__ Request request(const PromptParams &p, int r, int *er
 
 __device__ __forceinline__ int tiles_of(const Request &q) { return q.T > 0 ? (q.n + kBlock - 1) / kBlock : 0; }
 
-// Pool row of page `page` of head h, or -1: past the tokens (not loaded, masked by position), or
-// out of reach (flagged).
-__device__ __forceinline__ int64_t page_row(const PromptParams &p, const Request &q, int h, int page, bool report)
+// The block table's entry of page `page` (any value where there is none: page_at tells).  Not looked
+// at before it is used: a batch of entries is read while the batch before is on its way.
+__device__ __forceinline__ int page_entry(const PromptParams &p, const Request &q, int page)
+{
+    int blk = 0;
+    if ((int64_t)page * 64 < q.n && page < p.max_blocks)
+        asm volatile("ld.global.nc.s32 %0, [%1];"
+                     : "=r"(blk)
+                     : "l"(p.block_tables + (int64_t)q.seq * p.max_blocks + page));
+    return blk;
+}
+
+// 1: entry blk of page `page` can be read; 0: the page is past the tokens (masked by position); -1:
+// out of reach, with *err set.
+__device__ __forceinline__ int page_at(const PromptParams &p, const Request &q, int page, int blk, int *err)
 {
     if ((int64_t)page * 64 >= q.n)
-        return -1;
-    if (page >= p.max_blocks) {
-        if (report)
-            set_err(p.dev_err, HSA_DEVERR_BAD_PAGE);
-        return -1;
-    }
-    const int blk = __ldg(p.block_tables + (int64_t)q.seq * p.max_blocks + page);
-    if (blk < 0 || blk >= p.num_blocks) {
-        if (report)
-            set_err(p.dev_err, HSA_DEVERR_BAD_BLOCK);
-        return -1;
-    }
-    return ((int64_t)blk * p.Hkv + h) * 64;
+        return 0;
+    if (page < p.max_blocks && blk >= 0 && blk < p.num_blocks)
+        return 1;
+    *err = page < p.max_blocks ? HSA_DEVERR_BAD_BLOCK : HSA_DEVERR_BAD_PAGE;
+    return -1;
 }
 
 struct Walk {
@@ -170,15 +178,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) {
         mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
-        mbar_init(&sh.done, 1);
+        mbar_init(&sh.q_empty, kIssuers);
+        mbar_init(&sh.done, kIssuers);
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&sh.k_full[s], 1);
-            mbar_init(&sh.k_empty[s], 1);
+            mbar_init(&sh.k_empty[s], kIssuers);
         }
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < kGroups; ++s) {
             mbar_init(&sh.s_full[s], 1);
-            mbar_init(&sh.s_empty[s], kBlock);
+            mbar_init(&sh.s_empty[s], kBlock / 32);
+            for (int e = 0; e < 2; ++e) {
+                mbar_init(&sh.sum_full[s][e], kBlock / 32);
+                mbar_init(&sh.sum_free[s][e], kBlock / 32);
+            }
         }
         fence_barrier_init();
     }
@@ -214,12 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         } while (x.nt == 0);
     };
     auto row_tiles = [&](const Walk &x) { return (x.q.T * p.G + kBlock - 1) / kBlock; };
+    // pairs are counted tiles x step + row tile, pair e going to warpgroup e mod 4
+    auto step_of = [](int nq) { return nq == 3 ? 4 : nq; };
 
     if (warp == 0) {
         // ------------------------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
-        int64_t k = 0;       // key tiles issued
-        int units = 0;
+        int st = 0;          // next stage, and the parity of its phase
+        uint32_t ph = 0;
+        int issued = 0, units = 0;
         bool ok = true;
         for (int64_t i = i0; i < i1 && ok; ++units) {
             const int64_t end = i + min((int64_t)(w.nt - w.j), i1 - i);
@@ -238,22 +253,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // pool rows of 32 pages (16 tiles) at a time, a lane each, a batch ahead
             int j = w.j, batch = w.j;
-            int64_t cur = page_row(p, w.q, w.h, 2 * batch + lane, PASS == 1);
-            int64_t nxt = page_row(p, w.q, w.h, 2 * batch + 32 + lane, PASS == 1);
-            for (; i < end; ++i, ++j, ++k) {
+            int cur = page_entry(p, w.q, 2 * batch + lane);
+            int nxt = page_entry(p, w.q, 2 * batch + 32 + lane);
+            // the pool row of a page, or -1; flagged once, by the first pass
+            auto pool_row = [&](int page, int blk) -> int64_t {
+                int err = 0;
+                if (page_at(p, w.q, page, blk, &err) > 0)
+                    return ((int64_t)blk * p.Hkv + w.h) * 64;
+                if (PASS == 1 && err)
+                    set_err(p.dev_err, err);
+                return -1;
+            };
+            for (; i < end; ++i, ++j) {
                 if (j - batch == 16) {
                     batch = j;
                     cur = nxt;
-                    nxt = page_row(p, w.q, w.h, 2 * batch + 32 + lane, PASS == 1);
+                    nxt = page_entry(p, w.q, 2 * batch + 32 + lane);
                 }
-                const int64_t y0 = __shfl_sync(0xffffffffu, cur, 2 * (j - batch));
-                const int64_t y1 = __shfl_sync(0xffffffffu, cur, 2 * (j - batch) + 1);
+                const int b0 = __shfl_sync(0xffffffffu, cur, 2 * (j - batch));
+                const int b1 = __shfl_sync(0xffffffffu, cur, 2 * (j - batch) + 1);
                 if (lane == 0 && ok) {
-                    const int st = (int)(k % stages);
-                    if (!mbar_wait_sleep(&sh.k_empty[st], (uint32_t)((k / stages) & 1) ^ 1)) {
+                    if (!mbar_wait_sleep(&sh.k_empty[st], ph ^ 1)) {
                         ok = false;
                     } else {
                         uint8_t *dst = sh.tile[q_tiles + st];
+                        const int64_t y0 = pool_row(2 * j, b0), y1 = pool_row(2 * j + 1, b1);
                         const int pages = (y0 >= 0) + (y1 >= 0);
                         if (pages == 0)
                             mbar_arrive(&sh.k_full[st]);
@@ -272,6 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok)
                     break;
+                issued = min(issued + 1, stages);
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
             next_unit(w);
         }
@@ -279,255 +308,287 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok)
                 set_err(p.dev_err, HSA_DEVERR_TIMEOUT);
             // no copy may still be in flight when the CTA exits
-            for (int64_t s = 0; s < stages && s < k; ++s) {
-                const int64_t last = s + ((k - 1 - s) / stages) * stages;
-                mbar_wait_sleep(&sh.k_full[s], (uint32_t)((last / stages) & 1));
-            }
+            for (int s = 0; s < issued; ++s)
+                mbar_wait_sleep(&sh.k_full[s], s < st ? ph : ph ^ 1);
             if (units > 0)
                 mbar_wait_sleep(&sh.q_full, (uint32_t)(units - 1) & 1);
         }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t dhi = smem_desc_sw128_hi(1024);
-            int64_t k = 0;
-            int units = 0;
-            uint32_t cnt0 = 0, cnt1 = 0;  // tiles handed to each warpgroup
-            bool ok = true;
-            for (int64_t i = i0; i < i1 && ok; ++units) {
-                const int64_t end = i + min((int64_t)(w.nt - w.j), i1 - i);
-                const int nq = row_tiles(w), rows = w.q.T * p.G;
-                ok = mbar_wait_sleep(&sh.q_full, (uint32_t)units & 1);
-                for (; i < end && ok; ++i, ++k) {
-                    const int st = (int)(k % stages);
-                    if (!(ok = mbar_wait_sleep(&sh.k_full[st], (uint32_t)((k / stages) & 1))))
+    } else if (warp <= kIssuers) {
+        // --------------------------------------------------------------------- MMA issuers
+        // Issuer u serves the warpgroups u and u + 2.  The whole warp runs the loop and one
+        // elected lane issues: control flow and descriptors stay uniform.
+        const int u = warp - 1;
+        const uint32_t dhi = smem_desc_sw128_hi(1024);
+        auto commit = [&](uint64_t *bar) {
+            if (elect_one())
+                tc_commit(bar);
+        };
+        int st = 0, units = 0;
+        uint32_t ph = 0;
+        uint32_t given = 0;  // bit wg: parity of the tiles handed to warpgroup wg
+        bool ok = true;
+        for (int64_t i = i0; i < i1 && ok; ++units) {
+            const int tiles = (int)min((int64_t)(w.nt - w.j), i1 - i);
+            const int nq = row_tiles(w), rows = w.q.T * p.G, step = step_of(nq);
+            ok = mbar_wait_sleep(&sh.q_full, (uint32_t)units & 1);
+            for (int e = 0; e < tiles && ok; ++e) {
+                if (!(ok = mbar_wait_sleep(&sh.k_full[st], ph)))
+                    break;
+                tc_fence_after();
+                const uint32_t kl = smem_desc_sw128_lo(smem_u32(sh.tile[q_tiles + st]), 16);
+                for (int t = 0; t < nq; ++t) {
+                    const int slot = (e * step + t) & (kGroups - 1);
+                    if ((slot & 1) != u)
+                        continue;
+                    if (!(ok = mbar_wait_sleep(&sh.s_empty[slot], (given >> slot & 1) ^ 1)))
                         break;
+                    given ^= 1u << slot;
                     tc_fence_after();
-                    const uint32_t kl = smem_desc_sw128_lo(smem_u32(sh.tile[q_tiles + st]), 16);
-                    for (int t = 0; t < nq; ++t) {
-                        const int wg = PASS == 2 || nq == 1 ? (int)(k & 1) : t & 1;
-                        const uint32_t c = wg ? cnt1++ : cnt0++;
-                        const int slot = 2 * wg + (c & 1);
-                        if (!(ok = mbar_wait_sleep(&sh.s_empty[slot], ((c >> 1) & 1) ^ 1)))
-                            break;
-                        tc_fence_after();
-                        const uint32_t ql = smem_desc_sw128_lo(smem_u32(sh.tile[t]), 16);
-                        const int cols = PASS == 1 ? kBlock : min(kBlock, (rows - t * kBlock + 15) & ~15);
-                        const uint32_t id = idesc_bf16_f32(kBlock, cols, 0, 0);
-                        const uint32_t a = PASS == 1 ? ql : kl, b = PASS == 1 ? kl : ql;
-                        const uint32_t d = tmem + slot * kBlock;
-                        tc_mma_ss_k<0>(d, desc_join(a, dhi), desc_join(b, dhi), id);
+                    const uint32_t ql = smem_desc_sw128_lo(smem_u32(sh.tile[t]), 16);
+                    const int cols = PASS == 1 ? kBlock : min(kBlock, (rows - t * kBlock + 15) & ~15);
+                    const uint32_t id = idesc_bf16_f32(kBlock, cols, 0, 0);
+                    const uint32_t a = PASS == 1 ? ql : kl, b = PASS == 1 ? kl : ql;
+                    const uint32_t d = tmem + slot * kBlock;
+                    const bool one = elect_one();
 #pragma unroll
-                        for (int ks = 1; ks < kD / 16; ++ks) {
-                            const uint32_t off = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
-                            tc_mma_ss_k<1>(d, desc_join(a + off, dhi), desc_join(b + off, dhi), id);
+                    for (int ks = 0; ks < kD / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
+                        if (one) {
+                            if (ks == 0)
+                                tc_mma_ss_k<0>(d, desc_join(a, dhi), desc_join(b, dhi), id);
+                            else
+                                tc_mma_ss_k<1>(d, desc_join(a + off, dhi), desc_join(b + off, dhi), id);
                         }
-                        tc_commit(&sh.s_full[slot]);
                     }
-                    if (ok)
-                        tc_commit(&sh.k_empty[st]);
+                    commit(&sh.s_full[slot]);
                 }
-                if (ok)
-                    tc_commit(&sh.q_empty);
-                next_unit(w);
+                if (!ok)
+                    break;
+                commit(&sh.k_empty[st]);  // arrives at once where nothing was issued
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
-            if (!ok)
-                set_err(p.dev_err, HSA_DEVERR_TIMEOUT);
-            tc_commit(&sh.done);  // every MMA done before TMEM is released
-            mbar_wait_sleep(&sh.done, 0);
+            if (ok)
+                commit(&sh.q_empty);
+            i += tiles;
+            next_unit(w);
         }
-    } else {
+        if (!ok && lane == 0)
+            set_err(p.dev_err, HSA_DEVERR_TIMEOUT);
+        commit(&sh.done);  // every MMA done before TMEM is released
+        mbar_wait_sleep(&sh.done, 0);
+    } else if (warp >= 4) {
         // ------------------------------------------------------------- rows' or keys' threads
-        const int wg = (warp - 2) >> 2, wq = warp & 3;
+        const int wg = (warp - 4) >> 2, wq = warp & 3;
         const int me = wq * 32 + lane;  // TMEM lane
-        const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t taddr = tmem + ((uint32_t)(wq * 32) << 16) + wg * kBlock;
         const uint64_t sc2 = f2_make(p.scale_log2, p.scale_log2);
-        const int row_cap = q_tiles * kBlock;
-        uint32_t cnt = 0;
-        int64_t k = 0;
+        uint32_t cnt = 0;       // tiles taken
+        uint32_t handed = 0;    // pass 2: byte g: sums that warpgroup g has handed over, mod 4
         bool ok = true;
         // bit e: page 2 batch + e can be read
         auto pages_ok = [&](int batch) {
             const int page = 2 * batch + lane;
-            return __ballot_sync(0xffffffffu, (int64_t)page * 64 >= w.q.n || page_row(p, w.q, w.h, page, false) >= 0);
+            int err;
+            return __ballot_sync(0xffffffffu, page_at(p, w.q, page, page_entry(p, w.q, page), &err) >= 0);
         };
-        // the next TMEM slot of this warpgroup.  After a wait that gave up no further one is
-        // made, but every tile is walked through: the warpgroup's barriers count on all of it.
-        auto take = [&]() -> uint32_t {
-            const uint32_t slot = 2 * wg + (cnt & 1);
-            if (ok && !mbar_wait_sleep(&sh.s_full[slot], (cnt >> 1) & 1)) {
+        // After a wait that gave up no further one is made, but every tile is walked through: the
+        // warpgroup's barriers count on all of it.
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok && !mbar_wait_sleep(bar, parity)) {
                 set_err(p.dev_err, HSA_DEVERR_TIMEOUT);
                 ok = false;
             }
             __syncwarp();
-            tc_fence_after();
-            return slot;
         };
-        auto give = [&](uint32_t slot) {
+        auto take = [&] {
+            wait(&sh.s_full[wg], cnt & 1);
+            tc_fence_after();
+        };
+        auto arrive = [&](uint64_t *bar) {  // a warp's one
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
+        auto give = [&] {
             tc_fence_before();
-            mbar_arrive(&sh.s_empty[slot]);
+            arrive(&sh.s_empty[wg]);
             ++cnt;
         };
         for (int64_t i = i0; i < i1;) {
             const int64_t unit = (int64_t)w.r * p.Hkv + w.h;
-            const int64_t end = i + min((int64_t)(w.nt - w.j), i1 - i);
-            const int nq = row_tiles(w), n = w.q.n, T = w.q.T, rows = T * p.G;
-            int j = w.j, batch = w.j;
+            const int tiles = (int)min((int64_t)(w.nt - w.j), i1 - i);
+            const int nq = row_tiles(w), step = step_of(nq), n = w.q.n, T = w.q.T, rows = T * p.G;
+            const int t = wg % step;  // this warpgroup's row tile
+            const int row0 = t * kBlock;
+            int batch = w.j;
             uint32_t good = pages_ok(batch);
             if constexpr (PASS == 1) {
-                // the sums with what their roundings lost (a row has up to a million terms)
-                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
-                for (; i < end; ++i, ++j, ++k) {
-                    if (j - batch == 16) {
-                        batch = j;
+                // the sum with what its roundings lost (a row has up to a million terms)
+                float m = -INFINITY, l = 0.f, lost = 0.f;
+                for (int e = wg / step; t < nq && e < tiles; e += kGroups / step) {
+                    const int j = w.j + e;
+                    if (j - batch >= 16) {
+                        batch += (j - batch) & ~15;
                         good = pages_ok(batch);
                     }
                     const uint32_t pair = good >> (2 * (j - batch)) & 3u;
+                    // keys of the tile this row sees: 0 .. hi - 1
+                    const int hi = min(n, n - T + (row0 + me) / p.G + 1) - j * kBlock;
+                    const bool whole = __all_sync(0xffffffffu, hi >= kBlock) && pair == 3u;
+                    take();
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kBlock; c0 += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(taddr + c0, x);
+                        tmem_wait_ld();
+                        if (c0 == kBlock - 32)
+                            give();
+                        if (!whole) {
+                            const int top = (pair >> (c0 >> 6) & 1u) ? hi - c0 : 0;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = nq == 1 ? 0 : wg + 2 * e;
-                        if (t >= nq || (nq == 1 && (e == 1 || (int)(k & 1) != wg)))
-                            continue;
-                        const uint32_t slot = take();
-                        // keys of the tile this row sees: 0 .. hi - 1
-                        const int hi = min(n, n - T + (t * kBlock + me) / p.G + 1) - j * kBlock;
-                        const bool whole = __all_sync(0xffffffffu, hi >= kBlock) && pair == 3u;
+                            for (int c = 0; c < 32; ++c)
+                                if (c >= top)
+                                    x[c] = __float_as_uint(-INFINITY);
+                        }
+                        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t x[2][32];
-                            tmem_ld32(lane_addr + slot * kBlock + half * 64, x[0]);
-                            tmem_ld32(lane_addr + slot * kBlock + half * 64 + 32, x[1]);
-                            tmem_wait_ld();
-                            if (half == 1)
-                                give(slot);
-                            if (!whole) {
-                                const int top = (pair >> half & 1u) ? hi - half * 64 : 0;
+                        for (int c = 0; c < 32; c += 2)
+                            mx[c >> 1 & 1] = fmax3(mx[c >> 1 & 1], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        const float top = fmaxf(mx[0], mx[1]) * p.scale_log2;
+                        if (top != -INFINITY && (m == -INFINITY || top > m + kSlack)) {
+                            const float f = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                            l *= f;
+                            lost *= f;
 #pragma unroll
-                                for (int c = 0; c < 64; ++c)
-                                    if (c >= top)
-                                        x[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-                            }
-                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            for (int c = 0; c < 4; ++c)
+                                acc[c] *= f;
+                            m = top;
+                        }
+                        const float base = m == -INFINITY ? 0.f : m;
+                        const uint64_t nb2 = f2_make(-base, -base);
 #pragma unroll
-                            for (int c = 0; c < 64; c += 8)
-#pragma unroll
-                                for (int f = 0; f < 4; ++f)
-                                    mx[f] = fmax3(mx[f], __uint_as_float(x[c >> 5][(c & 31) + 2 * f]),
-                                                  __uint_as_float(x[c >> 5][(c & 31) + 2 * f + 1]));
-                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                            if (top != -INFINITY && (m[e] == -INFINITY || top > m[e] + kSlack)) {
-                                const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - top);
-                                l[e] *= f;
-                                lost[e] *= f;
-                                m[e] = top;
-                            }
-                            const float base = m[e] == -INFINITY ? 0.f : m[e];
-                            const uint64_t nb2 = f2_make(-base, -base);
-                            uint64_t acc[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-#pragma unroll
-                            for (int c = 0; c < 64; c += 2) {
-                                float a, b;
-                                f2_split(f2_fma(f2_make(__uint_as_float(x[c >> 5][c & 31]),
-                                                        __uint_as_float(x[c >> 5][(c & 31) + 1])),
-                                                sc2, nb2),
-                                         a, b);
-                                acc[c >> 1 & 1] = f2_add(acc[c >> 1 & 1], f2_make(fast_exp2(a), fast_exp2(b)));
-                            }
+                        for (int c = 0; c < 32; c += 2) {
                             float a, b;
-                            f2_split(f2_add(acc[0], acc[1]), a, b);
-                            const float add = (a + b) - lost[e], sum = l[e] + add;
-                            lost[e] = (sum - l[e]) - add;
-                            l[e] = sum;
+                            f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, nb2), a, b);
+                            acc[c & 2] += fast_exp2(a);
+                            acc[(c & 2) + 1] += fast_exp2(b);
                         }
                     }
+                    const float add = ((acc[0] + acc[1]) + (acc[2] + acc[3])) - lost, sum = l + add;
+                    lost = (sum - l) - add;
+                    l = sum;
                 }
-                // this CTA's part of the unit's rows (both warpgroups' where there is one row tile)
-                float2 *const to = p.part + ((unit + blockIdx.x) * 2 + wg) * row_cap + me;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = nq == 1 ? 0 : wg + 2 * e;
-                    if (t < nq && (nq > 1 || e == 0))
-                        to[t * kBlock] = make_float2(m[e], l[e]);
-                }
+                p.part[((unit + blockIdx.x) * kGroups + wg) * kBlock + me] = make_float2(m, l);
             } else {
-                // ---- the rows' lse, out of the states of every CTA that met the unit ----------
+                // ---- the rows' lse, out of the states of every CTA that met the unit: those of
+                // the warpgroups t, t + step, .. of each
                 {
                     const int64_t u0 = i - w.j, u1 = u0 + w.nt;
                     const int64_t c_lo = ((u0 + 1) * C - 1) / N, c_hi = (u1 * C - 1) / N;
-                    named_bar_sync(1 + wg, kBlock);  // the last unit's readers are done
-                    for (int t = 0; t < nq; ++t) {
-                        float M = -INFINITY, L = 0.f;
-                        for (int64_t c = c_lo; c <= c_hi; ++c)
-                            for (int g = nq == 1 ? 0 : t & 1; g <= (nq == 1 ? 1 : t & 1); ++g) {
-                                const float2 s = __ldcg(p.part + ((unit + c) * 2 + g) * row_cap + t * kBlock + me);
-                                const float top = fmaxf(M, s.x);
-                                if (top != -INFINITY)
-                                    L = L * fast_exp2(M - top) + s.y * fast_exp2(s.x - top);
-                                M = top;
-                            }
-                        const bool on = t * kBlock + me < rows && L > 0.f;
-                        sh.neg_lse[wg][t * kBlock + me] = on ? -(M + log2f(L)) : -INFINITY;
+                    const float2 *const part = p.part + (unit + c_lo) * kGroups * kBlock + me;
+                    const int states = (int)(c_hi - c_lo + 1) * kGroups;
+                    float M = -INFINITY, L = 0.f;
+                    for (int e0 = t; e0 < states; e0 += 8 * step) {
+                        float2 s[8];
+                        float top = M;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            s[e] = make_float2(-INFINITY, 0.f);
+                            if (e0 + e * step < states)
+                                s[e] = __ldcg(part + (int64_t)(e0 + e * step) * kBlock);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            top = fmaxf(top, s[e].x);
+                        if (top != -INFINITY) {
+                            L *= fast_exp2(M - top);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                L += s[e].y * fast_exp2(s[e].x - top);
+                        }
+                        M = top;
                     }
+                    const bool on = row0 + me < rows && L > 0.f;
+                    named_bar_sync(1 + wg, kBlock);  // the last unit's readers are done
+                    sh.neg_lse[wg][me] = on ? -(M + log2f(L)) : -INFINITY;
                     named_bar_sync(1 + wg, kBlock);
                 }
                 const int64_t at = ((int64_t)w.q.seq * p.Hkv + w.h) * p.w_stride;
-                for (; i < end; ++i, ++j, ++k) {
-                    if (j - batch == 16) {
-                        batch = j;
+                const int top = min(kBlock, rows - row0);
+                uint32_t turn = 0;  // key tiles of this warpgroup (and of those it shares them with)
+                for (int e = wg / step; t < nq && e < tiles; e += kGroups / step, ++turn) {
+                    const int j = w.j + e;
+                    if (j - batch >= 16) {
+                        batch += (j - batch) & ~15;
                         good = pages_ok(batch);
                     }
-                    if ((int)(k & 1) != wg)
-                        continue;
                     const int pos = j * kBlock + me;
-                    const int first = max(0, pos - (n - T)) * p.G;  // rows that see this key: first ..
-                    const bool all = __all_sync(0xffffffffu, first == 0);
-                    const float old = p.w_prev && pos < n - w.q.m ? p.w_prev[at + pos] : 0.f;
-                    uint64_t acc[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-                    for (int t = 0; t < nq; ++t) {
-                        const uint32_t slot = take();
-                        const int top = min(kBlock, rows - t * kBlock);
-                        for (int c0 = 0; c0 < top; c0 += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(lane_addr + slot * kBlock + c0, x);
-                            const float4 *const nl = reinterpret_cast<const float4 *>(&sh.neg_lse[wg][t * kBlock + c0]);
-                            tmem_wait_ld();
-                            if (all && c0 + 32 <= top) {
+                    const int first = max(0, pos - (n - T)) * p.G - row0;  // of the tile's rows, first .. see the key
+                    const bool all = __all_sync(0xffffffffu, first <= 0);
+                    const float old = t == 0 && p.w_prev && pos < n - w.q.m ? p.w_prev[at + pos] : 0.f;
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    take();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < top; c0 += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(taddr + c0, x);
+                        const float4 *const nl = reinterpret_cast<const float4 *>(&sh.neg_lse[wg][c0]);
+                        tmem_wait_ld();
+                        if (c0 + 32 >= top)
+                            give();
+                        if (all && c0 + 32 <= top) {
 #pragma unroll
-                                for (int c = 0; c < 32; c += 4) {
-                                    const float4 y = nl[c >> 2];
-                                    float a, b, d, e;
-                                    f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2,
-                                                    f2_make(y.x, y.y)), a, b);
-                                    f2_split(f2_fma(f2_make(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2,
-                                                    f2_make(y.z, y.w)), d, e);
-                                    acc[0] = f2_add(acc[0], f2_make(fast_exp2(a), fast_exp2(b)));
-                                    acc[1] = f2_add(acc[1], f2_make(fast_exp2(d), fast_exp2(e)));
-                                }
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) {
-                                    const int row = t * kBlock + c0 + c;
-                                    if (row >= first && row < rows) {
-                                        const float a = fast_exp2(
-                                            fmaf(__uint_as_float(x[c]), p.scale_log2, sh.neg_lse[wg][row]));
-                                        acc[c & 1] = f2_add(acc[c & 1], f2_make(a, 0.f));
-                                    }
-                                }
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 y = nl[c >> 2];
+                                float a, b, d, f;
+                                f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2,
+                                                f2_make(y.x, y.y)), a, b);
+                                f2_split(f2_fma(f2_make(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2,
+                                                f2_make(y.z, y.w)), d, f);
+                                acc[0] += fast_exp2(a);
+                                acc[1] += fast_exp2(b);
+                                acc[2] += fast_exp2(d);
+                                acc[3] += fast_exp2(f);
                             }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c0 + c >= first && c0 + c < top)
+                                    acc[c & 3] +=
+                                        fast_exp2(fmaf(__uint_as_float(x[c]), p.scale_log2, sh.neg_lse[wg][c0 + c]));
                         }
-                        give(slot);
+                    }
+                    float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                    if (t > 0) {  // over to the key tile's first warpgroup
+                        const uint32_t c = (handed >> (8 * wg)) + turn;
+                        wait(&sh.sum_free[wg][c & 1], (c >> 1 & 1) ^ 1);
+                        sh.sum[wg][c & 1][me] = sum;
+                        arrive(&sh.sum_full[wg][c & 1]);
+                        continue;
+                    }
+                    for (int g = wg + 1; g < wg + nq; ++g) {
+                        const uint32_t c = (handed >> (8 * g)) + turn;
+                        wait(&sh.sum_full[g][c & 1], c >> 1 & 1);
+                        sum += sh.sum[g][c & 1][me];
+                        arrive(&sh.sum_free[g][c & 1]);
                     }
                     if (ok && pos < n) {
-                        float a, b;
-                        f2_split(f2_add(acc[0], acc[1]), a, b);
-                        const bool there = good >> (2 * (j - batch) + (me >> 6)) & 1u;
-                        float sum = there ? a + b : 0.f;
+                        sum = good >> (2 * (j - batch) + (me >> 6)) & 1u ? sum : 0.f;
                         if (p.w_prev && pos < n - w.q.m)
                             sum = fmaf(p.decay, old, sum);
                         p.w[at + pos] = sum;
                     }
                 }
+                for (int g = 0; g < kGroups; ++g)
+                    if (g % step > 0 && g % step < nq)
+                        handed += (uint32_t)max(0, (tiles - g / step + kGroups / step - 1) / (kGroups / step)) % 4 << (8 * g);
+                handed &= 0x03030303u;
             }
+            i += tiles;
             next_unit(w);
         }
     }
@@ -544,9 +605,9 @@ int row_tiles_of(int G, int window) { return (G * window + kBlock - 1) / kBlock;
 
 }  // namespace
 
-size_t prompt_workspace_bytes(int ctas, int R, int Hkv, int G, int window)
+size_t prompt_workspace_bytes(int ctas, int R, int Hkv)
 {
-    return ((size_t)R * Hkv + ctas) * 2 * row_tiles_of(G, window) * kBlock * sizeof(float2);
+    return ((size_t)R * Hkv + ctas) * kGroups * kBlock * sizeof(float2);
 }
 
 cudaError_t launch_prompt_weights(const CUtensorMap &tmK, const CUtensorMap &tmQ, const PromptParams &p, int ctas,

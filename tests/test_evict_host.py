@@ -160,7 +160,7 @@ def test_prefill_weights_arguments_refused():
     assert call(p=ctypes.byref(cabi._pools(hsa, fp8=[0, 1]))) == SHAPE
     assert call(R=0, q=None, w=None) == OK and call(rows=0, q=None) == OK
     size = lambda R, n: L.hsa_prefill_weights_workspace_bytes(base["p"], R, n)  # noqa: E731
-    assert size(2, 16) > 0 and size(2, 64) == 4 * size(2, 16) and size(-1, 4) == 0 and size(1, 0) == 0
+    assert size(2, 64) >= size(2, 16) > size(1, 16) > 0 and size(-1, 4) == 0 and size(1, 0) == 0
 
 
 def test_prefill_weights_binding_checks(fake, monkeypatch):
