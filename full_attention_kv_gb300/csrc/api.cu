@@ -878,7 +878,7 @@ hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_
     if (R < 0 || batch < 0 || heads < 1 || budget < 0 || sinks < 0 || recent < 0 || reach < 0 ||
         (int64_t)sinks + recent > budget)
         return HSA_INVALID_ARG;
-    if (reach > 7)
+    if (reach > 7 || w_stride > (1 << 22))
         return HSA_UNSUPPORTED_SHAPE;
     if (R == 0)
         return HSA_OK;

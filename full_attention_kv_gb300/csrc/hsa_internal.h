@@ -264,7 +264,7 @@ struct SelectParams {            // kv_select.cu
     const int32_t *kv_len, *seq_idx;
     int32_t *keep, *new_len, *dev_err;
     int32_t w_stride, batch, heads, R, budget, sinks, recent, reach;
-    int32_t held;                // keys a CTA keeps in shared memory (set by launch_select)
+    int32_t held;                // keys a CTA keeps the high halves of (set by launch_select)
 };
 cudaError_t launch_select(SelectParams &p, int sms, cudaStream_t stream);
 

@@ -5,16 +5,24 @@
 // ascending.  A score is the largest weight among a position and its `reach` neighbours.
 //
 // A score becomes a 32-bit integer of the same order (sign flipped, negatives inverted), and the
-// left-th largest is found digit by digit (11, 11 and 10 bits): a histogram of the digit among
-// the keys that agree so far, summed from the top until it holds the rank.  No sort, and no
-// order of atomics that shows: the histogram's sums and the prefix counts are exact.  Then every
-// key above that value stays, and the first `need` keys equal to it, each key's place being the
-// number that stay before it (warp scans over contiguous ranges).
+// left-th largest is found digit by digit (9, 7, 8 and 8 bits): a histogram of the digit among the
+// keys that agree so far, summed from the top until it holds the rank.  No sort, and no order of
+// atomics that shows: the histogram's sums and the prefix counts are exact.  Then every key above
+// that value stays, and the first `need` keys equal to it, each key's place being the number that
+// stay before it (warp scans over contiguous ranges).
 //
-// A cluster of 1 to 8 CTAs takes a row, each a contiguous part, read from memory once: a thread
-// keeps its own keys in shared memory (as far as they fit; the others are read again, out of
-// L2), so the passes over them need no barrier.  Histograms are summed over the cluster through
-// distributed shared memory.
+// A cluster of 1 to 6 CTAs takes a row, each a contiguous part; a lane takes 16 positions at a time
+// (4 of short rows), so that neighbours' weights are read and prefix counts scanned once for all of
+// them.  A thread keeps the high halves of its own keys in shared memory, so the passes over them
+// need no barrier, and half as much of it as whole keys would: few keys share their high half with
+// the value sought, and only those are made again from the weights.  Each CTA writes its counters
+// into the shared memory of all of the cluster (reading the others' instead is two round trips and a
+// second barrier a digit, 3 to 6 us).
+//
+// The first digit, sign and exponent, is every key's, and weights share a few exponents: lanes of
+// a warp that add to one counter do so one after another.  So each lane has counters of its own, 16
+// bits wide, in a bank that it shares with one other lane.  The later digits are few keys' and
+// differ.
 #include <cooperative_groups.h>
 
 #include "hsa_device.cuh"
@@ -25,20 +33,22 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kMaxWarps = 32;
+constexpr int kFirstBins = 512;              // of sign and exponent
 constexpr int kMaxReach = 7;
+constexpr int kMaxCtas = 6;                  // of a row
 
-struct alignas(16) SelectSmem {  // the held keys follow
-    uint32_t hist[kBins];
-    uint32_t scan[kWarps];
-    uint32_t warp_gt[kWarps], warp_eq[kWarps];
-    uint32_t cta_gt, cta_eq;
+struct alignas(16) SelectSmem {              // the held halves follow
+    uint32_t lanes[kFirstBins * 16];         // lane l: half l / 16 of word l % 16 of a bin's 16
+    uint32_t own[kFirstBins];                // this CTA's counters of a digit
+    uint32_t all[2][kMaxCtas][kFirstBins];   // every CTA's, of this digit and the one before
+    uint32_t scan[kMaxWarps];
+    uint32_t warp_gt[kMaxWarps], warp_eq[kMaxWarps];
+    uint32_t cta_gt[kMaxCtas], cta_eq[kMaxCtas];
     uint32_t digit, need;
     int32_t done;
 };
-static_assert(sizeof(SelectSmem) % 16 == 0, "the keys behind it are read 16 bytes at a time");
+static_assert(sizeof(SelectSmem) % 16 == 0, "the halves behind it");
 
 // An integer of the value's order; NaN as -infinity, -0 as 0.  Never 0, which marks a position
 // that does not compete.
@@ -49,50 +59,57 @@ __device__ __forceinline__ uint32_t order_key(float x)
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// Keys of positions 4 quad .. 4 quad + 3 of a row of n weights (16-byte aligned, readable up to
-// a multiple of 4); those outside lo .. hi - 1 do not compete.
-__device__ __forceinline__ uint4 load_keys(const float *row, int quad, int n, int lo, int hi, int reach)
+// Keys of the kKeys positions from p (a multiple of them) of a row of n weights (16-byte aligned,
+// readable up to a multiple of 4); those outside lo .. hi - 1 do not compete.
+template <int kKeys>
+__device__ __forceinline__ void load_keys(uint32_t (&k)[kKeys], const float *row, int p, int n, int lo, int hi,
+                                          int reach)
 {
-    const int p = 4 * quad;
-    float v[4];
-    if (reach == 0) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(row) + quad);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-        float x[20];  // positions p - 8 .. p + 11
+    float x[kKeys + 16];  // positions p - 8 .. p + 23
 #pragma unroll
-        for (int c = 0; c < 5; ++c) {
-            const int at = p - 8 + 4 * c;
-            float4 y = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (at >= 0 && at < n)
-                y = __ldg(reinterpret_cast<const float4 *>(row + at));
-            x[4 * c] = y.x;
-            x[4 * c + 1] = at + 1 < n ? y.y : -INFINITY;
-            x[4 * c + 2] = at + 2 < n ? y.z : -INFINITY;
-            x[4 * c + 3] = at + 3 < n ? y.w : -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = x[8 + e];
-#pragma unroll
-        for (int d = 1; d <= kMaxReach; ++d)
-            if (d <= reach)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = fmax3(v[e], x[8 + e - d], x[8 + e + d]);  // a NaN gives way to a number
+    for (int c = 0; c < kKeys / 4 + 4; ++c) {
+        const int at = p - 8 + 4 * c;
+        const bool inner = c >= 2 && c < kKeys / 4 + 2, near = c >= 1 && c < kKeys / 4 + 3;
+        float4 y = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if ((inner || (near ? reach > 0 : reach > 4)) && at >= 0 && at < n)
+            y = __ldg(reinterpret_cast<const float4 *>(row + at));
+        x[4 * c] = y.x, x[4 * c + 1] = y.y, x[4 * c + 2] = y.z, x[4 * c + 3] = y.w;
     }
-    uint32_t k[4];
+    if (p + kKeys + 8 > n) {  // behind the row's end
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        k[e] = p + e >= lo && p + e < hi ? order_key(v[e]) : 0u;
-    return make_uint4(k[0], k[1], k[2], k[3]);
+        for (int e = 8; e < kKeys + 16; ++e)
+            x[e] = p - 8 + e < n ? x[e] : -INFINITY;
+    }
+    float v[kKeys];
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e)
+        v[e] = x[8 + e];
+#pragma unroll
+    for (int d = 1; d <= kMaxReach; ++d)
+        if (d <= reach)
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e)
+                v[e] = fmax3(v[e], x[8 + e - d], x[8 + e + d]);  // a NaN gives way to a number
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e)
+        k[e] = order_key(v[e]);
+    if (p < lo || p + kKeys > hi) {
+#pragma unroll
+        for (int e = 0; e < kKeys; ++e)
+            if (p + e < lo || p + e >= hi)
+                k[e] = 0;
+    }
 }
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
+template <int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const SelectParams p)
 {
+    constexpr int kWarps = kThreads / 32;
+    constexpr int kChunk = 32 * kKeys;  // positions a warp takes at a time
+    constexpr uint32_t kAll = (1u << kKeys) - 1;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SelectSmem &sh = *reinterpret_cast<SelectSmem *>(smem_raw);
-    uint4 *const held = reinterpret_cast<uint4 *>(smem_raw + sizeof(SelectSmem));
+    uint32_t *const held = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectSmem));
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -128,17 +145,31 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
         keep[p.budget - p.recent + i] = hi + i;
     if (left == 0)
         return;
+    if (C > 1)  // every CTA of the cluster runs, before another writes into its shared memory
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-    // ---- this thread's quads of positions: q_begin + lane, + 32, ... < q_end ----------------
+    // ---- this warp's positions: chunks k_begin .. k_end - 1 ----------------------------------
     const float *const row = p.w + ((int64_t)seq * p.heads + h) * p.w_stride;
-    const int quads = (n + 3) / 4;
-    const int per_cta = (quads + C - 1) / C;
-    const int c0 = min(quads, rank * per_cta), c1 = min(quads, c0 + per_cta);
-    const int per_warp = ((per_cta + kWarps - 1) / kWarps + 31) & ~31;
-    const int q_begin = min(c1, c0 + warp * per_warp), q_end = min(c1, q_begin + per_warp);
-    const int held_quads = p.held / 4;
-    auto keys = [&](int q) {
-        return q - c0 < held_quads ? held[q - c0] : load_keys(row, q, n, lo, hi, p.reach);
+    const int chunks = (n + kChunk - 1) / kChunk;
+    const int cta_chunks = (chunks + C - 1) / C, warp_chunks = (cta_chunks + kWarps - 1) / kWarps;
+    const int k0 = min(chunks, rank * cta_chunks), k1 = min(chunks, k0 + cta_chunks);
+    const int k_begin = min(k1, k0 + warp * warp_chunks), k_end = min(k1, k_begin + warp_chunks);
+    const int held_chunks = p.held / kChunk;
+    // word e of this lane's high halves of chunk c: keys 2 e, 2 e + 1
+    auto slot = [&](int c) { return held + (c - k0) * (kChunk / 2) + lane; };
+    auto position = [&](int c) { return c * kChunk + lane * kKeys; };
+    auto fresh = [&](int c, uint32_t(&k)[kKeys]) { load_keys<kKeys>(k, row, position(c), n, lo, hi, p.reach); };
+    // bit e: the high half of key e, as far as `bits` says, is `value`
+    auto match = [&](int c, uint32_t bits, uint32_t value) {
+        const uint32_t *const x = slot(c);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e) {
+            const uint32_t y = x[32 * e] ^ (value | value << 16);
+            m |= (y & bits) == 0 ? 1u << (2 * e) : 0u;
+            m |= (y & bits << 16) == 0 ? 2u << (2 * e) : 0u;
+        }
+        return m;
     };
 
     // ---- the left-th largest key, digit by digit --------------------------------------------
@@ -146,42 +177,90 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
     bool exact = false;  // need ends inside the digit's keys (else all of them stay)
     int shift = 32;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int bits = pass < 2 ? 11 : 10;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int bits = pass == 0 ? 9 : pass == 1 ? 7 : 8, bins = 1 << bits;
         const int above = shift;  // bits above the digit agree with prefix
         shift -= bits;
-        for (int b = tid; b < kBins; b += kThreads)
-            sh.hist[b] = 0;
-        __syncthreads();
-        for (int q = q_begin + lane; q < q_end; q += 32) {
-            uint4 k4;
-            if (pass == 0) {
-                k4 = load_keys(row, q, n, lo, hi, p.reach);
-                if (q - c0 < held_quads)
-                    held[q - c0] = k4;
-            } else {
-                k4 = keys(q);
-            }
-            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (k[e] != 0 && (pass == 0 || (k[e] >> above) == prefix))
-                    atomicAdd(&sh.hist[(k[e] >> shift) & ((1u << bits) - 1)], 1u);
-        }
-        if (C > 1)
-            cluster.sync();
-        else
+        if (pass == 0) {
+            for (int b = tid; b < kFirstBins * 4; b += kThreads)
+                reinterpret_cast<uint4 *>(sh.lanes)[b] = make_uint4(0, 0, 0, 0);
             __syncthreads();
-        // thread t sums bins 2047 - 4t .. 2044 - 4t over the cluster: the top ones first
-        uint32_t cnt[4] = {0, 0, 0, 0};
-        const int b0 = kBins - 4 - 4 * tid;
-#pragma unroll 1
-        for (int c = 0; c < C; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(
-                C > 1 ? cluster.map_shared_rank(&sh.hist[b0], c) : &sh.hist[b0]);
-            cnt[0] += x.w, cnt[1] += x.z, cnt[2] += x.y, cnt[3] += x.x;
+            const uint32_t one = lane < 16 ? 1u : 0x10000u;
+            for (int c = k_begin; c < k_end; ++c) {
+                uint32_t k[kKeys];
+                fresh(c, k);
+                if (c - k0 < held_chunks) {
+                    uint32_t *const x = slot(c);
+#pragma unroll
+                    for (int e = 0; e < kKeys / 2; ++e)
+                        x[32 * e] = __byte_perm(k[2 * e], k[2 * e + 1], 0x7632);
+                }
+#pragma unroll
+                for (int e = 0; e < kKeys; ++e)
+                    if (k[e] != 0)
+                        atomicAdd(&sh.lanes[(k[e] >> 23) * 16 + (lane & 15)], one);
+            }
+            __syncthreads();
+            for (int b = tid; b < kFirstBins; b += kThreads) {
+                uint32_t sum = 0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t x = sh.lanes[b * 16 + ((j + b) & 15)];
+                    sum += (x & 0xffffu) + (x >> 16);
+                }
+                sh.own[b] = sum;
+            }
+        } else {
+            for (int b = tid; b < bins; b += kThreads)
+                sh.own[b] = 0;
+            __syncthreads();
+            // (few keys agree with the digits so far: bits are cheaper than a branch for each)
+            const uint32_t known = above >= 16 ? 0xffffu << (above - 16) & 0xffffu : 0xffffu;
+            const uint32_t half = above >= 16 ? prefix << (above - 16) : prefix >> (16 - above);
+            for (int c = k_begin; c < k_end; ++c) {
+                const bool there = c - k0 < held_chunks;
+                uint32_t m = there ? match(c, known, half) : kAll;
+                if (pass == 1 && there) {
+                    for (; m; m &= m - 1) {
+                        const int e = __ffs(m) - 1;
+                        const uint32_t k = slot(c)[32 * (e >> 1)] >> (16 * (e & 1)) & 0xffffu;
+                        if (k != 0)
+                            atomicAdd(&sh.own[k & (bins - 1)], 1u);
+                    }
+                } else if (m) {
+                    uint32_t k[kKeys];
+                    fresh(c, k);
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e)
+                        if (k[e] != 0 && (k[e] >> above) == prefix)
+                            atomicAdd(&sh.own[(k[e] >> shift) & (bins - 1)], 1u);
+                }
+            }
         }
-        const uint32_t mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+        __syncthreads();
+        const uint32_t(*const all)[kFirstBins] = sh.all[pass & 1];
+        if (C > 1) {
+            if (pass == 0)
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            for (int i = tid; i < C * (bins / 4); i += kThreads) {
+                const int to = i / (bins / 4), at = i % (bins / 4);
+                reinterpret_cast<uint4 *>(cluster.map_shared_rank(sh.all[pass & 1][rank], to))[at] =
+                    reinterpret_cast<const uint4 *>(sh.own)[at];
+            }
+            cluster.sync();  // (and all have read what was written two digits ago)
+        }
+        // the digit that holds the rank: a counter a thread, the top one in thread 0
+        static_assert(kThreads >= kFirstBins, "a counter a thread");
+        uint32_t mine = 0;
+        if (tid < bins) {
+            if (C == 1) {
+                mine = sh.own[bins - 1 - tid];
+            } else {
+#pragma unroll
+                for (int c = 0; c < kMaxCtas; ++c)
+                    mine += c < C ? all[c][bins - 1 - tid] : 0u;
+            }
+        }
         uint32_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -192,39 +271,62 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
         if (lane == 31)
             sh.scan[warp] = incl;
         __syncthreads();
-        uint32_t before = incl - mine;
-        for (int w = 0; w < warp; ++w)
-            before += sh.scan[w];
-        if (before < need && before + mine >= need) {  // one thread
-            int e = 0;
-            while (before + cnt[e] < need)
-                before += cnt[e++];
-            sh.digit = (uint32_t)(b0 + 3 - e);
-            sh.need = need - before;
-            sh.done = need - before == cnt[e];
+        if (tid < bins) {
+            uint32_t before = incl - mine;
+            const uint32_t w = lane < warp ? sh.scan[lane] : 0u;  // at most 16 warps hold counters
+            before += __reduce_add_sync(0xffffffffu, w);
+            if (before < need && before + mine >= need) {  // one thread
+                sh.digit = (uint32_t)(bins - 1 - tid);
+                sh.need = need - before;
+                sh.done = need - before == mine;
+            }
         }
-        if (C > 1)
-            cluster.sync();  // every CTA has read the histograms
-        else
-            __syncthreads();
+        __syncthreads();
         prefix = (prefix << bits) | sh.digit;
         need = sh.need;
-        if (sh.done)
+        if (sh.done)  // (the next digit's counts come behind a barrier)
             break;
-        exact = pass == 2;
+        exact = pass == 3;
     }
     // keys above `edge` stay, and of those equal to it the first `need` (none: the last digit's
     // keys all stay, and edge is the value below them)
-    const uint32_t edge = exact ? prefix : (prefix << shift) - 1u;
+    const uint32_t edge = exact ? prefix : max(prefix << shift, 1u) - 1u;
     if (!exact)
         need = 0;
 
-    // ---- how many stay before each warp's range ---------------------------------------------
+    // ---- which stay: bit e of a word key e above the edge, bit 16 + e equal to it -----------
+    const uint32_t edge16 = edge >> 16;
+    auto marks = [&](int c) {
+        uint32_t above = 0, level = kAll;
+        if (c - k0 < held_chunks) {
+            const uint32_t *const x = slot(c);
+            level = 0;
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) {
+                const uint32_t y = e & 1 ? x[32 * (e >> 1)] >> 16 : x[32 * (e >> 1)] & 0xffffu;
+                above |= y > edge16 ? 1u << e : 0u;
+                level |= y == edge16 ? 1u << e : 0u;
+            }
+        }
+        if (level) {  // a high half that does not tell
+            uint32_t k[kKeys];
+            fresh(c, k);
+            above = level = 0;
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) {
+                above |= k[e] > edge ? 1u << e : 0u;
+                level |= k[e] == edge && k[e] != 0 ? 0x10000u << e : 0u;
+            }
+        }
+        return above | level;
+    };
     uint32_t gt = 0, eq = 0;
-    for (int q = q_begin + lane; q < q_end; q += 32) {
-        const uint4 k = keys(q);
-        gt += (k.x > edge) + (k.y > edge) + (k.z > edge) + (k.w > edge);
-        eq += (k.x == edge) + (k.y == edge) + (k.z == edge) + (k.w == edge);
+    for (int c = k_begin; c < k_end; ++c) {
+        const uint32_t x = marks(c);
+        if (c - k0 < held_chunks)
+            *slot(c) = x;  // the halves are not needed any more
+        gt += __popc(x & 0xffffu);
+        eq += __popc(x >> 16);
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -233,59 +335,52 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
         sh.warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t g = 0, e = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            g += sh.warp_gt[w];
-            e += sh.warp_eq[w];
+    if (C > 1) {
+        if (tid < C) {
+            uint32_t g = 0, e = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                g += sh.warp_gt[w];
+                e += sh.warp_eq[w];
+            }
+            *cluster.map_shared_rank(&sh.cta_gt[rank], tid) = g;
+            *cluster.map_shared_rank(&sh.cta_eq[rank], tid) = e;
         }
-        sh.cta_gt = g;
-        sh.cta_eq = e;
+        cluster.sync();
     }
     uint32_t g0 = 0, e0 = 0;
+    for (int c = 0; c < rank; ++c) {
+        g0 += sh.cta_gt[c];
+        e0 += sh.cta_eq[c];
+    }
     for (int w = 0; w < warp; ++w) {
         g0 += sh.warp_gt[w];
         e0 += sh.warp_eq[w];
     }
-    if (C > 1) {
-        cluster.sync();
-        for (int c = 0; c < rank; ++c) {
-            g0 += *cluster.map_shared_rank(&sh.cta_gt, c);
-            e0 += *cluster.map_shared_rank(&sh.cta_eq, c);
-        }
-        cluster.sync();  // no CTA leaves while its counts are read
-    }
 
     // ---- the positions, each at the number that stay before it ------------------------------
     int32_t *const to = keep + p.sinks;
-    for (int q = q_begin; q < q_end; q += 32) {
-        uint4 k4 = make_uint4(0, 0, 0, 0);
-        if (q + lane < q_end)
-            k4 = keys(q + lane);
-        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-        uint32_t c = 0;  // keys above the edge, and equal to it in the high half
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            c += (k[e] > edge) + ((uint32_t)(k[e] == edge && k[e] != 0) << 16);
-        if (!__any_sync(0xffffffffu, c != 0))
-            continue;
-        uint32_t incl = c;
+    for (int c = k_begin; c < k_end; ++c) {
+        const uint32_t x = c - k0 < held_chunks ? *slot(c) : marks(c);
+        const uint32_t mine = __popc(x & 0xffffu) | __popc(x >> 16) << 16;
+        uint32_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o)
-                incl += u;
+                incl += y;
         }
-        uint32_t g = g0 + ((incl - c) & 0xffffu), e2 = e0 + ((incl - c) >> 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (k[e] > edge) {
-                to[g + min(e2, need)] = 4 * (q + lane) + e;
-                ++g;
-            } else if (k[e] == edge) {
-                if (e2 < need)
-                    to[g + e2] = 4 * (q + lane) + e;
-                ++e2;
+        uint32_t g = g0 + ((incl - mine) & 0xffffu), e2 = e0 + ((incl - mine) >> 16);
+        if (need == 0) {
+            for (uint32_t m = x & 0xffffu; m; m &= m - 1)
+                to[g++] = position(c) + __ffs(m) - 1;
+        } else {
+            for (uint32_t m = (x | x >> 16) & 0xffffu; m; m &= m - 1) {
+                const int e = __ffs(m) - 1;
+                const bool above = x >> e & 1;
+                if (above || e2 < need)
+                    to[g + min(e2, need)] = position(c) + e;
+                g += above;
+                e2 += !above;
             }
         }
         const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
@@ -299,32 +394,42 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p)
 cudaError_t launch_select(SelectParams &p, int sms, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)p.R * p.heads;
-    // CTAs a row: as many as leave each at least 4096 positions and the grid at most two a SM
-    int C = 1;
-    while (C < 8 && rows * C <= sms && p.w_stride / C > 4096)
-        C *= 2;
-    const int per = ((p.w_stride + 3) / 4 + C - 1) / C * 4;
-    const int most = (rows * C <= sms ? 200 : 100) * 256;  // KB as keys
-    p.held = per < most ? per : most;
-    const size_t smem = sizeof(SelectSmem) + (size_t)p.held * 4;
-    static SmemOptIn opt;
-    const cudaError_t e = opt.set(select_kernel, sizeof(SelectSmem) + 200 * 1024);
+    // CTAs a row: as many as fill the SMs, with one CTA of 1024 threads each (64 registers a thread:
+    // they take all of an SM's) or, for more rows than half of the SMs, two of 512; 2048 positions a
+    // CTA at least, and 2^20 at most, for a lane's 16-bit counters (api.cu holds w_stride to 2^22).
+    // At most six: 23 clusters of six such CTAs find room at once, but 15 of seven or of eight, and
+    // the sixteenth of 16 rows began 34 us late.
+    const bool small = p.w_stride <= 8192;
+    const bool wide = rows * 2 <= sms && !small;
+    int64_t C = (wide ? 1 : 2) * sms / rows;
+    C = C < kMaxCtas ? C : kMaxCtas;
+    C = C < p.w_stride / 2048 ? C : p.w_stride / 2048;
+    C = C > (p.w_stride >> 20) + 1 ? C : (p.w_stride >> 20) + 1;
+    const int chunk = 32 * (small ? 4 : 16);
+    const int64_t chunks = ((int64_t)p.w_stride + chunk - 1) / chunk, per = (chunks + C - 1) / C * chunk;
+    // of an SM's 227 KB, for one CTA or for two
+    const int64_t most = ((wide ? 224 : 112) * 1024 - (int64_t)sizeof(SelectSmem)) / (2 * chunk) * chunk;
+    p.held = (int32_t)(per < most ? per : most);
+    const size_t smem = sizeof(SelectSmem) + (size_t)p.held * 2;
+    static SmemOptIn opt[3];
+    const auto kern = small ? select_kernel<512, 4> : wide ? select_kernel<1024, 16> : select_kernel<512, 16>;
+    const cudaError_t e = opt[small ? 0 : wide ? 1 : 2].set(kern, 224 * 1024);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(wide ? 1024 : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.x = (unsigned)C;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, select_kernel, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace hsa

@@ -443,7 +443,7 @@ hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void
 
 /*
  * The positions that stay.  Request r is row seq_idx[r] of w ([batch, heads, w_stride]), with
- * kv_len[r] positions.  For each of the `heads` rows, of n > budget positions stay the first
+ * kv_len[r] positions; w_stride at most 2^22 (else HSA_UNSUPPORTED_SHAPE).  For each of the `heads` rows, of n > budget positions stay the first
  * `sinks`, the last `recent` (sinks + recent <= budget) and, of the others, those of the
  * largest score until the budget is full: a position's score is the largest weight among
  * itself and its `reach` neighbours on each side (0 .. 7), NaN counting as -infinity and -0 as

@@ -107,6 +107,17 @@ def test_select_long_rows(kind, reach):
     assert new.tolist() == [budget] * 3
 
 
+@pytest.mark.parametrize("kind", ["equal", "close"])
+def test_select_longest_rows(kind):
+    """As many positions a CTA as its counters hold, all with one exponent."""
+    hsa = _hsa()
+    n, budget = 1 << 22, 70000
+    w = VALUES[kind](_gen(2), 1, 1, n)
+    keep, new = hsa.hsa_kv_select(w, _i32([n]), _i32([0]), budget)
+    want = w[0, 0].sort(descending=True, stable=True).indices[:budget].sort().values
+    assert torch.equal(keep[0, 0].long(), want) and new.tolist() == [budget]
+
+
 @pytest.mark.parametrize("R", [1, 20, 200])
 def test_select_many_rows(R):
     """Fewer and more rows than SMs: another number of CTAs a row."""
