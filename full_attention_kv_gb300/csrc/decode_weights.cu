@@ -17,7 +17,7 @@
 // to the workspace: no barrier among the consumers.  The new tokens are a tile of 16 keys that
 // one group takes at the unit's end.
 //
-// join_kernel: chunks of 1024 positions of all units, cut evenly.  A unit's states (those of the
+// join_kernel: chunks of positions of all units, cut evenly.  A unit's states (those of the
 // CTAs whose ranges met it lie side by side) give lse; then two floats to four a thread, the
 // scores become weights and are summed over the rows by shuffles.  Eight rows of output are an
 // item of their own.  The order of every sum is fixed by the sizes.
@@ -37,7 +37,9 @@ constexpr int kFp8TileBytes = kTileKeys * kD;
 constexpr int kFp8StageStride = 17408;           // codes of K and V, 2 x 64 scales, up to 1 KB
 constexpr int kLens = 1024;                      // sequences whose lengths are kept on chip
 constexpr int kJoinThreads = 256;
-constexpr int kChunk = 1024;                     // positions a join item
+constexpr int kJoinCtas = 3;                     // of it, an SM (85 registers a thread)
+constexpr int kBatch = 6;                        // loads of scores a thread has on the way
+constexpr float kUnused = -1.f;                  // sum of the rounded weights of a group without keys
 
 // Warps, groups and stages of an instantiation.  A stage belongs to one group (the stages are a
 // multiple of the groups), so that a parity never stands for two of its phases.
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(Shape<FP8, NT, RH>::kThreads, 1)
                 if (g == 0) {
                     part[row] = st.m[n][e];
                     part[RP + row] = l;
-                    part[2 * RP + row] = lr;
+                    part[2 * RP + row] = used ? lr : kUnused;
                 }
             }
         if (used) {
@@ -747,10 +749,14 @@ __device__ __forceinline__ void append_rows(const WeighParams &p, int b, int h, 
     }
 }
 
+constexpr int kMaxParts = 2048;                  // groups of all CTAs (152 x 8; launch_attend)
+
 struct JoinSmem {
     int32_t len[kLens];
     int32_t scan[kJoinThreads];
     float m[kMaxRows], lse[kMaxRows], norm[kMaxRows];
+    int32_t list[kMaxParts];  // the unit's states that hold keys
+    int32_t listed[kJoinThreads / 32];
     int32_t first_b, before, total;
     int32_t pages_total, pages_before;
 };
@@ -758,8 +764,10 @@ struct JoinSmem {
 // VEC scores a load, LK lanes a key: srow = VEC LK.  GW: groups of the attend kernel, RP its padded
 // rows, ctas its grid.
 template <int VEC, int LK>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const WeighParams p, int GW, int RP, int ctas)
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
+    join_kernel(const WeighParams p, int GW, int RP, int ctas)
 {
+    constexpr int kStep = kJoinThreads / LK, kChunk = kBatch * kStep;  // positions an item
     __shared__ JoinSmem sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
@@ -819,30 +827,65 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const WeighParams p,
             const int64_t c_lo = ((u0 + 1) * PC - 1) / PN, c_hi = (u1 * PC - 1) / PN;
             part = p.part + (unit + c_lo) * GW * slot_floats(RP);
             parts = (int)(c_hi - c_lo + 1) * GW;
+            __syncthreads();  // the last unit's readers are done
+            // of a few pages a CTA, most groups have none: their states are left out
+            int held = 0;
+            for (int e0 = 0; e0 < parts; e0 += kJoinThreads) {
+                const int e = e0 + tid;
+                const bool on = e < parts && __ldcg(part + (int64_t)e * slot_floats(RP) + 2 * RP) != kUnused;
+                const uint32_t bits = __ballot_sync(0xffffffffu, on);
+                if (lane == 0)
+                    sh.listed[warp] = __popc(bits);
+                __syncthreads();
+                int at = held + __popc(bits & ((1u << lane) - 1));
+                for (int w = 0; w < kJoinThreads / 32; ++w) {
+                    at += w < warp ? sh.listed[w] : 0;
+                    held += sh.listed[w];
+                }
+                if (on)
+                    sh.list[at] = e;
+                __syncthreads();
+            }
+            parts = held;
             const int row = tid >> 3, s8 = tid & 7;  // eight threads a row
             float M = -INFINITY, L = 0.f, R = 0.f;
-            if (row < rows) {
-                for (int e = s8; e < parts; e += 8)
-                    M = fmaxf(M, __ldcg(part + (int64_t)e * slot_floats(RP) + row));
+            constexpr int kAhead = 4;
+            for (int e0 = s8; row < rows && e0 < parts; e0 += 8 * kAhead) {
+                float m[kAhead], l[kAhead], r[kAhead], top = M;
+#pragma unroll
+                for (int e = 0; e < kAhead; ++e) {
+                    const bool on = e0 + 8 * e < parts;
+                    const float *q = part + (int64_t)sh.list[on ? e0 + 8 * e : 0] * slot_floats(RP) + row;
+                    m[e] = on ? __ldcg(q) : -INFINITY;
+                    l[e] = on ? __ldcg(q + RP) : 0.f;
+                    r[e] = on ? __ldcg(q + 2 * RP) : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < kAhead; ++e)
+                    top = fmaxf(top, m[e]);
+                const float base = top == -INFINITY ? 0.f : top, f = fast_exp2(M - base);
+                L *= f;
+                R *= f;
+#pragma unroll
+                for (int e = 0; e < kAhead; ++e) {
+                    const float a = fast_exp2(m[e] - base);
+                    L += l[e] * a;
+                    R += r[e] * a;
+                }
+                M = top;
             }
+            float top = M;
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float base = M == -INFINITY ? 0.f : M;
-            if (row < rows) {
-                for (int e = s8; e < parts; e += 8) {
-                    const float *q = part + (int64_t)e * slot_floats(RP) + row;
-                    const float a = fast_exp2(__ldcg(q) - base);
-                    L += __ldcg(q + RP) * a;
-                    R += __ldcg(q + 2 * RP) * a;
-                }
-            }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float base = top == -INFINITY ? 0.f : top, f = fast_exp2(M - base);
+            L *= f;
+            R *= f;
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) {
                 L += __shfl_xor_sync(0xffffffffu, L, o);
                 R += __shfl_xor_sync(0xffffffffu, R, o);
             }
-            __syncthreads();  // the last unit's readers are done
             if (s8 == 0) {
                 sh.m[row] = base;
                 sh.lse[row] = row < rows && L > 0.f ? base + log2f(L) : INFINITY;
@@ -859,17 +902,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const WeighParams p,
             if (row < rows) {
                 const float base = sh.m[row];
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int e = 0; e < parts; ++e) {
-                    const float *q = part + (int64_t)e * slot_floats(RP);
-                    const float m = __ldcg(q + row);
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(q + 3 * RP + row * kD) + lane);
-                    const float a = fast_exp2(m - base);
-                    const bool there = m != -INFINITY;  // a group without keys wrote no output
-                    acc.x += there ? x.x * a : 0.f;
-                    acc.y += there ? x.y * a : 0.f;
-                    acc.z += there ? x.z * a : 0.f;
-                    acc.w += there ? x.w * a : 0.f;
+                constexpr int kAhead = 8;
+                for (int e0 = 0; e0 < parts; e0 += kAhead) {
+                    float m[kAhead];
+                    float4 x[kAhead];
+#pragma unroll
+                    for (int e = 0; e < kAhead; ++e) {
+                        const bool on = e0 + e < parts;
+                        const float *q = part + (int64_t)sh.list[on ? e0 + e : 0] * slot_floats(RP);
+                        m[e] = on ? __ldcg(q + row) : -INFINITY;
+                        x[e] = on ? __ldcg(reinterpret_cast<const float4 *>(q + 3 * RP + row * kD) + lane)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kAhead; ++e) {
+                        const float a = fast_exp2(m[e] - base);
+                        acc.x += x[e].x * a;
+                        acc.y += x[e].y * a;
+                        acc.z += x[e].z * a;
+                        acc.w += x[e].w * a;
+                    }
                 }
                 const float f = sh.norm[row];
                 const int t = row / p.G, hh = row % p.G;
@@ -880,33 +932,44 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const WeighParams p,
             if (j == 0 && p.append)
                 append_rows(p, b, h, c, tid);
         } else {
-            // ---- the weights of 1024 positions ----------------------------------------------
+            // ---- the weights of 256 to 2048 positions -----------------------------------------
             const int first = (j - out_items) * kChunk, end = min(c + p.T, first + kChunk);
             const float *const score = p.score + unit * p.w_stride * p.srow;
             const int64_t at = unit * p.w_stride;
-            constexpr int kStep = kJoinThreads / LK;
-#pragma unroll 4
-            for (int k = 0; k < kChunk / kStep; ++k) {
-                const int pos = first + k * kStep + tid / LK;
-                float sum = 0.f;
-                if (pos < end) {
-                    const float *s = score + (int64_t)pos * p.srow + sub * VEC;
-                    if constexpr (VEC == 4) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(s));
-                        sum = (fast_exp2(x.x - lse[0]) + fast_exp2(x.y - lse[1])) +
-                              (fast_exp2(x.z - lse[2]) + fast_exp2(x.w - lse[3]));
-                    } else {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(s));
-                        sum = fast_exp2(x.x - lse[0]) + fast_exp2(x.y - lse[1]);
+            const int p0 = first + tid / LK;
+            // (the loads all ahead of the stores, which might be to the same weights)
+            {
+                float4 x[kBatch];
+                float old[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int pos = p0 + k * kStep;
+                    x[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    old[k] = 0.f;
+                    if (pos < end) {
+                        const float *s = score + (int64_t)pos * p.srow + sub * VEC;
+                        if constexpr (VEC == 4) {
+                            x[k] = __ldcg(reinterpret_cast<const float4 *>(s));
+                        } else {
+                            const float2 y = __ldcg(reinterpret_cast<const float2 *>(s));
+                            x[k].x = y.x;
+                            x[k].y = y.y;
+                        }
+                        if (sub == 0 && p.w_prev && pos < c)
+                            old[k] = p.w_prev[at + pos];
                     }
                 }
 #pragma unroll
-                for (int o = 1; o < LK; o <<= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (pos < end && sub == 0) {
-                    if (p.w_prev && pos < c)
-                        sum = fmaf(p.decay, p.w_prev[at + pos], sum);
-                    p.w[at + pos] = sum;
+                for (int k = 0; k < kBatch; ++k) {
+                    const int pos = p0 + k * kStep;
+                    float sum = fast_exp2(x[k].x - lse[0]) + fast_exp2(x[k].y - lse[1]);
+                    if constexpr (VEC == 4)
+                        sum += fast_exp2(x[k].z - lse[2]) + fast_exp2(x[k].w - lse[3]);
+#pragma unroll
+                    for (int o = 1; o < LK; o <<= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (pos < end && sub == 0)
+                        p.w[at + pos] = p.w_prev && pos < c ? fmaf(p.decay, old[k], sum) : sum;
                 }
             }
         }
@@ -941,6 +1004,7 @@ cudaError_t launch_attend(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
 {
     using S = Shape<FP8, NT, RH>;
     const size_t smem = sizeof(AttendSmem<FP8, NT, RH>) + 1024;
+    ctas = ctas < kMaxParts / S::kGroups ? ctas : kMaxParts / S::kGroups;
     static SmemOptIn opt;
     cudaError_t e = opt.set(attend_kernel<FP8, NT, RH>, smem);
     if (e != cudaSuccess)
@@ -958,7 +1022,7 @@ cudaError_t launch_attend(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
     e = cudaLaunchKernelEx(&cfg, attend_kernel<FP8, NT, RH>, tmK, tmV, p);
     if (e != cudaSuccess)
         return e;
-    cfg.gridDim = dim3((unsigned)(4 * sms));
+    cfg.gridDim = dim3((unsigned)(kJoinCtas * sms));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     void (*join)(WeighParams, int, int, int) = p.srow == 2   ? join_kernel<2, 1>

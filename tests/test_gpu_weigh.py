@@ -300,6 +300,21 @@ def test_values_out_of_reach():
     s.check(s.run(), prev=None)
 
 
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_nan_query_stays_in_its_head(fmt):
+    """A row of NaN: its output and its KV head's weights, and nothing else."""
+    s = Step(_hsa(), [300, 5000], 2, 16, 2, fmt)
+    ok, w = s.run().clone(), s.w.clone()
+    s.q[1, 0, 3, 7] = float("nan")
+    out = s.run()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[1, 0, 3] = True
+    assert bool(out[bad].isnan().all()) and torch.equal(out[~bad], ok[~bad])
+    assert bool(s.w[1, 0, :5001].isnan().all())
+    s.w[1, 0], w[1, 0] = 0.0, 0.0
+    assert torch.equal(s.w, w)
+
+
 def test_refusals():
     hsa = _hsa()
     s = Step(hsa, [100, 20], 1, 16, 2)
