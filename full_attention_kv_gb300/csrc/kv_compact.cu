@@ -7,11 +7,10 @@
 // One CTA a destination page of a head.  Its 64 source rows are found first (keep, then the block
 // table), then every 16-byte chunk is one thread's: 256 contiguous bytes a bf16 row, 128 an FP8 K
 // row.  An FP8 layer's V is stored transposed (64 keys of a dimension side by side), so a single
-// key is 128 bytes in as many sectors; the source pages are taken whole instead, one after another
-// (positions ascend, so a page's keys are neighbours in the list): 8 KB into shared memory, the
-// wanted bytes into the destination page's tile there, and the tile out in 16-byte stores.  A
-// word of either tile lies rotated by half its dimension, so that the 32 dimensions of a warp meet
-// 32 banks.
+// key is 128 bytes in as many sectors; the source pages are taken whole instead (positions ascend,
+// so a page's keys are neighbours in the list), 8 KB bulk copies into shared memory, kPages of them
+// at a time.  A lane then puts together the same four keys of eight dimensions: two rows of 64 bytes
+// a warp, which meet 32 banks whatever the keys, and leave as 128 contiguous bytes.
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"
@@ -22,19 +21,27 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPage = 64;
 
-// Word `w` (0 .. 15) of dimension `dim` in a V tile in shared memory.
-__device__ __forceinline__ int v_word(int dim, int w) { return dim * 16 + ((w + (dim >> 1)) & 15); }
+constexpr int kPages = 6;               // source pages of V held at a time
+constexpr int kPageBytes = kPage * 128; // FP8 codes
 
 // Byte of key `row` of a page in a V row.
 __device__ __forceinline__ int v_byte(int row) { return 16 * (row >> 4) + perm16(row & 15); }
+
+struct VPages {
+    alignas(128) uint8_t stage[kPages][kPageBytes];
+    alignas(8) uint64_t full;
+    int64_t page[kPage];  // pages in the order of the list
+    int32_t slot[kPage];  // each key's among them
+    int32_t n;
+};
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p)
 {
     __shared__ int64_t src[kPage];  // a head's row in the pool, or -1
     __shared__ uint32_t ok[2];      // bit i: row i is to be copied
-    __shared__ uint32_t from[FP8 ? 128 * 16 : 1], to[FP8 ? 128 * 16 : 1];
-    const int tid = threadIdx.x, lane = tid & 31;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pages = (p.budget + kPage - 1) / kPage;
     const int page = blockIdx.x % pages;
     const int64_t rh = blockIdx.x / pages;
@@ -123,6 +130,43 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
         const int64_t cb = fp8_codes_bytes(p.num_blocks, p.Hkv);
         float *const ks = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.k) + cb);
         float *const vs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.v) + cb);
+        // ---- V: the source pages, one for each run of the list ------------------------------
+        VPages &sh = *reinterpret_cast<VPages *>(smem_raw);
+        if (tid == 0) {
+            mbar_init(&sh.full, 1);
+            fence_barrier_init();
+        }
+        if (tid < kPage) {
+            const int64_t pg = src[tid] >= 0 ? src[tid] / kPage : -1;
+            int64_t last = -1;  // the page of the nearest row before that is copied
+            const uint64_t have = (uint64_t)ok[1] << 32 | ok[0], below = have & ((1ull << tid) - 1);
+            if (below)
+                last = src[63 - __clzll((long long)below)] / kPage;
+            const bool starts = pg >= 0 && pg != last;
+            const uint32_t bits = __ballot_sync(0xffffffffu, starts);
+            if (lane == 0)
+                sh.slot[warp] = __popc(bits);
+            named_bar_sync(1, kPage);
+            const int before = warp == 1 ? sh.slot[0] : 0, all = sh.slot[0] + sh.slot[1];
+            named_bar_sync(1, kPage);
+            const int at = before + __popc(bits & (2u << lane) - 1u) - 1;
+            sh.slot[tid] = pg >= 0 ? at : -1;
+            if (starts)
+                sh.page[at] = pg;
+            if (tid == 0)
+                sh.n = all;
+        }
+        __syncthreads();
+        auto fetch = [&](int s0) {
+            if (tid == 0 && s0 < sh.n) {
+                const int n = min(kPages, sh.n - s0);
+                mbar_arrive_expect_tx(&sh.full, n * kPageBytes);
+                for (int e = 0; e < n; ++e)
+                    bulk_load(sh.stage[e], p.v + sh.page[s0 + e] * 512, kPageBytes, &sh.full, policy_evict_first());
+            }
+        };
+        fetch(0);
+        // ---- K rows and the scales, meanwhile -----------------------------------------------
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int i = (tid >> 3) + 32 * j;
@@ -133,56 +177,54 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
             ks[dst_row + tid] = ks[src[tid]];
             vs[dst_row + tid] = vs[src[tid]];
         }
-        // V: source pages in runs of the list
-        const int dim = tid & 127, half = tid >> 7;
-        const uint8_t *const fb = reinterpret_cast<const uint8_t *>(from);
-        uint8_t *const tb = reinterpret_cast<uint8_t *>(to);
-        int i = 0;
-        while (i < kPage) {
-            if (src[i] < 0) {  // the same for every thread
-                ++i;
-                continue;
-            }
-            const int64_t pg = src[i] / kPage;
-            int end = i + 1;
-            while (end < kPage && src[end] >= 0 && src[end] / kPage == pg)
-                ++end;
-            __syncthreads();  // `from` is free again
+        // this lane's word of a V row: four keys, each a slot and a byte there
+        const int word = lane & 15;
+        int slot[4], off[4];
+        bool whole = true, some = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int e = tid + kThreads * j;  // chunk e % 4 of dimension e / 4
-                const uint4 x = __ldcs(p.v + pg * 512 + e);
-                const int d = e >> 2, w = 4 * (e & 3);
-                from[v_word(d, w)] = x.x;
-                from[v_word(d, w + 1)] = x.y;
-                from[v_word(d, w + 2)] = x.z;
-                from[v_word(d, w + 3)] = x.w;
-            }
-            __syncthreads();
-            for (int k = i + half; k < end; k += 2) {
-                const int a = v_byte((int)(src[k] % kPage)), b = v_byte(k);
-                tb[4 * v_word(dim, b >> 2) + (b & 3)] = fb[4 * v_word(dim, a >> 2) + (a & 3)];
-            }
-            i = end;
+        for (int e = 0; e < 4; ++e) {  // byte e of the word is this key (perm16 undone)
+            const int key = 16 * (word >> 2) + 2 * (word & 3) + (e & 1) + 8 * (e >> 1);
+            slot[e] = sh.slot[key];
+            off[e] = slot[e] >= 0 ? v_byte((int)(src[key] % kPage)) : 0;
+            whole &= slot[e] >= 0;
+            some |= slot[e] >= 0;
         }
-        __syncthreads();
-        const uint64_t have = (uint64_t)ok[1] << 32 | ok[0];
+        uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        bool done = true;
+        for (int s0 = 0, phase = 0; s0 < sh.n; s0 += kPages, phase ^= 1) {
+            if (!mbar_wait(&sh.full, phase)) {
+                set_err(p.dev_err, HSA_DEVERR_TIMEOUT);
+                done = false;
+            }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = tid + kThreads * j, d = e >> 2, g = e & 3;  // 16 keys from 16 g on
-            const uint4 x = make_uint4(to[v_word(d, 4 * g)], to[v_word(d, 4 * g + 1)],
-                                       to[v_word(d, 4 * g + 2)], to[v_word(d, 4 * g + 3)]);
-            uint4 *const at = p.v + dst_row * 8 + e;
-            const uint32_t got = (uint32_t)(have >> (16 * g)) & 0xffffu;
-            if (got == 0xffffu) {
-                *at = x;
-            } else if (got) {
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int e = 0; e < 4; ++e) {
+                const int st = slot[e] - s0;
+                if (slot[e] >= 0 && st >= 0 && st < kPages) {
+                    const uint8_t *const from = &sh.stage[st][(2 * warp + (lane >> 4)) * 64 + off[e]];
 #pragma unroll
-                for (int l = 0; l < 16; ++l)
-                    if (got >> l & 1)
-                        reinterpret_cast<uint8_t *>(at)[perm16(l)] =
-                            (uint8_t)(w[perm16(l) / 4] >> (8 * (perm16(l) % 4)));
+                    for (int j = 0; j < 8; ++j)  // dimensions 16 apart
+                        x[j] |= (uint32_t)from[j * 1024] << (8 * e);
+                }
+            }
+            done = __syncthreads_and(done);  // the stages are free again
+            if (!done) {
+                mbar_wait(&sh.full, phase);  // no copy may still be in flight when the CTA exits
+                break;
+            }
+            fetch(s0 + kPages);
+        }
+        uint32_t *const to = reinterpret_cast<uint32_t *>(p.v + dst_row * 8) + (2 * warp + (lane >> 4)) * 16 + word;
+        if (done && some) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (whole) {
+                    to[j * 256] = x[j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (slot[e] >= 0)
+                            reinterpret_cast<uint8_t *>(to + j * 256)[e] = (uint8_t)(x[j] >> (8 * e));
+                }
             }
         }
     }
@@ -193,9 +235,17 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
 cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream)
 {
     const int64_t ctas = (int64_t)p.R * p.Hkv * ((p.budget + kPage - 1) / kPage);
+    const size_t smem = p.fp8 ? sizeof(VPages) : 0;
+    static SmemOptIn opt;
+    if (p.fp8) {
+        const cudaError_t e = opt.set(compact_kernel<true>, smem);
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
