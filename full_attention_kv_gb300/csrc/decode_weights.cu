@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
             }
             if (s8 == 0) {
                 sh.m[row] = base;
-                sh.lse[row] = row < rows && L > 0.f ? base + log2f(L) : INFINITY;
+                sh.lse[row] = row < rows && L != 0.f ? base + log2f(L) : INFINITY;  // (NaN passes)
                 sh.norm[row] = R > 0.f ? 1.f / R : 0.f;
             }
             __syncthreads();

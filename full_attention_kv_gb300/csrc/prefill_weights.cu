@@ -35,7 +35,8 @@ constexpr int kGroups = 4;                  // warpgroups, and TMEM slots
 constexpr int kIssuers = 2;
 constexpr int kThreads = 128 + kGroups * 128;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kSlack = 60.0f;            // a running maximum may lag by so much (log2 units)
+constexpr int kCols = 32;                  // columns a thread takes at a time (16: 299 us for 291)
+constexpr float kFar = 0x1p60f;            // of a chunk's sum: its maximum has left the running one behind
 
 struct alignas(1024) PromptSmem {
     uint8_t tile[kTiles][kTileBytes];
@@ -105,6 +106,28 @@ __device__ __forceinline__ int page_at(const PromptParams &p, const Request &q, 
         return 1;
     *err = page < p.max_blocks ? HSA_DEVERR_BAD_BLOCK : HSA_DEVERR_BAD_PAGE;
     return -1;
+}
+
+// Four consecutive 32-bit TMEM columns of this thread's lane (warp-collective).
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+}
+
+// Four sums of 2^(x scale - base) over kCols columns (sc2: the scale twice).
+__device__ __forceinline__ void exp_sums(const uint32_t (&x)[kCols], uint64_t sc2, float base, float (&sum)[4])
+{
+    const uint64_t nb2 = f2_make(-base, -base);
+    sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2) {
+        float a, b;
+        f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, nb2), a, b);
+        sum[c & 2] += fast_exp2(a);
+        sum[(c & 2) + 1] += fast_exp2(b);
+    }
 }
 
 struct Walk {
@@ -441,42 +464,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                     take();
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kBlock; c0 += 32) {
-                        uint32_t x[32];
+                    for (int c0 = 0; c0 < kBlock; c0 += kCols) {
+                        uint32_t x[kCols];
                         tmem_ld32(taddr + c0, x);
                         tmem_wait_ld();
-                        if (c0 == kBlock - 32)
+                        if (c0 == kBlock - kCols)
                             give();
                         if (!whole) {
                             const int top = (pair >> (c0 >> 6) & 1u) ? hi - c0 : 0;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
+                            for (int c = 0; c < kCols; ++c)
                                 if (c >= top)
                                     x[c] = __float_as_uint(-INFINITY);
                         }
-                        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2)
-                            mx[c >> 1 & 1] = fmax3(mx[c >> 1 & 1], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                        const float top = fmaxf(mx[0], mx[1]) * p.scale_log2;
-                        if (top != -INFINITY && (m == -INFINITY || top > m + kSlack)) {
-                            const float f = m == -INFINITY ? 0.f : fast_exp2(m - top);
-                            l *= f;
-                            lost *= f;
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                acc[c] *= f;
-                            m = top;
-                        }
+                        // the exponents take the maximum as of the chunks before.  A sum that
+                        // leaves fp32's middle says that this chunk's is far above it; only
+                        // then, and at the first, is it sought.
+                        float part[4];
                         const float base = m == -INFINITY ? 0.f : m;
-                        const uint64_t nb2 = f2_make(-base, -base);
+                        exp_sums(x, sc2, base, part);
+                        const float all = (part[0] + part[1]) + (part[2] + part[3]);
+                        if (m == -INFINITY || !(all < kFar)) {
+                            float top = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float a, b;
-                            f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, nb2), a, b);
-                            acc[c & 2] += fast_exp2(a);
-                            acc[(c & 2) + 1] += fast_exp2(b);
+                            for (int c = 0; c < kCols; c += 2)
+                                top = fmax3(top, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                            top *= p.scale_log2;
+                            if (top != -INFINITY && (m == -INFINITY || top > m)) {
+                                const float f = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                                l *= f;
+                                lost *= f;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    acc[c] *= f;
+                                m = top;
+                                exp_sums(x, sc2, top, part);
+                            }
                         }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc[c] += part[c];
                     }
                     const float add = ((acc[0] + acc[1]) + (acc[2] + acc[3])) - lost, sum = l + add;
                     lost = (sum - l) - add;
@@ -504,17 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             top = fmaxf(top, s[e].x);
-                        if (top != -INFINITY) {
-                            L *= fast_exp2(M - top);
+                        const float base = top == -INFINITY ? 0.f : top;
+                        L *= fast_exp2(M - base);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                L += s[e].y * fast_exp2(s[e].x - top);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            L += s[e].y * fast_exp2(s[e].x - base);
                         M = top;
                     }
-                    const bool on = row0 + me < rows && L > 0.f;
+                    const float base = M == -INFINITY ? 0.f : M;
+                    const bool on = row0 + me < rows && L != 0.f;  // (NaN passes)
                     named_bar_sync(1 + wg, kBlock);  // the last unit's readers are done
-                    sh.neg_lse[wg][me] = on ? -(M + log2f(L)) : -INFINITY;
+                    sh.neg_lse[wg][me] = on ? -(base + log2f(L)) : -INFINITY;
                     named_bar_sync(1 + wg, kBlock);
                 }
                 const int64_t at = ((int64_t)w.q.seq * p.Hkv + w.h) * p.w_stride;
@@ -532,18 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float old = t == 0 && p.w_prev && pos < n - w.q.m ? p.w_prev[at + pos] : 0.f;
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
                     take();
+                    if (all && top == kBlock) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < top; c0 += 32) {
-                        uint32_t x[32];
-                        tmem_ld32(taddr + c0, x);
-                        const float4 *const nl = reinterpret_cast<const float4 *>(&sh.neg_lse[wg][c0]);
-                        tmem_wait_ld();
-                        if (c0 + 32 >= top)
-                            give();
-                        if (all && c0 + 32 <= top) {
+                        for (int c0 = 0; c0 < kBlock; c0 += kCols) {
+                            uint32_t x[kCols];
+                            tmem_ld32(taddr + c0, x);
+                            tmem_wait_ld();
+                            if (c0 == kBlock - kCols)
+                                give();
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const float4 y = nl[c >> 2];
+                            for (int c = 0; c < kCols; c += 4) {
+                                const float4 y = *reinterpret_cast<const float4 *>(&sh.neg_lse[wg][c0 + c]);
                                 float a, b, d, f;
                                 f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2,
                                                 f2_make(y.x, y.y)), a, b);
@@ -554,13 +580,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 acc[2] += fast_exp2(d);
                                 acc[3] += fast_exp2(f);
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (c0 + c >= first && c0 + c < top)
-                                    acc[c & 3] +=
-                                        fast_exp2(fmaf(__uint_as_float(x[c]), p.scale_log2, sh.neg_lse[wg][c0 + c]));
                         }
+                    } else {
+                        // rows that do not see the key, or that there are not
+#pragma unroll 1
+                        for (int c0 = 0; c0 < top; c0 += 4) {
+                            uint32_t x[4];
+                            tmem_ld4(taddr + c0, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c0 + c >= first && c0 + c < top)
+                                    acc[c] += fast_exp2(fmaf(__uint_as_float(x[c]), p.scale_log2, sh.neg_lse[wg][c0 + c]));
+                        }
+                        give();
                     }
                     float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
                     if (t > 0) {  // over to the key tile's first warpgroup
