@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(Shape<FP8, NT, RH>::kThreads, 1)
 
     if (warp == CW) {
         // ------------------------------------------------------------------------ producer
-        // lane l finds the pool row of page start + l, 32 pages at a time and a batch ahead;
-        // lane 0 issues the stages
+        // lane l finds the pool row of page start + l, 32 pages at a time and a batch ahead; the
+        // whole warp waits for the stages and one elected lane issues them
         const uint64_t pol = policy_evict_first();
         const int64_t cb = fp8_codes_bytes(p.num_blocks, p.Hkv);
         auto pool_row = [&](const UnitWalk &w) -> int64_t {
@@ -526,38 +526,35 @@ __global__ void __launch_bounds__(Shape<FP8, NT, RH>::kThreads, 1)
             const int cnt = (int)(i1 - ib < 32 ? i1 - ib : 32);
             for (int e = 0; e < cnt; ++e, ++k) {
                 const int64_t r = __shfl_sync(0xffffffffu, row, e);
-                int ok = 1;
-                if (lane == 0) {
-                    const int st = (int)(k % NS);
-                    if (!mbar_wait(&sh.empty[st], (uint32_t)((k / NS) & 1) ^ 1)) {
+                const int st = (int)(k % NS);
+                if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[st], (uint32_t)((k / NS) & 1) ^ 1))) {
+                    if (lane == 0)
                         set_err(p.dev_err, HSA_DEVERR_TIMEOUT);
-                        ok = 0;
-                    } else {
-                        uint8_t *dst = sh.stage + st * S::kStageStride;
-                        sh.tile_ok[st] = r >= 0;
-                        if (r < 0) {
-                            mbar_arrive(&sh.full[st]);
-                        } else if (FP8) {
-                            mbar_arrive_expect_tx(&sh.full[st], 2 * kFp8TileBytes + 2 * 256);
-                            tma_load_2d(dst, &tmK, &sh.full[st], 0, (int32_t)r, pol);
-                            tma_load_2d(dst + kFp8TileBytes, &tmV, &sh.full[st], 0, (int32_t)(2 * r), pol);
-                            bulk_load(dst + 2 * kFp8TileBytes, reinterpret_cast<const uint8_t *>(p.k_pool) + cb + r * 4,
-                                      256, &sh.full[st], pol);
-                            bulk_load(dst + 2 * kFp8TileBytes + 256,
-                                      reinterpret_cast<const uint8_t *>(p.v_pool) + cb + r * 4, 256, &sh.full[st], pol);
-                        } else {
-                            mbar_arrive_expect_tx(&sh.full[st], 2 * kTileBytes);
-                            tma_load_2d(dst, &tmK, &sh.full[st], 0, (int32_t)r, pol);
-                            tma_load_2d(dst + kTileBytes / 2, &tmK, &sh.full[st], 64, (int32_t)r, pol);
-                            tma_load_2d(dst + kTileBytes, &tmV, &sh.full[st], 0, (int32_t)r, pol);
-                            tma_load_2d(dst + kTileBytes + kTileBytes / 2, &tmV, &sh.full[st], 64, (int32_t)r, pol);
-                        }
-                    }
-                }
-                if (!__shfl_sync(0xffffffffu, ok, 0)) {
                     stop = true;
                     break;
                 }
+                uint8_t *const dst = sh.stage + st * S::kStageStride;
+                if (elect_one()) {
+                    sh.tile_ok[st] = r >= 0;
+                    if (r < 0) {
+                        mbar_arrive(&sh.full[st]);
+                    } else if (FP8) {
+                        mbar_arrive_expect_tx(&sh.full[st], 2 * kFp8TileBytes + 2 * 256);
+                        tma_load_2d(dst, &tmK, &sh.full[st], 0, (int32_t)r, pol);
+                        tma_load_2d(dst + kFp8TileBytes, &tmV, &sh.full[st], 0, (int32_t)(2 * r), pol);
+                        bulk_load(dst + 2 * kFp8TileBytes, reinterpret_cast<const uint8_t *>(p.k_pool) + cb + r * 4, 256,
+                                  &sh.full[st], pol);
+                        bulk_load(dst + 2 * kFp8TileBytes + 256, reinterpret_cast<const uint8_t *>(p.v_pool) + cb + r * 4,
+                                  256, &sh.full[st], pol);
+                    } else {
+                        mbar_arrive_expect_tx(&sh.full[st], 2 * kTileBytes);
+                        tma_load_2d(dst, &tmK, &sh.full[st], 0, (int32_t)r, pol);
+                        tma_load_2d(dst + kTileBytes / 2, &tmK, &sh.full[st], 64, (int32_t)r, pol);
+                        tma_load_2d(dst + kTileBytes, &tmV, &sh.full[st], 0, (int32_t)r, pol);
+                        tma_load_2d(dst + kTileBytes + kTileBytes / 2, &tmV, &sh.full[st], 64, (int32_t)r, pol);
+                    }
+                }
+                __syncwarp();
             }
             row = nrow;
         }

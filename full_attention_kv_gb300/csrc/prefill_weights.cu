@@ -10,7 +10,10 @@
 // Pass 1 takes the rows as TMEM lanes (S = Q K^T, 128 rows x 128 keys): a thread owns a row, keeps
 // its running maximum and sum over the keys, and leaves them in the workspace.  Pass 2 takes the
 // keys as lanes (S^T = K Q^T, the same tiles in shared memory with A and B exchanged): a thread
-// owns a key, and the sum over a tile's rows is its own.  Neither sums across threads.
+// owns a key, and the sum over a tile's rows is its own.  Neither sums across threads.  The lse
+// goes in through the product: 16 more columns, three ones a key against the three bf16 parts of a
+// row's -lse.  (Read from shared memory, 16 bytes to a warp for every four columns, beside the products'
+// own reads there, pass 2 took 5% longer.)
 //
 // Both: persistent, one CTA an SM; the 128-key tiles (two pages) of all (request, KV head) units
 // laid end to end and cut into equal ranges.  Warp 0 loads Q (up to four tiles of 128 rows) at a
@@ -31,6 +34,8 @@ constexpr int kHalfBytes = kBlock * 128;   // 128 rows x 64 bf16 (one swizzle co
 constexpr int kTileBytes = 2 * kHalfBytes; // 32 KB
 constexpr int kTiles = 6;                  // Q tiles and K stages together
 constexpr int kMaxStages = 4;
+constexpr int kMaxRowTiles = 4;
+constexpr int kAugBytes = kBlock * 16 * 2; // a tile of 16 columns, K-major without swizzle
 constexpr int kGroups = 4;                  // warpgroups, and TMEM slots
 constexpr int kIssuers = 2;
 constexpr int kThreads = 128 + kGroups * 128;
@@ -40,9 +45,10 @@ constexpr float kFar = 0x1p60f;            // of a chunk's sum: its maximum has 
 
 struct alignas(1024) PromptSmem {
     uint8_t tile[kTiles][kTileBytes];
-    alignas(16) float neg_lse[kGroups][kBlock];  // pass 2: of each warpgroup's rows
-    float sum[kGroups][2][kBlock];               // pass 2: its keys' sums, for the first one
-    alignas(8) uint64_t q_full, q_empty, done;
+    alignas(128) uint8_t ones[kAugBytes];           // pass 2: 16 more columns of K: three of 1
+    alignas(128) uint8_t aug[kMaxRowTiles][kAugBytes]; // and of Q: a row's -lse in three parts
+    float sum[kGroups][2][kBlock];                  // pass 2: a warpgroup's keys' sums, for the first one
+    alignas(8) uint64_t q_full, q_empty, aug_full, done;
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
     uint64_t s_full[kGroups], s_empty[kGroups];
     uint64_t sum_full[kGroups][2], sum_free[kGroups][2];
@@ -50,6 +56,10 @@ struct alignas(1024) PromptSmem {
     int32_t first_r, before, total;
     uint32_t tmem_base;
 };
+
+// First byte of a row's columns 0-7 in a tile of 16: groups of eight rows of 16 bytes, the columns
+// 8-15 (another such group, always zero here) 128 bytes behind.
+__device__ __forceinline__ int aug_offset(int row) { return row / 8 * 256 + row % 8 * 16; }
 
 struct Request {
     int n, m, T, seq, row0;  // tokens, new rows, queries, sequence, first query row; T = 0: left out
@@ -108,6 +118,13 @@ __device__ __forceinline__ int page_at(const PromptParams &p, const Request &q, 
     return -1;
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Four consecutive 32-bit TMEM columns of this thread's lane (warp-collective).
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4])
 {
@@ -128,6 +145,12 @@ __device__ __forceinline__ void exp_sums(const uint32_t (&x)[kCols], uint64_t sc
         sum[c & 2] += fast_exp2(a);
         sum[(c & 2) + 1] += fast_exp2(b);
     }
+}
+
+// A wait of a whole warp, whose lanes go on together also where it gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait_sleep(bar, parity));
 }
 
 struct Walk {
@@ -203,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, kIssuers);
         mbar_init(&sh.done, kIssuers);
+        mbar_init(&sh.aug_full, kGroups * kBlock / 32);
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&sh.k_full[s], 1);
             mbar_init(&sh.k_empty[s], kIssuers);
@@ -216,6 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         fence_barrier_init();
+    }
+    if (PASS == 2 && tid < kBlock) {
+        uint4 *const row = reinterpret_cast<uint4 *>(sh.ones + aug_offset(tid));
+        row[0] = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
+        row[8] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
     }
     if (warp == 1) {
         tmem_alloc(&sh.tmem_base, kTmemCols);
@@ -262,18 +292,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t i = i0; i < i1 && ok; ++units) {
             const int64_t end = i + min((int64_t)(w.nt - w.j), i1 - i);
             const int nq = row_tiles(w);
-            if (lane == 0) {
-                if (units > 0 && !mbar_wait_sleep(&sh.q_empty, (uint32_t)(units - 1) & 1)) {
-                    ok = false;
-                } else {
-                    mbar_arrive_expect_tx(&sh.q_full, nq * kTileBytes);
-                    for (int t = 0; t < nq; ++t) {
-                        const int row = w.q.row0 + t * (kBlock / p.G);
-                        tma_load_3d(sh.tile[t], &tmQ, &sh.q_full, 0, w.h * p.G, row, pol);
-                        tma_load_3d(sh.tile[t] + kHalfBytes, &tmQ, &sh.q_full, 64, w.h * p.G, row, pol);
-                    }
+            if (units > 0 && !(ok = warp_wait(&sh.q_empty, (uint32_t)(units - 1) & 1)))
+                break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sh.q_full, nq * kTileBytes);
+                for (int t = 0; t < nq; ++t) {
+                    const int row = w.q.row0 + t * (kBlock / p.G);
+                    tma_load_3d(sh.tile[t], &tmQ, &sh.q_full, 0, w.h * p.G, row, pol);
+                    tma_load_3d(sh.tile[t] + kHalfBytes, &tmQ, &sh.q_full, 64, w.h * p.G, row, pol);
                 }
             }
+            __syncwarp();
             // pool rows of 32 pages (16 tiles) at a time, a lane each, a batch ahead
             int j = w.j, batch = w.j;
             int cur = page_entry(p, w.q, 2 * batch + lane);
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int err = 0;
                 if (page_at(p, w.q, page, blk, &err) > 0)
                     return ((int64_t)blk * p.Hkv + w.h) * 64;
-                if (PASS == 1 && err)
+                if (PASS == 1 && err && lane == 0)
                     set_err(p.dev_err, err);
                 return -1;
             };
@@ -295,30 +324,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int b0 = __shfl_sync(0xffffffffu, cur, 2 * (j - batch));
                 const int b1 = __shfl_sync(0xffffffffu, cur, 2 * (j - batch) + 1);
-                if (lane == 0 && ok) {
-                    if (!mbar_wait_sleep(&sh.k_empty[st], ph ^ 1)) {
-                        ok = false;
-                    } else {
-                        uint8_t *dst = sh.tile[q_tiles + st];
-                        const int64_t y0 = pool_row(2 * j, b0), y1 = pool_row(2 * j + 1, b1);
-                        const int pages = (y0 >= 0) + (y1 >= 0);
-                        if (pages == 0)
-                            mbar_arrive(&sh.k_full[st]);
-                        else
-                            mbar_arrive_expect_tx(&sh.k_full[st], pages * (kTileBytes / 2));
-                        if (y0 >= 0) {
-                            tma_load_2d(dst, &tmK, &sh.k_full[st], 0, (int32_t)y0, pol);
-                            tma_load_2d(dst + kHalfBytes, &tmK, &sh.k_full[st], 64, (int32_t)y0, pol);
-                        }
-                        if (y1 >= 0) {
-                            tma_load_2d(dst + 8192, &tmK, &sh.k_full[st], 0, (int32_t)y1, pol);
-                            tma_load_2d(dst + kHalfBytes + 8192, &tmK, &sh.k_full[st], 64, (int32_t)y1, pol);
-                        }
+                const int64_t y0 = pool_row(2 * j, b0), y1 = pool_row(2 * j + 1, b1);
+                const int pages = (y0 >= 0) + (y1 >= 0);
+                if (!(ok = warp_wait(&sh.k_empty[st], ph ^ 1)))
+                    break;
+                uint8_t *dst = sh.tile[q_tiles + st];
+                if (elect_one()) {
+                    if (pages == 0)
+                        mbar_arrive(&sh.k_full[st]);
+                    else
+                        mbar_arrive_expect_tx(&sh.k_full[st], pages * (kTileBytes / 2));
+                    if (y0 >= 0) {
+                        tma_load_2d(dst, &tmK, &sh.k_full[st], 0, (int32_t)y0, pol);
+                        tma_load_2d(dst + kHalfBytes, &tmK, &sh.k_full[st], 64, (int32_t)y0, pol);
+                    }
+                    if (y1 >= 0) {
+                        tma_load_2d(dst + 8192, &tmK, &sh.k_full[st], 0, (int32_t)y1, pol);
+                        tma_load_2d(dst + kHalfBytes + 8192, &tmK, &sh.k_full[st], 64, (int32_t)y1, pol);
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok)
-                    break;
+                __syncwarp();
                 issued = min(issued + 1, stages);
                 if (++st == stages) {
                     st = 0;
@@ -346,6 +371,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one())
                 tc_commit(bar);
         };
+        // a tile of 16 columns: no swizzle, 128 bytes from its columns 0-7 to 8-15, 256 from eight
+        // rows to the next
+        auto aug_desc = [](const uint8_t *tile) -> uint64_t {
+            return (uint64_t)(smem_u32(tile) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | 1ull << 46;
+        };
         int st = 0, units = 0;
         uint32_t ph = 0;
         uint32_t given = 0;  // bit wg: parity of the tiles handed to warpgroup wg
@@ -353,9 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t i = i0; i < i1 && ok; ++units) {
             const int tiles = (int)min((int64_t)(w.nt - w.j), i1 - i);
             const int nq = row_tiles(w), rows = w.q.T * p.G, step = step_of(nq);
-            ok = mbar_wait_sleep(&sh.q_full, (uint32_t)units & 1);
+            ok = warp_wait(&sh.q_full, (uint32_t)units & 1) &&
+                 (PASS == 1 || warp_wait(&sh.aug_full, (uint32_t)units & 1));
             for (int e = 0; e < tiles && ok; ++e) {
-                if (!(ok = mbar_wait_sleep(&sh.k_full[st], ph)))
+                if (!(ok = warp_wait(&sh.k_full[st], ph)))
                     break;
                 tc_fence_after();
                 const uint32_t kl = smem_desc_sw128_lo(smem_u32(sh.tile[q_tiles + st]), 16);
@@ -363,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int slot = (e * step + t) & (kGroups - 1);
                     if ((slot & 1) != u)
                         continue;
-                    if (!(ok = mbar_wait_sleep(&sh.s_empty[slot], (given >> slot & 1) ^ 1)))
+                    if (!(ok = warp_wait(&sh.s_empty[slot], (given >> slot & 1) ^ 1)))
                         break;
                     given ^= 1u << slot;
                     tc_fence_after();
@@ -383,6 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tc_mma_ss_k<1>(d, desc_join(a + off, dhi), desc_join(b + off, dhi), id);
                         }
                     }
+                    if (PASS == 2 && one)  // S^T - lse
+                        tc_mma_ss_k<1>(d, aug_desc(sh.ones), aug_desc(sh.aug[t]), id);
                     commit(&sh.s_full[slot]);
                 }
                 if (!ok)
@@ -409,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t taddr = tmem + ((uint32_t)(wq * 32) << 16) + wg * kBlock;
         const uint64_t sc2 = f2_make(p.scale_log2, p.scale_log2);
         uint32_t cnt = 0;       // tiles taken
+        int units = 0;
         uint32_t handed = 0;    // pass 2: byte g: sums that warpgroup g has handed over, mod 4
         bool ok = true;
         // bit e: page 2 batch + e can be read
@@ -451,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (PASS == 1) {
                 // the sum with what its roundings lost (a row has up to a million terms)
                 float m = -INFINITY, l = 0.f, lost = 0.f;
+                const int sees = min(n, n - T + (row0 + me) / p.G + 1);  // keys that this row sees
                 for (int e = wg / step; t < nq && e < tiles; e += kGroups / step) {
                     const int j = w.j + e;
                     if (j - batch >= 16) {
@@ -459,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t pair = good >> (2 * (j - batch)) & 3u;
                     // keys of the tile this row sees: 0 .. hi - 1
-                    const int hi = min(n, n - T + (row0 + me) / p.G + 1) - j * kBlock;
+                    const int hi = sees - j * kBlock;
                     const bool whole = __all_sync(0xffffffffu, hi >= kBlock) && pair == 3u;
                     take();
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -538,11 +573,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             L += s[e].y * fast_exp2(s[e].x - base);
                         M = top;
                     }
-                    const float base = M == -INFINITY ? 0.f : M;
-                    const bool on = row0 + me < rows && L != 0.f;  // (NaN passes)
-                    named_bar_sync(1 + wg, kBlock);  // the last unit's readers are done
-                    sh.neg_lse[wg][me] = on ? -(base + log2f(L)) : -INFINITY;
-                    named_bar_sync(1 + wg, kBlock);
+                    // -lse in units of a raw score, as a sum of three bf16; where there is no row, or
+                    // no key, what leaves no weight.  (NaN passes.)
+                    const bool on = row0 + me < rows && L != 0.f;
+                    const float v = on ? -((M == -INFINITY ? 0.f : M) + log2f(L)) / p.scale_log2 : -1e30f;
+                    const uint32_t hi = pack_bf16(v, 0.f) & 0xffffu;
+                    const float rest = on ? v - bf16_lo(hi) : 0.f;
+                    const uint32_t mid = pack_bf16(rest, 0.f) & 0xffffu;
+                    const uint32_t lo = pack_bf16(on ? rest - bf16_lo(mid) : 0.f, 0.f) & 0xffffu;
+                    if (units > 0)
+                        wait(&sh.q_empty, (uint32_t)(units - 1) & 1);  // the last unit's products are done
+                    if (wg < step) {
+                        uint4 *const row = reinterpret_cast<uint4 *>(sh.aug[t] + aug_offset(me));
+                        row[0] = make_uint4(hi | mid << 16, lo, 0, 0);
+                        row[8] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    arrive(&sh.aug_full);
                 }
                 const int64_t at = ((int64_t)w.q.seq * p.Hkv + w.h) * p.w_stride;
                 const int top = min(kBlock, rows - row0);
@@ -568,17 +615,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (c0 == kBlock - kCols)
                                 give();
 #pragma unroll
-                            for (int c = 0; c < kCols; c += 4) {
-                                const float4 y = *reinterpret_cast<const float4 *>(&sh.neg_lse[wg][c0 + c]);
-                                float a, b, d, f;
-                                f2_split(f2_fma(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2,
-                                                f2_make(y.x, y.y)), a, b);
-                                f2_split(f2_fma(f2_make(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2,
-                                                f2_make(y.z, y.w)), d, f);
-                                acc[0] += fast_exp2(a);
-                                acc[1] += fast_exp2(b);
-                                acc[2] += fast_exp2(d);
-                                acc[3] += fast_exp2(f);
+                            for (int c = 0; c < kCols; c += 2) {
+                                float a, b;
+                                f2_split(f2_mul(f2_make(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2), a, b);
+                                acc[c & 2] += fast_exp2(a);
+                                acc[(c & 2) + 1] += fast_exp2(b);
                             }
                         }
                     } else {
@@ -591,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
                                 if (c0 + c >= first && c0 + c < top)
-                                    acc[c] += fast_exp2(fmaf(__uint_as_float(x[c]), p.scale_log2, sh.neg_lse[wg][c0 + c]));
+                                    acc[c] += fast_exp2(__uint_as_float(x[c]) * p.scale_log2);
                         }
                         give();
                     }
@@ -622,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 handed &= 0x03030303u;
             }
             i += tiles;
+            ++units;
             next_unit(w);
         }
     }
