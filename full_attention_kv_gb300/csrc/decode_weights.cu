@@ -768,7 +768,6 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
     __shared__ JoinSmem sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
-    grid_launch_dependents();
     const int rows = p.G * p.T, out_items = (rows + 7) / 8;
     auto items_of = [&](int c) { return c < 0 ? 0 : out_items + (c + p.T + kChunk - 1) / kChunk; };
     const int per = (p.B + kJoinThreads - 1) / kJoinThreads;

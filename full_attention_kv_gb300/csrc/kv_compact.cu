@@ -47,7 +47,6 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
     const int64_t rh = blockIdx.x / pages;
     const int h = (int)(rh % p.Hkv), r = (int)(rh / p.Hkv);
     grid_dependency_wait();
-    grid_launch_dependents();
 
     const int n = __ldg(p.new_len + r), seq = __ldg(p.seq_idx + r);
     const bool first = tid == 0 && h == 0 && page == 0;

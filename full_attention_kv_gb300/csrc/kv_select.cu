@@ -115,7 +115,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row_id = blockIdx.x / C, r = row_id / p.heads, h = row_id % p.heads;
     grid_dependency_wait();
-    grid_launch_dependents();
 
     const int seq = __ldg(p.seq_idx + r);
     int n = __ldg(p.kv_len + r);

@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     PromptSmem &sh = *reinterpret_cast<PromptSmem *>(align_smem_1024(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
-    grid_launch_dependents();
+    if (PASS == 1)
+        grid_launch_dependents();  // pass 2 (after which a kernel finds everything written)
 
     // ---- this CTA's contiguous range of key tiles ------------------------------------------
     const int per = (p.R + kThreads - 1) / kThreads;

@@ -24,7 +24,7 @@ def test_select_arguments_refused():
     L = hsa.lib()
     INV, OK = hsa.HSA_INVALID_ARG, hsa.HSA_OK
     base = dict(w=M, stride=64, batch=4, heads=2, n=256, seq=256, R=2, budget=16, sinks=4, recent=8, reach=1,
-                keep=2 * M, new=256)
+                keep=2 * M, new=512)
 
     def call(**kw):
         a = dict(base, **kw)
@@ -33,7 +33,7 @@ def test_select_arguments_refused():
     for kw in (dict(w=None), dict(w=M + 4), dict(stride=62), dict(stride=-4), dict(batch=-1), dict(heads=0),
                dict(n=None), dict(seq=None), dict(R=-1), dict(budget=-1), dict(sinks=-1), dict(recent=-1),
                dict(reach=-1), dict(sinks=9), dict(keep=None), dict(new=None), dict(R=1 << 27),
-               dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1)):
+               dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), dict(new=256), dict(new=260), dict(new=252)):
         assert call(**kw) == INV, kw
     assert call(reach=8) == hsa.HSA_UNSUPPORTED_SHAPE and call(stride=(1 << 22) + 4) == hsa.HSA_UNSUPPORTED_SHAPE
     assert call(R=0, w=None, n=None, seq=None, keep=None, new=None) == OK

@@ -44,6 +44,7 @@ VALUES = {
     "tiny": lambda g, *s: torch.randint(0, 9, s, generator=g, device="cuda") * 2.0 ** -149,
     "holes": lambda g, *s: torch.where(torch.rand(s, generator=g, device="cuda") < 0.3,
                                        torch.tensor(float("nan"), device="cuda"), _spread(g, *s)),
+    "nothing": lambda g, *s: torch.full(s, float("nan"), device="cuda"),
     "infinities": lambda g, *s: torch.where(torch.rand(s, generator=g, device="cuda") < 0.3,
                                             torch.tensor(float("inf"), device="cuda"), -torch.rand(s, generator=g, device="cuda") / 0),
 }
@@ -134,6 +135,37 @@ def test_select_many_rows(R):
     want = torch.where((n > 1000)[:, None, None], want,
                        torch.where(torch.arange(1000, device="cuda") < n[:, None], torch.arange(1000, device="cuda"), -1).int()[:, None])
     assert torch.equal(keep, want) and torch.equal(new, n.clamp(max=1000))
+
+
+def test_select_on_another_stream_and_captured_over_clusters():
+    hsa = _hsa()
+    g = _gen(7)
+    n, R = 30000, 5
+    w, length, seq = _spread(g, R, 2, n), _i32([n, 20000, 3, 29999, 4097]), _i32([4, 2, 0, 1, 3])
+    first = hsa.hsa_kv_select(w, length, seq, 2000, sinks=4, recent=100, reach=2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = hsa.hsa_kv_select(w, length, seq, 2000, sinks=4, recent=100, reach=2, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    keep, new = torch.empty_like(first[0]), torch.empty_like(first[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hsa.hsa_kv_select(w, length, seq, 2000, sinks=4, recent=100, reach=2, keep=keep, new_len=new)
+    for _ in range(3):
+        w.copy_(_spread(g, R, 2, n))
+        want = hsa.hsa_kv_select(w, length, seq, 2000, sinks=4, recent=100, reach=2)
+        keep.zero_()
+        graph.replay()
+        assert torch.equal(keep, want[0]) and torch.equal(new, want[1])
+
+
+def test_select_in_place_is_refused():
+    hsa = _hsa()
+    length = _i32([5, 9])
+    with pytest.raises(hsa.HsaError) as e:
+        hsa.hsa_kv_select(torch.zeros(2, 1, 16, device="cuda"), length, _i32([0, 1]), 4, new_len=length)
+    assert e.value.status == hsa.HSA_INVALID_ARG
 
 
 def test_select_flags():
