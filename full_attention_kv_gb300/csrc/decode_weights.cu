@@ -124,6 +124,7 @@ template <int NT>
 struct State {
     float m[NT][2], l[NT][2], lr[NT][2];  // lr: of the weights as the product takes them
     float o[kD / 16][NT][4];
+    int vexp;  // FP8: o is in units of 2^(vexp - 127); 0 before the first page with values
 };
 
 template <int NT>
@@ -143,6 +144,35 @@ __device__ __forceinline__ void clear(State<NT> &st)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 st.o[dt][n][e] = 0.f;
+    st.vexp = 0;
+}
+
+// 2^(e - 127), 0 for e <= 0.
+__device__ __forceinline__ float power(int e) { return __int_as_float(max(e, 0) << 23); }
+
+// V's scales go into P, which an FP8 page's product takes in fp16.  So they are taken relative to
+// a power of two that follows the largest scale of a page (the same in all lanes): at most 2^7 of
+// fp16's 2^16 above it, P's slack takes 2^8 more, and a row of small values keeps P's precision.
+template <int NT>
+__device__ __forceinline__ void follow_scale(State<NT> &st, const float *v_scale, int valid, int lane)
+{
+    const uint32_t a = lane < valid ? __float_as_uint(v_scale[lane]) : 0u;
+    const uint32_t b = lane + 32 < valid ? __float_as_uint(v_scale[lane + 32]) : 0u;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(a, b));
+    const int e = min(max((int)(top >> 23), 1), 250);
+    if (top == 0 || (st.vexp != 0 && e <= st.vexp + 6))
+        return;
+    if (st.vexp != 0) {
+        const float f = power(127 + st.vexp - e);
+#pragma unroll
+        for (int dt = 0; dt < kD / 16; ++dt)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    st.o[dt][n][k] *= f;
+    }
+    st.vexp = e;
 }
 
 // The running maxima raised by a tile's (x, in log2 units, the same in all lanes of a column);
@@ -300,8 +330,8 @@ __device__ __forceinline__ void tile_bf16(State<NT> &st, const uint32_t (&qb)[NT
 }
 
 // A page of an FP8 layer (tile_fp8_sw in decode.cu says how its words feed the MMAs): fp16
-// products, a key's scale on its scores, V's folded into P (E5M2: times 256, divided out at the
-// unit's end).  PART: keys >= valid are masked, their codes of V too.
+// products, a key's scale on its scores, V's folded into P (follow_scale).  PART: keys >= valid are
+// masked, their codes of V too.
 template <int NT, bool E5M2, bool PART>
 __device__ __forceinline__ void tile_fp8(State<NT> &st, const uint32_t (&qb)[NT][kD / 16][2],
                                          const uint8_t *sK, const uint8_t *sV, const float *k_scale,
@@ -343,7 +373,8 @@ __device__ __forceinline__ void tile_fp8(State<NT> &st, const uint32_t (&qb)[NT]
     float x[NT][2];
     column_max<NT, MTS>(s, x);
     raise(st, x);
-    constexpr float f = E5M2 ? 256.f : 1.f;
+    follow_scale(st, v_scale, PART ? valid : kTileKeys, lane);
+    const float f = power(254 - st.vexp);
 #pragma unroll
     for (int mt = 0; mt < MTS; ++mt) {
         const int ka = mt * 16 + g, kb = ka + 8;
@@ -630,14 +661,15 @@ __global__ void __launch_bounds__(Shape<FP8, NT, RH>::kThreads, 1)
             continue;
         }
         // ---- the end of the unit, or of this CTA's part of it ------------------------------
-        if constexpr (FP8 == 2) {
+        if constexpr (FP8 != 0) {
+            const float f = st.vexp != 0 ? power(st.vexp) : 1.f;
 #pragma unroll
             for (int dt = 0; dt < kD / 16; ++dt)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        st.o[dt][n][e] *= 1.f / 256.f;
+                        st.o[dt][n][e] *= f;
         }
         if constexpr (FP8 != 0) {  // the product takes P in fp16, finer than its sum needs to know
 #pragma unroll

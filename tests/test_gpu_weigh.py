@@ -39,7 +39,8 @@ def _perm(n):
 class Step:
     """Sequences of `cached` tokens in pages of random order, T new ones each."""
 
-    def __init__(self, hsa, cached, T, hq, hkv, fmt=None, seed=1, prev=True, decay=0.75, garbage=float("nan"), extra=5):
+    def __init__(self, hsa, cached, T, hq, hkv, fmt=None, seed=1, prev=True, decay=0.75, garbage=float("nan"), extra=5,
+                 vmag=None):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.hsa, self.cached, self.T, self.hq, self.hkv, self.fmt, self.decay = hsa, cached, T, hq, hkv, fmt, decay
@@ -51,6 +52,10 @@ class Step:
         self.table = _i32(table)
         k = torch.randn(self.nb, hkv, PAGE, D, generator=g, device="cuda").bfloat16()
         v = torch.randn(self.nb, hkv, PAGE, D, generator=g, device="cuda").bfloat16()
+        if vmag is not None:  # of position j, and of the new tokens
+            for i, c in enumerate(cached):
+                for j, block in enumerate(table[i][:pages[i]]):
+                    v[block] *= vmag(torch.arange(j * PAGE, j * PAGE + PAGE, device="cuda"))[:, None]
         if fmt is None:
             self.bufs, self.values = (k, v), (k, v)
         else:
@@ -64,6 +69,9 @@ class Step:
         self.q = (torch.randn(B, T, hq, D, generator=g, device="cuda") * 2).bfloat16()
         self.k = torch.randn(B, T, hkv, D, generator=g, device="cuda").bfloat16()
         self.v = torch.randn(B, T, hkv, D, generator=g, device="cuda").bfloat16()
+        if vmag is not None:
+            for i, c in enumerate(cached):
+                self.v[i] *= vmag(torch.arange(c, c + T, device="cuda"))[:, None, None]
         self.stride = (max(max(cached), 0) + T + extra + 3) // 4 * 4
         self.prev = torch.rand(B, hkv, self.stride, generator=g, device="cuda") if prev else None
         if prev:
@@ -82,7 +90,7 @@ class Step:
         bufs, values = [], []
         for x, is_v in ((k, False), (v, True)):
             scale = x.float().abs().amax(-1) / top
-            code = (x.float() / scale[..., None]).clamp(-top, top).to(t)
+            code = (x.float() / scale[..., None]).nan_to_num(0.0).clamp(-top, top).to(t)
             buf = torch.empty(self.nb * self.hkv * PAGE * (D + 4), dtype=torch.uint8, device="cuda")
             if is_v:
                 buf[:cb].view(self.nb, self.hkv, D, PAGE)[..., _perm(PAGE)] = code.view(torch.uint8).transpose(-1, -2)
@@ -170,6 +178,26 @@ def test_weights_and_output(case, fmt):
     cached, T, hq, hkv = CASES[case]
     s = Step(_hsa(), cached, T, hq, hkv, fmt)
     out = s.run()
+    assert int(s.err) == 0
+    s.check(out)
+
+
+VALUES = {
+    "tiny": lambda at: torch.full_like(at, 2.0 ** -30, dtype=torch.bfloat16),
+    "large": lambda at: torch.full_like(at, 2.0 ** 30, dtype=torch.bfloat16),
+    "unlike": lambda at: torch.exp2((at * 7919 % 25 - 12).float()).bfloat16(),
+    "rising": lambda at: torch.exp2((at // PAGE).float() * 3 - 60).bfloat16(),
+    "falling": lambda at: torch.exp2(60 - (at // PAGE).float() * 3).bfloat16(),
+    "zero at first": lambda at: (at >= 100).bfloat16(),
+}
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e5m2"])
+@pytest.mark.parametrize("values", sorted(VALUES))
+def test_values_of_any_size(values, fmt):
+    # an FP8 layer's P, times V's scale, is fp16: its precision follows the values' size
+    s = Step(_hsa(), [2500, 64, 127], 2, 16, 2, fmt, garbage=None, vmag=VALUES[values])
+    out = s.run(max_ctas=5)
     assert int(s.err) == 0
     s.check(out)
 
