@@ -37,6 +37,8 @@ constexpr int kMaxWarps = 32;
 constexpr int kFirstBins = 512;              // of sign and exponent
 constexpr int kMaxReach = 7;
 constexpr int kMaxCtas = 6;                  // of a row
+constexpr int kSampleFrom = 16384;           // positions
+constexpr int kSample = 2048;
 
 struct alignas(16) SelectSmem {              // the held halves follow
     uint32_t lanes[kFirstBins * 16];         // lane l: half l / 16 of word l % 16 of a bin's 16
@@ -47,6 +49,8 @@ struct alignas(16) SelectSmem {              // the held halves follow
     uint32_t cta_gt[kMaxCtas], cta_eq[kMaxCtas];
     uint32_t digit, need;
     int32_t done;
+    uint32_t bound[2], rest[2];              // of the sample: digits, and the ranks inside them
+    uint32_t listed, above;
 };
 static_assert(sizeof(SelectSmem) % 16 == 0, "the halves behind it");
 
@@ -156,6 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     const int held_chunks = p.held / kChunk;
     // word e of this lane's high halves of chunk c: keys 2 e, 2 e + 1
     auto slot = [&](int c) { return held + (c - k0) * (kChunk / 2) + lane; };
+    // of the chunks behind those, a word a lane from the third digit on (in the first's counters):
+    // its marks, as below, by high half
+    constexpr int kTail = kFirstBins * 16 / 32;
+    auto in_tail = [&](int c) { return c - k0 >= held_chunks && c - k0 < held_chunks + kTail; };
+    auto tail = [&](int c) { return sh.lanes + (c - k0 - held_chunks) * 32 + lane; };
     auto position = [&](int c) { return c * kChunk + lane * kKeys; };
     auto fresh = [&](int c, uint32_t(&k)[kKeys]) { load_keys<kKeys>(k, row, position(c), n, lo, hi, p.reach); };
     // bit e: the high half of key e, as far as `bits` says, is `value`
@@ -171,16 +180,194 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
         return m;
     };
 
+    // exclusive sum over the threads before (the first 512 of them at most hold anything); a barrier
+    auto sum_before = [&](uint32_t mine) {
+        uint32_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += u;
+        }
+        if (lane == 31)
+            sh.scan[warp] = incl;
+        __syncthreads();
+        const uint32_t w = lane < warp ? sh.scan[lane] : 0u;
+        return incl - mine + __reduce_add_sync(0xffffffffu, w);
+    };
+    bool waited = C == 1;
+    auto may_push = [&] {
+        if (!waited)
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        waited = true;
+    };
+
+    // ---- long rows: between two keys of a sample ----------------------------------------------
+    uint32_t prefix = 0, need = (uint32_t)left, low = 0;
+    bool listed = false;
+    int shift = 32, list_size = 0;
+    uint32_t *const mark = held;  // a word a lane and chunk
+    uint2 *const list = reinterpret_cast<uint2 *>(held + cta_chunks * 32);
+    const int room = p.held / 4 - cta_chunks * 16;
+    if (kKeys == 16 && n >= kSampleFrom && room >= 256) {
+        constexpr int kRounds = kSample / 2 / kThreads;
+        uint32_t k2[kRounds][2];
+        const int spans = (n + kKeys - 1) / kKeys;
+        int there = 0;
+#pragma unroll
+        for (int e = 0; e < kRounds; ++e) {
+            uint32_t k[kKeys];
+            const int at = (int)((int64_t)(e * kThreads + tid) * spans / (kRounds * kThreads));
+            load_keys<kKeys>(k, row, at * kKeys, n, lo, hi, p.reach);
+            k2[e][0] = k[0];
+            k2[e][1] = k[kKeys / 2];
+            there += (k2[e][0] != 0) + (k2[e][1] != 0);
+        }
+        if (tid < kFirstBins)
+            sh.own[tid] = 0;
+        if (tid == 0)
+            sh.listed = sh.above = 0;
+        there = (int)__reduce_add_sync(0xffffffffu, (uint32_t)there);
+        if (lane == 0)
+            sh.warp_gt[warp] = (uint32_t)there;
+        __syncthreads();
+        there = (int)__reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_gt[lane] : 0u);
+#pragma unroll
+        for (int e = 0; e < 2 * kRounds; ++e)
+            if (k2[e >> 1][e & 1] != 0)
+                atomicAdd(&sh.own[k2[e >> 1][e & 1] >> 23], 1u);
+        // five standard deviations of the rank on each side
+        const float share = (float)left / (float)(hi - lo), mean = share * (float)there;
+        const float dev = 5.f * sqrtf(mean * (1.f - share)) + 3.f;
+        const int ra = (int)(mean - dev), rb = (int)(mean + dev) + 1;
+        if (tid < 2) {  // where there is no such rank: no bound
+            sh.bound[tid] = tid == 0 ? 0xffffu : 0u;
+            sh.rest[tid] = 0;
+        }
+        __syncthreads();
+        uint32_t mine = tid < kFirstBins ? sh.own[kFirstBins - 1 - tid] : 0u;
+        uint32_t before = sum_before(mine);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int rank_e = e == 0 ? ra : rb;
+            if (rank_e >= 1 && rank_e <= there && (int)before < rank_e && (int)(before + mine) >= rank_e) {
+                sh.bound[e] = (uint32_t)(kFirstBins - 1 - tid);
+                sh.rest[e] = (uint32_t)rank_e - before;
+            }
+        }
+        __syncthreads();
+        const uint32_t da = sh.bound[0], db = sh.bound[1], na = sh.rest[0], nb = sh.rest[1];
+        if (tid < 256)
+            sh.own[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 2 * kRounds; ++e) {
+            const uint32_t k = k2[e >> 1][e & 1];
+            if (na != 0 && k >> 23 == da)
+                atomicAdd(&sh.own[k >> 16 & 127], 1u);
+            if (nb != 0 && k >> 23 == db)
+                atomicAdd(&sh.own[128 + (k >> 16 & 127)], 1u);
+        }
+        __syncthreads();
+        mine = tid < 256 ? sh.own[(tid & 128) + 127 - (tid & 127)] : 0u;
+        before = sum_before(mine);
+        if (tid == 128)
+            sh.digit = before;
+        __syncthreads();
+        if (tid < 256) {
+            const int e = tid >> 7;
+            const uint32_t b = before - (e ? sh.digit : 0u), want = e ? nb : na;
+            if (want != 0 && b < want && b + mine >= want)
+                sh.bound[e] = (e ? db : da) << 7 | (uint32_t)(127 - (tid & 127));
+        }
+        __syncthreads();
+        const uint32_t high = sh.bound[0] << 16 | 0xffffu;
+        low = max(sh.bound[1] << 16, 1u);
+
+        // the positions above, and a list of those between
+        uint32_t gt = 0;
+        for (int c = k_begin; c < k_end; ++c) {
+            uint32_t k[kKeys], above = 0, level = 0;
+            fresh(c, k);
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) {
+                above |= k[e] > high ? 1u << e : 0u;
+                level |= k[e] >= low ? 1u << e : 0u;
+            }
+            level &= ~above;
+            mark[(c - k0) * 32 + lane] = above;
+            gt += __popc(above);
+            if (!__any_sync(0xffffffffu, level != 0))
+                continue;
+            const uint32_t count = __popc(level);
+            uint32_t incl = count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += u;
+            }
+            uint32_t at = 0;
+            if (lane == 31)
+                at = atomicAdd(&sh.listed, incl);
+            at = __shfl_sync(0xffffffffu, at, 31) + incl - count;
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e)
+                if (level >> e & 1) {
+                    if (at < (uint32_t)room)
+                        list[at] = make_uint2(k[e], (uint32_t)((c - k0) * kChunk + lane * kKeys + e));
+                    ++at;
+                }
+        }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        if (lane == 0 && gt != 0)
+            atomicAdd(&sh.above, gt);
+        __syncthreads();
+        list_size = min((int)sh.listed, room);
+        uint32_t total_gt = sh.above, total = sh.listed;
+        bool fits = total <= (uint32_t)room;
+        if (C > 1) {
+            may_push();
+            if (tid < C) {
+                *cluster.map_shared_rank(&sh.cta_gt[rank], tid) = total_gt;
+                *cluster.map_shared_rank(&sh.cta_eq[rank], tid) = fits ? total : 1u << 30;
+            }
+            cluster.sync();
+            total_gt = total = 0;
+            for (int c = 0; c < C; ++c) {
+                total_gt += sh.cta_gt[c];
+                total += min(sh.cta_eq[c], 1u << 28);
+                fits &= sh.cta_eq[c] != 1u << 30;
+            }
+        }
+        listed = fits && total_gt < (uint32_t)left && total_gt + total >= (uint32_t)left;
+        if (!listed)
+            low = 0;  // every key, as if there had been no sample
+        if (listed) {
+            need = (uint32_t)left - total_gt;
+            shift = max((39 - __clz(high - low)) / 8, 1) * 8;  // digits of eight bits of key - low
+        }
+        __syncthreads();
+    }
+
     // ---- the left-th largest key, digit by digit --------------------------------------------
-    uint32_t prefix = 0, need = (uint32_t)left;
+    bool tailed = false;
     bool exact = false;  // need ends inside the digit's keys (else all of them stay)
-    int shift = 32;
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
-        const int bits = pass == 0 ? 9 : pass == 1 ? 7 : 8, bins = 1 << bits;
+        const int bits = listed ? 8 : pass == 0 ? 9 : pass == 1 ? 7 : 8, bins = 1 << bits;
         const int above = shift;  // bits above the digit agree with prefix
         shift -= bits;
-        if (pass == 0) {
+        if (listed) {
+            if (tid < bins)
+                sh.own[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < list_size; i += kThreads) {
+                const uint32_t k = list[i].x - low;
+                if (pass == 0 || k >> above == prefix)
+                    atomicAdd(&sh.own[k >> shift & 255], 1u);
+            }
+        } else if (pass == 0) {
             for (int b = tid; b < kFirstBins * 4; b += kThreads)
                 reinterpret_cast<uint4 *>(sh.lanes)[b] = make_uint4(0, 0, 0, 0);
             __syncthreads();
@@ -218,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
             const uint32_t half = above >= 16 ? prefix << (above - 16) : prefix >> (16 - above);
             for (int c = k_begin; c < k_end; ++c) {
                 const bool there = c - k0 < held_chunks;
-                uint32_t m = there ? match(c, known, half) : kAll;
+                uint32_t m = there ? match(c, known, half) : pass == 3 && in_tail(c) ? *tail(c) >> 16 : kAll;
                 if (pass == 1 && there) {
                     for (; m; m &= m - 1) {
                         const int e = __ffs(m) - 1;
@@ -229,6 +416,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
                 } else if (m) {
                     uint32_t k[kKeys];
                     fresh(c, k);
+                    if (pass == 2 && in_tail(c)) {
+                        uint32_t x = 0;
+#pragma unroll
+                        for (int e = 0; e < kKeys; ++e) {
+                            x |= k[e] >> 16 > prefix ? 1u << e : 0u;
+                            x |= k[e] >> 16 == prefix ? 0x10000u << e : 0u;
+                        }
+                        *tail(c) = x;
+                    }
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e)
                         if (k[e] != 0 && (k[e] >> above) == prefix)
@@ -236,11 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
                 }
             }
         }
+        tailed = !listed && pass >= 2;
         __syncthreads();
         const uint32_t(*const all)[kFirstBins] = sh.all[pass & 1];
         if (C > 1) {
-            if (pass == 0)
-                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            may_push();
             for (int i = tid; i < C * (bins / 4); i += kThreads) {
                 const int to = i / (bins / 4), at = i % (bins / 4);
                 reinterpret_cast<uint4 *>(cluster.map_shared_rank(sh.all[pass & 1][rank], to))[at] =
@@ -260,20 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
                     mine += c < C ? all[c][bins - 1 - tid] : 0u;
             }
         }
-        uint32_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += u;
-        }
-        if (lane == 31)
-            sh.scan[warp] = incl;
-        __syncthreads();
+        const uint32_t before = sum_before(mine);
         if (tid < bins) {
-            uint32_t before = incl - mine;
-            const uint32_t w = lane < warp ? sh.scan[lane] : 0u;  // at most 16 warps hold counters
-            before += __reduce_add_sync(0xffffffffu, w);
             if (before < need && before + mine >= need) {  // one thread
                 sh.digit = (uint32_t)(bins - 1 - tid);
                 sh.need = need - before;
@@ -285,17 +469,29 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
         need = sh.need;
         if (sh.done)  // (the next digit's counts come behind a barrier)
             break;
-        exact = pass == 3;
+        exact = shift == 0;
+        if (exact)
+            break;
     }
     // keys above `edge` stay, and of those equal to it the first `need` (none: the last digit's
     // keys all stay, and edge is the value below them)
-    const uint32_t edge = exact ? prefix : max(prefix << shift, 1u) - 1u;
+    const uint32_t edge = exact ? low + prefix : max(low + (prefix << shift), 1u) - 1u;
     if (!exact)
         need = 0;
+    if (listed) {
+        for (int i = tid; i < list_size; i += kThreads) {
+            const uint2 x = list[i];
+            if (x.x > edge || (x.x == edge && need != 0))
+                atomicOr(&mark[x.y >> 4], (x.x > edge ? 1u : 0x10000u) << (x.y & 15));
+        }
+        __syncthreads();
+    }
 
     // ---- which stay: bit e of a word key e above the edge, bit 16 + e equal to it -----------
     const uint32_t edge16 = edge >> 16;
     auto marks = [&](int c) {
+        if (listed)
+            return mark[(c - k0) * 32 + lane];
         uint32_t above = 0, level = kAll;
         if (c - k0 < held_chunks) {
             const uint32_t *const x = slot(c);
@@ -306,6 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
                 above |= y > edge16 ? 1u << e : 0u;
                 level |= y == edge16 ? 1u << e : 0u;
             }
+        } else if (tailed && in_tail(c)) {
+            const uint32_t x = *tail(c);
+            above = x & 0xffffu;
+            level = x >> 16;
         }
         if (level) {  // a high half that does not tell
             uint32_t k[kKeys];
@@ -322,8 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     uint32_t gt = 0, eq = 0;
     for (int c = k_begin; c < k_end; ++c) {
         const uint32_t x = marks(c);
-        if (c - k0 < held_chunks)
+        if (listed)
+            ;
+        else if (c - k0 < held_chunks)
             *slot(c) = x;  // the halves are not needed any more
+        else if (in_tail(c))
+            *tail(c) = x;
         gt += __popc(x & 0xffffu);
         eq += __popc(x >> 16);
     }
@@ -359,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     // ---- the positions, each at the number that stay before it ------------------------------
     int32_t *const to = keep + p.sinks;
     for (int c = k_begin; c < k_end; ++c) {
-        const uint32_t x = c - k0 < held_chunks ? *slot(c) : marks(c);
+        const uint32_t x = listed ? marks(c) : c - k0 < held_chunks ? *slot(c) : in_tail(c) ? *tail(c) : marks(c);
         const uint32_t mine = __popc(x & 0xffffu) | __popc(x >> 16) << 16;
         uint32_t incl = mine;
 #pragma unroll
