@@ -4,25 +4,40 @@
 // the rest the left = budget - sinks - recent of the largest score, ties to the lowest position;
 // ascending.  A score is the largest weight among a position and its `reach` neighbours.
 //
-// A score becomes a 32-bit integer of the same order (sign flipped, negatives inverted), and the
-// left-th largest is found digit by digit (9, 7, 8 and 8 bits): a histogram of the digit among the
-// keys that agree so far, summed from the top until it holds the rank.  No sort, and no order of
-// atomics that shows: the histogram's sums and the prefix counts are exact.  Then every key above
-// that value stays, and the first `need` keys equal to it, each key's place being the number that
-// stay before it (warp scans over contiguous ranges).
+// A score becomes a 32-bit integer of the same order (sign flipped, negatives inverted), its key.
+// The left-th largest key is found without a sort, and with no order of atomics that shows: counts
+// and prefix sums are exact.
 //
 // A cluster of 1 to 6 CTAs takes a row, each a contiguous part; a lane takes 16 positions at a time
 // (4 of short rows), so that neighbours' weights are read and prefix counts scanned once for all of
-// them.  A thread keeps the high halves of its own keys in shared memory, so the passes over them
-// need no barrier, and half as much of it as whole keys would: few keys share their high half with
-// the value sought, and only those are made again from the weights.  Each CTA writes its counters
-// into the shared memory of all of the cluster (reading the others' instead is two round trips and a
-// second barrier a digit, 3 to 6 us).
+// them.
 //
-// The first digit, sign and exponent, is every key's, and weights share a few exponents: lanes of
-// a warp that add to one counter do so one after another.  So each lane has counters of its own, 16
-// bits wide, in a bank that it shares with one other lane.  The later digits are few keys' and
+// Long rows: two keys of a sample of 2048 positions, five standard deviations of the rank to each
+// side, hold the key sought between them.  One pass marks the positions above both and lists those
+// between (a few percent); their numbers say whether the rank lies there.  Then the key is found
+// digit by digit (8 bits of its distance from the lower bound): a histogram of the digit among the
+// listed keys that agree so far, summed from the top until it holds the rank.
+//
+// Other rows, and those whose sample missed (or whose list did not fit: many ties): the same over
+// all positions, digits of 9, 7, 8 and 8 bits.  A thread keeps the high halves of its own keys in
+// shared memory, so the passes over them need no barrier, and half as much of it as whole keys
+// would: few keys share their high half with the value sought, and only those are made again from
+// the weights.  Of those for which there is no room, two bits a key are kept from the third digit
+// on.  The first digit, sign and exponent, is every key's, and weights share a few exponents: lanes
+// of a warp that add to one counter do so one after another.  So each lane has counters of its own,
+// 16 bits wide, in a bank that it shares with one other lane.  The later digits are few keys' and
 // differ.
+//
+// Each CTA writes its counters into the shared memory of all of the cluster (reading the others'
+// instead is two round trips and a second barrier a digit, 3 to 6 us).
+//
+// Then every key above that value stays, and the first `need` keys equal to it, each key's place
+// being the number that stay before it (warp scans over contiguous ranges).
+//
+// What bounds it: 16 rows of 262144 to 1000000 positions take 48 us (digits over all of them: 75)
+// for 6.4 of HBM: launch and sample 14, the pass over the longest row's sixth 17 (instructions: 64
+// registers a thread, nothing loaded ahead), digits 9, places 7.  128 rows of 8192 to 65536 with a
+// reach of 3: 40 (2.8).  8 rows of up to 2048: 7, latency.
 #include <cooperative_groups.h>
 
 #include "hsa_device.cuh"
@@ -37,7 +52,7 @@ constexpr int kMaxWarps = 32;
 constexpr int kFirstBins = 512;              // of sign and exponent
 constexpr int kMaxReach = 7;
 constexpr int kMaxCtas = 6;                  // of a row
-constexpr int kSampleFrom = 16384;           // positions
+constexpr int kSampleFrom = 16384;           // positions of a row (4096 to 30000: no difference)
 constexpr int kSample = 2048;
 
 struct alignas(16) SelectSmem {              // the held halves follow
@@ -63,11 +78,10 @@ __device__ __forceinline__ uint32_t order_key(float x)
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// Keys of the kKeys positions from p (a multiple of them) of a row of n weights (16-byte aligned,
-// readable up to a multiple of 4); those outside lo .. hi - 1 do not compete.
+// Scores of the kKeys positions from p (a multiple of them) of a row of n weights (16-byte aligned,
+// readable up to a multiple of 4).
 template <int kKeys>
-__device__ __forceinline__ void load_keys(uint32_t (&k)[kKeys], const float *row, int p, int n, int lo, int hi,
-                                          int reach)
+__device__ __forceinline__ void load_scores(float (&v)[kKeys], const float *row, int p, int n, int reach)
 {
     float x[kKeys + 16];  // positions p - 8 .. p + 23
 #pragma unroll
@@ -84,7 +98,6 @@ __device__ __forceinline__ void load_keys(uint32_t (&k)[kKeys], const float *row
         for (int e = 8; e < kKeys + 16; ++e)
             x[e] = p - 8 + e < n ? x[e] : -INFINITY;
     }
-    float v[kKeys];
 #pragma unroll
     for (int e = 0; e < kKeys; ++e)
         v[e] = x[8 + e];
@@ -94,6 +107,15 @@ __device__ __forceinline__ void load_keys(uint32_t (&k)[kKeys], const float *row
 #pragma unroll
             for (int e = 0; e < kKeys; ++e)
                 v[e] = fmax3(v[e], x[8 + e - d], x[8 + e + d]);  // a NaN gives way to a number
+}
+
+// Their keys; those outside lo .. hi - 1 do not compete.
+template <int kKeys>
+__device__ __forceinline__ void load_keys(uint32_t (&k)[kKeys], const float *row, int p, int n, int lo, int hi,
+                                          int reach)
+{
+    float v[kKeys];
+    load_scores<kKeys>(v, row, p, n, reach);
 #pragma unroll
     for (int e = 0; e < kKeys; ++e)
         k[e] = order_key(v[e]);
@@ -103,6 +125,21 @@ __device__ __forceinline__ void load_keys(uint32_t (&k)[kKeys], const float *row
             if (p + e < lo || p + e >= hi)
                 k[e] = 0;
     }
+}
+
+// The key of a position that competes.
+__device__ __forceinline__ uint32_t one_key(const float *row, int p, int n, int reach)
+{
+    float v = __ldg(row + p);
+    for (int d = 1; d <= reach; ++d)
+        v = fmax3(v, p >= d ? __ldg(row + p - d) : -INFINITY, p + d < n ? __ldg(row + p + d) : -INFINITY);
+    return order_key(v);
+}
+
+// The value of a key.
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
 }
 
 template <int kThreads, int kKeys>
@@ -157,6 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     const int cta_chunks = (chunks + C - 1) / C, warp_chunks = (cta_chunks + kWarps - 1) / kWarps;
     const int k0 = min(chunks, rank * cta_chunks), k1 = min(chunks, k0 + cta_chunks);
     const int k_begin = min(k1, k0 + warp * warp_chunks), k_end = min(k1, k_begin + warp_chunks);
+    if (kKeys == 16 && k_begin < k_end && elect_one()) {  // into L2 (43 -> 41 us for 32 x 4 rows of 8192 to 65536)
+        const int at = k_begin * kChunk, end = min(k_end * kChunk, (n + 3) & ~3);
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row + at), "r"((end - at) * 4));
+    }
     const int held_chunks = p.held / kChunk;
     // word e of this lane's high halves of chunk c: keys 2 e, 2 e + 1
     auto slot = [&](int c) { return held + (c - k0) * (kChunk / 2) + lane; };
@@ -286,13 +327,24 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
 
         // the positions above, and a list of those between
         uint32_t gt = 0;
+        // (compared as values: bounds that are no numbers, where there is none, hold nothing, and the
+        // numbers below then tell)
+        const float above_v = key_value(high), level_v = key_value(low);
         for (int c = k_begin; c < k_end; ++c) {
-            uint32_t k[kKeys], above = 0, level = 0;
-            fresh(c, k);
+            float v[kKeys];
+            uint32_t above = 0, level = 0;
+            const int at = position(c);
+            load_scores<kKeys>(v, row, at, n, p.reach);
 #pragma unroll
             for (int e = 0; e < kKeys; ++e) {
-                above |= k[e] > high ? 1u << e : 0u;
-                level |= k[e] >= low ? 1u << e : 0u;
+                above |= v[e] > above_v ? 1u << e : 0u;
+                level |= v[e] >= level_v ? 1u << e : 0u;
+            }
+            if (at < lo || at + kKeys > hi) {
+                const uint32_t in = (hi - at >= kKeys ? kAll : hi > at ? (1u << (hi - at)) - 1 : 0u) &
+                                    (lo <= at ? kAll : lo - at < kKeys ? kAll << (lo - at) : 0u);
+                above &= in;
+                level &= in;
             }
             level &= ~above;
             mark[(c - k0) * 32 + lane] = above;
@@ -307,23 +359,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
                 if (lane >= o)
                     incl += u;
             }
-            uint32_t at = 0;
+            uint32_t to = 0;
             if (lane == 31)
-                at = atomicAdd(&sh.listed, incl);
-            at = __shfl_sync(0xffffffffu, at, 31) + incl - count;
-#pragma unroll
-            for (int e = 0; e < kKeys; ++e)
-                if (level >> e & 1) {
-                    if (at < (uint32_t)room)
-                        list[at] = make_uint2(k[e], (uint32_t)((c - k0) * kChunk + lane * kKeys + e));
-                    ++at;
-                }
+                to = atomicAdd(&sh.listed, incl);
+            to = __shfl_sync(0xffffffffu, to, 31) + incl - count;
+            for (uint32_t m = level; m; m &= m - 1, ++to)
+                if (to < (uint32_t)room)
+                    list[to].y = (uint32_t)((c - k0) * kChunk + lane * kKeys + __ffs(m) - 1);
         }
         gt = __reduce_add_sync(0xffffffffu, gt);
         if (lane == 0 && gt != 0)
             atomicAdd(&sh.above, gt);
         __syncthreads();
         list_size = min((int)sh.listed, room);
+        for (int i = tid; i < list_size; i += kThreads)
+            list[i].x = one_key(row, k0 * kChunk + (int)list[i].y, n, p.reach);
         uint32_t total_gt = sh.above, total = sh.listed;
         bool fits = total <= (uint32_t)room;
         if (C > 1) {
