@@ -108,6 +108,35 @@ def test_select_long_rows(kind, reach):
     assert new.tolist() == [budget] * 3
 
 
+@pytest.mark.parametrize("n,budget,reach", [(16384, 100, 0), (40000, 3000, 0), (40000, 3000, 1), (300000, 20000, 0), (300000, 299000, 0)])
+@pytest.mark.parametrize("kind", ["spread", "one in eight", "steps", "sorted", "few large"])
+def test_select_where_a_sample_misleads(kind, n, budget, reach):
+    """Rows that a sample of positions, evenly spaced, tells little or wrong things about."""
+    hsa = _hsa()
+    g = _gen(n)
+    w = _spread(g, 2, 1, n)
+    at = torch.arange(n, device="cuda")
+    if kind == "one in eight":
+        w = torch.where(at % 8 == 1, w * 1e6, w)
+    elif kind == "steps":
+        w = torch.where(at < n // 3, 1.0, torch.where(at < n // 2, 1.0 + 2.0 ** -23, 0.5)).expand(2, 1, n).contiguous()
+    elif kind == "sorted":
+        w = w.sort(dim=-1, descending=True).values
+    elif kind == "few large":
+        w = torch.where(at % 3001 == 7, w + 1e9, torch.zeros_like(w))
+    keep, new = hsa.hsa_kv_select(w, _i32([n, n - 1]), _i32([0, 1]), budget, sinks=1, recent=2, reach=reach)
+    for r in range(2):
+        m = n - r
+        x = w[r, 0, :m]
+        score = x.clone()
+        for d in range(1, reach + 1):
+            score[d:] = torch.maximum(score[d:], x[:-d])
+            score[:-d] = torch.maximum(score[:-d], x[d:])
+        mid = score[1:m - 2].sort(descending=True, stable=True).indices[:budget - 3] + 1
+        assert torch.equal(keep[r, 0, 1:-2].long(), mid.sort().values)
+    assert new.tolist() == [budget] * 2
+
+
 @pytest.mark.parametrize("kind", ["equal", "close"])
 def test_select_longest_rows(kind):
     """As many positions a CTA as its counters hold, all with one exponent."""
