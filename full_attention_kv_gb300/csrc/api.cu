@@ -33,21 +33,36 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
+// Encodes; the driver wants a current context, which a host thread that has called nothing of the
+// runtime's that needs one does not have yet.
+template <typename... A>
+bool encode(const A &...args)
+{
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    CUresult r = fn(args...);
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)
+            return false;
+        r = fn(args...);
+    }
+    return r == CUDA_SUCCESS;
+}
+
 // 2-D bf16 tensor map over `rows` rows of `cols` elements with a row pitch of
 // `pitch_elems`; box = box_cols x box_rows; 128-byte swizzle.
 bool encode_2d(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
                uint64_t pitch_elems, uint32_t box_cols, uint32_t box_rows)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn)
-        return false;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {pitch_elems * 2};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 3-D bf16 tensor map over a packed [d2][d1][d0] tensor (d0 = 128 elements);
@@ -55,32 +70,26 @@ bool encode_2d(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
 bool encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                uint32_t box0, uint32_t box2, uint32_t box1 = 1)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn)
-        return false;
     cuuint64_t dims[3] = {d0, d1, d2};
     cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
     cuuint32_t box[3] = {box0, box1, box2};
     cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2-D byte tensor map (E4M3 codes): rows of `cols` bytes, row pitch `cols`.
 bool encode_2d_u8(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
                   uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn)
-        return false;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
