@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
     constexpr int kStep = kJoinThreads / LK, kChunk = kBatch * kStep;  // positions an item
     __shared__ JoinSmem sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dependency_wait();
+    // (the lengths are no work of the attend kernel's, which itself waited for what was queued before
+    // it: this CTA's range is found meanwhile.  few 20.4 -> 18.4 us, verify 120 -> 118)
     const int rows = p.G * p.T, out_items = (rows + 7) / 8;
     auto items_of = [&](int c) { return c < 0 ? 0 : out_items + (c + p.T + kChunk - 1) / kChunk; };
     const int per = (p.B + kJoinThreads - 1) / kJoinThreads;
@@ -821,8 +822,10 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
     __syncthreads();
     const int64_t N = (int64_t)block_scan<kJoinThreads>(sh.scan, &sh.total, local, tid) * p.Hkv;
     const int64_t C = N < (int64_t)gridDim.x ? N : (int64_t)gridDim.x;
-    if ((int64_t)blockIdx.x >= C)
+    if ((int64_t)blockIdx.x >= C) {
+        grid_dependency_wait();  // no end of this grid before the attend kernel's
         return;
+    }
     const int64_t i0 = (int64_t)blockIdx.x * N / C, i1 = ((int64_t)blockIdx.x + 1) * N / C;
     {
         int before = sh.scan[tid], pb = pages_before;
@@ -838,6 +841,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
         }
     }
     __syncthreads();
+    grid_dependency_wait();
     int b = sh.first_b, c = length(b), n = items_of(c);
     int64_t pb = sh.pages_before;
     const int64_t off = i0 - (int64_t)sh.before * p.Hkv;

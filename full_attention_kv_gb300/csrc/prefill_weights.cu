@@ -171,9 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     PromptSmem &sh = *reinterpret_cast<PromptSmem *>(align_smem_1024(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dependency_wait();
-    if (PASS == 1)
-        grid_launch_dependents();  // pass 2 (after which a kernel finds everything written)
+    if (PASS == 1) {  // (pass 2 waits for it where it needs its sums: the requests are none of its work)
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
 
     // ---- this CTA's contiguous range of key tiles ------------------------------------------
     const int per = (p.R + kThreads - 1) / kThreads;
@@ -214,8 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     const int64_t N = (int64_t)sh.total * p.Hkv;
     const int64_t C = N < (int64_t)gridDim.x ? N : (int64_t)gridDim.x;
-    if ((int64_t)blockIdx.x >= C)
+    if ((int64_t)blockIdx.x >= C) {
+        if (PASS == 2)
+            grid_dependency_wait();  // no end of this grid before pass 1's
         return;
+    }
     const int64_t i0 = (int64_t)blockIdx.x * N / C, i1 = ((int64_t)blockIdx.x + 1) * N / C;
     {
         int before = sh.scan[tid], err = 0;
@@ -261,6 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
+    if (PASS == 2)
+        grid_dependency_wait();
 
     Walk w;
     int err_unused = 0;
