@@ -24,8 +24,8 @@
 //
 // What bounds it: HBM, the reads of K and V and the scores' way out and in.  32 sequences of 8192 to
 // 65536 tokens, 8 rows a head: attend 429 us (6.3 TB/s of K and V, 0.92 of a copy's rate, scores
-// beside them), join 45.  32 rows a head (16 sequences x 4 tokens): 87 and 30; there a page's chain in
-// its two warps, and in the join instructions (issue 50%).  FP8: 54, conversions and the chain, and 22.
+// beside them), join 44.  32 rows a head (16 sequences x 4 tokens): 87 and 30; there a page's chain in
+// its two warps, and in the join instructions (issue 50%).  FP8: 54, conversions and the chain, and 20.
 #include "decode_tile.cuh"
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
@@ -41,7 +41,7 @@ constexpr int kFp8StageStride = 17408;           // codes of K and V, 2 x 64 sca
 constexpr int kLens = 1024;                      // sequences whose lengths are kept on chip
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 3;                     // of it, an SM (85 registers a thread)
-constexpr int kBatch = 6;                        // loads of scores a thread has on the way
+constexpr int kBatch = 6;                        // loads of scores a thread has on the way (4, 8: no better)
 constexpr float kUnused = -1.f;                  // sum of the rounded weights of a group without keys
 
 // Warps, groups and stages of an instantiation.  A stage belongs to one group (the stages are a
@@ -967,46 +967,53 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas)
             if (j == 0 && p.append)
                 append_rows(p, b, h, c, tid);
         } else {
-            // ---- the weights of 256 to 2048 positions -----------------------------------------
-            const int first = (j - out_items) * kChunk, end = min(c + p.T, first + kChunk);
+            // ---- the weights of the unit's positions in this CTA's range ----------------------
+            // kBatch positions a thread are on the way all the time: the next ones' loads go out as
+            // each is used, ahead of its store (which might be to the same weights)
+            const int items = (int)min((int64_t)(n - j), i1 - i);
+            const int first = (j - out_items) * kChunk, end = min(c + p.T, first + items * kChunk);
             const float *const score = p.score + unit * p.w_stride * p.srow;
             const int64_t at = unit * p.w_stride;
-            const int p0 = first + tid / LK;
-            // (the loads all ahead of the stores, which might be to the same weights)
-            {
-                float4 x[kBatch];
-                float old[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int pos = p0 + k * kStep;
-                    x[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    old[k] = 0.f;
-                    if (pos < end) {
-                        const float *s = score + (int64_t)pos * p.srow + sub * VEC;
-                        if constexpr (VEC == 4) {
-                            x[k] = __ldcg(reinterpret_cast<const float4 *>(s));
-                        } else {
-                            const float2 y = __ldcg(reinterpret_cast<const float2 *>(s));
-                            x[k].x = y.x;
-                            x[k].y = y.y;
-                        }
-                        if (sub == 0 && p.w_prev && pos < c)
-                            old[k] = p.w_prev[at + pos];
+            float4 x[kBatch];
+            float old[kBatch];
+            auto fetch = [&](int k, int pos) {
+                x[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                old[k] = 0.f;
+                if (pos < end) {
+                    const float *s = score + (int64_t)pos * p.srow + sub * VEC;
+                    if constexpr (VEC == 4) {
+                        x[k] = __ldcg(reinterpret_cast<const float4 *>(s));
+                    } else {
+                        const float2 y = __ldcg(reinterpret_cast<const float2 *>(s));
+                        x[k].x = y.x;
+                        x[k].y = y.y;
                     }
+                    if (sub == 0 && p.w_prev && pos < c)
+                        old[k] = p.w_prev[at + pos];
                 }
+            };
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                fetch(k, first + tid / LK + k * kStep);
+            for (int p0 = first; p0 < end; p0 += kChunk) {
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    const int pos = p0 + k * kStep;
-                    float sum = fast_exp2(x[k].x - lse[0]) + fast_exp2(x[k].y - lse[1]);
+                    const int pos = p0 + tid / LK + k * kStep;
+                    const float4 y = x[k];
+                    const float before = old[k];
+                    fetch(k, pos + kChunk);
+                    float sum = fast_exp2(y.x - lse[0]) + fast_exp2(y.y - lse[1]);
                     if constexpr (VEC == 4)
-                        sum += fast_exp2(x[k].z - lse[2]) + fast_exp2(x[k].w - lse[3]);
+                        sum += fast_exp2(y.z - lse[2]) + fast_exp2(y.w - lse[3]);
 #pragma unroll
                     for (int o = 1; o < LK; o <<= 1)
                         sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (pos < end && sub == 0)
-                        p.w[at + pos] = p.w_prev && pos < c ? fmaf(p.decay, old[k], sum) : sum;
+                        p.w[at + pos] = p.w_prev && pos < c ? fmaf(p.decay, before, sum) : sum;
                 }
             }
+            i += items - 1;
+            j += items - 1;
         }
         if (++j < n)
             continue;
