@@ -24,8 +24,9 @@
 //
 // What bounds it: HBM, the reads of K and V and the scores' way out and in.  32 sequences of 8192 to
 // 65536 tokens, 8 rows a head: attend 429 us (6.3 TB/s of K and V, 0.92 of a copy's rate, scores
-// beside them), join 44.  32 rows a head (16 sequences x 4 tokens): 87 and 30; there a page's chain in
-// its two warps, and in the join instructions (issue 50%).  FP8: 54, conversions and the chain, and 20.
+// beside them), join 44.  32 rows a head (16 sequences x 4 tokens): 87 and 30; about
+// 10 us of it are the kernel's start and end, in the join instructions (issue 50%).  FP8: 54 and 20, the
+// same.  (Six consuming warps and stages, FP8 six to twelve: no change.)
 #include "decode_tile.cuh"
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
