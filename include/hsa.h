@@ -471,7 +471,8 @@ hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_
  *  keep     int32 [R, heads, budget] as hsa_kv_select gives them, heads = Hkv or 1 (one
  *           list for every head; else HSA_UNSUPPORTED_SHAPE)
  *  w, w_dst [batch, Hkv, w_stride] or both NULL: the weights moved along, w_dst[seq][h][i] =
- *           w[seq][h][keep[r][h][i]]; must not overlap
+ *           w[seq][h][keep[r][h][i]]; must not overlap.  With them a sequence may appear in
+ *           one request per call; without, it may be moved to the pages of several
  * Rows of a destination page at new_len[r] and past it are left as they were.  Flagged, and
  * not copied: a position outside the block table (HSA_DEVERR_BAD_PAGE; a negative one, or
  * new_len[r] outside 0 .. budget, HSA_DEVERR_BAD_LEN), a bad block on either side

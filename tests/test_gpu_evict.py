@@ -59,6 +59,7 @@ SIZES = [
     ([5000, 4097, 9001], 9004, 1, 1, 0, 0, 0),
     ([20000, 333, 16384], 20000, 4, 4096, 3, 100, 7),
     ([20001], 40000, 1, 20000, 0, 0, 5),             # all but one
+    ([20000, 18006, 18005, 18004], 20000, 2, 18005, 9000, 9000, 3),  # few of few
 ]
 
 
@@ -317,6 +318,19 @@ def test_compact_any_order(fmt):
     want = m.moved()
     m.run()
     m.check(want)
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_the_same_sequence_twice(fmt):
+    """Two cuts of one sequence (branches of a search), each to pages of its own."""
+    hsa = _hsa()
+    m = Moves(hsa, [700, 700], 150, fmt, 2, 2, seed=6)
+    a = hsa.hsa_kv_select(m.w, _i32([700, 700]), _i32([m.seq[0]] * 2), 150, sinks=3, dev_err=m.err)
+    assert torch.equal(a[0][0], a[0][1]) and a[1].tolist() == [150, 150]
+    m.table[m.seq[1]] = m.table[m.seq[0]]
+    want = m.moved()[0]
+    hsa.hsa_kv_compact(m.pool, 0, _i32(m.keep), _i32(m.kept), _i32([m.seq[0]] * 2), _i32(m.dst), dev_err=m.err)
+    m.check((want, m.w_dst.cpu()))
 
 
 @pytest.mark.parametrize("fmt", [None, "e5m2"])

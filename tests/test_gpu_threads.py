@@ -1,5 +1,5 @@
-"""Calls from a host thread that has called nothing of CUDA's before: the tensor maps are encoded by
-the driver, which wants the thread to have a current context."""
+"""Calls from host threads: one that has called nothing of CUDA's before (the tensor maps are encoded
+by the driver, which wants the thread to have a current context), and two at once."""
 import threading
 
 import pytest
@@ -75,3 +75,63 @@ def test_first_call_of_a_thread(name):
     if name != "prompt weights":
         assert torch.equal(out, want[0])
     assert torch.equal(w, want[1])
+
+
+class Cut:
+    """A sequence cut to a budget, then a step: the four calls of an eviction, on pages of its own."""
+
+    def __init__(self, hsa, n, hq, hkv, seed):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        bf = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+        self.hsa, self.n, self.budget, d = hsa, n, n // 3, 128
+        pages, kept = (n + 63) // 64, (self.budget + 64) // 64
+        self.dst = _i32([list(range(pages, pages + kept))])
+        self.old = _i32([list(range(pages))])
+        self.new = _i32([list(range(pages, pages + kept)) + [0] * (pages - kept)])
+        self.pool = hsa.DualPool.allocate([True], pages + kept, 1, self.old.clone(), _i32([0]), hq, hkv)
+        self.q, self.k, self.v = bf(n, hq, d), bf(n, hkv, d), bf(n, hkv, d)
+        self.step = bf(1, 1, hq, d), bf(1, 1, hkv, d), bf(1, 1, hkv, d)
+        self.cu, self.len, self.zero, self.err = _i32([0, n]), _i32([n]), _i32([0]), _i32([0])
+        self.w = torch.zeros(2, 1, hkv, pages * 64, device="cuda")
+        self.ws = hsa.prefill_weights_workspace(self.pool, 1, 64), hsa.decode_weights_workspace(self.pool, 1, 1, pages * 64)
+
+    def run(self):
+        hsa, w, kept = self.hsa, self.w[0], self.w[1]
+        self.pool.block_tables.copy_(self.old)
+        hsa.hsa_kv_append(self.pool, 0, self.k, self.v, self.cu, self.zero, self.zero, dev_err=self.err)
+        hsa.hsa_prefill_weights(self.pool, 0, self.q, self.cu, self.len, self.zero, 64, 0.1, w, workspace=self.ws[0],
+                                dev_err=self.err)
+        keep, left = hsa.hsa_kv_select(w, self.len, self.zero, self.budget, sinks=4, recent=16, reach=1, dev_err=self.err)
+        hsa.hsa_kv_compact(self.pool, 0, keep, left, self.zero, self.dst, w=w, w_dst=kept, dev_err=self.err)
+        self.pool.block_tables.copy_(self.new)
+        out = hsa.hsa_decode_attn_weights(self.pool, 0, *self.step, left, 0.1, kept, w_prev=kept, workspace=self.ws[1],
+                                          append=True, dev_err=self.err)
+        return keep, out, kept[..., :self.budget + 1].clone()
+
+
+def test_evictions_from_two_host_threads_at_once():
+    hsa = _hsa()
+    cases = [Cut(hsa, 50000, 32, 4, 1), Cut(hsa, 3001, 16, 2, 2)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got = c.run()
+                    s.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                        bad.append("values")
+        except Exception as e:  # noqa: BLE001 - told by the test's thread
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and all(int(c.err) == 0 for c in cases)
