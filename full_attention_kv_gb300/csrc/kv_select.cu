@@ -37,7 +37,7 @@
 // What bounds it: 16 rows of 262144 to 1000000 positions take 48 us (digits over all of them: 75)
 // for 6.4 of HBM: launch and sample 14, the pass over the longest row's sixth 17 (instructions: 64
 // registers a thread, nothing loaded ahead), digits 9, places 7.  128 rows of 8192 to 65536 with a
-// reach of 3: 40 (2.8).  8 rows of up to 2048: 7, latency.
+// reach of 3: 33 (2.8).  8 rows of up to 2048: 7, latency.
 #include <cooperative_groups.h>
 
 #include "hsa_device.cuh"
@@ -648,12 +648,12 @@ cudaError_t launch_select(SelectParams &p, int sms, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)p.R * p.heads;
     // CTAs a row: as many as fill the SMs, with one CTA of 1024 threads each (64 registers a thread:
-    // they take all of an SM's) or, for more rows than half of the SMs, two of 512; 2048 positions a
-    // CTA at least, and 2^20 at most, for a lane's 16-bit counters (api.cu holds w_stride to 2^22).
+    // they take all of an SM's) or, for more rows than SMs, two of 512 (128 rows: 33 us with a whole
+    // SM each, 40 with two halves of one that exchange); 2048 positions a CTA at least, and 2^20 at most, for a lane's 16-bit counters (api.cu holds w_stride to 2^22).
     // At most six: 23 clusters of six such CTAs find room at once, but 15 of seven or of eight, and
     // the sixteenth of 16 rows began 34 us late.
     const bool small = p.w_stride <= 8192;
-    const bool wide = rows * 2 <= sms && !small;
+    const bool wide = rows <= sms && !small;
     int64_t C = (wide ? 1 : 2) * sms / rows;
     C = C < kMaxCtas ? C : kMaxCtas;
     C = C < p.w_stride / 2048 ? C : p.w_stride / 2048;
