@@ -649,9 +649,10 @@ cudaError_t launch_select(SelectParams &p, int sms, cudaStream_t stream)
     const int64_t rows = (int64_t)p.R * p.heads;
     // CTAs a row: as many as fill the SMs, with one CTA of 1024 threads each (64 registers a thread:
     // they take all of an SM's) or, for more rows than SMs, two of 512 (128 rows: 33 us with a whole
-    // SM each, 40 with two halves of one that exchange); 2048 positions a CTA at least, and 2^20 at most, for a lane's 16-bit counters (api.cu holds w_stride to 2^22).
-    // At most six: 23 clusters of six such CTAs find room at once, but 15 of seven or of eight, and
-    // the sixteenth of 16 rows began 34 us late.
+    // SM each, 40 with two halves of one that exchange); 2048 positions a CTA at least (8192: the
+    // same), and 2^20 at most, for a lane's 16-bit counters (api.cu holds w_stride to 2^22).  At most
+    // six: 23 clusters of six such CTAs find room at once, but 15 of seven or of eight, and the
+    // sixteenth of 16 rows began 34 us late.
     const bool small = p.w_stride <= 8192;
     const bool wide = rows <= sms && !small;
     int64_t C = (wide ? 1 : 2) * sms / rows;

@@ -12,15 +12,15 @@
 // keys as lanes (S^T = K Q^T, the same tiles in shared memory with A and B exchanged): a thread
 // owns a key, and the sum over a tile's rows is its own.  Neither sums across threads.  The lse
 // goes in through the product: 16 more columns, three ones a key against the three bf16 parts of a
-// row's -lse.  (Read from shared memory, 16 bytes to a warp for every four columns, beside the products'
-// own reads there, pass 2 took 5% longer.)
+// row's -lse.  (Read from shared memory, 16 bytes to a warp for every four columns, beside the
+// products' own reads there, pass 2 took 5% longer.)
 //
 // Both: persistent, one CTA an SM; the 128-key tiles (two pages) of all (request, KV head) units
 // laid end to end and cut into equal ranges.  Warp 0 loads Q (up to four tiles of 128 rows) at a
 // unit's start and streams K; warps 1 and 2 issue the MMAs into four TMEM slots of 128 columns, one
 // a warpgroup; the four warpgroups of warps 4-19 take the (key tile, row tile) pairs in turn, a
-// unit's row tiles (1, 2 or 4 of them in the count: three as four) always the same ones.  In pass 2 the warpgroups of a key tile hand
-// their sums to the first of them through shared memory.
+// unit's row tiles (1, 2 or 4 of them in the count: three as four) always the same ones.  In pass 2
+// the warpgroups of a key tile hand their sums to the first of them through shared memory.
 // The states of a unit's CTAs lie side by side, and every order of summation is fixed.
 //
 // What bounds it: a warpgroup's chain a tile (2500 cycles for 128 columns; the exponentials alone 2048

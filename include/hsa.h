@@ -380,8 +380,9 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  * hsa_rope_kv_append), not the cache's.
  *
  * Weights are fp32 rows w[sequence][KV head][w_stride], one value a cache position, w_stride a
- * multiple of 4, at most 2^30 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and the query
- * heads of the KV head of exp(scale q.k - lse), lse the query's log of the sum over every key
+ * multiple of 4, at most 2^30 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and
+ * the query heads of the KV head of exp(scale q.k - lse), lse the query's log of the sum over
+ * every key
  * that it sees.  Both calls write w[j] = decay * w_prev[j] + sum; w_prev (same layout) may be
  * w itself, or NULL: nothing before.  Positions that are new in the call count nothing from
  * w_prev.  Entries past a sequence's tokens are left as they were.  Sums are fp32, in an
@@ -443,11 +444,12 @@ hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void
 
 /*
  * The positions that stay.  Request r is row seq_idx[r] of w ([batch, heads, w_stride]), with
- * kv_len[r] positions; w_stride at most 2^22 (else HSA_UNSUPPORTED_SHAPE).  For each of the `heads` rows, of n > budget positions stay the first
- * `sinks`, the last `recent` (sinks + recent <= budget) and, of the others, those of the
- * largest score until the budget is full: a position's score is the largest weight among
- * itself and its `reach` neighbours on each side (0 .. 7), NaN counting as -infinity and -0 as
- * 0; of equal scores the lowest position.  Of n <= budget positions all stay.
+ * kv_len[r] positions; w_stride at most 2^22 (else HSA_UNSUPPORTED_SHAPE).  For each of the
+ * `heads` rows, of n > budget positions stay the first `sinks`, the last `recent` (sinks +
+ * recent <= budget) and, of the others, those of the largest score until the budget is full: a
+ * position's score is the largest weight among itself and its `reach` neighbours on each side
+ * (0 .. 7), NaN counting as -infinity and -0 as 0; of equal scores the lowest position.  Of n <=
+ * budget positions all stay.
  *  keep     int32 [R, heads, budget]: the positions, ascending; -1 past new_len[r]
  *  new_len  int32 [R]: min(kv_len[r], budget); must not overlap kv_len (HSA_INVALID_ARG)
  * heads is Hkv where every KV head keeps its own, or 1 for weights that the caller has summed.
