@@ -382,9 +382,8 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  * Weights are fp32 rows w[sequence][KV head][w_stride], one value a cache position, w_stride a
  * multiple of 4, at most 2^30 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and
  * the query heads of the KV head of exp(scale q.k - lse), lse the query's log of the sum over
- * every key
- * that it sees.  Both calls write w[j] = decay * w_prev[j] + sum; w_prev (same layout) may be
- * w itself, or NULL: nothing before.  Positions that are new in the call count nothing from
+ * every key that it sees.  Both calls write w[j] = decay * w_prev[j] + sum; w_prev (same layout)
+ * may be w itself, or NULL: nothing before.  Positions that are new in the call count nothing from
  * w_prev.  Entries past a sequence's tokens are left as they were.  Sums are fp32, in an
  * order that does not change from call to call.
  */
