@@ -128,7 +128,6 @@ template <int NT>
 struct State {
     float m[NT][2], l[NT][2], lr[NT][2];  // lr: of the weights as the product takes them
     float o[kD / 16][NT][4];
-    int vexp;  // FP8: o is in units of 2^(vexp - 127); 0 before the first page with values
 };
 
 template <int NT>
@@ -148,35 +147,6 @@ __device__ __forceinline__ void clear(State<NT> &st)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 st.o[dt][n][e] = 0.f;
-    st.vexp = 0;
-}
-
-// 2^(e - 127), 0 for e <= 0.
-__device__ __forceinline__ float power(int e) { return __int_as_float(max(e, 0) << 23); }
-
-// V's scales go into P, which an FP8 page's product takes in fp16.  So they are taken relative to
-// a power of two that follows the largest scale of a page (the same in all lanes): at most 2^7 of
-// fp16's 2^16 above it, P's slack takes 2^8 more, and a row of small values keeps P's precision.
-template <int NT>
-__device__ __forceinline__ void follow_scale(State<NT> &st, const float *v_scale, int valid, int lane)
-{
-    const uint32_t a = lane < valid ? __float_as_uint(v_scale[lane]) : 0u;
-    const uint32_t b = lane + 32 < valid ? __float_as_uint(v_scale[lane + 32]) : 0u;
-    const uint32_t top = __reduce_max_sync(0xffffffffu, max(a, b));
-    const int e = min(max((int)(top >> 23), 1), 250);
-    if (top == 0 || (st.vexp != 0 && e <= st.vexp + 6))
-        return;
-    if (st.vexp != 0) {
-        const float f = power(127 + st.vexp - e);
-#pragma unroll
-        for (int dt = 0; dt < kD / 16; ++dt)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    st.o[dt][n][k] *= f;
-    }
-    st.vexp = e;
 }
 
 // The running maxima raised by a tile's (x, in log2 units, the same in all lanes of a column);
@@ -334,8 +304,14 @@ __device__ __forceinline__ void tile_bf16(State<NT> &st, const uint32_t (&qb)[NT
 }
 
 // A page of an FP8 layer (tile_fp8_sw in decode.cu says how its words feed the MMAs): fp16
-// products, a key's scale on its scores, V's folded into P (follow_scale).  PART: keys >= valid are
-// masked, their codes of V too.
+// products, a key's scale on its scores, V's folded into P.  PART: keys >= valid are masked, their
+// codes of V too.
+//
+// P times V's scale rounds to fp16, which is fine (2^-11 of itself, where bf16 has 2^-9) as long as
+// it stays clear of fp16's small end.  So a row's are taken in units of a power of two that puts
+// the page's largest between 2^14 and 2^15, and the page's product joins O in fp32, scaled back:
+// those down to 2^-28 of a page's largest keep all their bits, those below are off by 2^-39 of it.
+// A key of large V that has no weight, or of much weight that has no V, is no largest.
 template <int NT, bool E5M2, bool PART>
 __device__ __forceinline__ void tile_fp8(State<NT> &st, const uint32_t (&qb)[NT][kD / 16][2],
                                          const uint8_t *sK, const uint8_t *sV, const float *k_scale,
@@ -377,38 +353,65 @@ __device__ __forceinline__ void tile_fp8(State<NT> &st, const uint32_t (&qb)[NT]
     float x[NT][2];
     column_max<NT, MTS>(s, x);
     raise(st, x);
-    follow_scale(st, v_scale, PART ? valid : kTileKeys, lane);
-    const float f = power(254 - st.vexp);
+    // P V-scale in place of the scores, and each column's largest
+    float top[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MTS; ++mt) {
-        const int ka = mt * 16 + g, kb = ka + 8;
-        const float va = (!PART || ka < valid ? v_scale[ka] : 0.f) * f;
-        const float vb = (!PART || kb < valid ? v_scale[kb] : 0.f) * f;
-        uint32_t pb[NT][2];
+    for (int n = 0; n < NT; ++n) {
+        const float base0 = st.m[n][0] == -INFINITY ? 0.f : st.m[n][0];
+        const float base1 = st.m[n][1] == -INFINITY ? 0.f : st.m[n][1];
+        top[n][0] = top[n][1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float base0 = st.m[n][0] == -INFINITY ? 0.f : st.m[n][0];
-            const float base1 = st.m[n][1] == -INFINITY ? 0.f : st.m[n][1];
+        for (int mt = 0; mt < MTS; ++mt) {
+            const int ka = mt * 16 + g, kb = ka + 8;
+            const float va = !PART || ka < valid ? v_scale[ka] : 0.f;
+            const float vb = !PART || kb < valid ? v_scale[kb] : 0.f;
             const float p0 = fast_exp2(s[mt][n][0] - base0), p1 = fast_exp2(s[mt][n][1] - base1);
             const float p2 = fast_exp2(s[mt][n][2] - base0), p3 = fast_exp2(s[mt][n][3] - base1);
             st.l[n][0] += p0 + p2;
             st.l[n][1] += p1 + p3;
-            pb[n][0] = movmatrix_trans(pack_f16(p0 * va, p1 * va));
-            pb[n][1] = movmatrix_trans(pack_f16(p2 * vb, p3 * vb));
+            f2_split(f2_mul(f2_make(p0, p1), f2_make(va, va)), s[mt][n][0], s[mt][n][1]);
+            f2_split(f2_mul(f2_make(p2, p3), f2_make(vb, vb)), s[mt][n][2], s[mt][n][3]);
+            top[n][0] = fmax3(top[n][0], s[mt][n][0], s[mt][n][2]);
+            top[n][1] = fmax3(top[n][1], s[mt][n][1], s[mt][n][3]);
         }
-        // a thread's word holds the codes of keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of the 16
-        uint32_t mask = 0xffffffffu;
-        if (PART) {
-            const int k0 = mt * 16 + 2 * tq;
-            mask = (k0 < valid ? 0xffu : 0u) | (k0 + 1 < valid ? 0xff00u : 0u) |
-                   (k0 + 8 < valid ? 0xff0000u : 0u) | (k0 + 9 < valid ? 0xff000000u : 0u);
-        }
+    }
+    uint32_t pb[MTS][NT][2];
+    uint64_t back[NT];
 #pragma unroll
-        for (int dt = 0; dt < kD / 16; ++dt) {
-            const int da = dt * 16 + g, db = da + 8;
+    for (int n = 0; n < NT; ++n) {
+        // the exponents alone, two columns in a word (both are positive)
+        uint32_t t = __byte_perm(__float_as_uint(top[n][0]), __float_as_uint(top[n][1]), 0x7632);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+            t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+        const uint32_t e0 = max(t >> 7 & 0xffu, 15u), e1 = max(t >> 23, 15u);  // 2^(e - 127), or 2^-112
+        const uint64_t f = f2_make(__uint_as_float((268 - e0) << 23), __uint_as_float((268 - e1) << 23));
+        back[n] = f2_make(__uint_as_float((e0 - 14) << 23), __uint_as_float((e1 - 14) << 23));
+#pragma unroll
+        for (int mt = 0; mt < MTS; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // keys 0-7 of the 16, keys 8-15
+                float x0, x1;
+                f2_split(f2_mul(f2_make(s[mt][n][2 * e], s[mt][n][2 * e + 1]), f), x0, x1);
+                pb[mt][n][e] = movmatrix_trans(pack_f16(x0, x1));
+            }
+    }
+#pragma unroll
+    for (int dt = 0; dt < kD / 16; ++dt) {
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        const int da = dt * 16 + g, db = da + 8;
+#pragma unroll
+        for (int mt = 0; mt < MTS; ++mt) {
             uint32_t wa = *reinterpret_cast<const uint32_t *>(sV + da * 64 + ((mt ^ ((da >> 1) & 3)) << 4) + 4 * tq);
             uint32_t wb = *reinterpret_cast<const uint32_t *>(sV + db * 64 + ((mt ^ ((db >> 1) & 3)) << 4) + 4 * tq);
             if (PART) {
+                // a thread's word holds the codes of keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of the 16
+                const int k0 = mt * 16 + 2 * tq;
+                const uint32_t mask = (k0 < valid ? 0xffu : 0u) | (k0 + 1 < valid ? 0xff00u : 0u) |
+                                      (k0 + 8 < valid ? 0xff0000u : 0u) | (k0 + 9 < valid ? 0xff000000u : 0u);
                 wa &= mask;
                 wb &= mask;
             }
@@ -416,8 +419,14 @@ __device__ __forceinline__ void tile_fp8(State<NT> &st, const uint32_t (&qb)[NT]
                                    fp8x2_hi<E5M2>(wb)};
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                mma_f16_16816(st.o[dt][n], a, pb[n][0], pb[n][1]);
+                mma_f16_16816(acc[n], a, pb[mt][n][0], pb[mt][n][1]);
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)  // rows 2 tq, 2 tq + 1 of dimension da, then of db
+                f2_split(f2_fma(f2_make(acc[n][e], acc[n][e + 1]), back[n], f2_make(st.o[dt][n][e], st.o[dt][n][e + 1])),
+                         st.o[dt][n][e], st.o[dt][n][e + 1]);
     }
 }
 
@@ -665,17 +674,7 @@ __global__ void __launch_bounds__(Shape<FP8, NT, RH>::kThreads, 1)
             continue;
         }
         // ---- the end of the unit, or of this CTA's part of it ------------------------------
-        if constexpr (FP8 != 0) {
-            const float f = st.vexp != 0 ? power(st.vexp) : 1.f;
-#pragma unroll
-            for (int dt = 0; dt < kD / 16; ++dt)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        st.o[dt][n][e] *= f;
-        }
-        if constexpr (FP8 != 0) {  // the product takes P in fp16, finer than its sum needs to know
+        if constexpr (FP8 != 0) {  // fp16 roundings (tile_fp8): 2^-11 of a weight, the sum does without
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll

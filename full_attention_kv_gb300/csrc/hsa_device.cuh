@@ -371,7 +371,7 @@ __device__ __forceinline__ float fast_exp2(float x)
 }
 
 // ---------------------------------------------------------------- packed fp32 pairs
-// sm_100-family instructions that issue once for two fp32 lanes (f32x2 FMA / add)
+// sm_100-family instructions that issue once for two fp32 lanes (f32x2 FMA / multiply / add)
 // or fold two comparisons into one (three-input max).
 __device__ __forceinline__ uint64_t f2_make(float lo, float hi)
 {
@@ -389,6 +389,13 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t d;
     asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 
