@@ -375,9 +375,17 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  * full layer grows with its sequence, and these calls bound it: hsa_prefill_weights and
  * hsa_decode_attn_weights sum the softmax weight that each cached key gets, hsa_kv_select
  * chooses the positions of a budget, and hsa_kv_compact moves their rows to pages of their
- * own, after which the sequence goes on as one of that many cached tokens.  Keys keep the
- * rotation they were appended with: give later tokens their own positions (`positions` of
- * hsa_rope_kv_append), not the cache's.
+ * own, after which the full layers go on as those of a sequence of that many cached tokens.
+ *
+ * From then on a sequence has two lengths.  Calls on a full layer take new_len plus the tokens
+ * since.  Calls on a sliding layer take the number of all its tokens, as if nothing had been
+ * evicted, and so do hsa_window_safe_len and the rotary positions (`positions` of hsa_rope and
+ * hsa_rope_kv_append; keys keep the rotation they were appended with).  A ring's slots and
+ * window go by position: given the shorter length, the attention reads the wrong keys and the
+ * append overwrites slots that are still seen, and nothing flags it.  All full layers of a model
+ * share one block table and so one length: they are evicted together, each by its own weights.
+ * A page of an evicted sequence no longer holds 64 consecutive positions: give a prefix tree its
+ * pages before.
  *
  * Weights are fp32 rows w[sequence][KV head][w_stride], one value a cache position, w_stride a
  * multiple of 4, at most 2^30 (else HSA_INVALID_ARG).  An entry is the sum over the queries t and
@@ -468,7 +476,8 @@ hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_
  * HSA_UNSUPPORTED_SHAPE).  The destination pages are the caller's to hand out, and no request
  * of the call may read or write them otherwise: a sequence's old pages, which other sequences
  * may share, stay as they were.  Once every full layer is compacted, the destination pages
- * become the sequence's row of the block table and new_len[r] its cached tokens.
+ * become the sequence's row of the block table and new_len[r] its cached tokens in the full
+ * layers (sliding layers keep theirs, above).
  *  keep     int32 [R, heads, budget] as hsa_kv_select gives them, heads = Hkv or 1 (one
  *           list for every head; else HSA_UNSUPPORTED_SHAPE)
  *  w, w_dst [batch, Hkv, w_stride] or both NULL: the weights moved along, w_dst[seq][h][i] =
