@@ -413,6 +413,9 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  *  options    HSA_DECODE_APPEND (other bits: HSA_INVALID_ARG)
  *  scale      > 0
  * A key whose page cannot be read is absent (flagged as in hsa_decode_attn): its weight is 0.
+ * With T > 1 all T queries weigh, those of drafts that are rejected later among them, and a sum
+ * cannot be taken apart again.  Where they should not count, let w be another buffer than w_prev,
+ * and call again from the same w_prev with the accepted tokens alone (that call can append them).
  */
 size_t hsa_decode_weights_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
                                           int32_t w_stride);

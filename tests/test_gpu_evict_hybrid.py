@@ -2,12 +2,13 @@
 from its shorter length, the sliding layer beside it goes on from the true one, past the ring's end
 and through a second eviction.  Both layers' outputs against 64 bits, the ring bit for bit.  The
 prompt comes in two chunks, the second weighed on the first one's weights; an FP8 layer's by the
-append, weighed by its last token's decode."""
+append, weighed by its last token's decode.  And a verify step made again for the accepted tokens."""
 import pytest
 import torch
 
 import evict_ref as ref
 import test_gpu_evict_run as run
+import test_gpu_weigh as weigh
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +144,16 @@ def test_full_layer_evicted_beside_a_ring(fmt):
             s.evict(192, sinks=1, recent=64, reach=0)
     s.check_ring()
     assert int(s.err) == 0 and s.n == [192 + 69] * 2 and length == [840, 473]
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+@pytest.mark.parametrize("accepted", [1, 2, 3])
+def test_verify_step_again_for_the_accepted_tokens(fmt, accepted):
+    """w_prev kept: the accepted tokens' weights without the rejected ones'."""
+    s = weigh.Step(weigh._hsa(), [300, 64, 1000], 4, HQ, HKV, fmt)
+    s.check(s.run())
+    s.T = accepted
+    s.q, s.k, s.v = (x[:, :accepted].contiguous() for x in (s.q, s.k, s.v))
+    s.w.fill_(-7.0)
+    s.check(s.run(append=True))
+    assert int(s.err) == 0
