@@ -111,6 +111,14 @@ int device_sms()
     return sms;
 }
 
+bool heads_ok(const hsa_pools *p)
+{
+    if (p->Hkv <= 0 || p->Hq <= 0 || p->Hq % p->Hkv != 0)
+        return false;
+    const int G = p->Hq / p->Hkv;
+    return G == 1 || G == 2 || G == 4 || G == 8;
+}
+
 hsa_status check_pools(const hsa_pools *p, int32_t layer)
 {
     if (!p || !p->layer_is_full || !p->k || !p->v)
@@ -119,10 +127,7 @@ hsa_status check_pools(const hsa_pools *p, int32_t layer)
         return HSA_INVALID_ARG;
     if (p->d != 128 || p->page_size != 64 || p->W < 64 || p->W > 256 || p->W % 64 != 0)
         return HSA_UNSUPPORTED_SHAPE;
-    if (p->Hkv <= 0 || p->Hq <= 0 || p->Hq % p->Hkv != 0)
-        return HSA_UNSUPPORTED_SHAPE;
-    const int G = p->Hq / p->Hkv;
-    if (G != 1 && G != 2 && G != 4 && G != 8)
+    if (!heads_ok(p))
         return HSA_UNSUPPORTED_SHAPE;
     if (p->batch < 0 || p->num_blocks < 0 || p->max_blocks < 0 || p->n_ring_rows < 0)
         return HSA_INVALID_ARG;
@@ -713,10 +718,15 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
     return e == cudaSuccess ? HSA_OK : HSA_CUDA_ERROR;
 }
 
+static bool stride_ok(int32_t w_stride)
+{
+    return w_stride >= 0 && w_stride % 4 == 0 && w_stride <= (1 << 30);
+}
+
 // The weights' rows of an eviction call: fp32, w_stride a multiple of 4.
 static hsa_status check_weights(const float *w_prev, float decay, const float *w, int32_t w_stride)
 {
-    if (w_stride < 0 || w_stride % 4 != 0 || w_stride > (1 << 30) || !std::isfinite(decay))
+    if (!stride_ok(w_stride) || !std::isfinite(decay))
         return HSA_INVALID_ARG;
     return w && aligned16(w) && aligned16(w_prev) ? HSA_OK : HSA_INVALID_ARG;
 }
@@ -730,7 +740,7 @@ static bool floats_apart(const float *a, const float *b, int64_t n, bool own)
 size_t hsa_decode_weights_workspace_bytes(const hsa_pools *pools, int32_t B, int32_t T,
                                           int32_t w_stride)
 {
-    if (!pools || pools->Hkv <= 0 || pools->Hq <= 0 || B < 0 || T < 1 || w_stride < 0)
+    if (!pools || !heads_ok(pools) || B < 0 || T < 1 || T > 4 || !stride_ok(w_stride))
         return 0;
     return hsa::weigh_layout(std::max(device_sms(), 1), B, T, pools->Hq / pools->Hkv, pools->Hkv,
                              w_stride).total;
@@ -813,7 +823,7 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
 
 size_t hsa_prefill_weights_workspace_bytes(const hsa_pools *pools, int32_t R, int32_t window)
 {
-    if (!pools || pools->Hkv <= 0 || pools->Hq <= 0 || R < 0 || window < 1)
+    if (!pools || !heads_ok(pools) || R < 0 || window < 1 || window > 64)
         return 0;
     return hsa::prompt_workspace_bytes(std::max(device_sms(), 1), R, pools->Hkv);
 }

@@ -405,7 +405,8 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  *             (HSA_DEVERR_BAD_LEN) and left out, its rows of out and w as they were, and not
  *             appended
  *  workspace  at least hsa_decode_weights_workspace_bytes() bytes for this B, T and w_stride;
- *             its contents do not matter before or after.  It holds every score in fp32:
+ *             its contents do not matter before or after (0 bytes: a shape that the call
+ *             refuses).  It holds every score in fp32:
  *             4 * T * Hq * B * w_stride bytes (T and Hq / Hkv's product rounded up to a
  *             power of two) and the partial states.  Calls sharing one must
  *             not run concurrently.
