@@ -816,7 +816,7 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
     p.fp8 = fmt == HSA_KV_E5M2 ? 2 : fmt ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.decay = decay;
-    return hsa::launch_weigh(tmK, tmV, p, ctas, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return hsa::launch_weigh(tmK, tmV, p, sms, max_ctas, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? HSA_OK
                : HSA_CUDA_ERROR;
 }

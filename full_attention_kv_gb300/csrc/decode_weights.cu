@@ -1042,7 +1042,7 @@ int score_rows(int rows)
 
 template <int FP8, int NT, int RH>
 cudaError_t launch_attend(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &p, int ctas,
-                          int sms, cudaStream_t stream)
+                          int join_ctas, cudaStream_t stream)
 {
     using S = Shape<FP8, NT, RH>;
     const size_t smem = sizeof(AttendSmem<FP8, NT, RH>) + 1024;
@@ -1064,7 +1064,7 @@ cudaError_t launch_attend(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
     e = cudaLaunchKernelEx(&cfg, attend_kernel<FP8, NT, RH>, tmK, tmV, p);
     if (e != cudaSuccess)
         return e;
-    cfg.gridDim = dim3((unsigned)(kJoinCtas * sms));
+    cfg.gridDim = dim3((unsigned)join_ctas);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     void (*join)(WeighParams, int, int, int) = p.srow == 2   ? join_kernel<2, 1>
@@ -1076,13 +1076,13 @@ cudaError_t launch_attend(const CUtensorMap &tmK, const CUtensorMap &tmV, const 
 }
 
 template <int FP8>
-cudaError_t launch_rows(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &p, int ctas, int sms,
-                        cudaStream_t stream)
+cudaError_t launch_rows(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &p, int ctas,
+                        int join_ctas, cudaStream_t stream)
 {
     const int rows = p.G * p.T;
-    return rows <= 8    ? launch_attend<FP8, 1, 1>(tmK, tmV, p, ctas, sms, stream)
-           : rows <= 16 ? launch_attend<FP8, 2, 1>(tmK, tmV, p, ctas, sms, stream)
-                        : launch_attend<FP8, 2, 2>(tmK, tmV, p, ctas, sms, stream);
+    return rows <= 8    ? launch_attend<FP8, 1, 1>(tmK, tmV, p, ctas, join_ctas, stream)
+           : rows <= 16 ? launch_attend<FP8, 2, 1>(tmK, tmV, p, ctas, join_ctas, stream)
+                        : launch_attend<FP8, 2, 2>(tmK, tmV, p, ctas, join_ctas, stream);
 }
 
 }  // namespace
@@ -1098,14 +1098,16 @@ WeighLayout weigh_layout(int ctas, int B, int T, int G, int Hkv, int w_stride)
     return lay;
 }
 
-cudaError_t launch_weigh(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &params, int ctas,
-                         int sms, cudaStream_t stream)
+cudaError_t launch_weigh(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &params, int sms,
+                         int max_ctas, cudaStream_t stream)
 {
+    const int most = max_ctas > 0 ? max_ctas : INT32_MAX;  // of each launch
+    const int ctas = sms < most ? sms : most, join_ctas = kJoinCtas * sms < most ? kJoinCtas * sms : most;
     WeighParams p = params;
     p.srow = score_rows(p.G * p.T);
-    return p.fp8 == 2   ? launch_rows<2>(tmK, tmV, p, ctas, sms, stream)
-           : p.fp8 == 1 ? launch_rows<1>(tmK, tmV, p, ctas, sms, stream)
-                        : launch_rows<0>(tmK, tmV, p, ctas, sms, stream);
+    return p.fp8 == 2   ? launch_rows<2>(tmK, tmV, p, ctas, join_ctas, stream)
+           : p.fp8 == 1 ? launch_rows<1>(tmK, tmV, p, ctas, join_ctas, stream)
+                        : launch_rows<0>(tmK, tmV, p, ctas, join_ctas, stream);
 }
 
 }  // namespace hsa

@@ -241,7 +241,7 @@ struct WeighLayout {             // byte offsets in the workspace
 };
 WeighLayout weigh_layout(int ctas, int B, int T, int G, int Hkv, int w_stride);
 cudaError_t launch_weigh(const CUtensorMap &tmK, const CUtensorMap &tmV, const WeighParams &p,
-                         int ctas, int sms, cudaStream_t stream);
+                         int sms, int max_ctas, cudaStream_t stream);
 
 struct PromptParams {            // prefill_weights.cu
     const int32_t *cu_rows;      // [R+1]

@@ -410,7 +410,7 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  *             4 * T * Hq * B * w_stride bytes (T and Hq / Hkv's product rounded up to a
  *             power of two) and the partial states.  Calls sharing one must
  *             not run concurrently.
- *  max_ctas   as in hsa_decode_attn
+ *  max_ctas   as in hsa_decode_attn, of each of the two launches
  *  options    HSA_DECODE_APPEND (other bits: HSA_INVALID_ARG)
  *  scale      > 0
  * A key whose page cannot be read is absent (flagged as in hsa_decode_attn): its weight is 0.
