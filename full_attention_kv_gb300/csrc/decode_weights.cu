@@ -535,6 +535,8 @@ __global__ void __launch_bounds__(Shape<FP8, NT, RH>::kThreads, 1)
         // ------------------------------------------------------------------------ producer
         // lane l finds the pool row of page start + l, 32 pages at a time and a batch ahead; the
         // whole warp waits for the stages and one elected lane issues them
+        if (kWithholdLoads)
+            return;
         const uint64_t pol = policy_evict_first();
         const int64_t cb = fp8_codes_bytes(p.num_blocks, p.Hkv);
         auto pool_row = [&](const UnitWalk &w) -> int64_t {

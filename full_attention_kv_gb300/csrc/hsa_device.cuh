@@ -98,6 +98,14 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 
+// Test-only builds (never the product library) issue no load and no arrival for one: what waits for
+// a load runs out after HSA_WAIT_NS, and the kernel must flag HSA_DEVERR_TIMEOUT and return.
+#ifdef HSA_TEST_WITHHOLD_LOADS
+constexpr bool kWithholdLoads = true;
+#else
+constexpr bool kWithholdLoads = false;
+#endif
+
 // Bounded wait whose polls sleep (up to 20 us each) until the phase completes.
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity)
 {

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
         }
         __syncthreads();
         auto fetch = [&](int s0) {
-            if (tid == 0 && s0 < sh.n) {
+            if (tid == 0 && s0 < sh.n && !kWithholdLoads) {
                 const int n = min(kPages, sh.n - s0);
                 mbar_arrive_expect_tx(&sh.full, n * kPageBytes);
                 for (int e = 0; e < n; ++e)

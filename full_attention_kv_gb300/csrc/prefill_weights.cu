@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         int issued = 0, units = 0;
         bool ok = true;
-        for (int64_t i = i0; i < i1 && ok; ++units) {
+        for (int64_t i = kWithholdLoads ? i1 : i0; i < i1 && ok; ++units) {
             const int64_t end = i + min((int64_t)(w.nt - w.j), i1 - i);
             const int nq = row_tiles(w);
             if (units > 0 && !(ok = warp_wait(&sh.q_empty, (uint32_t)(units - 1) & 1)))
