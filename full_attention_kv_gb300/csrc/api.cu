@@ -906,8 +906,8 @@ hsa_status hsa_kv_select(const float *w, int32_t w_stride, int32_t batch, int32_
         return st;
     if (!kv_len || !seq_idx || !new_len || (!keep && budget > 0) || (int64_t)R * heads > (1 << 27))
         return HSA_INVALID_ARG;
-    // every CTA of a request reads its length, the first writes the new one
-    if (new_len < kv_len + R && kv_len < new_len + R)
+    // every CTA of a request reads its length and its sequence, the first writes the new length
+    if ((new_len < kv_len + R && kv_len < new_len + R) || (new_len < seq_idx + R && seq_idx < new_len + R))
         return HSA_INVALID_ARG;
     hsa::SelectParams p{};
     p.w = w;

@@ -462,7 +462,7 @@ hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void
  * (0 .. 7), NaN counting as -infinity and -0 as 0; of equal scores the lowest position.  Of n <=
  * budget positions all stay.
  *  keep     int32 [R, heads, budget]: the positions, ascending; -1 past new_len[r]
- *  new_len  int32 [R]: min(kv_len[r], budget); must not overlap kv_len (HSA_INVALID_ARG)
+ *  new_len  int32 [R]: min(kv_len[r], budget); must overlap neither kv_len nor seq_idx (HSA_INVALID_ARG)
  * heads is Hkv where every KV head keeps its own, or 1 for weights that the caller has summed.
  * kv_len[r] outside 0 .. w_stride (HSA_DEVERR_BAD_LEN) and a bad sequence (HSA_DEVERR_BAD_SEQ)
  * are flagged: nothing stays of them (new_len 0).
