@@ -718,6 +718,10 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
     return e == cudaSuccess ? HSA_OK : HSA_CUDA_ERROR;
 }
 
+// A scale by which a log of a sum may be divided and multiplied in fp32 (the prompt's goes through
+// the product in units of a raw score).
+static bool weigh_scale_ok(float scale) { return scale >= 0x1p-96f && scale <= 0x1p96f; }
+
 static bool stride_ok(int32_t w_stride)
 {
     return w_stride >= 0 && w_stride % 4 == 0 && w_stride <= (1 << 30);
@@ -763,7 +767,7 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
         return st;
     if (!pools->layer_is_full[layer])
         return HSA_UNSUPPORTED_SHAPE;
-    if (!(scale > 0.f) || !std::isfinite(scale))
+    if (!weigh_scale_ok(scale))
         return HSA_INVALID_ARG;
     if (done)
         return HSA_OK;
@@ -840,7 +844,7 @@ hsa_status hsa_prefill_weights(const hsa_pools *pools, int32_t layer, const void
         return st;
     if (!pools->layer_is_full[layer] || layer_fp8(pools, layer) || window > 64)
         return HSA_UNSUPPORTED_SHAPE;
-    if (R < 0 || rows < 0 || window < 1 || !(scale > 0.f) || !std::isfinite(scale))
+    if (R < 0 || rows < 0 || window < 1 || !weigh_scale_ok(scale))
         return HSA_INVALID_ARG;
     if (R == 0 || rows == 0)
         return HSA_OK;

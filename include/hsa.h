@@ -412,7 +412,7 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  *             not run concurrently.
  *  max_ctas   as in hsa_decode_attn, of each of the two launches
  *  options    HSA_DECODE_APPEND (other bits: HSA_INVALID_ARG)
- *  scale      > 0
+ *  scale      2^-96 .. 2^96 (else HSA_INVALID_ARG)
  * A key whose page cannot be read is absent (flagged as in hsa_decode_attn): its weight is 0.
  * With T > 1 all T queries weigh, those of drafts that are rejected later among them, and a sum
  * cannot be taken apart again.  Where they should not count, let w be another buffer than w_prev,
@@ -437,7 +437,7 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
  * kv_len[r] - n + i.  The weights are row seq_idx[r] of w ([pools->batch, Hkv, w_stride]).
  *  window     1 .. 64 (else HSA_UNSUPPORTED_SHAPE)
  *  workspace  at least hsa_prefill_weights_workspace_bytes(); as above
- *  decay finite, scale > 0
+ *  decay finite, scale 2^-96 .. 2^96 (else HSA_INVALID_ARG), scores scale q.k below 2^30
  * bf16 full layers (a sliding or FP8 layer: HSA_UNSUPPORTED_SHAPE, as prefill itself refuses
  * FP8).  A sequence may appear in at most one request per call.  A request without rows is left
  * out.  So is one that is flagged: offsets out of order or past `rows`, more rows than
