@@ -22,11 +22,13 @@
 // scores become weights and are summed over the rows by shuffles.  Eight rows of output are an
 // item of their own.  The order of every sum is fixed by the sizes.
 //
-// What bounds it: HBM, the reads of K and V and the scores' way out and in.  32 sequences of 8192 to
-// 65536 tokens, 8 rows a head: attend 429 us (6.3 TB/s of K and V, 0.92 of a copy's rate, scores
-// beside them), join 44.  32 rows a head (16 sequences x 4 tokens): 87 and 30; about
-// 10 us of it are the kernel's start and end, in the join instructions (issue 50%).  FP8: 54 and 20, the
-// same.  (Six consuming warps and stages, FP8 six to twelve: no change.)
+// What bounds it: HBM, the reads of K and V and the scores' way out and in.  Attend and, behind it,
+// join: 32 sequences of 8192 to 65536 tokens, 8 rows a head: 424 us (6.4 TB/s of K and V, 0.94 of a
+// copy's rate, scores beside them) and 41.  32 rows a head (16 sequences of 3001 to 20000 x 4 tokens):
+// 83 and 27; about 10 us of it are the kernel's start and end, in the join instructions (issue 50%).
+// FP8, 8 sequences of 8192 to 65536: 50 and 20, the same; 32 rows a head as above: 92 and 22, one warp
+// a scheduler, bound by its chain a page.  (Six consuming warps and stages, FP8 six to twelve: no
+// change.)
 #include "decode_tile.cuh"
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
@@ -233,6 +235,8 @@ __device__ __forceinline__ void store_scores(const float (&s)[MTS][NT][4], float
 
 // A bf16 tile of 16 MTS keys in shared memory (rows of the swizzle: tile_rows).  Keys >= valid
 // and, of the new tokens (causal), those after a row's own are masked: row r sees key <= r / G.
+// P rounds to bf16 for the product with V, 2^-9 of itself whatever its size; the output is divided
+// by the sum of the rounded ones (lr), the weights' lse takes the sum in fp32 (l).
 template <int NT, int MTS>
 __device__ __forceinline__ void tile_bf16(State<NT> &st, const uint32_t (&qb)[NT][kD / 16][2],
                                           uint32_t sK, uint32_t sV, int tile_rows, int valid,
@@ -430,7 +434,8 @@ __device__ __forceinline__ void tile_fp8(State<NT> &st, const uint32_t (&qb)[NT]
     }
 }
 
-// Q as the B operand: column g of n-tile n is row col0 + 8 n + g (zero past G T).
+// Q as the B operand: column g of n-tile n is row col0 + 8 n + g (zero past G T).  F16: for an FP8
+// page, whose codes are exact in fp16 (so is q between 2^-14 and 65504).
 template <int NT, bool F16>
 __device__ __forceinline__ void load_q(const WeighParams &p, int b, int h, int col0, int lane,
                                        uint32_t (&qb)[NT][kD / 16][2])

@@ -232,7 +232,7 @@ struct WeighParams {             // decode_weights.cu
     int32_t *dev_err;
     uint4 *k_pool, *v_pool;      // this layer's pools (FP8 scales; the append)
     int32_t max_blocks, num_blocks, B, Hkv, w_stride;
-    int32_t T, G, srow;          // srow: G T rounded up to even
+    int32_t T, G, srow;          // srow: G T rounded up to a power of two, at least 2
     int32_t append, fp8;         // fp8: 0 bf16, 1 E4M3, 2 E5M2
     float scale_log2, decay;
 };

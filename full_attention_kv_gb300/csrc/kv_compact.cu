@@ -12,8 +12,9 @@
 // at a time.  A lane then puts together the same four keys of eight dimensions: two rows of 64 bytes
 // a warp, which meet 32 banks whatever the keys, and leave as 128 contiguous bytes.
 //
-// What bounds it: HBM.  16 requests of 4096 rows x 4 heads, bf16: 42 us, 0.95 of a copy's rate.  FP8 (8
-// requests of 2000 rows out of 3000 to 9000): 19 us, 38 MB read for 17 kept, and the pages' latency.
+// What bounds it: HBM.  16 requests of 4096 rows x 4 heads, bf16: 45 us, 0.89 of a copy's rate.  FP8 (8
+// requests of 2000 rows out of 3000 to 9000): 19 us from a cold L2 (12 where it holds the pages), 38
+// MB read for 17 kept, and the pages' latency.
 #include "fp8_kv.cuh"
 #include "hsa_device.cuh"
 #include "hsa_internal.h"

@@ -34,10 +34,11 @@
 // Then every key above that value stays, and the first `need` keys equal to it, each key's place
 // being the number that stay before it (warp scans over contiguous ranges).
 //
-// What bounds it: 16 rows of 262144 to 1000000 positions take 48 us (digits over all of them: 75)
-// for 6.4 of HBM: launch and sample 14, the pass over the longest row's sixth 17 (instructions: 64
-// registers a thread, nothing loaded ahead), digits 9, places 7.  128 rows of 8192 to 65536 with a
-// reach of 3: 33 (2.8).  8 rows of up to 2048: 7, latency.
+// What bounds it (the kernel from a cold L2; calls one after the other: 45, 31 and 9 to 10): 16 rows
+// of 262144 to 1000000 positions take 48 us (digits over all of them: 75) for 6.4 of HBM: launch and
+// sample 14, the pass over the longest row's sixth 17 (instructions: 64 registers a thread, nothing
+// loaded ahead), digits 9, places 7.  128 rows of 8192 to 65536 with a reach of 3: 33 (2.8).  8 rows
+// of up to 2048: 7, latency.
 #include <cooperative_groups.h>
 
 #include "hsa_device.cuh"

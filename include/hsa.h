@@ -101,7 +101,8 @@ typedef int hsa_status;
  *                    layers; prefill rejects them (HSA_UNSUPPORTED_SHAPE), as does a
  *                    sliding layer flagged FP8.  Decode multiplies in fp16 there:
  *                    q, the new rows and |v| * 256 / 448 (E4M3) or |v| * 256 / 57344
- *                    (E5M2) must stay within fp16 range.
+ *                    (E5M2) must stay within fp16 range (hsa_decode_attn_weights: q
+ *                    alone).
  * Supported shape: d = 128, page_size = 64, W a multiple of 64 in [64, 256],
  * Hq a multiple of Hkv with Hq / Hkv in {1, 2, 4, 8}.
  */
@@ -408,7 +409,7 @@ hsa_status hsa_prefill_attn(const hsa_pools *pools, int32_t layer, const void *q
  *             its contents do not matter before or after (0 bytes: a shape that the call
  *             refuses).  It holds every score in fp32:
  *             4 * T * Hq * B * w_stride bytes (T and Hq / Hkv's product rounded up to a
- *             power of two) and the partial states.  Calls sharing one must
+ *             power of two, at least 2) and the partial states.  Calls sharing one must
  *             not run concurrently.
  *  max_ctas   as in hsa_decode_attn, of each of the two launches
  *  options    HSA_DECODE_APPEND (other bits: HSA_INVALID_ARG)
@@ -439,7 +440,7 @@ hsa_status hsa_decode_attn_weights(const hsa_pools *pools, int32_t layer, const 
  *  workspace  at least hsa_prefill_weights_workspace_bytes(); as above
  *  decay finite, scale 2^-96 .. 2^96 (else HSA_INVALID_ARG), scores scale q.k below 2^30
  * bf16 full layers (a sliding or FP8 layer: HSA_UNSUPPORTED_SHAPE, as prefill itself refuses
- * FP8).  A sequence may appear in at most one request per call.  A request without rows is left
+ * FP8; an FP8 layer's prompt is weighed by hsa_decode_attn_weights of its last tokens).  A sequence may appear in at most one request per call.  A request without rows is left
  * out.  So is one that is flagged: offsets out of order or past `rows`, more rows than
  * kv_len[r], kv_len[r] negative or past w_stride (HSA_DEVERR_BAD_LEN), a bad sequence
  * (HSA_DEVERR_BAD_SEQ).  A key whose page cannot be read is flagged and absent.
